@@ -311,6 +311,113 @@ int profk_stage_filter(const float* x, int64_t N, float tau_val, int64_t tau_idx
  */
 int profk_read_ceiling(const float* x, int64_t N, int32_t blocks_per_cu, uint64_t* out_fold, void* stream);
 
+/*
+ * Language-model operators: rows of logits turned into a choice.  Logits are
+ * fp32, fp16 or bf16 (PROFK_FP32 / _FP16 / _BF16), row r at logits + r*ld
+ * elements, any alignment of the element's own size.  Everything is enqueued on
+ * `stream` with no host wait and no allocation.  `scratch` is the CALLER's
+ * device memory, 256-byte aligned, of at least the size the operator's scratch
+ * query returns; it needs no initial contents, holds nothing between calls, and
+ * may be reused by the next call on the same stream.  So a call is capturable
+ * without a call before it, and a captured graph may be replayed beside eager
+ * calls that use scratch of their own.  PROFK_ESCRATCH: scratch_bytes is less
+ * than the query says.
+ */
+#define PROFK_FP32 0
+#define PROFK_FP16 1
+#define PROFK_BF16 2
+
+/*
+ * profk_sample_tokens: one token per row of logits[B][V] from a given uniform
+ * number.  Order a row by value descending, then lower index (-0.0 = +0.0), and
+ * let w_i = exp((l_i - max) / temperature).  Then
+ *   K = the first top_k entries (top_k <= 0 or >= V: all)
+ *   P = the shortest prefix of K with mass >= top_p * mass(K) (at least one
+ *       entry; top_p >= 1 or NaN: all of K)
+ *   F = the entries of P with w_i >= min_p (at least one; min_p <= 0 or NaN: all of P)
+ *   token = the first entry of F, in the order, where the cumulative mass of F
+ *       exceeds u * mass(F); logprob = ln(w_token / mass(F))
+ * temperature <= 0 (or NaN) keeps the first entry alone.  u is taken into
+ * [0, 1 - 2^-24], NaN as 0.  Entries of +inf share all the mass.  A row that
+ * holds a NaN gives token -1 and logprob NaN; a row with no entry above -inf
+ * gives token -1 and logprob -inf.  Weights are held as integers, in units of
+ * 2^-F of the largest, F = min(50, 62 - ceil(log2 V)): the token does not
+ * depend on how the work is split, and an entry below 2^-F of the largest
+ * counts as absent.
+ *   u             device, B floats
+ *   how           settings: each row_* pointer (device, B values) where not NULL,
+ *                 else the plain field for every row
+ *   out_tokens    device, B int64; out_logprobs device, B floats
+ *   Limits: V <= 2^24, B < 2^31 (PROFK_EUNSUPPORTED).  B = 0 does nothing.
+ */
+typedef struct profk_sampling {
+  float temperature, top_p, min_p;
+  int32_t reserved;
+  int64_t top_k;
+  const float* row_temperature;
+  const int64_t* row_top_k;
+  const float* row_top_p;
+  const float* row_min_p;
+} profk_sampling;
+
+int64_t profk_sample_tokens_scratch(int64_t B, int64_t V); /* bytes, or PROFK_EINVAL */
+
+int profk_sample_tokens(const void* logits, int32_t dtype, int64_t B, int64_t V, int64_t ld, const float* u,
+                        const profk_sampling* how, int64_t* out_tokens, float* out_logprobs, void* scratch,
+                        int64_t scratch_bytes, void* stream);
+
+/*
+ * profk_route_tokens: the k experts of each of T tokens from router logits
+ * [T][E].  A row is live when its mask byte is nonzero (mask NULL: every row)
+ * and it has an entry above -inf.  For a live row, p = softmax(row); its experts
+ * are the first k entries by value descending, then lower index (the order of
+ * profk_topk, NaN first), entries of -inf never; the gate weights are p there,
+ * divided by their sum with `normalize`.  Slots without an expert, and all slots
+ * of a row that is not live, hold expert -1 and weight 0.
+ *   out_weights   device, T*k floats;  out_experts device, T*k int64
+ *   out_counts    device, E int64: how often each expert was chosen
+ *   out_rows      device, 1 int64: n, the live rows
+ *   out_loss      device, 1 float, or NULL: the balance loss
+ *                 E * sum_e f_e P_e, f_e = counts_e / (n k), P_e = sum_t p_te / n
+ *                 (0 when n = 0)
+ *   Limits: E <= 1024, k <= 64, T < 2^31 (PROFK_EUNSUPPORTED); k <= E.
+ *   The loss has the same bits on every run.
+ */
+int64_t profk_route_scratch(int64_t T, int64_t E); /* bytes, or PROFK_EINVAL */
+
+int profk_route_tokens(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                       int64_t k, int32_t normalize, float* out_weights, int64_t* out_experts, int64_t* out_counts,
+                       int64_t* out_rows, float* out_loss, void* scratch, int64_t scratch_bytes, void* stream);
+
+/*
+ * profk_route_tokens_grad: the gradient of a scalar with respect to the router
+ * logits, from its gradients with respect to the gate weights (d_weights, T*k
+ * floats, or NULL) and to the balance loss (with counts and rows as the forward
+ * pass gave them, or both NULL: no such part).  The loss's gradient is
+ * d_loss_scale times *d_loss (device, or NULL: 1).  The counts are constants.
+ * Rows that are not live get 0.
+ *   experts       as the forward pass gave them; entries outside [0, E) are no
+ *                 slots (NULL only with d_weights NULL)
+ *   out_d_logits  device, T*E contiguous, of the logits' type, rounded once
+ */
+int profk_route_tokens_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                            int64_t k, int32_t normalize, const int64_t* experts, const float* d_weights,
+                            const int64_t* counts, const int64_t* rows, const float* d_loss, float d_loss_scale,
+                            void* out_d_logits, void* stream);
+
+/*
+ * profk_balance_loss / profk_balance_loss_grad: the same loss, counts and
+ * gradient for a choice made elsewhere (experts, T*k int64; entries outside
+ * [0, E) are dropped slots: not counted, and n k stays the divisor).
+ */
+int profk_balance_loss(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                       const int64_t* experts, int64_t k, int64_t* out_counts, int64_t* out_rows, float* out_loss,
+                       void* scratch, int64_t scratch_bytes, void* stream);
+
+int profk_balance_loss_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                            int64_t k, const int64_t* counts, const int64_t* rows, const float* d_loss,
+                            float d_loss_scale, void* out_d_logits, void* stream);
+
 /* Message for a status code (thread-local detail for PROFK_EHIP). */
 const char* profk_strerror(int code);
 

@@ -11,6 +11,11 @@ Functions mirror include/profk.h:
   topk_batched(x2d, k, eps=1e-3, seed=0, options=None, stats=False)
   solve(N, k, eps=1e-3, options=None) -> dict
   stage_sample / stage_threshold / stage_filter  (one stage each, for inspection)
+
+Language-model operators (operators.py), rows of logits turned into a choice:
+  sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None)
+  route_tokens(logits, k, normalize=True, mask=None, balance=False) and route_tokens_grad
+  balance_loss(logits, experts, mask=None) and balance_loss_grad
 """
 from __future__ import annotations
 
@@ -35,7 +40,9 @@ EXPORTED = ("profk_topk", "profk_topk_ex", "profk_topk_approx", "profk_topk_appr
             "profk_topk_batched_ex", "profk_topk_batched_approx",
             "profk_solve",
             "profk_stage_sample", "profk_stage_threshold", "profk_stage_batched_sample", "profk_stage_filter",
-            "profk_read_ceiling", "profk_strerror", "profk_release")
+            "profk_read_ceiling", "profk_strerror", "profk_release",
+            "profk_sample_tokens_scratch", "profk_sample_tokens", "profk_route_scratch", "profk_route_tokens",
+            "profk_route_tokens_grad", "profk_balance_loss", "profk_balance_loss_grad")
 
 
 class Options(ctypes.Structure):
@@ -124,6 +131,19 @@ def load_library():
     lib.profk_stage_filter.argtypes = [vp, i64, ctypes.c_float, i64, i64, vp, vp, vp]
     lib.profk_read_ceiling.argtypes = [vp, i64, i32, vp, vp]
     lib.profk_read_ceiling.restype = ctypes.c_int
+    lib.profk_sample_tokens_scratch.argtypes = [i64, i64]
+    lib.profk_sample_tokens.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp]
+    lib.profk_route_scratch.argtypes = [i64, i64]
+    lib.profk_route_tokens.argtypes = [vp, i32, i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.profk_route_tokens_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, vp, ctypes.c_float,
+                                            vp, vp]
+    lib.profk_balance_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, vp]
+    lib.profk_balance_loss_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, ctypes.c_float, vp, vp]
+    for name in ("profk_sample_tokens", "profk_route_tokens", "profk_route_tokens_grad", "profk_balance_loss",
+                 "profk_balance_loss_grad"):
+        getattr(lib, name).restype = ctypes.c_int
+    for name in ("profk_sample_tokens_scratch", "profk_route_scratch"):
+        getattr(lib, name).restype = i64
     lib.profk_strerror.argtypes = [ctypes.c_int]
     lib.profk_strerror.restype = ctypes.c_char_p
     lib.profk_release.argtypes = []
@@ -431,3 +451,7 @@ def read_ceiling(x, blocks_per_cu: int = 0, out=None):
 
 def release():
     load_library().profk_release()
+
+
+from .operators import (Balance, Routing, balance_loss, balance_loss_grad, route_tokens,  # noqa: E402
+                        route_tokens_grad, sample_tokens)

@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libprofk.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "k_sample.hip", "k_select.hip", "k_filter.hip", "k_refine.hip", "k_sort.hip", "k_batched.hip", "k_merge.hip", "k_probe.hip",
-           "solver.cpp"]
+           "k_tokens.hip", "k_route.hip", "solver.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",

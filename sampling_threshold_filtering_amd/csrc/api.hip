@@ -1084,6 +1084,34 @@ int topk_batched_rows(const float* x, u64 B, u64 N, u64 ld, u64 k, double eps, u
 }  // namespace
 }  // namespace profk
 
+namespace profk {
+namespace {
+
+// Arguments of the language-model operators.
+constexpr int64_t kOpMaxRows = 0x7FFFFFFF;
+constexpr int64_t kTokMaxV = int64_t(1) << 24;
+
+bool known_dtype(int32_t d) { return d == PROFK_FP32 || d == PROFK_FP16 || d == PROFK_BF16; }
+
+int check_scratch(const void* scratch, int64_t have, int64_t need) {
+  if (need == 0) return PROFK_OK;
+  if (!scratch || ((uintptr_t)scratch & 255)) return PROFK_EINVAL;
+  if (have < need) {
+    t_err = "the scratch given is smaller than the operator's scratch query says";
+    return PROFK_ESCRATCH;
+  }
+  return PROFK_OK;
+}
+
+int check_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, int64_t k) {
+  if (!known_dtype(dtype) || T < 0 || E < 1 || ld < E || k < 1 || (T && !logits)) return PROFK_EINVAL;
+  if (E > (int64_t)kRouteMaxExperts || k > (int64_t)kRouteMaxK || T > kOpMaxRows) return PROFK_EUNSUPPORTED;
+  return PROFK_OK;
+}
+
+}  // namespace
+}  // namespace profk
+
 using namespace profk;
 
 extern "C" {
@@ -1364,6 +1392,132 @@ int profk_read_ceiling(const float* x, int64_t N, int32_t blocks_per_cu, uint64_
                              (hipStream_t)stream),
          "launch read_ceiling");
   return PROFK_OK;
+}
+
+int64_t profk_sample_tokens_scratch(int64_t B, int64_t V) {
+  if (B < 0 || V < 1 || V > kTokMaxV) return PROFK_EINVAL;
+  return (int64_t)sample_tokens_scratch_bytes((u64)B, (u64)V);
+}
+
+int profk_sample_tokens(const void* logits, int32_t dtype, int64_t B, int64_t V, int64_t ld, const float* u,
+                        const profk_sampling* how, int64_t* out_tokens, float* out_logprobs, void* scratch,
+                        int64_t scratch_bytes, void* stream) {
+  if (!known_dtype(dtype) || B < 0 || V < 1 || ld < V || !how) return PROFK_EINVAL;
+  if (V > kTokMaxV || B > kOpMaxRows) return PROFK_EUNSUPPORTED;
+  if (B == 0) return PROFK_OK;
+  if (!logits || !u || !out_tokens || !out_logprobs) return PROFK_EINVAL;
+  const int rc = check_scratch(scratch, scratch_bytes, (int64_t)sample_tokens_scratch_bytes((u64)B, (u64)V));
+  if (rc) return rc;
+  TokenArgs a{};
+  a.x = logits;
+  a.B = (u64)B;
+  a.V = (u64)V;
+  a.ld = (u64)ld;
+  a.u = u;
+  a.t = how->temperature;
+  a.p = how->top_p;
+  a.m = how->min_p;
+  a.k = how->top_k;
+  a.t_row = how->row_temperature;
+  a.p_row = how->row_top_p;
+  a.m_row = how->row_min_p;
+  a.k_row = how->row_top_k;
+  a.tokens = out_tokens;
+  a.logprobs = out_logprobs;
+  a.scratch = (char*)scratch;
+  HIPCHK(launch_sample_tokens(a, dtype, (hipStream_t)stream), "launch sample_tokens");
+  return PROFK_OK;
+}
+
+int64_t profk_route_scratch(int64_t T, int64_t E) {
+  if (T < 0 || E < 1 || E > (int64_t)kRouteMaxExperts) return PROFK_EINVAL;
+  return (int64_t)route_scratch_bytes((u64)T, (u32)E);
+}
+
+int profk_route_tokens(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                       int64_t k, int32_t normalize, float* out_weights, int64_t* out_experts, int64_t* out_counts,
+                       int64_t* out_rows, float* out_loss, void* scratch, int64_t scratch_bytes, void* stream) {
+  int rc = check_route(logits, dtype, T, E, ld, k);
+  if (rc) return rc;
+  if (k > E || (T && (!out_weights || !out_experts)) || !out_counts || !out_rows) return PROFK_EINVAL;
+  rc = check_scratch(scratch, scratch_bytes, (int64_t)route_scratch_bytes((u64)T, (u32)E));
+  if (rc) return rc;
+  RouteArgs a{};
+  a.x = logits;
+  a.T = (u64)T;
+  a.ld = (u64)ld;
+  a.E = (u32)E;
+  a.k = (u32)k;
+  a.mask = mask;
+  a.normalize = normalize != 0;
+  a.weights = out_weights;
+  a.experts = out_experts;
+  a.counts = out_counts;
+  a.rows = out_rows;
+  a.loss = out_loss;
+  a.scratch = (char*)scratch;
+  HIPCHK(launch_route(a, dtype, (hipStream_t)stream), "launch route");
+  return PROFK_OK;
+}
+
+int profk_balance_loss(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                       const int64_t* experts, int64_t k, int64_t* out_counts, int64_t* out_rows, float* out_loss,
+                       void* scratch, int64_t scratch_bytes, void* stream) {
+  int rc = check_route(logits, dtype, T, E, ld, k);
+  if (rc) return rc;
+  if ((T && !experts) || !out_counts || !out_rows || !out_loss) return PROFK_EINVAL;
+  rc = check_scratch(scratch, scratch_bytes, (int64_t)route_scratch_bytes((u64)T, (u32)E));
+  if (rc) return rc;
+  RouteArgs a{};
+  a.x = logits;
+  a.T = (u64)T;
+  a.ld = (u64)ld;
+  a.E = (u32)E;
+  a.k = (u32)k;
+  a.mask = mask;
+  a.given = experts;
+  a.balance_only = true;
+  a.counts = out_counts;
+  a.rows = out_rows;
+  a.loss = out_loss;
+  a.scratch = (char*)scratch;
+  HIPCHK(launch_route(a, dtype, (hipStream_t)stream), "launch balance");
+  return PROFK_OK;
+}
+
+int profk_route_tokens_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                            int64_t k, int32_t normalize, const int64_t* experts, const float* d_weights,
+                            const int64_t* counts, const int64_t* rows, const float* d_loss, float d_loss_scale,
+                            void* out_d_logits, void* stream) {
+  const int rc = check_route(logits, dtype, T, E, ld, k);
+  if (rc) return rc;
+  if (T == 0) return PROFK_OK;
+  if (!out_d_logits || (d_weights && !experts) || (counts && !rows) || (!counts && !d_weights)) return PROFK_EINVAL;
+  RouteGradArgs a{};
+  a.x = logits;
+  a.T = (u64)T;
+  a.ld = (u64)ld;
+  a.E = (u32)E;
+  a.k = (u32)k;
+  a.mask = mask;
+  a.normalize = normalize != 0;
+  a.experts = experts;
+  a.d_weights = d_weights;
+  a.counts = counts;
+  a.rows = rows;
+  a.d_loss = d_loss;
+  a.d_loss_scale = d_loss_scale;
+  a.d_x = out_d_logits;
+  HIPCHK(launch_route_grad(a, dtype, (hipStream_t)stream), "launch route gradient");
+  return PROFK_OK;
+}
+
+int profk_balance_loss_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                            int64_t k, const int64_t* counts, const int64_t* rows, const float* d_loss,
+                            float d_loss_scale, void* out_d_logits, void* stream) {
+  if (!counts || !rows) return PROFK_EINVAL;
+  return profk_route_tokens_grad(logits, dtype, T, E, ld, mask, k, 0, nullptr, nullptr, counts, rows, d_loss,
+                                 d_loss_scale, out_d_logits, stream);
 }
 
 const char* profk_strerror(int code) {

@@ -282,6 +282,59 @@ hipError_t launch_merge_segments(const SegmentLists& L, float* out_vals, int64_t
 // Measurement helper (k_probe.hip): one dwordx4 non-temporal streaming read of x.
 hipError_t launch_read_ceiling(const float* x, u64 N, u32 blocks_per_cu, unsigned long long* out, hipStream_t s);
 
+// Language-model operators.  Sampling a token per row (k_tokens.hip).
+struct TokenArgs {
+  const void* x;  // logits, row r at x + r * ld entries
+  u64 B, V, ld;
+  const float* u;                                   // one per row
+  float t, p, m;                                    // settings of every row, where the pointers are null
+  int64_t k;
+  const float *t_row, *p_row, *m_row;
+  const int64_t* k_row;
+  int64_t* tokens;
+  float* logprobs;
+  char* scratch;
+};
+size_t sample_tokens_scratch_bytes(u64 B, u64 V);
+hipError_t launch_sample_tokens(const TokenArgs& a, int dtype, hipStream_t s);
+
+// Routing tokens to experts and the balance loss (k_route.hip).
+struct RouteArgs {
+  const void* x;  // logits, row t at x + t * ld entries
+  u64 T, ld;
+  u32 E, k;
+  const unsigned char* mask;   // nonzero: the row takes part; or nullptr
+  bool normalize;
+  bool balance_only;           // the choice is `given`: count it, choose nothing
+  const int64_t* given;        // T * k experts, with balance_only
+  float* weights;              // T * k
+  int64_t* experts;            // T * k
+  int64_t* counts;             // E
+  int64_t* rows;               // 1
+  float* loss;                 // 1, or nullptr
+  char* scratch;               // route_scratch_bytes
+  u32 blocks;                  // set by launch_route
+};
+struct RouteGradArgs {
+  const void* x;
+  u64 T, ld;
+  u32 E, k;
+  const unsigned char* mask;
+  bool normalize;
+  const int64_t* experts;      // with d_weights
+  const float* d_weights;      // T * k, or nullptr
+  const int64_t* counts;       // with the loss's gradient, else nullptr
+  const int64_t* rows;
+  const float* d_loss;         // 1, or nullptr
+  float d_loss_scale;
+  void* d_x;                   // T * E, contiguous, of the logits' type
+};
+constexpr u32 kRouteMaxExperts = 1024;
+constexpr u32 kRouteMaxK = 64;
+size_t route_scratch_bytes(u64 T, u32 E);
+hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
+hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s);
+
 hipError_t launch_sort_and_write(u64* buf0, u64* buf1, u32* hist, u32 k, const float* row, u64 N, float* out_vals,
                                  int64_t* out_idx, RowCtl* ctl, AttemptRecord* rec, hipStream_t s);
 u64 sort_hist_words(u64 k);
