@@ -28,6 +28,8 @@ namespace {
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr u32 kRouteMaxBlocks = 512;
+constexpr int kFinishThreads = 1024;
+constexpr u32 kFinishExperts = 16;
 
 // Sum / maximum over the G lanes of a group; every lane gets the result.
 template <int G, class V, class F>
@@ -94,12 +96,14 @@ struct Row {
   }
 };
 
+// A launch of several blocks leaves each block's counts, sums and live rows here for the
+// finishing launch; one block alone writes the outputs itself.
 struct RouteScratch {
-  u32* ticket;  // 1
-  u32* rows;    // blocks
-  u32* counts;  // blocks * E
-  float* sums;  // blocks * E
-  double* part; // one per finishing block
+  u32* ticket;   // finishing blocks that have left their part
+  double* part;  // one per finishing block
+  u32* rows;     // blocks
+  u32* counts;   // blocks * E
+  float* sums;   // blocks * E
 };
 
 __host__ __device__ inline RouteScratch route_scratch(char* s, u32 blocks, u32 E) {
@@ -110,6 +114,23 @@ __host__ __device__ inline RouteScratch route_scratch(char* s, u32 blocks, u32 E
   r.counts = r.rows + blocks;
   r.sums = (float*)(r.counts + (u64)blocks * E);
   return r;
+}
+
+// Sum of one double per thread over the block, in a fixed order; thread 0 has it.
+template <int WAVES>
+__device__ __forceinline__ double block_sum(double v, double* wave_tot) {
+#pragma unroll
+  for (int d = kWave / 2; d; d >>= 1) v += __shfl_down(v, d);
+  if (lane_id() == 0) wave_tot[threadIdx.x / kWave] = v;
+  __syncthreads();
+  double s = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) s += wave_tot[w];
+  return s;
+}
+
+__device__ __forceinline__ float balance_of(double total, u64 rows, u32 E, u32 k) {
+  return rows ? (float)((double)E * total / ((double)rows * (double)k * (double)rows)) : 0.f;
 }
 
 }  // namespace
@@ -194,7 +215,24 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   }
   if (rows) atomicAdd(&s_rows, rows);
   __syncthreads();
-  const RouteScratch sc = route_scratch(a.scratch, a.blocks, a.E);
+  if (gridDim.x == 1) {
+    double part = 0;
+    for (u32 e = threadIdx.x; e < a.E; e += kRouteThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRouteWaves; ++w) v += s_sum[w][e];
+      a.counts[e] = (int64_t)s_cnt[e];
+      part += (double)s_cnt[e] * (double)v;
+    }
+    __shared__ double s_part[kRouteWaves];
+    part = block_sum<kRouteWaves>(part, s_part);
+    if (threadIdx.x == 0) {
+      *a.rows = (int64_t)s_rows;
+      if (a.loss) *a.loss = balance_of(part, s_rows, a.E, a.k);
+    }
+    return;
+  }
+  const RouteScratch sc = route_scratch(a.scratch, gridDim.x, a.E);
   for (u32 e = threadIdx.x; e < a.E; e += kRouteThreads) {
     float v = 0.f;
 #pragma unroll
@@ -208,36 +246,62 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   }
 }
 
-// The blocks' counts and sums into the outputs: one block.
-__global__ __launch_bounds__(kRouteThreads) void route_finish_kernel(RouteArgs a) {
-  __shared__ double s_part[kRouteThreads];
-  __shared__ u32 s_n[kRouteThreads];
+// The blocks' counts and sums into the outputs.  A finishing block takes 16 experts, its
+// threads 64 slices of the blocks, so that a thread adds 8 of 512 (one block over all
+// experts, 512 each: 121 us).  The last block to leave its part of the loss adds the
+// parts, in their order.
+__global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs a) {
+  constexpr u32 kSlices = kFinishThreads / kFinishExperts;
+  __shared__ u64 s_c[kSlices][kFinishExperts + 1];
+  __shared__ double s_p[kSlices][kFinishExperts + 1];
+  __shared__ double s_part[kFinishThreads / kWave];
+  __shared__ u32 s_last;
   const RouteScratch sc = route_scratch(a.scratch, a.blocks, a.E);
-  u32 n = 0;
-  for (u32 b = threadIdx.x; b < a.blocks; b += kRouteThreads) n += sc.rows[b];
-  s_n[threadIdx.x] = n;
-  double part = 0;
-  for (u32 e = threadIdx.x; e < a.E; e += kRouteThreads) {
-    u64 c = 0;
-    double p = 0;
-    for (u32 b = 0; b < a.blocks; ++b) {
+  const u32 el = threadIdx.x % kFinishExperts, sl = threadIdx.x / kFinishExperts;
+  const u32 e = blockIdx.x * kFinishExperts + el;
+  u64 c = 0;
+  double p = 0;
+  if (e < a.E)
+    for (u32 b = sl; b < a.blocks; b += kSlices) {
       c += sc.counts[(u64)b * a.E + e];
       p += (double)sc.sums[(u64)b * a.E + e];
     }
-    a.counts[e] = (int64_t)c;
-    part += (double)c * p;
-  }
-  s_part[threadIdx.x] = part;
+  s_c[sl][el] = c;
+  s_p[sl][el] = p;
   __syncthreads();
+  double part = 0;
+  if (threadIdx.x < kFinishExperts && e < a.E) {
+    c = 0;
+    p = 0;
+    for (u32 i = 0; i < kSlices; ++i) {
+      c += s_c[i][el];
+      p += s_p[i][el];
+    }
+    a.counts[e] = (int64_t)c;
+    part = (double)c * p;
+  }
+  part = block_sum<kFinishThreads / kWave>(part, s_part);
   if (threadIdx.x == 0) {
-    u64 rows = 0;
-    double total = 0;
-    for (int i = 0; i < kRouteThreads; ++i) {
-      rows += s_n[i];
-      total += s_part[i];
+    s_last = 1;
+    if (gridDim.x > 1) {
+      __hip_atomic_store(&sc.part[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      s_last = __hip_atomic_fetch_add(sc.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  double rows = 0;  // exact: below 2^31
+  for (u32 b = threadIdx.x; b < a.blocks; b += kFinishThreads) rows += (double)sc.rows[b];
+  __syncthreads();
+  rows = block_sum<kFinishThreads / kWave>(rows, s_part);
+  if (threadIdx.x == 0) {
+    if (gridDim.x > 1) {
+      part = 0;
+      for (u32 b = 0; b < gridDim.x; ++b)
+        part += __hip_atomic_load(&sc.part[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     *a.rows = (int64_t)rows;
-    if (a.loss) *a.loss = rows ? (float)((double)a.E * total / ((double)rows * (double)a.k * (double)rows)) : 0.f;
+    if (a.loss) *a.loss = balance_of(part, (u64)rows, a.E, a.k);
   }
 }
 
@@ -342,8 +406,8 @@ hipError_t route_launch(const RouteArgs& a0, hipStream_t s) {
   else
     route_kernel<T, G, C, false><<<a.blocks, kRouteThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  route_finish_kernel<<<1, kRouteThreads, 0, s>>>(a);
+  if (e != hipSuccess || a.blocks == 1) return e;
+  route_finish_kernel<<<(a.E + kFinishExperts - 1) / kFinishExperts, kFinishThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
