@@ -12,12 +12,13 @@
 //   normalised weights:   dl_te = w_te (d_te - sum_j w_tj d_tj) at the chosen, else 0
 //     (they are the softmax over the chosen entries alone)
 //
-// Layout.  A group of G lanes takes a row, lane g its entries g, g + G, g + 2G, ... (C of
-// them, in registers), so that the loads of a wavefront are contiguous for any E and any
-// row stride, a row's maximum and sums are log2 G lane exchanges, and 64 / G rows share
-// every instruction.  A lane keeps the same experts for all of its rows, so P_e is summed
-// in its registers; lanes, wavefronts and blocks are then added in a fixed order (no
-// floating-point atomics: the loss has the same bits on every run).
+// Layout.  A group of G lanes takes a row and holds C entries of it per lane in registers,
+// so that a row's maximum and sums are log2 G lane exchanges and 64 / G rows share every
+// instruction.  A lane takes its entries four neighbours at a time where rows allow it (one
+// load of 16 or 8 bytes each), else lane g takes entries g, g + G, ...  A lane keeps the
+// same experts for all of its rows, so P_e is summed in its registers; lanes, wavefronts
+// and blocks are then added in a fixed order (no floating-point atomics: the loss has the
+// same bits on every run).
 #include "launch.h"
 #include "ops_device.h"
 
@@ -25,76 +26,149 @@ namespace profk {
 
 namespace {
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr u32 kRouteMaxBlocks = 512;
+constexpr int kGradThreads = 256;
 constexpr int kFinishThreads = 1024;
 constexpr u32 kFinishExperts = 16;
 
-// Sum / maximum over the G lanes of a group; every lane gets the result.
+// Sum / maximum over the G lanes of a group; every lane gets the result.  Within 16 lanes
+// the partner is a mirrored one, which holds the same partial result as the one across.
+template <int CTRL, class V>
+__device__ __forceinline__ V dpp(V v) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
 template <int G, class V, class F>
 __device__ __forceinline__ V group_reduce(V v, F f) {
-  const u32 lane = lane_id();
-  if constexpr (G > 1) v = f(v, __builtin_bit_cast(V, lane_xor_u32<1>(__builtin_bit_cast(u32, v), lane)));
-  if constexpr (G > 2) v = f(v, __builtin_bit_cast(V, lane_xor_u32<2>(__builtin_bit_cast(u32, v), lane)));
-  if constexpr (G > 4) v = f(v, __builtin_bit_cast(V, lane_xor_u32<4>(__builtin_bit_cast(u32, v), lane)));
-  if constexpr (G > 8) v = f(v, __builtin_bit_cast(V, lane_xor_u32<8>(__builtin_bit_cast(u32, v), lane)));
-  if constexpr (G > 16) v = f(v, __builtin_bit_cast(V, lane_xor_u32<16>(__builtin_bit_cast(u32, v), lane)));
-  if constexpr (G > 32) v = f(v, __builtin_bit_cast(V, lane_xor_u32<32>(__builtin_bit_cast(u32, v), lane)));
+  if constexpr (G > 1) v = f(v, dpp<0xB1>(v));    // quad_perm [1,0,3,2]
+  if constexpr (G > 2) v = f(v, dpp<0x4E>(v));    // quad_perm [2,3,0,1]
+  if constexpr (G > 4) v = f(v, dpp<0x141>(v));   // row_half_mirror
+  if constexpr (G > 8) v = f(v, dpp<0x140>(v));   // row_mirror
+  if constexpr (G > 16) v = f(v, __shfl_xor(v, 16));
+  if constexpr (G > 32) v = f(v, __shfl_xor(v, 32));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ u64 group_reduce64(u64 v) {  // the maximum
+#pragma unroll
+  for (int d = 1; d < G; d <<= 1) {
+    const u64 o = __shfl_xor(v, d);
+    v = o > v ? o : v;
+  }
   return v;
 }
 
 __device__ __forceinline__ float add_f(float a, float b) { return a + b; }
-// NaN wins, so that a row that holds one has NaN weights.
-__device__ __forceinline__ float max_f(float a, float b) { return a != a || a > b ? a : b; }
+__device__ __forceinline__ float max_f(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ u32 max_u(u32 a, u32 b) { return a > b ? a : b; }
-__device__ __forceinline__ u32 min_u(u32 a, u32 b) { return a < b ? a : b; }
 
 // e^x for x <= 0 to about one unit in the last place: the rounding of x log2(e), which
 // grows with |x|, is made up for by one more multiply-add.  Differences as far apart as the
-// type reaches (and -inf) are cut to one whose exponential is 0; NaN stays NaN.
+// type reaches (and -inf) are cut to one whose exponential is 0, and so is NaN: rows that
+// hold one are told apart beforehand.
 __device__ __forceinline__ float exp_f(float x) {
-  x = x < -150.f ? -150.f : x;
-  const float t = x * 1.44269502f;  // log2(e) = 1.44269502 + 1.925963e-8
-  const float r = __builtin_fmaf(x, 1.44269502f, -t) + x * 1.925963e-8f;
+  x = __builtin_fmaxf(x, -150.f);
+  const float t = x * 1.44269502f;
+  const float r = __builtin_fmaf(x, 1.44269502f, -t);
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e, r * 0.693147182f, e);
 }
 
-// One row in registers: its C entries per lane and what the softmax needs.
-template <int G, int C>
+// Four neighbouring entries with one load or store.
+template <class T>
+struct alignas(4 * sizeof(T)) Four {
+  T e[4];
+};
+
+constexpr float kNone = -__builtin_huge_valf();
+
+// One row in registers: C entries per lane, -0 as +0.  QUAD: four neighbours at a time.
+template <int G, int C, bool QUAD>
 struct Row {
   float v[C];
-  float p[C];
+  float e[C];  // exp(v - top)
   bool live;
-  float top, inv;  // the largest entry; 1 / sum of exp
+  float top;
 
+  static __device__ __forceinline__ u32 index(int i, u32 g) {
+    return QUAD ? (u32)(i / 4 * G) * 4 + (u32)(i % 4) + g * 4 : (u32)i * G + g;
+  }
+  // All loads go out before the first is used: places past the row's end read its start,
+  // rows past the last (x of a row that exists) are read and not taken.
   template <class T>
   __device__ __forceinline__ void load(const T* x, u32 E, u32 g, bool in) {
+    if constexpr (QUAD) {
+      Four<T> q[C / 4];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const u32 e = (u32)i * G + g;
-      v[i] = in && e < E ? to_f32(x[e]) : -__builtin_huge_valf();
+      for (int i = 0; i < C; i += 4) {  // E is a multiple of 4
+        const u32 at = index(i, g);
+        q[i / 4] = *reinterpret_cast<const Four<T>*>(x + (at < E ? at : 0u));
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = (in && index(i & ~3, g) < E ? to_f32(q[i / 4].e[i % 4]) : kNone) + 0.f;
+    } else {
+      T q[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) q[i] = x[index(i, g) < E ? index(i, g) : 0u];
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = (in && index(i, g) < E ? to_f32(q[i]) : kNone) + 0.f;
     }
   }
-  __device__ __forceinline__ void softmax(bool in) {
+  // The largest entry and the exponentials.  A row that holds a NaN has NaN for its top,
+  // and every NaN becomes the one that the order ranks first; there, and where the top is
+  // +inf, all exponentials are NaN.
+  __device__ __forceinline__ void weigh(bool in) {
     float m = v[0];
+    bool nan = false;
 #pragma unroll
     for (int i = 1; i < C; ++i) m = max_f(m, v[i]);
+#pragma unroll
+    for (int i = 0; i < C; i += 2) nan |= __builtin_isunordered(v[i], v[i + 1 < C ? i + 1 : i]);
     top = group_reduce<G>(m, max_f);
-    live = in && !(top == -__builtin_huge_valf());
+    live = in && !(top == kNone);
+    const float base = live ? top : 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) e[i] = exp_f(v[i] - base);  // entries of -inf: 0
+    if (__builtin_expect(__ballot(nan || top == __builtin_huge_valf()) != 0, 0)) {
+      const float first = __uint_as_float(0x7FFFFFFFu);
+      if (group_reduce<G>((u32)nan, max_u)) {
+        top = first;
+        live = true;
+      }
+      if (!(top < __builtin_huge_valf())) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          v[i] = v[i] != v[i] ? first : v[i];
+          e[i] = first;
+        }
+      }
+    }
+  }
+  // 1 / the row's sum; 0 for a row that is not live
+  __device__ __forceinline__ float inverse() const {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      p[i] = exp_f(v[i] - top);  // entries of -inf: 0
-      s += p[i];
-    }
+    for (int i = 0; i < C; ++i) s += e[i];
     s = group_reduce<G>(s, add_f);
-    inv = 1.f / s;
-#pragma unroll
-    for (int i = 0; i < C; ++i) p[i] = live ? p[i] * inv : 0.f;
+    return live ? 1.f / s : 0.f;
   }
 };
+
+// Selection keys of 32 bits: the value's ordered code with its low bits replaced by the
+// entry's complement, so that the largest key is the first entry by value, then lower
+// index, wherever the bits that are left tell the values apart.
+constexpr int key_bits(int entries) {
+  int b = 0;
+  while ((1 << b) < entries) ++b;
+  return b;
+}
+
+// Ordered code of a value as a Row holds it.
+__device__ __forceinline__ u32 ord_of(float v) {
+  const u32 b = __float_as_uint(v);
+  return b ^ ((u32)((int)b >> 31) | 0x80000000u);
+}
 
 // A launch of several blocks leaves each block's counts, sums and live rows here for the
 // finishing launch; one block alone writes the outputs itself.
@@ -135,8 +209,99 @@ __device__ __forceinline__ float balance_of(double total, u64 rows, u32 E, u32 k
 
 }  // namespace
 
+// The row's k experts, their weights and counts.  All keys are distinct, so the next one
+// below m is the largest of (key - m) modulo 2^32: those from m up wrap to the bottom, and
+// nothing has to be struck out.  In 32-bit types two neighbours among the first k + 1 keys
+// can agree in all of the value's bits that they hold; then the wavefront chooses again by
+// 64-bit keys.
+template <class T, int G, int C, bool QUAD>
+__device__ __forceinline__ void choose(const RouteArgs& a, const Row<G, C, QUAD>& row, const T* x, u64 t, u32 g,
+                                       float inv, u32* s_cnt) {
+  using R = Row<G, C, QUAD>;
+  constexpr int kBits = key_bits(G * C);
+  constexpr bool kExact = sizeof(T) == 2;  // the codes of fp16 end in 13 constant bits, of bf16 in 16
+  constexpr u32 kLow = (1u << kBits) - 1;
+  constexpr u32 kNoneTop = 0x007FFFFFu | kLow;  // the largest key of an entry of -inf
+  u32 key[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) key[i] = (ord_of(row.v[i]) & ~kLow) | (kLow - R::index(i, g));
+  const u64 at = t * a.k;
+  const bool here = t < a.T;
+  float chosen = 0.f, w = 0.f;
+  // lane g's slot j0 + g holds entry e, of value v
+  auto emit = [&](u32 j0, u32 nj, bool some, u32 e, float v) {
+    if (g >= nj || !here) return;
+    w = 0.f;
+    if (some) {
+      w = exp_f(v - row.top);
+      if (!(row.top < __builtin_huge_valf())) w = row.top - row.top;  // of +inf or NaN: NaN
+      if (!a.normalize) w *= inv;
+      atomicAdd(&s_cnt[e], 1u);
+    }
+    chosen += w;
+    a.experts[at + j0 + g] = some ? (int64_t)e : -1;
+    if (!a.normalize || a.k > (u32)G) a.weights[at + j0 + g] = w;
+  };
+  u32 m = 0;
+  auto next_key = [&]() {
+    u32 d = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) d = max_u(d, key[i] - m);
+    return m + group_reduce<G>(d, max_u);
+  };
+  bool unsure = false;
+  for (u32 j0 = 0; j0 < a.k; j0 += G) {
+    const u32 nj = a.k - j0 < (u32)G ? a.k - j0 : (u32)G;
+    u32 mine = 0;
+    for (u32 j = 0; j < nj; ++j) {
+      const u32 n = next_key();
+      if constexpr (!kExact) unsure |= j && !((m ^ n) & ~kLow) && n > kNoneTop;
+      m = n;
+      if (g == j) mine = m;
+    }
+    const u32 e = kLow - (mine & kLow);
+    const bool some = row.live && mine > kNoneTop;
+    if constexpr (kExact) {
+      emit(j0, nj, some, e, __uint_as_float(bits_of_ord32(mine & 0x80000000u ? mine & ~kLow : mine | kLow)));
+    } else {
+      if (j0 + nj < a.E) {  // the first one left out
+        const u32 n = next_key();
+        unsure |= !((m ^ n) & ~kLow) && n > kNoneTop;
+      }
+      if (__ballot(unsure && row.live) == 0) {
+        emit(j0, nj, some, e, some && g < nj ? to_f32(x[e]) : 0.f);
+        continue;
+      }
+      u64 last = ~0ull, own = 0;
+      for (u32 j = 0; j < a.k; ++j) {  // again from the first: slots before j0 have been given out
+        u64 n = 0;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          const u64 c = ((u64)ord_of(row.v[i]) << 32) | (u32)~R::index(i, g);
+          n = c < last && c > n ? c : n;
+        }
+        last = group_reduce64<G>(n);
+        if (g == j % G) own = last;
+        if (j >= j0 && (j % G == G - 1 || j + 1 == a.k))
+          emit(j / G * G, j % G + 1, row.live && (u32)(own >> 32) > 0x007FFFFFu, key_index(own),
+               __uint_as_float(bits_of_ord32((u32)(own >> 32))));
+      }
+      break;
+    }
+  }
+  if (!a.normalize) return;
+  chosen = group_reduce<G>(chosen, add_f);
+  const float r = row.live ? 1.f / chosen : 0.f;
+  if (!here) return;
+  if (a.k <= (u32)G) {
+    if (g < a.k) a.weights[at + g] = w * r;
+  } else {
+    for (u32 j = g; j < a.k; j += G) a.weights[at + j] *= r;
+  }
+}
+
 // GIVEN: the experts are a.given's (the balance loss of a choice made elsewhere).
-template <class T, int G, int C, bool GIVEN>
+template <class T, int G, int C, bool QUAD, bool GIVEN>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   constexpr int kGroups = kRouteThreads / G;
   __shared__ u32 s_cnt[G * C];
@@ -152,16 +317,20 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   for (int i = 0; i < C; ++i) sum[i] = 0.f;
   u32 rows = 0;
   const u64 step = (u64)gridDim.x * kGroups;
+  const bool balance = GIVEN || a.loss;
   for (u64 t0 = (u64)blockIdx.x * kGroups; t0 < a.T; t0 += step) {
-    const u64 t = t0 + grp;
-    const bool in = t < a.T && (!a.mask || a.mask[t]);
-    Row<G, C> row;
-    row.load(x + t * a.ld, a.E, g, in);
-    row.softmax(in);
+    const u64 t = t0 + grp, tr = t < a.T ? t : a.T - 1;
+    const bool in = (!a.mask || a.mask[tr]) && t < a.T;
+    Row<G, C, QUAD> row;
+    row.load(x + tr * a.ld, a.E, g, in);
+    row.weigh(in);
+    float inv = 0.f;
+    if (balance || !a.normalize) inv = row.inverse();
+    if (balance) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) sum[i] += row.p[i];
+      for (int i = 0; i < C; ++i) sum[i] = __builtin_fmaf(row.e[i], inv, sum[i]);
+    }
     rows += row.live && g == 0;
-    if (t >= a.T) continue;  // no lane exchange below crosses groups
     if constexpr (GIVEN) {
       if (row.live)
         for (u32 j = g; j < a.k; j += G) {
@@ -169,40 +338,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
           if (e >= 0 && e < (int64_t)a.E) atomicAdd(&s_cnt[e], 1u);
         }
     } else {
-      u32 key[C];
-#pragma unroll
-      for (int i = 0; i < C; ++i) key[i] = row.live && row.v[i] != -__builtin_huge_valf() ? ord32(__float_as_uint(row.v[i])) : 0u;
-      float chosen = 0.f;
-      for (u32 j = 0; j < a.k; ++j) {
-        u32 m = 0;
-#pragma unroll
-        for (int i = 0; i < C; ++i) m = max_u(m, key[i]);
-        m = group_reduce<G>(m, max_u);
-        u32 e = ~0u;
-        float p = 0.f;
-#pragma unroll
-        for (int i = C - 1; i >= 0; --i)
-          if (key[i] == m) e = (u32)i * G + g;
-        e = group_reduce<G>(e, min_u);
-        if (m == 0) e = ~0u;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-          if (e == (u32)i * G + g) {
-            key[i] = 0;
-            p = row.p[i];
-          }
-        p = group_reduce<G>(p, add_f);
-        chosen += p;
-        if (g == 0) {
-          a.experts[t * a.k + j] = m ? (int64_t)e : -1;
-          a.weights[t * a.k + j] = p;
-          if (m) atomicAdd(&s_cnt[e], 1u);
-        }
-      }
-      if (a.normalize && g == 0 && row.live) {
-        const float r = 1.f / chosen;
-        for (u32 j = 0; j < a.k; ++j) a.weights[t * a.k + j] *= r;
-      }
+      choose<T, G, C, QUAD>(a, row, x + tr * a.ld, t, g, inv, s_cnt);
     }
   }
   // the block's sums: the wavefront's groups, then its wavefronts
@@ -211,7 +347,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     float v = sum[i];
 #pragma unroll
     for (int d = G; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-    if (lane_id() < G) s_sum[threadIdx.x / kWave][i * G + g] = v;
+    if (lane_id() < G) s_sum[threadIdx.x / kWave][Row<G, C, QUAD>::index(i, g)] = v;
   }
   if (rows) atomicAdd(&s_rows, rows);
   __syncthreads();
@@ -247,104 +383,130 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 }
 
 // The blocks' counts and sums into the outputs.  A finishing block takes 16 experts, its
-// threads 64 slices of the blocks, so that a thread adds 8 of 512 (one block over all
-// experts, 512 each: 121 us).  The last block to leave its part of the loss adds the
-// parts, in their order.
+// threads 64 slices of the blocks, so that a thread adds 8 of 512, all loaded at once (one
+// block over all experts, 512 each: 121 us).  The last block to leave its part of the loss
+// adds the parts, in a fixed order.
 __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs a) {
   constexpr u32 kSlices = kFinishThreads / kFinishExperts;
-  __shared__ u64 s_c[kSlices][kFinishExperts + 1];
-  __shared__ double s_p[kSlices][kFinishExperts + 1];
-  __shared__ double s_part[kFinishThreads / kWave];
-  __shared__ u32 s_last;
+  constexpr u32 kEach = kRouteMaxBlocks / kSlices;
+  constexpr u32 kWaves = kFinishThreads / kWave;
+  __shared__ u32 s_c[kWaves][kFinishExperts];
+  __shared__ double s_p[kWaves][kFinishExperts];
+  __shared__ u32 s_rows[kWaves];
+  static_assert(kRouteMaxBlocks <= kFinishThreads, "a thread per block for the rows");
   const RouteScratch sc = route_scratch(a.scratch, a.blocks, a.E);
-  const u32 el = threadIdx.x % kFinishExperts, sl = threadIdx.x / kFinishExperts;
+  const u32 el = threadIdx.x % kFinishExperts, sl = threadIdx.x / kFinishExperts, wid = threadIdx.x / kWave;
   const u32 e = blockIdx.x * kFinishExperts + el;
-  u64 c = 0;
+  u32 cs[kEach];
+  float ps[kEach];
+  u32 rows = threadIdx.x < a.blocks ? sc.rows[threadIdx.x] : 0;
+#pragma unroll
+  for (u32 i = 0; i < kEach; ++i) {
+    const u32 b = sl + i * kSlices;
+    const bool some = e < a.E && b < a.blocks;
+    cs[i] = some ? sc.counts[(u64)b * a.E + e] : 0;
+    ps[i] = some && a.loss ? sc.sums[(u64)b * a.E + e] : 0.f;
+  }
+  u32 c = 0;  // at most T k < 2^37 slots in all; a thread's and a wavefront's are of 8 and 32 blocks
   double p = 0;
-  if (e < a.E)
-    for (u32 b = sl; b < a.blocks; b += kSlices) {
-      c += sc.counts[(u64)b * a.E + e];
-      p += (double)sc.sums[(u64)b * a.E + e];
-    }
-  s_c[sl][el] = c;
-  s_p[sl][el] = p;
+#pragma unroll
+  for (u32 i = 0; i < kEach; ++i) {
+    c += cs[i];
+    p += (double)ps[i];
+  }
+#pragma unroll
+  for (u32 d = kFinishExperts; d < (u32)kWave; d <<= 1) {
+    c += __shfl_xor(c, d);
+    p += __shfl_xor(p, d);
+  }
+#pragma unroll
+  for (u32 d = 1; d < (u32)kWave; d <<= 1) rows += __shfl_xor(rows, d);
+  if (lane_id() < kFinishExperts) {
+    s_c[wid][el] = c;
+    s_p[wid][el] = p;
+  }
+  if (lane_id() == 0) s_rows[wid] = rows;
   __syncthreads();
+  if (threadIdx.x >= kWave) return;
   double part = 0;
   if (threadIdx.x < kFinishExperts && e < a.E) {
-    c = 0;
+    u64 n = 0;
     p = 0;
-    for (u32 i = 0; i < kSlices; ++i) {
-      c += s_c[i][el];
-      p += s_p[i][el];
+#pragma unroll
+    for (u32 w = 0; w < kWaves; ++w) {
+      n += s_c[w][el];
+      p += s_p[w][el];
     }
-    a.counts[e] = (int64_t)c;
-    part = (double)c * p;
+    a.counts[e] = (int64_t)n;
+    part = (double)n * p;
   }
-  part = block_sum<kFinishThreads / kWave>(part, s_part);
-  if (threadIdx.x == 0) {
-    s_last = 1;
-    if (gridDim.x > 1) {
+  if (!a.loss && blockIdx.x) return;
+  u64 live = 0;
+#pragma unroll
+  for (u32 w = 0; w < kWaves; ++w) live += s_rows[w];
+  if (threadIdx.x == 0 && blockIdx.x == 0) *a.rows = (int64_t)live;
+  if (!a.loss) return;
+#pragma unroll
+  for (u32 d = 1; d < kFinishExperts; d <<= 1) part += __shfl_xor(part, d);
+  if (gridDim.x > 1) {
+    u32 last = 0;
+    if (threadIdx.x == 0) {
       __hip_atomic_store(&sc.part[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s_last = __hip_atomic_fetch_add(sc.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+      last = __hip_atomic_fetch_add(sc.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     }
+    if (!__builtin_amdgcn_readfirstlane(last)) return;
+    // at most 64 finishing blocks
+    part = threadIdx.x < gridDim.x
+               ? __hip_atomic_load(&sc.part[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+#pragma unroll
+    for (u32 d = 1; d < (u32)kWave; d <<= 1) part += __shfl_xor(part, d);
   }
-  __syncthreads();
-  if (!s_last) return;
-  double rows = 0;  // exact: below 2^31
-  for (u32 b = threadIdx.x; b < a.blocks; b += kFinishThreads) rows += (double)sc.rows[b];
-  __syncthreads();
-  rows = block_sum<kFinishThreads / kWave>(rows, s_part);
-  if (threadIdx.x == 0) {
-    if (gridDim.x > 1) {
-      part = 0;
-      for (u32 b = 0; b < gridDim.x; ++b)
-        part += __hip_atomic_load(&sc.part[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    *a.rows = (int64_t)rows;
-    if (a.loss) *a.loss = balance_of(part, (u64)rows, a.E, a.k);
-  }
+  if (threadIdx.x == 0) *a.loss = balance_of(part, live, a.E, a.k);
 }
 
-template <class T, int G, int C>
-__global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteGradArgs a) {
-  constexpr int kGroups = kRouteThreads / G;
-  __shared__ float s_d[kGroups][G * C];
+template <class T, int G, int C, bool QUAD>
+__global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs a) {
+  using R = Row<G, C, QUAD>;
+  constexpr int kGroups = kGradThreads / G;
+  __shared__ float s_d[kGroups][G * C];  // the chosen entries' part, 0 elsewhere
   const u32 g = threadIdx.x % G, grp = threadIdx.x / G;
   float* d = s_d[grp];
+  if (a.d_weights)
 #pragma unroll
-  for (int i = 0; i < C; ++i) d[i * G + g] = 0.f;
+    for (int i = 0; i < C; ++i) d[i * G + g] = 0.f;
   const T* x = reinterpret_cast<const T*>(a.x);
   T* dx = reinterpret_cast<T*>(a.d_x);
-  float f[C];
+  float f[C];  // the balance loss's constant factors, scale among them
 #pragma unroll
   for (int i = 0; i < C; ++i) f[i] = 0.f;
-  float scale = 0.f;
   if (a.counts) {
     const double n = (double)*a.rows;
     if (n > 0) {
-      scale = (float)((double)(a.d_loss ? *a.d_loss : 1.f) * (double)a.d_loss_scale * (double)a.E / n);
+      const double scale =
+          (double)(a.d_loss ? *a.d_loss : 1.f) * (double)a.d_loss_scale * (double)a.E / (n * n * (double)a.k);
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const u32 e = (u32)i * G + g;
-        if (e < a.E) f[i] = (float)((double)a.counts[e] / (n * (double)a.k));
+        const u32 e = R::index(i, g);
+        if (e < a.E) f[i] = (float)(scale * (double)a.counts[e]);
       }
     }
   }
   const u64 step = (u64)gridDim.x * kGroups;
   for (u64 t0 = (u64)blockIdx.x * kGroups; t0 < a.T; t0 += step) {
-    const u64 t = t0 + grp;
-    const bool in = t < a.T && (!a.mask || a.mask[t]);
-    Row<G, C> row;
-    row.load(x + t * a.ld, a.E, g, in);
-    row.softmax(in);
+    const u64 t = t0 + grp, tr = t < a.T ? t : a.T - 1;
+    const bool in = (!a.mask || a.mask[tr]) && t < a.T;
+    R row;
+    row.load(x + tr * a.ld, a.E, g, in);
+    row.weigh(in);
+    const float inv = row.inverse();
     float out[C];
-    // the loss's part: constant factors f
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) dot += row.p[i] * f[i];
+    for (int i = 0; i < C; ++i) {
+      row.e[i] *= inv;  // p
+      dot = __builtin_fmaf(row.e[i], f[i], dot);
+    }
     dot = group_reduce<G>(dot, add_f);
-#pragma unroll
-    for (int i = 0; i < C; ++i) out[i] = scale * row.p[i] * (f[i] - dot);
     if (a.d_weights) {
       // the chosen entries: lane g takes slots g, g + G, ...
       float wsum = 0.f, wd = 0.f;
@@ -352,41 +514,55 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteGradArgs
         for (u32 j = g; j < a.k; j += G) {
           const int64_t e = a.experts[t * a.k + j];
           if (e < 0 || e >= (int64_t)a.E) continue;
-          const float p = exp_f(to_f32(x[t * a.ld + e]) - row.top) * row.inv;
+          const float p = exp_f(to_f32(x[t * a.ld + e]) - row.top) * inv;
           wsum += p;
-          wd += p * a.d_weights[t * a.k + j];
+          wd = __builtin_fmaf(p, a.d_weights[t * a.k + j], wd);
         }
       wsum = group_reduce<G>(wsum, add_f);
       wd = group_reduce<G>(wd, add_f);
       const float r = a.normalize ? 1.f / wsum : 1.f;
-      const float mean = a.normalize ? wd * r : wd;
+      const float mean = wd * r;
+      if (!a.normalize) dot += mean;
       if (row.live)
         for (u32 j = g; j < a.k; j += G) {
           const int64_t e = a.experts[t * a.k + j];
           if (e < 0 || e >= (int64_t)a.E) continue;
-          const float p = exp_f(to_f32(x[t * a.ld + e]) - row.top) * row.inv * r;
+          const float p = exp_f(to_f32(x[t * a.ld + e]) - row.top) * inv * r;
           const float dw = a.d_weights[t * a.k + j];
           atomicAdd(&d[e], p * (a.normalize ? dw - mean : dw));
         }
       wave_lds_sync();
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        out[i] += d[i * G + g];
-        if (!a.normalize) out[i] -= row.p[i] * mean;
-      }
+      for (int i = 0; i < C; ++i) out[i] = __builtin_fmaf(row.e[i], f[i] - dot, d[R::index(i, g)]);
       wave_lds_sync();
+      if (row.live)
+        for (u32 j = g; j < a.k; j += G) {
+          const int64_t e = a.experts[t * a.k + j];
+          if (e >= 0 && e < (int64_t)a.E) d[e] = 0.f;
+        }
+      wave_lds_sync();
+    } else {
 #pragma unroll
-      for (int i = 0; i < C; ++i) d[i * G + g] = 0.f;
-      wave_lds_sync();
+      for (int i = 0; i < C; ++i) out[i] = row.e[i] * (f[i] - dot);
     }
-    if (t < a.T)
+    if (t >= a.T) continue;  // no lane exchange below
+    T* to = dx + t * a.E;
+    if constexpr (QUAD) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4) {
+        Four<T> q;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) from_f32(row.live ? out[i + w] : 0.f, q.e[w]);
+        if (R::index(i, g) < a.E) *reinterpret_cast<Four<T>*>(to + R::index(i, g)) = q;
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const u32 e = (u32)i * G + g;
         T o;
         from_f32(row.live ? out[i] : 0.f, o);
-        if (e < a.E) dx[t * a.E + e] = o;
+        if (R::index(i, g) < a.E) to[R::index(i, g)] = o;
       }
+    }
   }
 }
 
@@ -397,44 +573,57 @@ u32 route_blocks(u64 T, u32 groups) {
   return (u32)(b < kRouteMaxBlocks ? (b ? b : 1) : kRouteMaxBlocks);
 }
 
-template <class T, int G, int C>
+template <class T, int G, int C, bool QUAD>
 hipError_t route_launch(const RouteArgs& a0, hipStream_t s) {
   RouteArgs a = a0;
   a.blocks = route_blocks(a.T, kRouteThreads / G);
   if (a.balance_only)
-    route_kernel<T, G, C, true><<<a.blocks, kRouteThreads, 0, s>>>(a);
+    route_kernel<T, G, C, QUAD, true><<<a.blocks, kRouteThreads, 0, s>>>(a);
   else
-    route_kernel<T, G, C, false><<<a.blocks, kRouteThreads, 0, s>>>(a);
+    route_kernel<T, G, C, QUAD, false><<<a.blocks, kRouteThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.blocks == 1) return e;
   route_finish_kernel<<<(a.E + kFinishExperts - 1) / kFinishExperts, kFinishThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <class T, int G, int C>
+template <class T, int G, int C, bool QUAD>
 hipError_t route_launch(const RouteGradArgs& a, hipStream_t s) {
-  const u64 b = (a.T + kRouteThreads / G - 1) / (kRouteThreads / G);
+  const u64 b = (a.T + kGradThreads / G - 1) / (kGradThreads / G);
   const u64 cap = (u64)device_cu_count() * 8;
-  route_grad_kernel<T, G, C><<<(u32)(b < cap ? (b ? b : 1) : cap), kRouteThreads, 0, s>>>(a);
+  route_grad_kernel<T, G, C, QUAD><<<(u32)(b < cap ? (b ? b : 1) : cap), kGradThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// Lanes per row and entries per lane: the smallest C of the list that holds the row.
-template <class T, class A>
+// Lanes per row and entries per lane: the smallest that hold the row.
+template <class T, bool QUAD, class A>
 hipError_t route_shape(const A& a, hipStream_t s) {
-  if (a.E <= 16) return route_launch<T, 16, 1>(a, s);
-  if (a.E <= 64) return route_launch<T, 16, 4>(a, s);
-  if (a.E <= 128) return route_launch<T, 16, 8>(a, s);
-  if (a.E <= 256) return route_launch<T, 16, 16>(a, s);
-  if (a.E <= 512) return route_launch<T, 64, 8>(a, s);
-  return route_launch<T, 64, 16>(a, s);
+  if (a.E <= 16) return route_launch<T, 4, 4, QUAD>(a, s);
+  if (a.E <= 64) return route_launch<T, 16, 4, QUAD>(a, s);
+  if (a.E <= 128) return route_launch<T, 16, 8, QUAD>(a, s);
+  if (a.E <= 192) return route_launch<T, 16, 12, QUAD>(a, s);
+  if (a.E <= 256) return route_launch<T, 16, 16, QUAD>(a, s);
+  if (a.E <= 512) return route_launch<T, 64, 8, QUAD>(a, s);
+  return route_launch<T, 64, 16, QUAD>(a, s);
+}
+
+inline const void* written(const RouteArgs&) { return nullptr; }
+inline const void* written(const RouteGradArgs& a) { return a.d_x; }
+
+// Four entries at a time where every row starts at a multiple of four entries' bytes and
+// ends with a whole four.
+template <class T, class A>
+hipError_t route_rows(const A& a, hipStream_t s) {
+  const uintptr_t bases = (uintptr_t)a.x | (uintptr_t)written(a);
+  if (a.E % 4 == 0 && a.ld % 4 == 0 && bases % (4 * sizeof(T)) == 0) return route_shape<T, true>(a, s);
+  return route_shape<T, false>(a, s);
 }
 
 template <class A>
 hipError_t route_type(const A& a, int dtype, hipStream_t s) {
-  if (dtype == PROFK_FP32) return route_shape<float>(a, s);
-  if (dtype == PROFK_FP16) return route_shape<Half16>(a, s);
-  return route_shape<Brain16>(a, s);
+  if (dtype == PROFK_FP32) return route_rows<float>(a, s);
+  if (dtype == PROFK_FP16) return route_rows<Half16>(a, s);
+  return route_rows<Brain16>(a, s);
 }
 
 }  // namespace

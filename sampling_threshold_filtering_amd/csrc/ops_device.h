@@ -24,8 +24,8 @@ __device__ __forceinline__ void from_f32(float v, Half16& out) {
   __builtin_memcpy(&out.bits, &h, 2);
 }
 __device__ __forceinline__ void from_f32(float v, Brain16& out) {
-  const u32 b = __float_as_uint(v);
-  out.bits = (v != v) ? (unsigned short)((b >> 16) | 0x40u) : (unsigned short)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
+  const __bf16 b = (__bf16)v;  // one instruction on gfx950
+  __builtin_memcpy(&out.bits, &b, 2);
 }
 
 }  // namespace profk
