@@ -12,7 +12,7 @@
 // sorted in LDS (a bin too full for that is split into finer bins by key first).
 //
 // Exactness.  Weights are integers q_i = round(w_i 2^F), with F as large as lets a row's
-// sum fit 63 bits (F = 46 at 2^17 entries), from exp2 in 64 bits.  Integer sums do not
+// sum fit 63 bits (F = 46 at 2^17 entries), from 64-bit floats.  Integer sums do not
 // depend on their order, so LDS atomics and any split of the row give the same bits, and
 // the rounding of a weight (2^-(F+1) of the largest) is far below what a 24-bit u can
 // tell apart.  An entry below 2^-F of the largest counts as absent.
@@ -89,6 +89,28 @@ __device__ __forceinline__ void for_each_entry(const T* row, u32 V, F f) {
   for (u32 i = head + nvec * W + threadIdx.x; i < V; i += kThreads) f(to_f32(row[i]), i);
 }
 
+// 2^y for y <= 0: y = n + f with |f| <= 1/2, the Taylor series of e^(f ln 2) to the power
+// 13 (the next term is below 2^-57), scaled by 2^n.  2^0 is exactly 1.
+__device__ __forceinline__ double pow2(double y) {
+  y = y < -2000.0 ? -2000.0 : y;
+  const double n = rint(y), x = (y - n) * 0.69314718055994530942;
+  double e = 1.0 / 6227020800.0;
+  e = __builtin_fma(e, x, 1.0 / 479001600.0);
+  e = __builtin_fma(e, x, 1.0 / 39916800.0);
+  e = __builtin_fma(e, x, 1.0 / 3628800.0);
+  e = __builtin_fma(e, x, 1.0 / 362880.0);
+  e = __builtin_fma(e, x, 1.0 / 40320.0);
+  e = __builtin_fma(e, x, 1.0 / 5040.0);
+  e = __builtin_fma(e, x, 1.0 / 720.0);
+  e = __builtin_fma(e, x, 1.0 / 120.0);
+  e = __builtin_fma(e, x, 1.0 / 24.0);
+  e = __builtin_fma(e, x, 1.0 / 6.0);
+  e = __builtin_fma(e, x, 0.5);
+  e = __builtin_fma(e, x, 1.0);
+  e = __builtin_fma(e, x, 1.0);
+  return __builtin_ldexp(e, (int)n);
+}
+
 // The row's weights relative to its largest value.
 struct Weigher {
   float top;     // the largest value
@@ -100,7 +122,7 @@ struct Weigher {
     return v == top ? 0.0 : ((double)v - (double)top) * c;  // 0 also where both are +inf
   }
   __device__ __forceinline__ bool present(double y) const { return y >= limit; }  // false for NaN
-  __device__ __forceinline__ u64 weight(double y) const { return (u64)rint(exp2(y) * scale); }
+  __device__ __forceinline__ u64 weight(double y) const { return (u64)rint(pow2(y) * scale); }
   __device__ __forceinline__ u32 bin(double y) const {  // monotone in the value
     const double b = -y * bins;
     return b >= (double)(kTokBins - 1) ? kTokBins - 1 : (u32)b;
@@ -205,7 +227,7 @@ __device__ inline void value_histogram(TokLds& L, const T* row, u32 V, const Wei
   for_each_entry(row, V, [&](float v, u32) {
     const double y = w.exponent(v);
     if (!w.present(y)) return;
-    const double e = exp2(y);
+    const double e = pow2(y);
     const u64 q = (u64)rint(e * w.scale);
     const u32 b = w.bin(y);
     atomicAdd(&L.mass[b], q);
@@ -333,12 +355,9 @@ __device__ __forceinline__ RowSettings row_settings(const TokenArgs& a, u64 r) {
   return s;
 }
 
-}  // namespace
-
+// One row by value bins: any type, any length.
 template <class T>
-__global__ __launch_bounds__(kThreads) void sample_tokens_kernel(TokenArgs a) {
-  __shared__ TokLds L;
-  const u64 r = blockIdx.x;
+__device__ void sample_row_by_value(TokLds& L, const TokenArgs& a, u64 r) {
   const T* row = reinterpret_cast<const T*>(a.x) + r * a.ld;
   const u32 V = (u32)a.V;
   const RowSettings s = row_settings(a, r);
@@ -405,6 +424,538 @@ __global__ __launch_bounds__(kThreads) void sample_tokens_kernel(TokenArgs a) {
     a.logprobs[r] = (float)(y * 0.69314718055994530942 - log((double)keep.mass / w.scale));
   }
 }
+
+
+// ---------------------------------------------------------------------------------------
+// Rows of 16-bit logits: a counter for every value.
+//
+// A row of such logits has few different values, so it is enough to count them: 65536
+// counters of 16 bits fill 128 KB of LDS, an entry costs one LDS addition and no
+// exponential, and the weights are worked out once per value that occurs, not once per
+// entry.  (512 rows of 131072 by value bins, two passes with an exponential and two 64-bit
+// additions per entry: 356 us.)  Codes go down with the value: code(h) = h ^ 0x7FFF for
+// h >= 0, else h, so -0 comes right after +0; a positive value's counter is the low half of
+// word code, a negative one's the high half of word code - 0x8000.  A counter that
+// overflows makes the counters' sum differ from the number of entries counted, since each
+// carry takes 65536 or 65535 from it; such a row goes by value bins.
+//
+// Eight neighbouring codes (a cell) lie within one binade, so their weights are a geometric
+// series: two exponentials give all eight.  In the largest value's cell each is worked out
+// by itself, so that equal largest entries weigh exactly 2^F.  Cells are summed in 64-bit
+// floats and rounded to integers; sums of cells are exact, so the answer depends on the
+// counters alone.
+constexpr u32 kCodeWords = 32768;
+constexpr u32 kCellCodes = 8;
+constexpr u32 kGroupCodes = kCellCodes * kWave;  // one wavefront's step: 512 codes
+constexpr u32 kGroups = 65536 / kGroupCodes;
+constexpr u32 kMatchCap = 1024;
+
+struct CodeLds {
+  u32 cnt[kCodeWords];
+  u64 mass[kGroups];
+  u32 n[kGroups];
+  u32 match[kMatchCap];
+  u64 scan[kWaves];
+  u32 top, abs_max, counted, matches;
+  u32 code, pair, j, done;
+};
+
+union SampleLds {
+  CodeLds code;
+  TokLds value;
+};
+
+template <class T> struct CodeOf;
+template <> struct CodeOf<Half16> { static constexpr u32 inf = 0x7C00; };
+template <> struct CodeOf<Brain16> { static constexpr u32 inf = 0x7F80; };
+
+template <class T>
+__device__ __forceinline__ float value_of_code(u32 c) {
+  T h;
+  h.bits = (unsigned short)(c < 0x8000u ? c ^ 0x7FFFu : c);
+  return to_f32(h);
+}
+
+__device__ __forceinline__ u32 code_of_bits(u32 h) { return h < 0x8000u ? h ^ 0x7FFFu : h; }
+
+// A code at or past that of every value >= lim, and of a number.
+template <class T>
+__device__ __forceinline__ u32 code_past(float lim) {
+  constexpr u32 lowest = 0x8000u | (CodeOf<T>::inf - 1);
+  if (!(lim > -3.4e38f)) return lowest;
+  T h;
+  from_f32(lim, h);
+  const u32 c = code_of_bits(h.bits) + 1;
+  return c < lowest ? c : lowest;
+}
+
+// The last code that counts, below a largest value of code `top`: entries under 2^-F of it
+// are absent.
+template <class T>
+__device__ __forceinline__ u32 last_code(u32 top, float t, float F) {
+  const float v = value_of_code<T>(top);
+  if (!(v < __builtin_huge_valf())) return top;
+  return code_past<T>(v - F * 0.69314718f * t);
+}
+
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u32 pk_codes(u32 w) {  // two codes
+  const i16x2 sign = __builtin_bit_cast(i16x2, w) >> 15;
+  return w ^ (0x7FFF7FFFu & ~__builtin_bit_cast(u32, sign));
+}
+__device__ __forceinline__ u32 pk_min(u32 a, u32 b) {
+  const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
+  return __builtin_bit_cast(u32, __builtin_elementwise_min(x, y));
+}
+__device__ __forceinline__ u32 pk_max(u32 a, u32 b) {
+  const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
+  return __builtin_bit_cast(u32, __builtin_elementwise_max(x, y));
+}
+__device__ __forceinline__ u32 wave_min(u32 v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const u32 o = __shfl_xor(v, d);
+    v = o < v ? o : v;
+  }
+  return v;
+}
+template <class V>
+__device__ __forceinline__ V wave_sum(V v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {  // inclusive
+#pragma unroll
+  for (u32 d = 1; d < (u32)kWave; d <<= 1) {
+    const V o = __shfl_up(v, d);
+    if (lane_id() >= d) v += o;
+  }
+  return v;
+}
+
+// Loads of U vectors per thread and batch, the next batch's in flight while f runs on one.
+template <int U, class F>
+__device__ __forceinline__ void for_each_batch(const uint4* vec, u32 nvec, u32 fill, F f) {
+  uint4 cur[U], nxt[U];
+  auto load = [&](uint4 (&b)[U], u32 at) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const u32 j = at + (u32)i * kThreads;
+      b[i] = j < nvec ? vec[j] : make_uint4(fill, fill, fill, fill);
+    }
+  };
+  load(cur, threadIdx.x);
+  for (u32 at = threadIdx.x; at - threadIdx.x < nvec; at += U * kThreads) {
+    load(nxt, at + U * kThreads);
+    f(cur, at);
+#pragma unroll
+    for (int i = 0; i < U; ++i) cur[i] = nxt[i];
+  }
+}
+
+// The cell of code c0 (a multiple of 8): how often each code up to `last` occurs, and the
+// running sums of count times weight.
+template <class T>
+struct Cell {
+  u32 c0;
+  u32 n[kCellCodes];
+  double sum[kCellCodes];
+
+  __device__ __forceinline__ bool read(const CodeLds& L, u32 first, u32 last) {
+    c0 = first;
+    const u32 at = first & 0x7FFFu, shift = first >> 15 << 4;
+    const uint4 a = *reinterpret_cast<const uint4*>(&L.cnt[at]), b = *reinterpret_cast<const uint4*>(&L.cnt[at + 4]);
+    const u32 w[kCellCodes] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    u32 any = 0;
+#pragma unroll
+    for (u32 i = 0; i < kCellCodes; ++i) {
+      n[i] = first + i <= last ? w[i] >> shift & 0xFFFFu : 0u;
+      any |= n[i];
+    }
+    return any != 0;
+  }
+  __device__ __forceinline__ void weigh(const Weigher& w, u32 top) {
+    const double v0 = (double)value_of_code<T>(c0), v1 = (double)value_of_code<T>(c0 + 1);
+    double p = pow2((v0 - (double)w.top) * w.c) * w.scale, s = 0;
+    const double rho = pow2((v1 - v0) * w.c);
+    const bool first = c0 <= top;  // codes before the largest value's do not occur
+    if (__ballot(first)) {
+#pragma unroll
+      for (u32 i = 0; i < kCellCodes; ++i) {
+        const double q = first ? pow2(w.exponent(value_of_code<T>(c0 + i))) * w.scale : p;
+        sum[i] = s = __builtin_fma((double)n[i], n[i] ? q : 0.0, s);
+        p *= rho;
+      }
+    } else {
+#pragma unroll
+      for (u32 i = 0; i < kCellCodes; ++i) {
+        sum[i] = s = __builtin_fma((double)n[i], p, s);
+        p *= rho;
+      }
+    }
+  }
+  __device__ __forceinline__ u64 mass() const { return (u64)rint(sum[kCellCodes - 1]); }
+  __device__ __forceinline__ u32 count() const {
+    u32 c = 0;
+#pragma unroll
+    for (u32 i = 0; i < kCellCodes; ++i) c += n[i];
+    return c;
+  }
+};
+
+// A code and the prefix of the order before it and through it.
+struct CodePlace {
+  u32 code;
+  u64 n0, m0, n1, m1;
+  // entries of this code up to the first whose prefix's mass reaches Q
+  __device__ __forceinline__ u64 entries(u64 Q) const {
+    const u64 cnt = n1 - n0, D = m1 - m0;
+    if (Q <= m0 || cnt <= 1) return 1;
+    const u64 X = Q - m0;
+    u64 j;
+    if (D % cnt == 0 && D >= cnt)
+      j = (X + D / cnt - 1) / (D / cnt);
+    else
+      j = (u64)ceil((double)X * (double)cnt / (double)D);
+    return j < 1 ? 1 : j > cnt ? cnt : j;
+  }
+  __device__ __forceinline__ u64 mass_through(u64 j) const {
+    const u64 cnt = n1 - n0, D = m1 - m0;
+    if (j == cnt) return m1;
+    return m0 + (D % cnt == 0 ? j * (D / cnt) : (u64)rint((double)D * (double)j / (double)cnt));
+  }
+};
+
+enum class Ask { kCount, kMass, kCode };
+
+// Where the running count or mass reaches Q, or the place of code Q.  One wavefront: a
+// scan over the groups, then over the cells of one group, then the codes of one cell.
+template <class T>
+__device__ CodePlace find_code(const CodeLds& L, const Weigher& w, u32 top, u32 last, Ask ask, u64 Q) {
+  const u32 lane = lane_id();
+  static_assert(kGroups == 2 * kWave, "a lane holds two groups");
+  const u64 ma = L.mass[2 * lane], mb = L.mass[2 * lane + 1];
+  const u32 na = L.n[2 * lane], nb = L.n[2 * lane + 1];
+  u64 m = wave_scan(ma + mb);
+  u32 n = wave_scan(na + nb);
+  u32 g;
+  if (ask == Ask::kCode) {
+    g = (u32)Q / kGroupCodes;
+  } else {
+    const u64 reach = __ballot(ask == Ask::kMass ? m >= Q : (u64)n >= Q);
+    const u32 at = reach ? (u32)__builtin_ctzll(reach) : kWave - 1;
+    const u64 half = ask == Ask::kMass ? m - mb : (u64)(n - nb);
+    g = 2 * at + (__shfl(half, (int)at) < Q ? 1u : 0u);
+  }
+  u64 m0 = __shfl(g & 1 ? m - mb : m - mb - ma, (int)(g / 2));
+  u64 n0 = __shfl(g & 1 ? n - nb : n - nb - na, (int)(g / 2));
+  Cell<T> c;
+  c.read(L, g * kGroupCodes + lane * kCellCodes, last);
+  c.weigh(w, top);
+  const u64 cm = c.mass();
+  const u32 cn = c.count();
+  m = m0 + wave_scan(cm);
+  const u64 nn = n0 + wave_scan(cn);
+  u32 at;
+  if (ask == Ask::kCode) {
+    at = (u32)Q % kGroupCodes / kCellCodes;
+  } else {
+    const u64 reach = __ballot(ask == Ask::kMass ? m >= Q : nn >= Q);
+    at = reach ? (u32)__builtin_ctzll(reach) : kWave - 1;
+  }
+  m0 = m - cm;
+  n0 = nn - cn;
+  CodePlace r = {c.c0, n0, m0, n0, m0};
+  u64 ni = n0;
+  bool found = false;
+#pragma unroll
+  for (u32 i = 0; i < kCellCodes; ++i) {
+    const u64 mi = m0 + (u64)rint(c.sum[i]);
+    ni += c.n[i];
+    if (!found && (ask == Ask::kCode || c.n[i])) {
+      r.n0 = r.n1;
+      r.m0 = r.m1;
+      r.n1 = ni;
+      r.m1 = mi;
+      r.code = c.c0 + i;
+    }
+    found |= ask == Ask::kCode ? c.c0 + i == (u32)Q : (ask == Ask::kMass ? mi >= Q : ni >= Q) && c.n[i];
+  }
+  r.code = __shfl(r.code, (int)at);
+  r.n0 = __shfl(r.n0, (int)at);
+  r.m0 = __shfl(r.m0, (int)at);
+  r.n1 = __shfl(r.n1, (int)at);
+  r.m1 = __shfl(r.m1, (int)at);
+  return r;
+}
+
+// The last code whose weight is at least m: each of three steps tries 64 codes at a time.
+template <class T>
+__device__ u32 last_code_of_weight(const Weigher& w, u32 top, u32 last, float m) {
+  u32 lo = top, len = last - top + 1;  // code lo has it
+  while (len > 1) {
+    const u32 step = (len + kWave - 1) / kWave;
+    const u32 c = lo + lane_id() * step;
+    const u64 has = __ballot(c < lo + len && pow2(w.exponent(value_of_code<T>(c))) >= (double)m);
+    const u32 at = has ? 63u - (u32)__builtin_clzll(has) : 0u;
+    const u32 end = lo + len;
+    lo += at * step;
+    len = end - lo < step ? end - lo : step;
+  }
+  return lo;
+}
+
+// The three filters and the draw, in one wavefront.
+template <class T>
+__device__ void answer_codes(CodeLds& L, const TokenArgs& a, u64 r, const RowSettings& s, const Weigher& w, u32 top,
+                             u32 last) {
+  const u32 lane = lane_id();
+  const u64 N = wave_sum((u64)L.n[2 * lane] + L.n[2 * lane + 1]);
+  u64 kn = N, km = wave_sum(L.mass[2 * lane] + L.mass[2 * lane + 1]);
+  if (s.k && s.k < N) {
+    const CodePlace c = find_code<T>(L, w, top, last, Ask::kCount, s.k);
+    kn = s.k;
+    km = c.mass_through(s.k - c.n0);
+  }
+  if (s.p < 1.f) {
+    u64 Q = (u64)ceil((double)s.p * (double)km);
+    if (Q < 1 || !(s.p > 0.f)) Q = 1;
+    if (Q < km) {
+      const CodePlace c = find_code<T>(L, w, top, last, Ask::kMass, Q);
+      const u64 j = c.entries(Q);
+      kn = c.n0 + j;
+      km = c.mass_through(j);
+    }
+  }
+  if (s.m > 0.f) {
+    const CodePlace c = find_code<T>(L, w, top, last, Ask::kCode, last_code_of_weight<T>(w, top, last, s.m));
+    if (c.n1 < kn) {
+      kn = c.n1;
+      km = c.m1;
+    }
+  }
+  u64 Q = (u64)((double)s.u * (double)km) + 1;
+  if (Q > km) Q = km;
+  const CodePlace c = find_code<T>(L, w, top, last, Ask::kMass, Q);
+  if (lane == 0) {
+    L.code = c.code;
+    L.j = (u32)c.entries(Q);
+    const double y = w.exponent(value_of_code<T>(c.code));
+    a.logprobs[r] = (float)(y * 0.69314718055994530942 - log((double)km / w.scale));
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs& a, u64 r) {
+  CodeLds& L = S.code;
+  constexpr u32 kInf = CodeOf<T>::inf;
+  constexpr u32 kLowest = 0x8000u | (kInf - 1);  // the lowest number's code
+  constexpr u32 kFill = (0x8000u | kInf) * 0x10001u;  // two entries of -inf
+  const unsigned short* row = reinterpret_cast<const unsigned short*>(a.x) + r * a.ld;
+  const u32 V = (u32)a.V;
+  const RowSettings s = row_settings(a, r);
+  u32 lg = 0;
+  while ((1ull << lg) < a.V) ++lg;
+  const int F = 62 - (int)lg < 50 ? 62 - (int)lg : 50;
+  u32 head = (u32)((16 - ((uintptr_t)row & 15)) & 15) / 2;
+  if (head > V) head = V;
+  const u32 nvec = (V - head) / 8, tail = head + nvec * 8;
+  const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+  for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads)
+    reinterpret_cast<uint4*>(L.cnt)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) {
+    L.top = 0xFFFFu;
+    L.abs_max = L.counted = L.matches = 0;
+  }
+  __syncthreads();
+  // 1. count every entry that may be present: of the largest value so far, or less than
+  // 2^-(F+1) below it, so that a masked row's lowest values do not queue for one counter
+  u32 tops = 0xFFFFFFFFu, abs_max = 0, thr = 0, counted = 0;
+  bool first = true;
+  auto count = [&](u32 c) {
+    if (c <= thr) {
+      atomicAdd(&L.cnt[c & 0x7FFFu], c & 0x8000u ? 0x10000u : 1u);
+      ++counted;
+    }
+  };
+  auto threshold = [&]() {
+    const u32 t2 = tops & 0xFFFFu, t1 = tops >> 16;
+    const u32 top = wave_min(t1 < t2 ? t1 : t2);
+    thr = top > kLowest ? kLowest : s.t > 0.f ? last_code<T>(top, s.t, (float)(F + 1)) : top;
+  };
+  u32 edge = kFill;  // the entries before and after the vectors: at most 7 and 7
+  if (threadIdx.x < head) edge = row[threadIdx.x] | (kFill & 0xFFFF0000u);
+  if (threadIdx.x < V - tail) edge = (edge & 0xFFFFu) | (u32)row[tail + threadIdx.x] << 16;
+  tops = pk_codes(edge);
+  abs_max = edge & 0x7FFF7FFFu;
+  if (nvec == 0) threshold();
+  for_each_batch<4>(vec, nvec, kFill, [&](const uint4 (&b)[4], u32) {
+    u32 c[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32 w[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        c[i * 4 + k] = pk_codes(w[k]);
+        abs_max = pk_max(abs_max, w[k] & 0x7FFF7FFFu);
+        tops = pk_min(tops, c[i * 4 + k]);
+      }
+    }
+    if (first) threshold();
+    first = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      count(c[i] & 0xFFFFu);
+      count(c[i] >> 16);
+    }
+  });
+  {
+    const u32 c = pk_codes(edge);
+    count(c & 0xFFFFu);
+    count(c >> 16);
+  }
+  {
+    const u32 t2 = tops & 0xFFFFu, t1 = tops >> 16, m2 = abs_max & 0xFFFFu, m1 = abs_max >> 16;
+    const u32 t = wave_min(t1 < t2 ? t1 : t2), m = ~wave_min(~(m1 > m2 ? m1 : m2)), n = wave_sum(counted);
+    if (lane_id() == 0) {
+      atomicMin(&L.top, t);
+      atomicMax(&L.abs_max, m);
+      atomicAdd(&L.counted, n);
+    }
+  }
+  __syncthreads();
+  const u32 top = L.top;
+  if (L.abs_max > kInf || top > kLowest) {
+    if (threadIdx.x == 0) {
+      a.tokens[r] = -1;
+      a.logprobs[r] = L.abs_max > kInf ? __uint_as_float(0x7FC00000u) : -__builtin_huge_valf();
+    }
+    return;
+  }
+  if (V > 0xFFFFu) {  // may a counter have overflowed?
+    u32 n = 0;
+    for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads) {
+      const uint4 w = reinterpret_cast<const uint4*>(L.cnt)[i];
+      n = __builtin_amdgcn_sad_u16(w.x, 0, n);
+      n = __builtin_amdgcn_sad_u16(w.y, 0, n);
+      n = __builtin_amdgcn_sad_u16(w.z, 0, n);
+      n = __builtin_amdgcn_sad_u16(w.w, 0, n);
+    }
+    n = wave_sum(n);
+    if (lane_id() == 0) L.scan[threadIdx.x / kWave] = n;
+    __syncthreads();
+    u32 total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) total += (u32)L.scan[w];
+    const bool lost = total != L.counted;
+    __syncthreads();
+    if (lost) return sample_row_by_value<T>(S.value, a, r);
+  }
+  // 2. the groups' counts and masses, then the questions
+  if (s.t > 0.f) {
+    Weigher w;
+    w.top = value_of_code<T>(top);
+    w.c = 1.4426950408889634074 / (double)s.t;
+    w.scale = (double)(1ull << F);
+    const u32 last = last_code<T>(top, s.t, (float)F);
+    for (u32 g = threadIdx.x / kWave; g < kGroups; g += kWaves) {
+      u64 m = 0;
+      u32 n = 0;
+      if (g * kGroupCodes + kGroupCodes > top && g * kGroupCodes <= last) {
+        Cell<T> c;
+        if (__ballot(c.read(L, g * kGroupCodes + lane_id() * kCellCodes, last))) {
+          c.weigh(w, top);
+          m = wave_sum(c.mass());
+          n = wave_sum(c.count());
+        }
+      }
+      if (lane_id() == 0) {
+        L.mass[g] = m;
+        L.n[g] = n;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < kWave) answer_codes<T>(L, a, r, s, w, top, last);
+  } else if (threadIdx.x == 0) {
+    L.code = top;
+    L.j = 1;
+    a.logprobs[r] = 0.f;
+  }
+  __syncthreads();
+  // 3. the j-th entry of that code, by index
+  const u32 code = L.code;
+  const bool zero = code == 0x7FFFu || code == 0x8000u;
+  const u32 j = L.j + (code == 0x8000u ? L.cnt[0x7FFF] & 0xFFFFu : 0u);
+  const u32 want = zero ? 0u : (code < 0x8000u ? code ^ 0x7FFFu : code) * 0x10001u;
+  const u32 mask = zero ? 0x7FFF7FFFu : 0xFFFFFFFFu;
+  auto match = [&](u32 i) {
+    const u32 at = atomicAdd(&L.matches, 1u);
+    if (at < kMatchCap) L.match[at] = i;
+  };
+  auto look = [&](u32 x, u32 i) {  // x: two entries, equal ones 0
+    if ((x & 0xFFFFu) == 0) match(i);
+    if (x < 0x10000u) match(i + 1);
+  };
+  if (threadIdx.x < head && (((edge ^ want) & mask) & 0xFFFFu) == 0) match(threadIdx.x);
+  if (threadIdx.x < V - tail && ((edge ^ want) & mask) < 0x10000u) match(tail + threadIdx.x);
+  for_each_batch<4>(vec, nvec, ~want, [&](const uint4 (&b)[4], u32 at) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32 x[4] = {(b[i].x ^ want) & mask, (b[i].y ^ want) & mask, (b[i].z ^ want) & mask, (b[i].w ^ want) & mask};
+      u32 some = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) some |= (x[k] - 0x00010001u) & ~x[k] & 0x80008000u;
+      if (some) {
+        const u32 e = head + (at + (u32)i * kThreads) * 8;
+#pragma unroll
+        for (u32 k = 0; k < 4; ++k) look(x[k], e + 2 * k);
+      }
+    }
+  });
+  __syncthreads();
+  const u32 n = L.matches;
+  if (n <= kMatchCap) {
+    if (threadIdx.x < n) {
+      const u32 mine = L.match[threadIdx.x];
+      u32 rank = 0;
+      for (u32 i = 0; i < n; ++i) rank += L.match[i] < mine;
+      if (rank == j - 1) a.tokens[r] = mine;
+    }
+    return;
+  }
+  // many of them: counts per stretch of the row, then one stretch
+  const u32 per = (V + kThreads - 1) / kThreads;
+  const u32 i0 = threadIdx.x * per, i1 = i0 + per < V ? i0 + per : V;
+  u32 c = 0;
+  for (u32 i = i0; i < i1; ++i) c += (((u32)row[i] ^ want) & mask & 0xFFFFu) == 0;
+  const u64 upto = block_scan_u64(c, L.scan);
+  if (upto >= j && upto - c < j) {
+    u64 left = j - (upto - c);
+    for (u32 i = i0; i < i1; ++i)
+      if ((((u32)row[i] ^ want) & mask & 0xFFFFu) == 0 && --left == 0) {
+        a.tokens[r] = i;
+        break;
+      }
+  }
+}
+
+}  // namespace
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void sample_tokens_kernel(TokenArgs a) {
+  if constexpr (sizeof(T) == 2) {
+    __shared__ SampleLds S;
+    sample_row_by_code<T>(S, a, blockIdx.x);
+  } else {
+    __shared__ TokLds S;
+    sample_row_by_value<T>(S, a, blockIdx.x);
+  }
+}
+
 
 size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
 
