@@ -53,18 +53,56 @@ struct TokLds {
   u32 minp_n;
 };
 
+// Lane exchanges of a scan over the wavefront, as DPP moves (a shuffle through LDS takes
+// about ten times as long, and every answer waits for several scans): within rows of 16 by
+// 1, 2, 4, 8, then each row's last lane to the rows after it.  Lanes without a partner get
+// `none`.
+template <int STEP>
+__device__ __forceinline__ u32 scan_from(u32 v, u32 none) {
+  constexpr int ctrl = STEP < 4 ? 0x110 | 1 << STEP : STEP == 4 ? 0x142 : 0x143;
+  constexpr int rows = STEP < 4 ? 0xF : STEP == 4 ? 0xA : 0xC;
+  return (u32)__builtin_amdgcn_update_dpp((int)none, (int)v, ctrl, rows, 0xF, false);
+}
+template <int STEP>
+__device__ __forceinline__ u64 scan_from(u64 v, u64 none) {
+  return (u64)scan_from<STEP>((u32)(v >> 32), (u32)(none >> 32)) << 32 | scan_from<STEP>((u32)v, (u32)none);
+}
+template <class V, class F>
+__device__ __forceinline__ V wave_scan(V v, V none, F f) {  // inclusive
+  v = f(v, scan_from<0>(v, none));
+  v = f(v, scan_from<1>(v, none));
+  v = f(v, scan_from<2>(v, none));
+  v = f(v, scan_from<3>(v, none));
+  v = f(v, scan_from<4>(v, none));
+  return f(v, scan_from<5>(v, none));
+}
+__device__ __forceinline__ u32 of_lane(u32 v, u32 lane) {  // the lane is the same for all
+  return (u32)__builtin_amdgcn_readlane((int)v, (int)lane);
+}
+__device__ __forceinline__ u64 of_lane(u64 v, u32 lane) {
+  return (u64)of_lane((u32)(v >> 32), lane) << 32 | of_lane((u32)v, lane);
+}
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {
+  return wave_scan(v, (V)0, [](V x, V y) { return x + y; });
+}
+template <class V>
+__device__ __forceinline__ V wave_sum(V v) {
+  return of_lane(wave_scan(v), kWave - 1);
+}
+template <class V>
+__device__ __forceinline__ V wave_min(V v) {
+  return of_lane(wave_scan(v, (V)~(V)0, [](V x, V y) { return x < y ? x : y; }), kWave - 1);
+}
+
 // Inclusive scan over the block, one u64 per thread.
 __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* wave_tot) {
-  const u32 lane = lane_id(), wid = threadIdx.x / kWave;
-#pragma unroll
-  for (u32 d = 1; d < (u32)kWave; d <<= 1) {
-    const u64 o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  if (lane == kWave - 1) wave_tot[wid] = v;
+  v = wave_scan(v);
+  const u32 wid = threadIdx.x / kWave;
+  if (lane_id() == kWave - 1) wave_tot[wid] = v;
   __syncthreads();
-  u64 before = 0;
-  for (u32 w = 0; w < wid; ++w) before += wave_tot[w];
+  const u64 t = wave_scan(lane_id() < (u32)kWaves ? wave_tot[lane_id()] : 0);
+  const u64 before = wid ? of_lane(t, __builtin_amdgcn_readfirstlane(wid) - 1) : 0;
   __syncthreads();
   return v + before;
 }
@@ -89,25 +127,20 @@ __device__ __forceinline__ void for_each_entry(const T* row, u32 V, F f) {
   for (u32 i = head + nvec * W + threadIdx.x; i < V; i += kThreads) f(to_f32(row[i]), i);
 }
 
+// 1 / i! for i = 13, 12, ... 0, read into scalar registers.
+__constant__ const double kInverseFactorials[14] = {
+    1.0 / 6227020800.0, 1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+    1.0 / 40320.0,      1.0 / 5040.0,      1.0 / 720.0,      1.0 / 120.0,     1.0 / 24.0,
+    1.0 / 6.0,          0.5,               1.0,              1.0};
+
 // 2^y for y <= 0: y = n + f with |f| <= 1/2, the Taylor series of e^(f ln 2) to the power
-// 13 (the next term is below 2^-57), scaled by 2^n.  2^0 is exactly 1.
+// 13 (the next term is below 2^-57), scaled by 2^n.  2^0 is exactly 1; NaN gives 0.
 __device__ __forceinline__ double pow2(double y) {
-  y = y < -2000.0 ? -2000.0 : y;
+  y = __builtin_fmax(y, -2000.0);
   const double n = rint(y), x = (y - n) * 0.69314718055994530942;
-  double e = 1.0 / 6227020800.0;
-  e = __builtin_fma(e, x, 1.0 / 479001600.0);
-  e = __builtin_fma(e, x, 1.0 / 39916800.0);
-  e = __builtin_fma(e, x, 1.0 / 3628800.0);
-  e = __builtin_fma(e, x, 1.0 / 362880.0);
-  e = __builtin_fma(e, x, 1.0 / 40320.0);
-  e = __builtin_fma(e, x, 1.0 / 5040.0);
-  e = __builtin_fma(e, x, 1.0 / 720.0);
-  e = __builtin_fma(e, x, 1.0 / 120.0);
-  e = __builtin_fma(e, x, 1.0 / 24.0);
-  e = __builtin_fma(e, x, 1.0 / 6.0);
-  e = __builtin_fma(e, x, 0.5);
-  e = __builtin_fma(e, x, 1.0);
-  e = __builtin_fma(e, x, 1.0);
+  double e = kInverseFactorials[0];
+#pragma unroll
+  for (int i = 1; i < 14; ++i) e = __builtin_fma(e, x, kInverseFactorials[i]);
   return __builtin_ldexp(e, (int)n);
 }
 
@@ -155,7 +188,7 @@ __device__ __forceinline__ void scan_bins(TokLds& L) {
 }
 
 // Sorts L.list[0..n) descending and fills L.cum with the inclusive masses.
-__device__ inline void sort_and_weigh(TokLds& L, u32 n, const Weigher& w) {
+__device__ __forceinline__ void sort_and_weigh(TokLds& L, u32 n, const Weigher& w) {
   u32 P = 1;
   while (P < n) P <<= 1;
   for (u32 i = n + threadIdx.x; i < P; i += kThreads) L.list[i] = 0;
@@ -176,7 +209,7 @@ __device__ inline void sort_and_weigh(TokLds& L, u32 n, const Weigher& w) {
 
 // The answer inside the sorted list, whose first entry comes after `n0` entries and
 // `m0` mass of the order.
-__device__ inline Prefix find_in_list(TokLds& L, u32 n, u64 n0, u64 m0, bool by_mass, u64 Q) {
+__device__ __forceinline__ Prefix find_in_list(TokLds& L, u32 n, u64 n0, u64 m0, bool by_mass, u64 Q) {
   if (by_mass) {
     for (u32 i = threadIdx.x; i < n; i += kThreads) {
       const u64 here = m0 + L.cum[i], before = i ? m0 + L.cum[i - 1] : m0;
@@ -196,7 +229,7 @@ __device__ inline Prefix find_in_list(TokLds& L, u32 n, u64 n0, u64 m0, bool by_
 // Collects the entries accepted by `pick(value, exponent)` into L.list (at most kListCap;
 // the caller knows the number).
 template <class T, class F>
-__device__ inline u32 collect(TokLds& L, const T* row, u32 V, const Weigher& w, F pick) {
+__device__ __forceinline__ u32 collect(TokLds& L, const T* row, u32 V, const Weigher& w, F pick) {
   if (threadIdx.x == 0) L.list_n = 0;
   __syncthreads();
   for_each_entry(row, V, [&](float v, u32 i) {
@@ -214,7 +247,7 @@ __device__ inline u32 collect(TokLds& L, const T* row, u32 V, const Weigher& w, 
 
 // Histogram of the row's present entries into the value bins, as prefix sums.
 template <class T>
-__device__ inline void value_histogram(TokLds& L, const T* row, u32 V, const Weigher& w, float min_p) {
+__device__ __forceinline__ void value_histogram(TokLds& L, const T* row, u32 V, const Weigher& w, float min_p) {
   L.mass[threadIdx.x] = 0;
   L.cnt[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
@@ -248,7 +281,7 @@ __device__ inline void value_histogram(TokLds& L, const T* row, u32 V, const Wei
 // Position in the order of the first prefix whose count / mass reaches Q.  The value
 // histogram (prefix sums) is in L; hist_lost is set where a bin had to be split in its place.
 template <class T>
-__device__ Prefix resolve(TokLds& L, const T* row, u32 V, const Weigher& w, bool by_mass, u64 Q, bool want_key,
+__device__ __forceinline__ Prefix resolve(TokLds& L, const T* row, u32 V, const Weigher& w, bool by_mass, u64 Q, bool want_key,
                           bool& hist_lost) {
   const u32 b = find_bin(L, by_mass, Q);
   u64 n0 = b ? L.cnt[b - 1] : 0, m0 = b ? L.mass[b - 1] : 0;
@@ -357,7 +390,7 @@ __device__ __forceinline__ RowSettings row_settings(const TokenArgs& a, u64 r) {
 
 // One row by value bins: any type, any length.
 template <class T>
-__device__ void sample_row_by_value(TokLds& L, const TokenArgs& a, u64 r) {
+__device__ __forceinline__ void sample_row_by_value(TokLds& L, const TokenArgs& a, u64 r) {
   const T* row = reinterpret_cast<const T*>(a.x) + r * a.ld;
   const u32 V = (u32)a.V;
   const RowSettings s = row_settings(a, r);
@@ -399,32 +432,44 @@ __device__ void sample_row_by_value(TokLds& L, const TokenArgs& a, u64 r) {
   const u64 N = L.cnt[kTokBins - 1], Z = L.mass[kTokBins - 1];
   const u64 mn = L.minp_n, mm = L.minp_mass;
   __syncthreads();
+  u64 kn = N, km = Z;  // what is kept: entries and mass
   bool lost = false;
-  auto ask = [&](bool by_mass, u64 Q, bool want_key) {
+  for (int step = 0; step < 4; ++step) {  // one place where the search is inlined
+    bool by_mass = true;
+    u64 Q;
+    if (step == 0) {
+      if (!s.k || s.k >= kn) continue;
+      by_mass = false;
+      Q = s.k;
+    } else if (step == 1) {
+      Q = (u64)ceil((double)s.p * (double)km);
+      if (Q < 1 || !(s.p > 0.f)) Q = 1;
+      if (s.p >= 1.f || Q >= km) continue;
+    } else if (step == 2) {
+      if (s.m > 0.f && mn < kn) {
+        kn = mn;
+        km = mm;
+      }
+      continue;
+    } else {
+      Q = (u64)((double)s.u * (double)km) + 1;
+      if (Q > km) Q = km;
+    }
     if (lost) {
       value_histogram(L, row, V, w, 0.f);
       lost = false;
     }
-    return resolve(L, row, V, w, by_mass, Q, want_key, lost);
-  };
-  Prefix keep = {N, Z, 0};
-  if (s.k && s.k < N) keep = ask(false, s.k, false);
-  if (s.p < 1.f) {
-    u64 Q = (u64)ceil((double)s.p * (double)keep.mass);
-    if (Q < 1 || !(s.p > 0.f)) Q = 1;
-    if (Q < keep.mass) keep = ask(true, Q, false);
-  }
-  if (s.m > 0.f && mn < keep.n) keep = {mn, mm, 0};
-  u64 Q = (u64)((double)s.u * (double)keep.mass) + 1;
-  if (Q > keep.mass) Q = keep.mass;
-  const Prefix at = ask(true, Q, true);
-  if (threadIdx.x == 0) {
-    const double y = w.exponent(value_of_key(at.key));
-    a.tokens[r] = (int64_t)key_index(at.key);
-    a.logprobs[r] = (float)(y * 0.69314718055994530942 - log((double)keep.mass / w.scale));
+    const Prefix at = resolve(L, row, V, w, by_mass, Q, step == 3, lost);
+    if (step < 3) {
+      kn = at.n;
+      km = at.mass;
+    } else if (threadIdx.x == 0) {
+      const double y = w.exponent(value_of_key(at.key));
+      a.tokens[r] = (int64_t)key_index(at.key);
+      a.logprobs[r] = (float)(y * 0.69314718055994530942 - log((double)km / w.scale));
+    }
   }
 }
-
 
 // ---------------------------------------------------------------------------------------
 // Rows of 16-bit logits: a counter for every value.
@@ -440,8 +485,7 @@ __device__ void sample_row_by_value(TokLds& L, const TokenArgs& a, u64 r) {
 // carry takes 65536 or 65535 from it; such a row goes by value bins.
 //
 // Eight neighbouring codes (a cell) lie within one binade, so their weights are a geometric
-// series: two exponentials give all eight.  In the largest value's cell each is worked out
-// by itself, so that equal largest entries weigh exactly 2^F.  Cells are summed in 64-bit
+// series: two exponentials give all eight, and equal largest entries weigh exactly 2^F.  Cells are summed in 64-bit
 // floats and rounded to integers; sums of cells are exact, so the answer depends on the
 // counters alone.
 constexpr u32 kCodeWords = 32768;
@@ -513,99 +557,75 @@ __device__ __forceinline__ u32 pk_max(u32 a, u32 b) {
   const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
   return __builtin_bit_cast(u32, __builtin_elementwise_max(x, y));
 }
-__device__ __forceinline__ u32 wave_min(u32 v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const u32 o = __shfl_xor(v, d);
-    v = o < v ? o : v;
-  }
-  return v;
-}
-template <class V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-  return v;
-}
-template <class V>
-__device__ __forceinline__ V wave_scan(V v) {  // inclusive
-#pragma unroll
-  for (u32 d = 1; d < (u32)kWave; d <<= 1) {
-    const V o = __shfl_up(v, d);
-    if (lane_id() >= d) v += o;
-  }
-  return v;
-}
+// The 16-byte vectors of a row, `kBatch` a thread at a time.  NV > 0: all of a thread's NV
+// vectors stay in registers, loaded at once, so that a second pass reads no memory (NV = 16
+// holds 131072 entries in 64 registers a thread; one workgroup fills a CU by its LDS, so
+// they are there).  NV = 0: the next batch is in flight while one is dealt with.
+constexpr int kBatch = 4;
+template <int NV>
+struct RowVectors {
+  const uint4* vec;
+  u32 nvec, fill;
+  uint4 held[NV ? NV : 1];
 
-// Loads of U vectors per thread and batch, the next batch's in flight while f runs on one.
-template <int U, class F>
-__device__ __forceinline__ void for_each_batch(const uint4* vec, u32 nvec, u32 fill, F f) {
-  uint4 cur[U], nxt[U];
-  auto load = [&](uint4 (&b)[U], u32 at) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const u32 j = at + (u32)i * kThreads;
-      b[i] = j < nvec ? vec[j] : make_uint4(fill, fill, fill, fill);
-    }
-  };
-  load(cur, threadIdx.x);
-  for (u32 at = threadIdx.x; at - threadIdx.x < nvec; at += U * kThreads) {
-    load(nxt, at + U * kThreads);
-    f(cur, at);
-#pragma unroll
-    for (int i = 0; i < U; ++i) cur[i] = nxt[i];
+  __device__ __forceinline__ uint4 at(u32 j) const {
+    return j < nvec ? vec[j] : make_uint4(fill, fill, fill, fill);
   }
-}
-
-// The cell of code c0 (a multiple of 8): how often each code up to `last` occurs, and the
-// running sums of count times weight.
-template <class T>
-struct Cell {
-  u32 c0;
-  u32 n[kCellCodes];
-  double sum[kCellCodes];
-
-  __device__ __forceinline__ bool read(const CodeLds& L, u32 first, u32 last) {
-    c0 = first;
-    const u32 at = first & 0x7FFFu, shift = first >> 15 << 4;
-    const uint4 a = *reinterpret_cast<const uint4*>(&L.cnt[at]), b = *reinterpret_cast<const uint4*>(&L.cnt[at + 4]);
-    const u32 w[kCellCodes] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    u32 any = 0;
+  __device__ __forceinline__ RowVectors(const uint4* v, u32 n, u32 f) : vec(v), nvec(n), fill(f) {
 #pragma unroll
-    for (u32 i = 0; i < kCellCodes; ++i) {
-      n[i] = first + i <= last ? w[i] >> shift & 0xFFFFu : 0u;
-      any |= n[i];
-    }
-    return any != 0;
+    for (int i = 0; i < NV; ++i) held[i] = at(threadIdx.x + (u32)i * kThreads);
   }
-  __device__ __forceinline__ void weigh(const Weigher& w, u32 top) {
-    const double v0 = (double)value_of_code<T>(c0), v1 = (double)value_of_code<T>(c0 + 1);
-    double p = pow2((v0 - (double)w.top) * w.c) * w.scale, s = 0;
-    const double rho = pow2((v1 - v0) * w.c);
-    const bool first = c0 <= top;  // codes before the largest value's do not occur
-    if (__ballot(first)) {
+  template <class F>  // f(the batch, the first one's place)
+  __device__ __forceinline__ void for_each(F f) {
+    if constexpr (NV > 0) {
 #pragma unroll
-      for (u32 i = 0; i < kCellCodes; ++i) {
-        const double q = first ? pow2(w.exponent(value_of_code<T>(c0 + i))) * w.scale : p;
-        sum[i] = s = __builtin_fma((double)n[i], n[i] ? q : 0.0, s);
-        p *= rho;
+      for (int i = 0; i < NV; i += kBatch) {
+        const uint4 b[kBatch] = {held[i], held[i + 1], held[i + 2], held[i + 3]};
+        f(b, threadIdx.x + (u32)i * kThreads);
+        __builtin_amdgcn_sched_barrier(0);  // one batch's work at a time: registers
       }
     } else {
+      uint4 cur[kBatch], nxt[kBatch];
 #pragma unroll
-      for (u32 i = 0; i < kCellCodes; ++i) {
-        sum[i] = s = __builtin_fma((double)n[i], p, s);
-        p *= rho;
+      for (int i = 0; i < kBatch; ++i) cur[i] = at(threadIdx.x + (u32)i * kThreads);
+      for (u32 j = threadIdx.x; j - threadIdx.x < nvec; j += kBatch * kThreads) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) nxt[i] = at(j + (u32)(kBatch + i) * kThreads);
+        f(cur, j);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) cur[i] = nxt[i];
       }
     }
   }
-  __device__ __forceinline__ u64 mass() const { return (u64)rint(sum[kCellCodes - 1]); }
-  __device__ __forceinline__ u32 count() const {
-    u32 c = 0;
-#pragma unroll
-    for (u32 i = 0; i < kCellCodes; ++i) c += n[i];
-    return c;
-  }
 };
+
+// How many entries the cell of code c0 (a multiple of 8) holds up to code `last`, and their
+// mass.  The largest value's cell begins at that value: the codes before it do not occur.
+template <class T>
+__device__ __forceinline__ u32 cell_counters(const CodeLds& L, u32 c0, u32 last, u32 (&n)[kCellCodes]) {
+  const u32 at = c0 & 0x7FFFu, shift = c0 >> 15 << 4;
+  const uint4 a = *reinterpret_cast<const uint4*>(&L.cnt[at]), b = *reinterpret_cast<const uint4*>(&L.cnt[at + 4]);
+  const u32 w[kCellCodes] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  u32 sum = 0;
+#pragma unroll
+  for (u32 i = 0; i < kCellCodes; ++i) {
+    n[i] = c0 + i <= last ? w[i] >> shift & 0xFFFFu : 0u;
+    sum += n[i];
+  }
+  return sum;
+}
+template <class T>
+__device__ __forceinline__ u64 cell_mass(const Weigher& w, u32 top, u32 c0, const u32 (&n)[kCellCodes]) {
+  const double v0 = (double)value_of_code<T>(c0), v1 = (double)value_of_code<T>(c0 + 1);
+  const double rho = pow2((v1 - v0) * w.c);
+  double p = c0 <= top ? w.scale : pow2((v0 - (double)w.top) * w.c) * w.scale, s = 0;
+#pragma unroll
+  for (u32 i = 0; i < kCellCodes; ++i) {
+    s = __builtin_fma((double)n[i], p, s);
+    if (c0 + i >= top) p *= rho;
+  }
+  return (u64)rint(s);
+}
 
 // A code and the prefix of the order before it and through it.
 struct CodePlace {
@@ -635,62 +655,51 @@ enum class Ask { kCount, kMass, kCode };
 // Where the running count or mass reaches Q, or the place of code Q.  One wavefront: a
 // scan over the groups, then over the cells of one group, then the codes of one cell.
 template <class T>
-__device__ CodePlace find_code(const CodeLds& L, const Weigher& w, u32 top, u32 last, Ask ask, u64 Q) {
+__device__ __forceinline__ CodePlace find_code(const CodeLds& L, const Weigher& w, u32 top, u32 last, Ask ask, u64 Q) {
   const u32 lane = lane_id();
   static_assert(kGroups == 2 * kWave, "a lane holds two groups");
   const u64 ma = L.mass[2 * lane], mb = L.mass[2 * lane + 1];
   const u32 na = L.n[2 * lane], nb = L.n[2 * lane + 1];
-  u64 m = wave_scan(ma + mb);
-  u32 n = wave_scan(na + nb);
+  const u64 m = wave_scan(ma + mb);
+  const u32 n = wave_scan(na + nb);
   u32 g;
   if (ask == Ask::kCode) {
-    g = (u32)Q / kGroupCodes;
+    g = __builtin_amdgcn_readfirstlane((u32)Q) / kGroupCodes;
   } else {
     const u64 reach = __ballot(ask == Ask::kMass ? m >= Q : (u64)n >= Q);
     const u32 at = reach ? (u32)__builtin_ctzll(reach) : kWave - 1;
-    const u64 half = ask == Ask::kMass ? m - mb : (u64)(n - nb);
-    g = 2 * at + (__shfl(half, (int)at) < Q ? 1u : 0u);
+    g = 2 * at + (of_lane(ask == Ask::kMass ? m - mb : (u64)(n - nb), at) < Q ? 1u : 0u);
   }
-  u64 m0 = __shfl(g & 1 ? m - mb : m - mb - ma, (int)(g / 2));
-  u64 n0 = __shfl(g & 1 ? n - nb : n - nb - na, (int)(g / 2));
-  Cell<T> c;
-  c.read(L, g * kGroupCodes + lane * kCellCodes, last);
-  c.weigh(w, top);
-  const u64 cm = c.mass();
-  const u32 cn = c.count();
-  m = m0 + wave_scan(cm);
-  const u64 nn = n0 + wave_scan(cn);
+  const u64 gm = of_lane(g & 1 ? m - mb : m - mb - ma, g / 2);
+  const u32 gn = of_lane(g & 1 ? n - nb : n - nb - na, g / 2);
+  const u32 c0 = g * kGroupCodes + lane * kCellCodes;
+  u32 cnt[kCellCodes];
+  const u32 cn = cell_counters<T>(L, c0, last, cnt), n1 = gn + wave_scan(cn);
+  const u64 cm = cell_mass<T>(w, top, c0, cnt), m1 = gm + wave_scan(cm);
   u32 at;
   if (ask == Ask::kCode) {
-    at = (u32)Q % kGroupCodes / kCellCodes;
+    at = __builtin_amdgcn_readfirstlane((u32)Q) % kGroupCodes / kCellCodes;
   } else {
-    const u64 reach = __ballot(ask == Ask::kMass ? m >= Q : nn >= Q);
+    const u64 reach = __ballot(ask == Ask::kMass ? m1 >= Q : (u64)n1 >= Q);
     at = reach ? (u32)__builtin_ctzll(reach) : kWave - 1;
   }
-  m0 = m - cm;
-  n0 = nn - cn;
-  CodePlace r = {c.c0, n0, m0, n0, m0};
-  u64 ni = n0;
-  bool found = false;
-#pragma unroll
-  for (u32 i = 0; i < kCellCodes; ++i) {
-    const u64 mi = m0 + (u64)rint(c.sum[i]);
-    ni += c.n[i];
-    if (!found && (ask == Ask::kCode || c.n[i])) {
-      r.n0 = r.n1;
-      r.m0 = r.m1;
-      r.n1 = ni;
-      r.m1 = mi;
-      r.code = c.c0 + i;
-    }
-    found |= ask == Ask::kCode ? c.c0 + i == (u32)Q : (ask == Ask::kMass ? mi >= Q : ni >= Q) && c.n[i];
+  // the cell's codes, a lane each
+  const u32 first = of_lane(c0, at);
+  const u64 ms = of_lane(m1 - cm, at);
+  const u32 ns = of_lane(n1 - cn, at), code = first + lane;
+  const bool mine = lane < kCellCodes && code >= top && code <= last;
+  const u32 nc = mine ? L.cnt[code & 0x7FFFu] >> (code >> 15 << 4) & 0xFFFFu : 0u;
+  const double q = mine ? pow2(w.exponent(value_of_code<T>(code))) * w.scale : 0.0;
+  const u64 mc = (u64)rint((double)nc * q), mi = ms + wave_scan(mc);
+  const u32 ni = ns + wave_scan(nc);
+  u32 i;
+  if (ask == Ask::kCode) {
+    i = __builtin_amdgcn_readfirstlane((u32)Q) % kCellCodes;
+  } else {
+    const u64 some = __ballot(nc != 0), reach = some & __ballot(ask == Ask::kMass ? mi >= Q : (u64)ni >= Q);
+    i = reach ? (u32)__builtin_ctzll(reach) : some ? 63u - (u32)__builtin_clzll(some) : 0u;
   }
-  r.code = __shfl(r.code, (int)at);
-  r.n0 = __shfl(r.n0, (int)at);
-  r.m0 = __shfl(r.m0, (int)at);
-  r.n1 = __shfl(r.n1, (int)at);
-  r.m1 = __shfl(r.m1, (int)at);
-  return r;
+  return {first + i, of_lane(ni - nc, i), of_lane(mi - mc, i), of_lane(ni, i), of_lane(mi, i)};
 }
 
 // The last code whose weight is at least m: each of three steps tries 64 codes at a time.
@@ -711,45 +720,46 @@ __device__ u32 last_code_of_weight(const Weigher& w, u32 top, u32 last, float m)
 
 // The three filters and the draw, in one wavefront.
 template <class T>
-__device__ void answer_codes(CodeLds& L, const TokenArgs& a, u64 r, const RowSettings& s, const Weigher& w, u32 top,
-                             u32 last) {
+__device__ __forceinline__ void answer_codes(CodeLds& L, const TokenArgs& a, u64 r, const RowSettings& s,
+                                             const Weigher& w, u32 top, u32 last) {
   const u32 lane = lane_id();
-  const u64 N = wave_sum((u64)L.n[2 * lane] + L.n[2 * lane + 1]);
-  u64 kn = N, km = wave_sum(L.mass[2 * lane] + L.mass[2 * lane + 1]);
-  if (s.k && s.k < N) {
-    const CodePlace c = find_code<T>(L, w, top, last, Ask::kCount, s.k);
-    kn = s.k;
-    km = c.mass_through(s.k - c.n0);
-  }
-  if (s.p < 1.f) {
-    u64 Q = (u64)ceil((double)s.p * (double)km);
-    if (Q < 1 || !(s.p > 0.f)) Q = 1;
-    if (Q < km) {
-      const CodePlace c = find_code<T>(L, w, top, last, Ask::kMass, Q);
-      const u64 j = c.entries(Q);
+  u64 kn = wave_sum(L.n[2 * lane] + L.n[2 * lane + 1]);  // what is kept: entries and mass
+  u64 km = wave_sum(L.mass[2 * lane] + L.mass[2 * lane + 1]);
+  for (int step = 0; step < 4; ++step) {  // one place where the search is inlined
+    Ask ask = Ask::kMass;
+    u64 Q;
+    if (step == 0) {
+      if (!s.k || s.k >= kn) continue;
+      ask = Ask::kCount;
+      Q = s.k;
+    } else if (step == 1) {
+      Q = (u64)ceil((double)s.p * (double)km);
+      if (Q < 1 || !(s.p > 0.f)) Q = 1;
+      if (s.p >= 1.f || Q >= km) continue;
+    } else if (step == 2) {
+      if (!(s.m > 0.f)) continue;
+      ask = Ask::kCode;
+      Q = last_code_of_weight<T>(w, top, last, s.m);
+    } else {
+      Q = (u64)((double)s.u * (double)km) + 1;
+      if (Q > km) Q = km;
+    }
+    const CodePlace c = find_code<T>(L, w, top, last, ask, Q);
+    if (step == 2 && c.n1 >= kn) continue;
+    const u64 j = step == 0 ? Q - c.n0 : step == 2 ? c.n1 - c.n0 : c.entries(Q);
+    if (step < 3) {
       kn = c.n0 + j;
       km = c.mass_through(j);
+    } else if (lane == 0) {
+      L.code = c.code;
+      L.j = (u32)j;
+      const double y = w.exponent(value_of_code<T>(c.code));
+      a.logprobs[r] = (float)(y * 0.69314718055994530942 - log((double)km / w.scale));
     }
-  }
-  if (s.m > 0.f) {
-    const CodePlace c = find_code<T>(L, w, top, last, Ask::kCode, last_code_of_weight<T>(w, top, last, s.m));
-    if (c.n1 < kn) {
-      kn = c.n1;
-      km = c.m1;
-    }
-  }
-  u64 Q = (u64)((double)s.u * (double)km) + 1;
-  if (Q > km) Q = km;
-  const CodePlace c = find_code<T>(L, w, top, last, Ask::kMass, Q);
-  if (lane == 0) {
-    L.code = c.code;
-    L.j = (u32)c.entries(Q);
-    const double y = w.exponent(value_of_code<T>(c.code));
-    a.logprobs[r] = (float)(y * 0.69314718055994530942 - log((double)km / w.scale));
   }
 }
 
-template <class T>
+template <class T, int NV>
 __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs& a, u64 r) {
   CodeLds& L = S.code;
   constexpr u32 kInf = CodeOf<T>::inf;
@@ -764,7 +774,7 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
   u32 head = (u32)((16 - ((uintptr_t)row & 15)) & 15) / 2;
   if (head > V) head = V;
   const u32 nvec = (V - head) / 8, tail = head + nvec * 8;
-  const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+  RowVectors<NV> vectors(reinterpret_cast<const uint4*>(row + head), nvec, kFill);
   for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads)
     reinterpret_cast<uint4*>(L.cnt)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
@@ -793,10 +803,10 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
   tops = pk_codes(edge);
   abs_max = edge & 0x7FFF7FFFu;
   if (nvec == 0) threshold();
-  for_each_batch<4>(vec, nvec, kFill, [&](const uint4 (&b)[4], u32) {
-    u32 c[16];
+  vectors.for_each([&](const uint4 (&b)[kBatch], u32) {
+    u32 c[4 * kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       const u32 w[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -808,7 +818,7 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
     if (first) threshold();
     first = false;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 4 * kBatch; ++i) {
       count(c[i] & 0xFFFFu);
       count(c[i] >> 16);
     }
@@ -836,7 +846,7 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
     }
     return;
   }
-  if (V > 0xFFFFu) {  // may a counter have overflowed?
+  if (NV != 4 && V > 0xFFFFu) {  // may a counter have overflowed?
     u32 n = 0;
     for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads) {
       const uint4 w = reinterpret_cast<const uint4*>(L.cnt)[i];
@@ -853,7 +863,10 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
     for (int w = 0; w < kWaves; ++w) total += (u32)L.scan[w];
     const bool lost = total != L.counted;
     __syncthreads();
-    if (lost) return sample_row_by_value<T>(S.value, a, r);
+    if (lost) {
+      if constexpr (NV != 4) sample_row_by_value<T>(S.value, a, r);
+      return;
+    }
   }
   // 2. the groups' counts and masses, then the questions
   if (s.t > 0.f) {
@@ -866,12 +879,10 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
       u64 m = 0;
       u32 n = 0;
       if (g * kGroupCodes + kGroupCodes > top && g * kGroupCodes <= last) {
-        Cell<T> c;
-        if (__ballot(c.read(L, g * kGroupCodes + lane_id() * kCellCodes, last))) {
-          c.weigh(w, top);
-          m = wave_sum(c.mass());
-          n = wave_sum(c.count());
-        }
+        const u32 c0 = g * kGroupCodes + lane_id() * kCellCodes;
+        u32 cnt[kCellCodes];
+        n = wave_sum(cell_counters<T>(L, c0, last, cnt));
+        if (n) m = wave_sum(cell_mass<T>(w, top, c0, cnt));
       }
       if (lane_id() == 0) {
         L.mass[g] = m;
@@ -902,9 +913,9 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
   };
   if (threadIdx.x < head && (((edge ^ want) & mask) & 0xFFFFu) == 0) match(threadIdx.x);
   if (threadIdx.x < V - tail && ((edge ^ want) & mask) < 0x10000u) match(tail + threadIdx.x);
-  for_each_batch<4>(vec, nvec, ~want, [&](const uint4 (&b)[4], u32 at) {
+  vectors.for_each([&](const uint4 (&b)[kBatch], u32 at) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       const u32 x[4] = {(b[i].x ^ want) & mask, (b[i].y ^ want) & mask, (b[i].z ^ want) & mask, (b[i].w ^ want) & mask};
       u32 some = 0;
 #pragma unroll
@@ -946,26 +957,40 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
 }  // namespace
 
 template <class T>
-__global__ __launch_bounds__(kThreads) void sample_tokens_kernel(TokenArgs a) {
-  if constexpr (sizeof(T) == 2) {
-    __shared__ SampleLds S;
-    sample_row_by_code<T>(S, a, blockIdx.x);
-  } else {
-    __shared__ TokLds S;
-    sample_row_by_value<T>(S, a, blockIdx.x);
-  }
+__global__ __launch_bounds__(kThreads) void sample_values_kernel(TokenArgs a) {
+  __shared__ TokLds S;
+  sample_row_by_value<T>(S, a, blockIdx.x);
 }
 
+template <class T, int NV>
+__global__ __launch_bounds__(kThreads) void sample_codes_kernel(TokenArgs a) {
+  __shared__ SampleLds S;
+  sample_row_by_code<T, NV>(S, a, blockIdx.x);
+}
+
+template <class T>
+static void launch_codes(const TokenArgs& a, hipStream_t s) {
+  const u32 B = (u32)a.B;
+  const u64 vectors = (a.V + 7) / 8;
+  if (vectors <= 4 * kThreads)
+    sample_codes_kernel<T, 4><<<B, kThreads, 0, s>>>(a);
+  else if (vectors <= 8 * kThreads)
+    sample_codes_kernel<T, 8><<<B, kThreads, 0, s>>>(a);
+  else if (vectors <= 16 * kThreads)
+    sample_codes_kernel<T, 16><<<B, kThreads, 0, s>>>(a);
+  else
+    sample_codes_kernel<T, 0><<<B, kThreads, 0, s>>>(a);
+}
 
 size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
 
 hipError_t launch_sample_tokens(const TokenArgs& a, int dtype, hipStream_t s) {
   if (dtype == PROFK_FP32)
-    sample_tokens_kernel<float><<<(u32)a.B, kThreads, 0, s>>>(a);
+    sample_values_kernel<float><<<(u32)a.B, kThreads, 0, s>>>(a);
   else if (dtype == PROFK_FP16)
-    sample_tokens_kernel<Half16><<<(u32)a.B, kThreads, 0, s>>>(a);
+    launch_codes<Half16>(a, s);
   else
-    sample_tokens_kernel<Brain16><<<(u32)a.B, kThreads, 0, s>>>(a);
+    launch_codes<Brain16>(a, s);
   return hipGetLastError();
 }
 
