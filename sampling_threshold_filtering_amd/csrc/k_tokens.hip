@@ -95,6 +95,13 @@ __device__ __forceinline__ V wave_min(V v) {
   return of_lane(wave_scan(v, (V)~(V)0, [](V x, V y) { return x < y ? x : y; }), kWave - 1);
 }
 
+// A barrier that waits for LDS accesses alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Inclusive scan over the block, one u64 per thread.
 __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* wave_tot) {
   v = wave_scan(v);
@@ -482,15 +489,16 @@ __device__ __forceinline__ void sample_row_by_value(TokLds& L, const TokenArgs& 
 // h >= 0, else h, so -0 comes right after +0; a positive value's counter is the low half of
 // word code, a negative one's the high half of word code - 0x8000.  A counter that
 // overflows makes the counters' sum differ from the number of entries counted, since each
-// carry takes 65536 or 65535 from it; such a row goes by value bins.
+// carry takes 65536 or 65535 from it; such a row (it holds 65536 equal entries) is left to
+// a second launch, by value bins.
 //
-// Eight neighbouring codes (a cell) lie within one binade, so their weights are a geometric
-// series: two exponentials give all eight, and equal largest entries weigh exactly 2^F.  Cells are summed in 64-bit
+// Sixteen neighbouring codes (a cell) lie within one binade, so their weights are a geometric
+// series: two exponentials give all of them, and equal largest entries weigh exactly 2^F.  Cells are summed in 64-bit
 // floats and rounded to integers; sums of cells are exact, so the answer depends on the
 // counters alone.
 constexpr u32 kCodeWords = 32768;
-constexpr u32 kCellCodes = 8;
-constexpr u32 kGroupCodes = kCellCodes * kWave;  // one wavefront's step: 512 codes
+constexpr u32 kCellCodes = 16;
+constexpr u32 kGroupCodes = kCellCodes * kWave;  // one wavefront's step: 1024 codes
 constexpr u32 kGroups = 65536 / kGroupCodes;
 constexpr u32 kMatchCap = 1024;
 
@@ -504,10 +512,14 @@ struct CodeLds {
   u32 code, pair, j, done;
 };
 
-union SampleLds {
-  CodeLds code;
-  TokLds value;
-};
+constexpr int64_t kByValue = -2;  // a row's token until the second launch
+
+// The counters' words, permuted so that 16 lanes that read four words each of 16
+// neighbouring cells use all banks.
+__device__ __forceinline__ u32 counter_word(u32 code) {
+  const u32 w = code & 0x7FFFu;
+  return w ^ (w >> 4 & 0xCu);
+}
 
 template <class T> struct CodeOf;
 template <> struct CodeOf<Half16> { static constexpr u32 inf = 0x7C00; };
@@ -558,9 +570,8 @@ __device__ __forceinline__ u32 pk_max(u32 a, u32 b) {
   return __builtin_bit_cast(u32, __builtin_elementwise_max(x, y));
 }
 // The 16-byte vectors of a row, `kBatch` a thread at a time.  NV > 0: all of a thread's NV
-// vectors stay in registers, loaded at once, so that a second pass reads no memory (NV = 16
-// holds 131072 entries in 64 registers a thread; one workgroup fills a CU by its LDS, so
-// they are there).  NV = 0: the next batch is in flight while one is dealt with.
+// vectors stay in registers, loaded at once, so that a second pass reads no memory.
+// NV = 0: the next batch is in flight while one is dealt with.
 constexpr int kBatch = 4;
 template <int NV>
 struct RowVectors {
@@ -568,10 +579,13 @@ struct RowVectors {
   u32 nvec, fill;
   uint4 held[NV ? NV : 1];
 
-  __device__ __forceinline__ uint4 at(u32 j) const {
-    return j < nvec ? vec[j] : make_uint4(fill, fill, fill, fill);
+  __device__ __forceinline__ uint4 at(u32 j) const { return vec[j < nvec ? j : nvec - 1]; }
+  __device__ __forceinline__ uint4 filled(uint4 v, u32 j) const {
+    return j < nvec ? v : make_uint4(fill, fill, fill, fill);
   }
-  __device__ __forceinline__ RowVectors(const uint4* v, u32 n, u32 f) : vec(v), nvec(n), fill(f) {
+  __device__ __forceinline__ RowVectors(const uint4* v, u32 n, u32 f) : vec(v), nvec(n), fill(f) { load(); }
+  __device__ __forceinline__ void load() {
+    if (nvec == 0) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i) held[i] = at(threadIdx.x + (u32)i * kThreads);
   }
@@ -580,7 +594,10 @@ struct RowVectors {
     if constexpr (NV > 0) {
 #pragma unroll
       for (int i = 0; i < NV; i += kBatch) {
-        const uint4 b[kBatch] = {held[i], held[i + 1], held[i + 2], held[i + 3]};
+        if ((u32)i * kThreads >= nvec) break;
+        uint4 b[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) b[k] = filled(held[i + k], threadIdx.x + (u32)(i + k) * kThreads);
         f(b, threadIdx.x + (u32)i * kThreads);
         __builtin_amdgcn_sched_barrier(0);  // one batch's work at a time: registers
       }
@@ -591,6 +608,8 @@ struct RowVectors {
       for (u32 j = threadIdx.x; j - threadIdx.x < nvec; j += kBatch * kThreads) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) nxt[i] = at(j + (u32)(kBatch + i) * kThreads);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) cur[i] = filled(cur[i], j + (u32)i * kThreads);
         f(cur, j);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) cur[i] = nxt[i];
@@ -599,107 +618,106 @@ struct RowVectors {
   }
 };
 
-// How many entries the cell of code c0 (a multiple of 8) holds up to code `last`, and their
-// mass.  The largest value's cell begins at that value: the codes before it do not occur.
-template <class T>
+// How often each code of the cell of code c0 (a multiple of 16) occurs, and their number.
+// EDGE: the group holds the largest value's code `top` or the last that counts.
+template <bool EDGE>
 __device__ __forceinline__ u32 cell_counters(const CodeLds& L, u32 c0, u32 last, u32 (&n)[kCellCodes]) {
-  const u32 at = c0 & 0x7FFFu, shift = c0 >> 15 << 4;
-  const uint4 a = *reinterpret_cast<const uint4*>(&L.cnt[at]), b = *reinterpret_cast<const uint4*>(&L.cnt[at + 4]);
-  const u32 w[kCellCodes] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const u32 shift = c0 >> 15 << 4;
   u32 sum = 0;
 #pragma unroll
-  for (u32 i = 0; i < kCellCodes; ++i) {
-    n[i] = c0 + i <= last ? w[i] >> shift & 0xFFFFu : 0u;
-    sum += n[i];
+  for (u32 i = 0; i < kCellCodes; i += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(&L.cnt[counter_word(c0 + i)]);
+    const u32 w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (u32 k = 0; k < 4; ++k) {
+      n[i + k] = w[k] >> shift & 0xFFFFu;
+      if (EDGE && c0 + i + k > last) n[i + k] = 0;
+      sum += n[i + k];
+    }
   }
   return sum;
 }
-template <class T>
+// Their mass.  The largest value's cell begins at that value: the codes before it do not
+// occur.
+template <class T, bool EDGE>
 __device__ __forceinline__ u64 cell_mass(const Weigher& w, u32 top, u32 c0, const u32 (&n)[kCellCodes]) {
   const double v0 = (double)value_of_code<T>(c0), v1 = (double)value_of_code<T>(c0 + 1);
   const double rho = pow2((v1 - v0) * w.c);
-  double p = c0 <= top ? w.scale : pow2((v0 - (double)w.top) * w.c) * w.scale, s = 0;
+  double p = EDGE && c0 <= top ? w.scale : pow2((v0 - (double)w.top) * w.c) * w.scale, s = 0;
 #pragma unroll
   for (u32 i = 0; i < kCellCodes; ++i) {
     s = __builtin_fma((double)n[i], p, s);
-    if (c0 + i >= top) p *= rho;
+    if (!EDGE || c0 + i >= top) p *= rho;
   }
   return (u64)rint(s);
 }
+__device__ __forceinline__ bool edge_group(u32 g, u32 top, u32 last) { return g == top / kGroupCodes || g == last / kGroupCodes; }
 
-// A code and the prefix of the order before it and through it.
+// A code, the prefix of the order before it and through it, and one entry's weight.
 struct CodePlace {
   u32 code;
-  u64 n0, m0, n1, m1;
+  u32 n0, n1;
+  u64 m0, m1, q;
   // entries of this code up to the first whose prefix's mass reaches Q
-  __device__ __forceinline__ u64 entries(u64 Q) const {
-    const u64 cnt = n1 - n0, D = m1 - m0;
-    if (Q <= m0 || cnt <= 1) return 1;
+  __device__ __forceinline__ u32 entries(u64 Q) const {
+    const u32 cnt = n1 - n0;
+    if (Q <= m0 || cnt <= 1 || q == 0) return 1;
     const u64 X = Q - m0;
-    u64 j;
-    if (D % cnt == 0 && D >= cnt)
-      j = (X + D / cnt - 1) / (D / cnt);
-    else
-      j = (u64)ceil((double)X * (double)cnt / (double)D);
-    return j < 1 ? 1 : j > cnt ? cnt : j;
+    double e = ceil((double)X / (double)q);
+    u64 j = e >= (double)cnt ? cnt : (u64)e;  // off by at most one
+    if (j * q < X) ++j;
+    if (j > 1 && (j - 1) * q >= X) --j;
+    return j < 1 ? 1 : j > cnt ? cnt : (u32)j;
   }
-  __device__ __forceinline__ u64 mass_through(u64 j) const {
-    const u64 cnt = n1 - n0, D = m1 - m0;
-    if (j == cnt) return m1;
-    return m0 + (D % cnt == 0 ? j * (D / cnt) : (u64)rint((double)D * (double)j / (double)cnt));
+  __device__ __forceinline__ u64 mass_through(u32 j) const {
+    const u64 m = m0 + j * q;
+    return n0 + j == n1 || m > m1 ? m1 : m;
   }
 };
 
 enum class Ask { kCount, kMass, kCode };
 
-// Where the running count or mass reaches Q, or the place of code Q.  One wavefront: a
-// scan over the groups, then over the cells of one group, then the codes of one cell.
+// Where the running count or mass reaches Q, or the place of code Q, in one wavefront: a
+// step over the groups (lane g holds the count n and the mass m through group g), a scan
+// over the cells of one group, then over the codes of one cell.
 template <class T>
-__device__ __forceinline__ CodePlace find_code(const CodeLds& L, const Weigher& w, u32 top, u32 last, Ask ask, u64 Q) {
+__device__ __forceinline__ CodePlace find_code(const CodeLds& L, const Weigher& w, u32 top, u32 last, u64 m, u32 n,
+                                               Ask ask, u64 Q) {
   const u32 lane = lane_id();
-  static_assert(kGroups == 2 * kWave, "a lane holds two groups");
-  const u64 ma = L.mass[2 * lane], mb = L.mass[2 * lane + 1];
-  const u32 na = L.n[2 * lane], nb = L.n[2 * lane + 1];
-  const u64 m = wave_scan(ma + mb);
-  const u32 n = wave_scan(na + nb);
-  u32 g;
-  if (ask == Ask::kCode) {
-    g = __builtin_amdgcn_readfirstlane((u32)Q) / kGroupCodes;
-  } else {
-    const u64 reach = __ballot(ask == Ask::kMass ? m >= Q : (u64)n >= Q);
-    const u32 at = reach ? (u32)__builtin_ctzll(reach) : kWave - 1;
-    g = 2 * at + (of_lane(ask == Ask::kMass ? m - mb : (u64)(n - nb), at) < Q ? 1u : 0u);
-  }
-  const u64 gm = of_lane(g & 1 ? m - mb : m - mb - ma, g / 2);
-  const u32 gn = of_lane(g & 1 ? n - nb : n - nb - na, g / 2);
+  static_assert(kGroups == kWave, "a lane holds a group");
+  auto where = [&](u64 some, u64 mass, u32 count, u32 of_code) -> u32 {
+    if (ask == Ask::kCode) return of_code;
+    const u64 reach = some & __ballot(ask == Ask::kMass ? mass >= Q : (u64)count >= Q);
+    return reach ? (u32)__builtin_ctzll(reach) : some ? 63u - (u32)__builtin_clzll(some) : 0u;
+  };
+  const u32 qc = __builtin_amdgcn_readfirstlane((u32)Q);
+  const u32 g = where(~0ull, m, n, qc / kGroupCodes);
+  const u64 gm = g ? of_lane(m, g - 1) : 0;
+  const u32 gn = g ? of_lane(n, g - 1) : 0;
   const u32 c0 = g * kGroupCodes + lane * kCellCodes;
-  u32 cnt[kCellCodes];
-  const u32 cn = cell_counters<T>(L, c0, last, cnt), n1 = gn + wave_scan(cn);
-  const u64 cm = cell_mass<T>(w, top, c0, cnt), m1 = gm + wave_scan(cm);
-  u32 at;
-  if (ask == Ask::kCode) {
-    at = __builtin_amdgcn_readfirstlane((u32)Q) % kGroupCodes / kCellCodes;
+  u32 cnt[kCellCodes], cn;
+  u64 cm;
+  if (edge_group(g, top, last)) {
+    cn = cell_counters<true>(L, c0, last, cnt);
+    cm = cell_mass<T, true>(w, top, c0, cnt);
   } else {
-    const u64 reach = __ballot(ask == Ask::kMass ? m1 >= Q : (u64)n1 >= Q);
-    at = reach ? (u32)__builtin_ctzll(reach) : kWave - 1;
+    cn = cell_counters<false>(L, c0, last, cnt);
+    cm = cell_mass<T, false>(w, top, c0, cnt);
   }
+  const u32 n1 = gn + wave_scan(cn);
+  const u64 m1 = gm + wave_scan(cm);
+  const u32 at = where(~0ull, m1, n1, qc % kGroupCodes / kCellCodes);
   // the cell's codes, a lane each
   const u32 first = of_lane(c0, at);
   const u64 ms = of_lane(m1 - cm, at);
   const u32 ns = of_lane(n1 - cn, at), code = first + lane;
   const bool mine = lane < kCellCodes && code >= top && code <= last;
-  const u32 nc = mine ? L.cnt[code & 0x7FFFu] >> (code >> 15 << 4) & 0xFFFFu : 0u;
+  const u32 nc = mine ? L.cnt[counter_word(code)] >> (code >> 15 << 4) & 0xFFFFu : 0u;
   const double q = mine ? pow2(w.exponent(value_of_code<T>(code))) * w.scale : 0.0;
   const u64 mc = (u64)rint((double)nc * q), mi = ms + wave_scan(mc);
   const u32 ni = ns + wave_scan(nc);
-  u32 i;
-  if (ask == Ask::kCode) {
-    i = __builtin_amdgcn_readfirstlane((u32)Q) % kCellCodes;
-  } else {
-    const u64 some = __ballot(nc != 0), reach = some & __ballot(ask == Ask::kMass ? mi >= Q : (u64)ni >= Q);
-    i = reach ? (u32)__builtin_ctzll(reach) : some ? 63u - (u32)__builtin_clzll(some) : 0u;
-  }
-  return {first + i, of_lane(ni - nc, i), of_lane(mi - mc, i), of_lane(ni, i), of_lane(mi, i)};
+  const u32 i = where(__ballot(nc != 0), mi, ni, qc % kCellCodes);
+  return {first + i, of_lane(ni - nc, i), of_lane(ni, i), of_lane(mi - mc, i), of_lane(mi, i), of_lane((u64)rint(q), i)};
 }
 
 // The last code whose weight is at least m: each of three steps tries 64 codes at a time.
@@ -723,8 +741,9 @@ template <class T>
 __device__ __forceinline__ void answer_codes(CodeLds& L, const TokenArgs& a, u64 r, const RowSettings& s,
                                              const Weigher& w, u32 top, u32 last) {
   const u32 lane = lane_id();
-  u64 kn = wave_sum(L.n[2 * lane] + L.n[2 * lane + 1]);  // what is kept: entries and mass
-  u64 km = wave_sum(L.mass[2 * lane] + L.mass[2 * lane + 1]);
+  const u64 m = wave_scan(L.mass[lane]);
+  const u32 n = wave_scan(L.n[lane]);
+  u64 kn = of_lane(n, kWave - 1), km = of_lane(m, kWave - 1);  // what is kept: entries and mass
   for (int step = 0; step < 4; ++step) {  // one place where the search is inlined
     Ask ask = Ask::kMass;
     u64 Q;
@@ -744,15 +763,15 @@ __device__ __forceinline__ void answer_codes(CodeLds& L, const TokenArgs& a, u64
       Q = (u64)((double)s.u * (double)km) + 1;
       if (Q > km) Q = km;
     }
-    const CodePlace c = find_code<T>(L, w, top, last, ask, Q);
+    const CodePlace c = find_code<T>(L, w, top, last, m, n, ask, Q);
     if (step == 2 && c.n1 >= kn) continue;
-    const u64 j = step == 0 ? Q - c.n0 : step == 2 ? c.n1 - c.n0 : c.entries(Q);
+    const u32 j = step == 0 ? (u32)Q - c.n0 : step == 2 ? c.n1 - c.n0 : c.entries(Q);
     if (step < 3) {
       kn = c.n0 + j;
       km = c.mass_through(j);
     } else if (lane == 0) {
       L.code = c.code;
-      L.j = (u32)j;
+      L.j = j;
       const double y = w.exponent(value_of_code<T>(c.code));
       a.logprobs[r] = (float)(y * 0.69314718055994530942 - log((double)km / w.scale));
     }
@@ -760,8 +779,7 @@ __device__ __forceinline__ void answer_codes(CodeLds& L, const TokenArgs& a, u64
 }
 
 template <class T, int NV>
-__device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs& a, u64 r) {
-  CodeLds& L = S.code;
+__device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& a, u64 r) {
   constexpr u32 kInf = CodeOf<T>::inf;
   constexpr u32 kLowest = 0x8000u | (kInf - 1);  // the lowest number's code
   constexpr u32 kFill = (0x8000u | kInf) * 0x10001u;  // two entries of -inf
@@ -781,14 +799,14 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
     L.top = 0xFFFFu;
     L.abs_max = L.counted = L.matches = 0;
   }
-  __syncthreads();
+  lds_barrier();  // the row's loads stay in flight
   // 1. count every entry that may be present: of the largest value so far, or less than
   // 2^-(F+1) below it, so that a masked row's lowest values do not queue for one counter
   u32 tops = 0xFFFFFFFFu, abs_max = 0, thr = 0, counted = 0;
   bool first = true;
   auto count = [&](u32 c) {
     if (c <= thr) {
-      atomicAdd(&L.cnt[c & 0x7FFFu], c & 0x8000u ? 0x10000u : 1u);
+      atomicAdd(&L.cnt[counter_word(c)], c & 0x8000u ? 0x10000u : 1u);
       ++counted;
     }
   };
@@ -846,28 +864,6 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
     }
     return;
   }
-  if (NV != 4 && V > 0xFFFFu) {  // may a counter have overflowed?
-    u32 n = 0;
-    for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads) {
-      const uint4 w = reinterpret_cast<const uint4*>(L.cnt)[i];
-      n = __builtin_amdgcn_sad_u16(w.x, 0, n);
-      n = __builtin_amdgcn_sad_u16(w.y, 0, n);
-      n = __builtin_amdgcn_sad_u16(w.z, 0, n);
-      n = __builtin_amdgcn_sad_u16(w.w, 0, n);
-    }
-    n = wave_sum(n);
-    if (lane_id() == 0) L.scan[threadIdx.x / kWave] = n;
-    __syncthreads();
-    u32 total = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) total += (u32)L.scan[w];
-    const bool lost = total != L.counted;
-    __syncthreads();
-    if (lost) {
-      if constexpr (NV != 4) sample_row_by_value<T>(S.value, a, r);
-      return;
-    }
-  }
   // 2. the groups' counts and masses, then the questions
   if (s.t > 0.f) {
     Weigher w;
@@ -878,11 +874,16 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
     for (u32 g = threadIdx.x / kWave; g < kGroups; g += kWaves) {
       u64 m = 0;
       u32 n = 0;
-      if (g * kGroupCodes + kGroupCodes > top && g * kGroupCodes <= last) {
+      if (g >= top / kGroupCodes && g <= last / kGroupCodes) {
         const u32 c0 = g * kGroupCodes + lane_id() * kCellCodes;
         u32 cnt[kCellCodes];
-        n = wave_sum(cell_counters<T>(L, c0, last, cnt));
-        if (n) m = wave_sum(cell_mass<T>(w, top, c0, cnt));
+        if (edge_group(g, top, last)) {
+          n = wave_sum(cell_counters<true>(L, c0, last, cnt));
+          if (n) m = wave_sum(cell_mass<T, true>(w, top, c0, cnt));
+        } else {
+          n = wave_sum(cell_counters<false>(L, c0, last, cnt));
+          if (n) m = wave_sum(cell_mass<T, false>(w, top, c0, cnt));
+        }
       }
       if (lane_id() == 0) {
         L.mass[g] = m;
@@ -890,6 +891,29 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
       }
     }
     __syncthreads();
+    // A counter may have overflowed, or entries been counted that are absent.
+    if (NV != 4 && V > 0xFFFFu && wave_sum(L.n[lane_id()]) != L.counted) {
+      u32 n = 0;
+      for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads) {
+        const uint4 c = reinterpret_cast<const uint4*>(L.cnt)[i];
+        n = __builtin_amdgcn_sad_u16(c.x, 0, n);
+        n = __builtin_amdgcn_sad_u16(c.y, 0, n);
+        n = __builtin_amdgcn_sad_u16(c.z, 0, n);
+        n = __builtin_amdgcn_sad_u16(c.w, 0, n);
+      }
+      n = wave_sum(n);
+      if (lane_id() == 0) L.scan[threadIdx.x / kWave] = n;
+      __syncthreads();
+      u32 total = 0;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) total += (u32)L.scan[i];
+      const bool lost = total != L.counted;
+      __syncthreads();
+      if (lost) {
+        if (threadIdx.x == 0) a.tokens[r] = kByValue;
+        return;
+      }
+    }
     if (threadIdx.x < kWave) answer_codes<T>(L, a, r, s, w, top, last);
   } else if (threadIdx.x == 0) {
     L.code = top;
@@ -900,7 +924,7 @@ __device__ __forceinline__ void sample_row_by_code(SampleLds& S, const TokenArgs
   // 3. the j-th entry of that code, by index
   const u32 code = L.code;
   const bool zero = code == 0x7FFFu || code == 0x8000u;
-  const u32 j = L.j + (code == 0x8000u ? L.cnt[0x7FFF] & 0xFFFFu : 0u);
+  const u32 j = L.j + (code == 0x8000u ? L.cnt[counter_word(0x7FFFu)] & 0xFFFFu : 0u);
   const u32 want = zero ? 0u : (code < 0x8000u ? code ^ 0x7FFFu : code) * 0x10001u;
   const u32 mask = zero ? 0x7FFF7FFFu : 0xFFFFFFFFu;
   auto match = [&](u32 i) {
@@ -962,9 +986,20 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(TokenArgs a) {
   sample_row_by_value<T>(S, a, blockIdx.x);
 }
 
+// The rows whose counters overflowed.
+template <class T>
+__global__ __launch_bounds__(kThreads) void sample_left_kernel(TokenArgs a) {
+  __shared__ TokLds S;
+  for (u64 r = blockIdx.x; r < a.B; r += gridDim.x) {
+    if (a.tokens[r] != kByValue) continue;
+    __syncthreads();
+    sample_row_by_value<T>(S, a, r);
+  }
+}
+
 template <class T, int NV>
 __global__ __launch_bounds__(kThreads) void sample_codes_kernel(TokenArgs a) {
-  __shared__ SampleLds S;
+  __shared__ CodeLds S;
   sample_row_by_code<T, NV>(S, a, blockIdx.x);
 }
 
@@ -976,10 +1011,9 @@ static void launch_codes(const TokenArgs& a, hipStream_t s) {
     sample_codes_kernel<T, 4><<<B, kThreads, 0, s>>>(a);
   else if (vectors <= 8 * kThreads)
     sample_codes_kernel<T, 8><<<B, kThreads, 0, s>>>(a);
-  else if (vectors <= 16 * kThreads)
-    sample_codes_kernel<T, 16><<<B, kThreads, 0, s>>>(a);
   else
     sample_codes_kernel<T, 0><<<B, kThreads, 0, s>>>(a);
+  if (a.V > 0xFFFFu) sample_left_kernel<T><<<B < 256 ? B : 256, kThreads, 0, s>>>(a);
 }
 
 size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
