@@ -508,17 +508,25 @@ struct CodeLds {
   u32 n[kGroups];
   u32 match[kMatchCap];
   u64 scan[kWaves];
-  u32 top, abs_max, counted, matches;
-  u32 code, pair, j, done;
+  u32 top, end, counted, matches;  // the first and the last code; the entries counted
+  u32 code, j;
 };
 
 constexpr int64_t kByValue = -2;  // a row's token until the second launch
+
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 
 // The counters' words, permuted so that 16 lanes that read four words each of 16
 // neighbouring cells use all banks.
 __device__ __forceinline__ u32 counter_word(u32 code) {
   const u32 w = code & 0x7FFFu;
   return w ^ (w >> 4 & 0xCu);
+}
+
+__device__ __forceinline__ u32 pk_counter_words(u32 codes) {
+  const u32 w = codes & 0x7FFF7FFFu;
+  return w ^ (__builtin_bit_cast(u32, __builtin_bit_cast(u16x2, w) >> 4) & 0x000C000Cu);
 }
 
 template <class T> struct CodeOf;
@@ -554,12 +562,12 @@ __device__ __forceinline__ u32 last_code(u32 top, float t, float F) {
   return code_past<T>(v - F * 0.69314718f * t);
 }
 
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef short i16x2 __attribute__((ext_vector_type(2)));
 
+__device__ __forceinline__ u32 pk_signs(u32 w) {  // 0 or 0xFFFF each
+  return __builtin_bit_cast(u32, __builtin_bit_cast(i16x2, w) >> 15);
+}
 __device__ __forceinline__ u32 pk_codes(u32 w) {  // two codes
-  const i16x2 sign = __builtin_bit_cast(i16x2, w) >> 15;
-  return w ^ (0x7FFF7FFFu & ~__builtin_bit_cast(u32, sign));
+  return w ^ (0x7FFF7FFFu & ~pk_signs(w));
 }
 __device__ __forceinline__ u32 pk_min(u32 a, u32 b) {
   const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
@@ -570,50 +578,54 @@ __device__ __forceinline__ u32 pk_max(u32 a, u32 b) {
   return __builtin_bit_cast(u32, __builtin_elementwise_max(x, y));
 }
 // The 16-byte vectors of a row, `kBatch` a thread at a time.  NV > 0: all of a thread's NV
-// vectors stay in registers, loaded at once, so that a second pass reads no memory.
+// vectors are loaded at once and stay in registers for the second pass.
 // NV = 0: the next batch is in flight while one is dealt with.
 constexpr int kBatch = 4;
 template <int NV>
 struct RowVectors {
+  static constexpr int kHeld = NV ? NV : kBatch;
   const uint4* vec;
   u32 nvec, fill;
-  uint4 held[NV ? NV : 1];
+  uint4 held[kHeld];
 
-  __device__ __forceinline__ uint4 at(u32 j) const { return vec[j < nvec ? j : nvec - 1]; }
+  __device__ __forceinline__ uint4 at(u32 j) const {  // 32-bit offsets from a scalar base
+    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(vec) + (j < nvec ? j : nvec - 1) * 16u);
+  }
   __device__ __forceinline__ uint4 filled(uint4 v, u32 j) const {
     return j < nvec ? v : make_uint4(fill, fill, fill, fill);
   }
-  __device__ __forceinline__ RowVectors(const uint4* v, u32 n, u32 f) : vec(v), nvec(n), fill(f) { load(); }
-  __device__ __forceinline__ void load() {
-    if (nvec == 0) return;
+  __device__ __forceinline__ void load() {  // of a row of at least one vector
 #pragma unroll
-    for (int i = 0; i < NV; ++i) held[i] = at(threadIdx.x + (u32)i * kThreads);
+    for (int i = 0; i < kHeld; ++i) held[i] = at(threadIdx.x + (u32)i * kThreads);
   }
-  template <class F>  // f(the batch, the first one's place)
+  template <class F>
+  __device__ __forceinline__ void first_batch(F f) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) f(filled(held[i], threadIdx.x + (u32)i * kThreads));
+  }
+  template <class F>  // f(the vector, its place)
   __device__ __forceinline__ void for_each(F f) {
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int i = 0; i < NV; i += kBatch) {
-        if ((u32)i * kThreads >= nvec) break;
-        uint4 b[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) b[k] = filled(held[i + k], threadIdx.x + (u32)(i + k) * kThreads);
-        f(b, threadIdx.x + (u32)i * kThreads);
-        __builtin_amdgcn_sched_barrier(0);  // one batch's work at a time: registers
+      for (int i = 0; i < NV; ++i) {
+        const u32 j = threadIdx.x + (u32)i * kThreads;
+        if ((u32)i * kThreads < nvec) f(filled(held[i], j), j);
+        __builtin_amdgcn_sched_barrier(0);  // one vector's work at a time: registers
       }
     } else {
-      uint4 cur[kBatch], nxt[kBatch];
+      u32 j = threadIdx.x;
+      for (; j - threadIdx.x + kBatch * kThreads <= nvec; j += kBatch * kThreads) {
+        uint4 next[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) cur[i] = at(threadIdx.x + (u32)i * kThreads);
-      for (u32 j = threadIdx.x; j - threadIdx.x < nvec; j += kBatch * kThreads) {
+        for (int i = 0; i < kBatch; ++i) next[i] = at(j + (u32)(kBatch + i) * kThreads);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) nxt[i] = at(j + (u32)(kBatch + i) * kThreads);
+        for (int i = 0; i < kBatch; ++i) f(held[i], j + (u32)i * kThreads);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) cur[i] = filled(cur[i], j + (u32)i * kThreads);
-        f(cur, j);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) cur[i] = nxt[i];
+        for (int i = 0; i < kBatch; ++i) held[i] = next[i];
       }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i, j += kThreads)
+        if (j - threadIdx.x < nvec) f(filled(held[i], j), j);
     }
   }
 };
@@ -792,75 +804,69 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   u32 head = (u32)((16 - ((uintptr_t)row & 15)) & 15) / 2;
   if (head > V) head = V;
   const u32 nvec = (V - head) / 8, tail = head + nvec * 8;
-  RowVectors<NV> vectors(reinterpret_cast<const uint4*>(row + head), nvec, kFill);
+  RowVectors<NV> vectors;
+  vectors.vec = reinterpret_cast<const uint4*>(row + head);
+  vectors.nvec = nvec;
+  vectors.fill = kFill;
+  if (nvec) vectors.load();
   for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads)
     reinterpret_cast<uint4*>(L.cnt)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     L.top = 0xFFFFu;
-    L.abs_max = L.counted = L.matches = 0;
+    L.end = L.counted = L.matches = 0;
   }
   lds_barrier();  // the row's loads stay in flight
   // 1. count every entry that may be present: of the largest value so far, or less than
   // 2^-(F+1) below it, so that a masked row's lowest values do not queue for one counter
-  u32 tops = 0xFFFFFFFFu, abs_max = 0, thr = 0, counted = 0;
-  bool first = true;
-  auto count = [&](u32 c) {
-    if (c <= thr) {
-      atomicAdd(&L.cnt[counter_word(c)], c & 0x8000u ? 0x10000u : 1u);
-      ++counted;
-    }
-  };
-  auto threshold = [&]() {
-    const u32 t2 = tops & 0xFFFFu, t1 = tops >> 16;
-    const u32 top = wave_min(t1 < t2 ? t1 : t2);
-    thr = top > kLowest ? kLowest : s.t > 0.f ? last_code<T>(top, s.t, (float)(F + 1)) : top;
+  u32 tops = 0xFFFFFFFFu, ends = 0, thr = 0, counted = 0;
+  auto count = [&](u32 w) {  // two entries, in packed 16-bit operations as far as they go
+    const u32 sign = pk_signs(w), c = w ^ (0x7FFF7FFFu & ~sign);
+    tops = pk_min(tops, c);
+    ends = pk_max(ends, c);
+    const u32 at = pk_counter_words(c);
+    const bool lo = (c & 0xFFFFu) <= thr, hi = c >> 16 <= thr;
+    if (lo) atomicAdd(&L.cnt[at & 0xFFFFu], (sign & 0xFFFFu) + 1);  // 1 or 2^16
+    if (hi) atomicAdd(&L.cnt[at >> 16], (sign >> 16) + 1);
+    counted += (u32)__builtin_popcountll(__builtin_amdgcn_ballot_w64(lo)) +
+               (u32)__builtin_popcountll(__builtin_amdgcn_ballot_w64(hi));
   };
   u32 edge = kFill;  // the entries before and after the vectors: at most 7 and 7
   if (threadIdx.x < head) edge = row[threadIdx.x] | (kFill & 0xFFFF0000u);
   if (threadIdx.x < V - tail) edge = (edge & 0xFFFFu) | (u32)row[tail + threadIdx.x] << 16;
   tops = pk_codes(edge);
-  abs_max = edge & 0x7FFF7FFFu;
-  if (nvec == 0) threshold();
-  vectors.for_each([&](const uint4 (&b)[kBatch], u32) {
-    u32 c[4 * kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const u32 w[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        c[i * 4 + k] = pk_codes(w[k]);
-        abs_max = pk_max(abs_max, w[k] & 0x7FFF7FFFu);
-        tops = pk_min(tops, c[i * 4 + k]);
-      }
-    }
-    if (first) threshold();
-    first = false;
-#pragma unroll
-    for (int i = 0; i < 4 * kBatch; ++i) {
-      count(c[i] & 0xFFFFu);
-      count(c[i] >> 16);
-    }
-  });
+  if (nvec)
+    vectors.first_batch([&](uint4 v) {
+      tops = pk_min(tops, pk_min(pk_min(pk_codes(v.x), pk_codes(v.y)), pk_min(pk_codes(v.z), pk_codes(v.w))));
+    });
   {
-    const u32 c = pk_codes(edge);
-    count(c & 0xFFFFu);
-    count(c >> 16);
+    const u32 t2 = tops & 0xFFFFu, t1 = tops >> 16;
+    const u32 top = wave_min(t1 < t2 ? t1 : t2);
+    thr = top > kLowest ? kLowest : s.t > 0.f ? last_code<T>(top, s.t, (float)(F + 1)) : top;
   }
+  if (nvec)
+    vectors.for_each([&](uint4 v, u32) {
+      count(v.x);
+      count(v.y);
+      count(v.z);
+      count(v.w);
+    });
+  count(edge);
   {
-    const u32 t2 = tops & 0xFFFFu, t1 = tops >> 16, m2 = abs_max & 0xFFFFu, m1 = abs_max >> 16;
-    const u32 t = wave_min(t1 < t2 ? t1 : t2), m = ~wave_min(~(m1 > m2 ? m1 : m2)), n = wave_sum(counted);
+    const u32 t2 = tops & 0xFFFFu, t1 = tops >> 16, e2 = ends & 0xFFFFu, e1 = ends >> 16;
+    const u32 t = wave_min(t1 < t2 ? t1 : t2), e = ~wave_min(~(e1 > e2 ? e1 : e2));
     if (lane_id() == 0) {
       atomicMin(&L.top, t);
-      atomicMax(&L.abs_max, m);
-      atomicAdd(&L.counted, n);
+      atomicMax(&L.end, e);
+      atomicAdd(&L.counted, counted);  // the wavefront's
     }
   }
   __syncthreads();
   const u32 top = L.top;
-  if (L.abs_max > kInf || top > kLowest) {
+  const bool nan = top < (0x7FFFu ^ kInf) || L.end > (0x8000u | kInf);
+  if (nan || top > kLowest) {
     if (threadIdx.x == 0) {
       a.tokens[r] = -1;
-      a.logprobs[r] = L.abs_max > kInf ? __uint_as_float(0x7FC00000u) : -__builtin_huge_valf();
+      a.logprobs[r] = nan ? __uint_as_float(0x7FC00000u) : -__builtin_huge_valf();
     }
     return;
   }
@@ -937,20 +943,20 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   };
   if (threadIdx.x < head && (((edge ^ want) & mask) & 0xFFFFu) == 0) match(threadIdx.x);
   if (threadIdx.x < V - tail && ((edge ^ want) & mask) < 0x10000u) match(tail + threadIdx.x);
-  vectors.for_each([&](const uint4 (&b)[kBatch], u32 at) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const u32 x[4] = {(b[i].x ^ want) & mask, (b[i].y ^ want) & mask, (b[i].z ^ want) & mask, (b[i].w ^ want) & mask};
+  if (nvec) {
+    if constexpr (NV == 0) vectors.load();
+    vectors.for_each([&](uint4 v, u32 at) {
+      const u32 x[4] = {(v.x ^ want) & mask, (v.y ^ want) & mask, (v.z ^ want) & mask, (v.w ^ want) & mask};
       u32 some = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) some |= (x[k] - 0x00010001u) & ~x[k] & 0x80008000u;
       if (some) {
-        const u32 e = head + (at + (u32)i * kThreads) * 8;
+        const u32 e = head + at * 8;
 #pragma unroll
         for (u32 k = 0; k < 4; ++k) look(x[k], e + 2 * k);
       }
-    }
-  });
+    });
+  }
   __syncthreads();
   const u32 n = L.matches;
   if (n <= kMatchCap) {
@@ -986,14 +992,27 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(TokenArgs a) {
   sample_row_by_value<T>(S, a, blockIdx.x);
 }
 
-// The rows whose counters overflowed.
+// The rows whose counters overflowed: a block looks at rows b, b + blocks, ..., a thread
+// each.
+constexpr u32 kLeftBlocks = 64;
 template <class T>
 __global__ __launch_bounds__(kThreads) void sample_left_kernel(TokenArgs a) {
   __shared__ TokLds S;
-  for (u64 r = blockIdx.x; r < a.B; r += gridDim.x) {
-    if (a.tokens[r] != kByValue) continue;
-    __syncthreads();
-    sample_row_by_value<T>(S, a, r);
+  __shared__ u32 left;
+  for (u64 r0 = blockIdx.x; r0 < a.B; r0 += (u64)kThreads * gridDim.x) {
+    const u64 r = r0 + (u64)threadIdx.x * gridDim.x;
+    u64 mine = r < a.B && a.tokens[r] == kByValue ? r : ~0ull;
+    for (;;) {
+      __syncthreads();
+      if (threadIdx.x == 0) left = ~0u;
+      __syncthreads();
+      if (mine != ~0ull) atomicMin(&left, threadIdx.x);
+      __syncthreads();
+      const u32 t = left;
+      if (t == ~0u) break;
+      if (threadIdx.x == t) mine = ~0ull;
+      sample_row_by_value<T>(S, a, r0 + (u64)t * gridDim.x);
+    }
   }
 }
 
@@ -1013,7 +1032,7 @@ static void launch_codes(const TokenArgs& a, hipStream_t s) {
     sample_codes_kernel<T, 8><<<B, kThreads, 0, s>>>(a);
   else
     sample_codes_kernel<T, 0><<<B, kThreads, 0, s>>>(a);
-  if (a.V > 0xFFFFu) sample_left_kernel<T><<<B < 256 ? B : 256, kThreads, 0, s>>>(a);
+  if (a.V > 0xFFFFu) sample_left_kernel<T><<<B < kLeftBlocks ? B : kLeftBlocks, kThreads, 0, s>>>(a);
 }
 
 size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
