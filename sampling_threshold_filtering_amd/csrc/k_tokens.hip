@@ -102,15 +102,25 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// The value of the lane across in a quad: quad_perm [1,0,3,2] or [2,3,0,1].
+template <int CTRL>
+__device__ __forceinline__ u32 quad_xor(u32 v) {
+  return (u32)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ u64 quad_xor(u64 v) {
+  return (u64)quad_xor<CTRL>((u32)(v >> 32)) << 32 | quad_xor<CTRL>((u32)v);
+}
+
 // Inclusive scan over the block, one u64 per thread.
 __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* wave_tot) {
   v = wave_scan(v);
   const u32 wid = threadIdx.x / kWave;
   if (lane_id() == kWave - 1) wave_tot[wid] = v;
-  __syncthreads();
+  lds_barrier();
   const u64 t = wave_scan(lane_id() < (u32)kWaves ? wave_tot[lane_id()] : 0);
   const u64 before = wid ? of_lane(t, __builtin_amdgcn_readfirstlane(wid) - 1) : 0;
-  __syncthreads();
+  lds_barrier();
   return v + before;
 }
 
@@ -134,21 +144,23 @@ __device__ __forceinline__ void for_each_entry(const T* row, u32 V, F f) {
   for (u32 i = head + nvec * W + threadIdx.x; i < V; i += kThreads) f(to_f32(row[i]), i);
 }
 
-// 1 / i! for i = 13, 12, ... 0, read into scalar registers.
-__constant__ const double kInverseFactorials[14] = {
-    1.0 / 6227020800.0, 1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
-    1.0 / 40320.0,      1.0 / 5040.0,      1.0 / 720.0,      1.0 / 120.0,     1.0 / 24.0,
-    1.0 / 6.0,          0.5,               1.0,              1.0};
-
 // 2^y for y <= 0: y = n + f with |f| <= 1/2, the Taylor series of e^(f ln 2) to the power
 // 13 (the next term is below 2^-57), scaled by 2^n.  2^0 is exactly 1; NaN gives 0.
+// The factorials' inverses are read into scalar registers; the even and the odd powers are
+// summed apart, in half the steps.
+__constant__ const double kInverseFactorials[14] = {
+    1.0, 1.0, 0.5, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880,
+    1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600, 1.0 / 6227020800.0};
 __device__ __forceinline__ double pow2(double y) {
   y = __builtin_fmax(y, -2000.0);
-  const double n = rint(y), x = (y - n) * 0.69314718055994530942;
-  double e = kInverseFactorials[0];
+  const double n = rint(y), x = (y - n) * 0.69314718055994530942, xx = x * x;
+  double even = kInverseFactorials[12], odd = kInverseFactorials[13];
 #pragma unroll
-  for (int i = 1; i < 14; ++i) e = __builtin_fma(e, x, kInverseFactorials[i]);
-  return __builtin_ldexp(e, (int)n);
+  for (int i = 10; i >= 0; i -= 2) {
+    even = __builtin_fma(even, xx, kInverseFactorials[i]);
+    odd = __builtin_fma(odd, xx, kInverseFactorials[i + 1]);
+  }
+  return __builtin_ldexp(__builtin_fma(odd, x, even), (int)n);
 }
 
 // The row's weights relative to its largest value.
@@ -500,12 +512,15 @@ constexpr u32 kCodeWords = 32768;
 constexpr u32 kCellCodes = 16;
 constexpr u32 kGroupCodes = kCellCodes * kWave;  // one wavefront's step: 1024 codes
 constexpr u32 kGroups = 65536 / kGroupCodes;
+constexpr u32 kUnitCodes = kWave;  // what a question is answered to before it looks at codes
+constexpr u32 kUnits = 65536 / kUnitCodes;
+static_assert(kUnits == (u32)kThreads, "a thread per unit in the scans");
 constexpr u32 kMatchCap = 1024;
 
 struct CodeLds {
   u32 cnt[kCodeWords];
-  u64 mass[kGroups];
-  u32 n[kGroups];
+  u64 mass[kUnits];  // inclusive prefixes
+  u32 n[kUnits];
   u32 match[kMatchCap];
   u64 scan[kWaves];
   u32 top, end, counted, matches;  // the first and the last code; the entries counted
@@ -655,13 +670,27 @@ template <class T, bool EDGE>
 __device__ __forceinline__ u64 cell_mass(const Weigher& w, u32 top, u32 c0, const u32 (&n)[kCellCodes]) {
   const double v0 = (double)value_of_code<T>(c0), v1 = (double)value_of_code<T>(c0 + 1);
   const double rho = pow2((v1 - v0) * w.c);
-  double p = EDGE && c0 <= top ? w.scale : pow2((v0 - (double)w.top) * w.c) * w.scale, s = 0;
+  double p = EDGE && c0 <= top ? w.scale : pow2((v0 - (double)w.top) * w.c) * w.scale;
+  if constexpr (EDGE) {
+    double s = 0;
 #pragma unroll
-  for (u32 i = 0; i < kCellCodes; ++i) {
-    s = __builtin_fma((double)n[i], p, s);
-    if (!EDGE || c0 + i >= top) p *= rho;
+    for (u32 i = 0; i < kCellCodes; ++i) {
+      s = __builtin_fma((double)n[i], p, s);
+      if (c0 + i >= top) p *= rho;
+    }
+    return (u64)rint(s);
+  } else {  // the polynomial in rho by halves
+    double s[kCellCodes], power = rho;
+#pragma unroll
+    for (u32 i = 0; i < kCellCodes; ++i) s[i] = (double)n[i];
+#pragma unroll
+    for (u32 h = kCellCodes / 2; h; h /= 2) {
+#pragma unroll
+      for (u32 i = 0; i < h; ++i) s[i] = __builtin_fma(s[2 * i + 1], power, s[2 * i]);
+      power *= power;
+    }
+    return (u64)rint(s[0] * p);
   }
-  return (u64)rint(s);
 }
 __device__ __forceinline__ bool edge_group(u32 g, u32 top, u32 last) { return g == top / kGroupCodes || g == last / kGroupCodes; }
 
@@ -689,47 +718,37 @@ struct CodePlace {
 
 enum class Ask { kCount, kMass, kCode };
 
-// Where the running count or mass reaches Q, or the place of code Q, in one wavefront: a
-// step over the groups (lane g holds the count n and the mass m through group g), a scan
-// over the cells of one group, then over the codes of one cell.
+// Where the running count or mass reaches Q, or the place of code Q, in one wavefront: the
+// unit in two steps of LDS reads (64 sixteens of units, then the sixteen), then its codes, a
+// lane each.  A step that scanned a thousand codes' masses instead took three times as long.
 template <class T>
-__device__ __forceinline__ CodePlace find_code(const CodeLds& L, const Weigher& w, u32 top, u32 last, u64 m, u32 n,
-                                               Ask ask, u64 Q) {
+__device__ __forceinline__ CodePlace find_code(const CodeLds& L, const Weigher& w, u32 top, u32 last, Ask ask, u64 Q) {
   const u32 lane = lane_id();
-  static_assert(kGroups == kWave, "a lane holds a group");
-  auto where = [&](u64 some, u64 mass, u32 count, u32 of_code) -> u32 {
-    if (ask == Ask::kCode) return of_code;
-    const u64 reach = some & __ballot(ask == Ask::kMass ? mass >= Q : (u64)count >= Q);
-    return reach ? (u32)__builtin_ctzll(reach) : some ? 63u - (u32)__builtin_clzll(some) : 0u;
-  };
-  const u32 qc = __builtin_amdgcn_readfirstlane((u32)Q);
-  const u32 g = where(~0ull, m, n, qc / kGroupCodes);
-  const u64 gm = g ? of_lane(m, g - 1) : 0;
-  const u32 gn = g ? of_lane(n, g - 1) : 0;
-  const u32 c0 = g * kGroupCodes + lane * kCellCodes;
-  u32 cnt[kCellCodes], cn;
-  u64 cm;
-  if (edge_group(g, top, last)) {
-    cn = cell_counters<true>(L, c0, last, cnt);
-    cm = cell_mass<T, true>(w, top, c0, cnt);
-  } else {
-    cn = cell_counters<false>(L, c0, last, cnt);
-    cm = cell_mass<T, false>(w, top, c0, cnt);
+  u32 unit = __builtin_amdgcn_readfirstlane((u32)Q) / kUnitCodes;
+  if (ask != Ask::kCode) {
+    constexpr u32 kStep = kUnits / kWave;
+    auto reaches = [&](u32 u) { return ask == Ask::kMass ? L.mass[u] >= Q : (u64)L.n[u] >= Q; };
+    const u64 far = __builtin_amdgcn_ballot_w64(reaches(lane * kStep + kStep - 1));
+    unit = (far ? (u32)__builtin_ctzll(far) : (u32)kWave - 1) * kStep;
+    const u64 near = __builtin_amdgcn_ballot_w64(lane >= kStep - 1 || reaches(unit + lane));
+    unit += (u32)__builtin_ctzll(near);
   }
-  const u32 n1 = gn + wave_scan(cn);
-  const u64 m1 = gm + wave_scan(cm);
-  const u32 at = where(~0ull, m1, n1, qc % kGroupCodes / kCellCodes);
-  // the cell's codes, a lane each
-  const u32 first = of_lane(c0, at);
-  const u64 ms = of_lane(m1 - cm, at);
-  const u32 ns = of_lane(n1 - cn, at), code = first + lane;
-  const bool mine = lane < kCellCodes && code >= top && code <= last;
+  const u64 ms = unit ? L.mass[unit - 1] : 0;
+  const u32 ns = unit ? L.n[unit - 1] : 0;
+  const u32 code = unit * kUnitCodes + lane;
+  const bool mine = code >= top && code <= last;
   const u32 nc = mine ? L.cnt[counter_word(code)] >> (code >> 15 << 4) & 0xFFFFu : 0u;
   const double q = mine ? pow2(w.exponent(value_of_code<T>(code))) * w.scale : 0.0;
   const u64 mc = (u64)rint((double)nc * q), mi = ms + wave_scan(mc);
   const u32 ni = ns + wave_scan(nc);
-  const u32 i = where(__ballot(nc != 0), mi, ni, qc % kCellCodes);
-  return {first + i, of_lane(ni - nc, i), of_lane(ni, i), of_lane(mi - mc, i), of_lane(mi, i), of_lane((u64)rint(q), i)};
+  u32 i = __builtin_amdgcn_readfirstlane((u32)Q) % kUnitCodes;
+  if (ask != Ask::kCode) {
+    const u64 some = __builtin_amdgcn_ballot_w64(nc != 0);
+    const u64 reach = some & __builtin_amdgcn_ballot_w64(ask == Ask::kMass ? mi >= Q : (u64)ni >= Q);
+    i = reach ? (u32)__builtin_ctzll(reach) : some ? 63u - (u32)__builtin_clzll(some) : 0u;
+  }
+  return {unit * kUnitCodes + i, of_lane(ni - nc, i),       of_lane(ni, i),
+          of_lane(mi - mc, i),   of_lane(mi, i), of_lane((u64)rint(q), i)};
 }
 
 // The last code whose weight is at least m: each of three steps tries 64 codes at a time.
@@ -753,9 +772,7 @@ template <class T>
 __device__ __forceinline__ void answer_codes(CodeLds& L, const TokenArgs& a, u64 r, const RowSettings& s,
                                              const Weigher& w, u32 top, u32 last) {
   const u32 lane = lane_id();
-  const u64 m = wave_scan(L.mass[lane]);
-  const u32 n = wave_scan(L.n[lane]);
-  u64 kn = of_lane(n, kWave - 1), km = of_lane(m, kWave - 1);  // what is kept: entries and mass
+  u64 kn = L.n[kUnits - 1], km = L.mass[kUnits - 1];  // what is kept: entries and mass
   for (int step = 0; step < 4; ++step) {  // one place where the search is inlined
     Ask ask = Ask::kMass;
     u64 Q;
@@ -775,7 +792,7 @@ __device__ __forceinline__ void answer_codes(CodeLds& L, const TokenArgs& a, u64
       Q = (u64)((double)s.u * (double)km) + 1;
       if (Q > km) Q = km;
     }
-    const CodePlace c = find_code<T>(L, w, top, last, m, n, ask, Q);
+    const CodePlace c = find_code<T>(L, w, top, last, ask, Q);
     if (step == 2 && c.n1 >= kn) continue;
     const u32 j = step == 0 ? (u32)Q - c.n0 : step == 2 ? c.n1 - c.n0 : c.entries(Q);
     if (step < 3) {
@@ -860,7 +877,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
       atomicAdd(&L.counted, counted);  // the wavefront's
     }
   }
-  __syncthreads();
+  lds_barrier();
   const u32 top = L.top;
   const bool nan = top < (0x7FFFu ^ kInf) || L.end > (0x8000u | kInf);
   if (nan || top > kLowest) {
@@ -870,6 +887,8 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
     }
     return;
   }
+  if constexpr (NV == 0)  // the last pass's first vectors, on their way meanwhile
+    if (nvec) vectors.load();
   // 2. the groups' counts and masses, then the questions
   if (s.t > 0.f) {
     Weigher w;
@@ -884,21 +903,30 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
         const u32 c0 = g * kGroupCodes + lane_id() * kCellCodes;
         u32 cnt[kCellCodes];
         if (edge_group(g, top, last)) {
-          n = wave_sum(cell_counters<true>(L, c0, last, cnt));
-          if (n) m = wave_sum(cell_mass<T, true>(w, top, c0, cnt));
+          n = cell_counters<true>(L, c0, last, cnt);
+          if (__builtin_amdgcn_ballot_w64(n != 0)) m = cell_mass<T, true>(w, top, c0, cnt);
         } else {
-          n = wave_sum(cell_counters<false>(L, c0, last, cnt));
-          if (n) m = wave_sum(cell_mass<T, false>(w, top, c0, cnt));
+          n = cell_counters<false>(L, c0, last, cnt);
+          if (__builtin_amdgcn_ballot_w64(n != 0)) m = cell_mass<T, false>(w, top, c0, cnt);
         }
+        static_assert(kUnitCodes == 4 * kCellCodes, "four lanes' cells are a unit");
+        m += quad_xor<0xB1>(m);
+        n += quad_xor<0xB1>(n);
+        m += quad_xor<0x4E>(m);
+        n += quad_xor<0x4E>(n);
       }
-      if (lane_id() == 0) {
-        L.mass[g] = m;
-        L.n[g] = n;
+      if (lane_id() % 4 == 0) {
+        const u32 unit = (g * kGroupCodes + lane_id() * kCellCodes) / kUnitCodes;
+        L.mass[unit] = m;
+        L.n[unit] = n;
       }
     }
-    __syncthreads();
+    lds_barrier();
+    L.mass[threadIdx.x] = block_scan_u64(L.mass[threadIdx.x], L.scan);
+    L.n[threadIdx.x] = (u32)block_scan_u64(L.n[threadIdx.x], L.scan);
+    lds_barrier();
     // A counter may have overflowed, or entries been counted that are absent.
-    if (NV != 4 && V > 0xFFFFu && wave_sum(L.n[lane_id()]) != L.counted) {
+    if (NV != 4 && V > 0xFFFFu && L.n[kUnits - 1] != L.counted) {
       u32 n = 0;
       for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads) {
         const uint4 c = reinterpret_cast<const uint4*>(L.cnt)[i];
@@ -909,12 +937,12 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
       }
       n = wave_sum(n);
       if (lane_id() == 0) L.scan[threadIdx.x / kWave] = n;
-      __syncthreads();
+      lds_barrier();
       u32 total = 0;
 #pragma unroll
       for (int i = 0; i < kWaves; ++i) total += (u32)L.scan[i];
       const bool lost = total != L.counted;
-      __syncthreads();
+      lds_barrier();
       if (lost) {
         if (threadIdx.x == 0) a.tokens[r] = kByValue;
         return;
@@ -926,7 +954,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
     L.j = 1;
     a.logprobs[r] = 0.f;
   }
-  __syncthreads();
+  lds_barrier();
   // 3. the j-th entry of that code, by index
   const u32 code = L.code;
   const bool zero = code == 0x7FFFu || code == 0x8000u;
@@ -944,7 +972,6 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   if (threadIdx.x < head && (((edge ^ want) & mask) & 0xFFFFu) == 0) match(threadIdx.x);
   if (threadIdx.x < V - tail && ((edge ^ want) & mask) < 0x10000u) match(tail + threadIdx.x);
   if (nvec) {
-    if constexpr (NV == 0) vectors.load();
     vectors.for_each([&](uint4 v, u32 at) {
       const u32 x[4] = {(v.x ^ want) & mask, (v.y ^ want) & mask, (v.z ^ want) & mask, (v.w ^ want) & mask};
       u32 some = 0;
@@ -957,7 +984,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
       }
     });
   }
-  __syncthreads();
+  lds_barrier();
   const u32 n = L.matches;
   if (n <= kMatchCap) {
     if (threadIdx.x < n) {
