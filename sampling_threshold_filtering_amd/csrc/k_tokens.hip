@@ -124,6 +124,24 @@ __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* wave_tot) {
   return v + before;
 }
 
+// Both at once.
+__device__ __forceinline__ void block_scan(u64& m, u32& n, u64* wave_m, u32* wave_n) {
+  m = wave_scan(m);
+  n = wave_scan(n);
+  const u32 wid = threadIdx.x / kWave, lane = lane_id();
+  if (lane == kWave - 1) {
+    wave_m[wid] = m;
+    wave_n[wid] = n;
+  }
+  lds_barrier();
+  const u64 tm = wave_scan(lane < (u32)kWaves ? wave_m[lane] : 0);
+  const u32 tn = wave_scan(lane < (u32)kWaves ? wave_n[lane] : 0);
+  if (wid) {
+    m += of_lane(tm, __builtin_amdgcn_readfirstlane(wid) - 1);
+    n += of_lane(tn, __builtin_amdgcn_readfirstlane(wid) - 1);
+  }
+}
+
 // Calls f(value, index) for every entry of the row, each once, over the block's threads.
 // 16-byte loads between the row's first and last 16-byte boundaries.
 template <class T, class F>
@@ -144,23 +162,33 @@ __device__ __forceinline__ void for_each_entry(const T* row, u32 V, F f) {
   for (u32 i = head + nvec * W + threadIdx.x; i < V; i += kThreads) f(to_f32(row[i]), i);
 }
 
+// A constant in scalar registers: as a literal of a 64-bit instruction it would take two
+// vector moves.
+__device__ __forceinline__ double scalar(double v) {
+  asm("" : "+s"(v));
+  return v;
+}
+
 // 2^y for y <= 0: y = n + f with |f| <= 1/2, the Taylor series of e^(f ln 2) to the power
-// 13 (the next term is below 2^-57), scaled by 2^n.  2^0 is exactly 1; NaN gives 0.
-// The factorials' inverses are read into scalar registers; the even and the odd powers are
-// summed apart, in half the steps.
-__constant__ const double kInverseFactorials[14] = {
-    1.0, 1.0, 0.5, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880,
-    1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600, 1.0 / 6227020800.0};
-__device__ __forceinline__ double pow2(double y) {
+// 13 (the next term is below 2^-57), scaled by 2^n.  2^0 is exactly 1; NaN gives 0.  The
+// even and the odd powers are summed apart, in half the steps.
+__device__ __forceinline__ double pow2(double y, int F = 0) {  // times 2^F
   y = __builtin_fmax(y, -2000.0);
-  const double n = rint(y), x = (y - n) * 0.69314718055994530942, xx = x * x;
-  double even = kInverseFactorials[12], odd = kInverseFactorials[13];
-#pragma unroll
-  for (int i = 10; i >= 0; i -= 2) {
-    even = __builtin_fma(even, xx, kInverseFactorials[i]);
-    odd = __builtin_fma(odd, xx, kInverseFactorials[i + 1]);
-  }
-  return __builtin_ldexp(__builtin_fma(odd, x, even), (int)n);
+  const double n = rint(y), x = (y - n) * scalar(0.69314718055994530942), xx = x * x;
+  double even = scalar(1.0 / 479001600), odd = scalar(1.0 / 6227020800.0);
+  even = __builtin_fma(even, xx, scalar(1.0 / 3628800));
+  odd = __builtin_fma(odd, xx, scalar(1.0 / 39916800));
+  even = __builtin_fma(even, xx, scalar(1.0 / 40320));
+  odd = __builtin_fma(odd, xx, scalar(1.0 / 362880));
+  even = __builtin_fma(even, xx, scalar(1.0 / 720));
+  odd = __builtin_fma(odd, xx, scalar(1.0 / 5040));
+  even = __builtin_fma(even, xx, scalar(1.0 / 24));
+  odd = __builtin_fma(odd, xx, scalar(1.0 / 120));
+  even = __builtin_fma(even, xx, 0.5);
+  odd = __builtin_fma(odd, xx, scalar(1.0 / 6));
+  even = __builtin_fma(even, xx, 1.0);
+  odd = __builtin_fma(odd, xx, 1.0);
+  return __builtin_ldexp(__builtin_fma(odd, x, even), (int)n + F);
 }
 
 // The row's weights relative to its largest value.
@@ -174,6 +202,11 @@ struct Weigher {
     return v == top ? 0.0 : ((double)v - (double)top) * c;  // 0 also where both are +inf
   }
   __device__ __forceinline__ bool present(double y) const { return y >= limit; }  // false for NaN
+  // The weight as an integer: adding 2^52 leaves it, rounded, in the low bits (F <= 50).
+  __device__ __forceinline__ u64 whole(double y, int F) const {
+    const double p = pow2(y, F) + 0x1p52;
+    return __builtin_bit_cast(u64, p) - __builtin_bit_cast(u64, 0x1p52);
+  }
   __device__ __forceinline__ u64 weight(double y) const { return (u64)rint(pow2(y) * scale); }
   __device__ __forceinline__ u32 bin(double y) const {  // monotone in the value
     const double b = -y * bins;
@@ -523,6 +556,7 @@ struct CodeLds {
   u32 n[kUnits];
   u32 match[kMatchCap];
   u64 scan[kWaves];
+  u32 scan_n[kWaves];
   u32 top, end, counted, matches;  // the first and the last code; the entries counted
   u32 code, j;
 };
@@ -595,19 +629,20 @@ __device__ __forceinline__ u32 pk_max(u32 a, u32 b) {
 // The 16-byte vectors of a row, `kBatch` a thread at a time.  NV > 0: all of a thread's NV
 // vectors are loaded at once and stay in registers for the second pass.
 // NV = 0: the next batch is in flight while one is dealt with.
+typedef u32 u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBatch = 4;
 template <int NV>
 struct RowVectors {
   static constexpr int kHeld = NV ? NV : kBatch;
-  const uint4* vec;
+  const u32x4* vec;
   u32 nvec, fill;
-  uint4 held[kHeld];
+  u32x4 held[kHeld];
 
-  __device__ __forceinline__ uint4 at(u32 j) const {  // 32-bit offsets from a scalar base
-    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(vec) + (j < nvec ? j : nvec - 1) * 16u);
+  __device__ __forceinline__ u32x4 at(u32 j) const {  // 32-bit offsets from a scalar base
+    return *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(vec) + (j < nvec ? j : nvec - 1) * 16u);
   }
-  __device__ __forceinline__ uint4 filled(uint4 v, u32 j) const {
-    return j < nvec ? v : make_uint4(fill, fill, fill, fill);
+  __device__ __forceinline__ u32x4 filled(u32x4 v, u32 j) const {
+    return j < nvec ? v : (u32x4){fill, fill, fill, fill};
   }
   __device__ __forceinline__ void load() {  // of a row of at least one vector
 #pragma unroll
@@ -624,17 +659,22 @@ struct RowVectors {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const u32 j = threadIdx.x + (u32)i * kThreads;
+        // what is worked out of a vector in one pass is not kept for the next: registers
+        asm volatile("" : "+v"(held[i]));
         if ((u32)i * kThreads < nvec) f(filled(held[i], j), j);
         __builtin_amdgcn_sched_barrier(0);  // one vector's work at a time: registers
       }
     } else {
       u32 j = threadIdx.x;
       for (; j - threadIdx.x + kBatch * kThreads <= nvec; j += kBatch * kThreads) {
-        uint4 next[kBatch];
+        u32x4 next[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) next[i] = at(j + (u32)(kBatch + i) * kThreads);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) f(held[i], j + (u32)i * kThreads);
+        for (int i = 0; i < kBatch; ++i) {
+          f(held[i], j + (u32)i * kThreads);
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) held[i] = next[i];
       }
@@ -822,7 +862,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   if (head > V) head = V;
   const u32 nvec = (V - head) / 8, tail = head + nvec * 8;
   RowVectors<NV> vectors;
-  vectors.vec = reinterpret_cast<const uint4*>(row + head);
+  vectors.vec = reinterpret_cast<const u32x4*>(row + head);
   vectors.nvec = nvec;
   vectors.fill = kFill;
   if (nvec) vectors.load();
@@ -852,7 +892,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   if (threadIdx.x < V - tail) edge = (edge & 0xFFFFu) | (u32)row[tail + threadIdx.x] << 16;
   tops = pk_codes(edge);
   if (nvec)
-    vectors.first_batch([&](uint4 v) {
+    vectors.first_batch([&](u32x4 v) {
       tops = pk_min(tops, pk_min(pk_min(pk_codes(v.x), pk_codes(v.y)), pk_min(pk_codes(v.z), pk_codes(v.w))));
     });
   {
@@ -861,7 +901,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
     thr = top > kLowest ? kLowest : s.t > 0.f ? last_code<T>(top, s.t, (float)(F + 1)) : top;
   }
   if (nvec)
-    vectors.for_each([&](uint4 v, u32) {
+    vectors.for_each([&](u32x4 v, u32) {
       count(v.x);
       count(v.y);
       count(v.z);
@@ -922,8 +962,13 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
       }
     }
     lds_barrier();
-    L.mass[threadIdx.x] = block_scan_u64(L.mass[threadIdx.x], L.scan);
-    L.n[threadIdx.x] = (u32)block_scan_u64(L.n[threadIdx.x], L.scan);
+    {
+      u64 m = L.mass[threadIdx.x];
+      u32 n = L.n[threadIdx.x];
+      block_scan(m, n, L.scan, L.scan_n);
+      L.mass[threadIdx.x] = m;
+      L.n[threadIdx.x] = n;
+    }
     lds_barrier();
     // A counter may have overflowed, or entries been counted that are absent.
     if (NV != 4 && V > 0xFFFFu && L.n[kUnits - 1] != L.counted) {
@@ -972,7 +1017,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   if (threadIdx.x < head && (((edge ^ want) & mask) & 0xFFFFu) == 0) match(threadIdx.x);
   if (threadIdx.x < V - tail && ((edge ^ want) & mask) < 0x10000u) match(tail + threadIdx.x);
   if (nvec) {
-    vectors.for_each([&](uint4 v, u32 at) {
+    vectors.for_each([&](u32x4 v, u32 at) {
       const u32 x[4] = {(v.x ^ want) & mask, (v.y ^ want) & mask, (v.z ^ want) & mask, (v.w ^ want) & mask};
       u32 some = 0;
 #pragma unroll
@@ -1011,15 +1056,258 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   }
 }
 
-}  // namespace
+// ---------------------------------------------------------------------------------------
+// Rows of 32-bit logits.
+//
+// Almost every value differs, so each entry has its weight worked out, once: an LDS
+// histogram of 4096 value bins takes the integer weights (and the entries' number where a
+// top-k asks for it), and a question is answered to one bin by the bins' prefix sums and
+// inside it by ranks: each of the bin's entries adds up the weights of those before it.
+// Bins are cut from the 32-bit difference to the largest value, which rounds monotonously.
+// Rows of up to 16384 entries stay in registers between the passes.  A bin of more
+// than kListed entries is left to the launch that splits bins.
+constexpr u32 kFloatBins = 4096;
+constexpr u32 kListed = 1024;
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void sample_values_kernel(TokenArgs a) {
-  __shared__ TokLds S;
-  sample_row_by_value<T>(S, a, blockIdx.x);
+struct FloatLds {
+  u64 mass[kFloatBins];
+  u32 n[kFloatBins];
+  u64 key[kListed], weight[kListed], before[kListed];
+  u32 rank[kListed];
+  u64 scan[kWaves];
+  u32 scan_n[kWaves];
+  u32 top, nan, bin, listed, index;
+  u64 minp, total;
+  u64 ans_mass, ans_key;
+};
+
+template <int NV>
+__device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArgs& a, u64 r) {
+  const float* row = reinterpret_cast<const float*>(a.x) + r * a.ld;
+  const u32 V = (u32)a.V;
+  const RowSettings s = row_settings(a, r);
+  constexpr float kNone = -__builtin_huge_valf();
+  u32 head = (u32)((16 - ((uintptr_t)row & 15)) & 15) / 4;
+  if (head > V) head = V;
+  const u32 nvec = (V - head) / 4, tail = head + nvec * 4;
+  RowVectors<NV> vectors;
+  vectors.vec = reinterpret_cast<const u32x4*>(row + head);
+  vectors.nvec = nvec;
+  vectors.fill = __float_as_uint(kNone);
+  if (nvec) vectors.load();
+  // the entries before and after the vectors, at most 3 and 3: a thread each
+  u32 edge_at = threadIdx.x < head ? threadIdx.x : ~0u;
+  if (threadIdx.x >= 64 && threadIdx.x - 64 < V - tail) edge_at = tail + threadIdx.x - 64;
+  const float edge = edge_at != ~0u ? row[edge_at] : kNone;
+  auto for_each = [&](auto f) {  // f(value, index), once for every entry
+    f(edge, edge_at);
+    if (nvec)
+      vectors.for_each([&](u32x4 v, u32 j) {
+        const u32 i = head + 4 * j;
+        f(__uint_as_float(v.x), i);
+        f(__uint_as_float(v.y), i + 1);
+        f(__uint_as_float(v.z), i + 2);
+        f(__uint_as_float(v.w), i + 3);
+      });
+  };
+  for (u32 i = threadIdx.x; i < kFloatBins; i += kThreads) {
+    L.mass[i] = 0;
+    L.n[i] = 0;
+  }
+  if (threadIdx.x == 0) {
+    L.top = L.nan = 0;
+    L.minp = 0;
+    L.index = ~0u;
+  }
+  lds_barrier();
+  // 1. the largest value
+  {
+    float m = kNone;
+    bool nan = false;
+    for_each([&](float v, u32) {
+      m = __builtin_fmaxf(m, v);
+      nan |= v != v;
+    });
+    const u32 t = ~wave_min(~ord32(__float_as_uint(m)));
+    if (lane_id() == 0) atomicMax(&L.top, t);
+    if (nan) L.nan = 1;
+  }
+  if constexpr (NV == 0)
+    if (nvec) vectors.load();
+  lds_barrier();
+  const float top = __uint_as_float(bits_of_ord32(L.top));
+  if (L.nan || top == kNone) {
+    if (threadIdx.x == 0) {
+      a.tokens[r] = -1;
+      a.logprobs[r] = L.nan ? __uint_as_float(0x7FC00000u) : kNone;
+    }
+    return;
+  }
+  if (s.t == 0.f) {
+    u32 at = ~0u;
+    for_each([&](float v, u32 i) { at = v == top && i < at ? i : at; });
+    at = wave_min(at);
+    if (lane_id() == 0) atomicMin(&L.index, at);
+    lds_barrier();
+    if (threadIdx.x == 0) {
+      a.tokens[r] = L.index;
+      a.logprobs[r] = 0.f;
+    }
+    return;
+  }
+  u32 lg = 0;
+  while ((1ull << lg) < a.V) ++lg;
+  const int F = 62 - (int)lg < 50 ? 62 - (int)lg : 50;
+  Weigher w;
+  w.top = top;
+  w.c = 1.4426950408889634074 / (double)s.t;
+  w.scale = (double)(1ull << F);
+  const float reach = (float)F * 0.69314718f * s.t, bins = (float)(kFloatBins - 1) / reach;
+  // an entry's bin; kFloatBins: absent.  With every setting that makes reach 0, inf or NaN
+  // (t at the type's ends), equal entries still share bin 0.
+  auto bin_of = [&](float v) -> u32 {
+    const float d = v == top ? 0.f : top - v;
+    return d <= reach ? (u32)__builtin_fminf(d * bins, (float)(kFloatBins - 1)) : kFloatBins;
+  };
+  auto weight_of = [&](float v) { return w.whole(w.exponent(v), F); };
+  // 2. the histogram
+  {
+    const bool counts = s.k != 0;
+    u64 minp = 0;
+    for_each([&](float v, u32) {
+      const u32 b = bin_of(v);
+      if (b < kFloatBins) {
+        const double y = w.exponent(v);
+        const u64 q = w.whole(y, F);
+        atomicAdd(&L.mass[b], q);
+        if (counts) atomicAdd(&L.n[b], 1u);
+        if (s.m > 0.f && pow2(y) >= (double)s.m) minp += q;
+      }
+    });
+    if (s.m > 0.f) {
+      minp = wave_sum(minp);
+      if (lane_id() == 0) atomicAdd(&L.minp, minp);
+    }
+  }
+  lds_barrier();
+  u64 km;  // the mass that is kept
+  {
+    constexpr u32 kEach = kFloatBins / kThreads;
+    u64 m[kEach], sm = 0;
+    u32 n[kEach], sn = 0;
+#pragma unroll
+    for (u32 i = 0; i < kEach; ++i) {
+      m[i] = sm += L.mass[threadIdx.x * kEach + i];
+      n[i] = sn += L.n[threadIdx.x * kEach + i];
+    }
+    const u64 tm = sm;
+    const u32 tn = sn;
+    block_scan(sm, sn, L.scan, L.scan_n);
+#pragma unroll
+    for (u32 i = 0; i < kEach; ++i) {
+      L.mass[threadIdx.x * kEach + i] = sm - tm + m[i];
+      L.n[threadIdx.x * kEach + i] = sn - tn + n[i];
+    }
+    lds_barrier();
+    km = L.mass[kFloatBins - 1];
+  }
+  // 3. the questions
+  const u64 minp = L.minp, kn = L.n[kFloatBins - 1];
+  for (int step = 0; step < 4; ++step) {
+    bool by_mass = true;
+    u64 Q;
+    if (step == 0) {
+      if (!s.k || s.k >= kn) continue;
+      by_mass = false;
+      Q = s.k;
+    } else if (step == 1) {
+      Q = (u64)ceil((double)s.p * (double)km);
+      if (Q < 1 || !(s.p > 0.f)) Q = 1;
+      if (s.p >= 1.f || Q >= km) continue;
+    } else if (step == 2) {
+      if (s.m > 0.f && minp < km) km = minp;
+      continue;
+    } else {
+      Q = (u64)((double)s.u * (double)km) + 1;
+      if (Q > km) Q = km;
+    }
+    {
+      constexpr u32 kEach = kFloatBins / kThreads;
+#pragma unroll
+      for (u32 i = 0; i < kEach; ++i) {
+        const u32 b = threadIdx.x * kEach + i;
+        const u64 here = by_mass ? L.mass[b] : L.n[b], before = !b ? 0 : by_mass ? L.mass[b - 1] : L.n[b - 1];
+        if (here >= Q && before < Q) L.bin = b;
+      }
+      if (threadIdx.x == 0) L.listed = 0;
+    }
+    lds_barrier();
+    const u32 b = L.bin;
+    const u64 m0 = b ? L.mass[b - 1] : 0, n0 = b ? L.n[b - 1] : 0;
+    if constexpr (NV == 0)
+      if (nvec) vectors.load();
+    for_each([&](float v, u32 i) {
+      if (bin_of(v) == b) {
+        const u32 at = atomicAdd(&L.listed, 1u);
+        if (at < kListed) L.key[at] = make_key(__float_as_uint(v), i);
+      }
+    });
+    lds_barrier();
+    const u32 n = L.listed;
+    if (n > kListed) {
+      if (threadIdx.x == 0) a.tokens[r] = kByValue;
+      return;
+    }
+    if (threadIdx.x < n) {
+      L.weight[threadIdx.x] = weight_of(value_of_key(L.key[threadIdx.x]));
+      L.before[threadIdx.x] = 0;
+      L.rank[threadIdx.x] = 0;
+    }
+    lds_barrier();
+    // entry i's rank and the mass before it: by 1024 / P threads each, P >= n a power of 2
+    u32 P = 1;
+    while (P < n) P <<= 1;
+    const u32 i = threadIdx.x & (P - 1);
+    if (i < n) {
+      const u64 mine = L.key[i];
+      u64 before = 0;
+      u32 rank = 0;
+      for (u32 j = threadIdx.x / P; j < n; j += kThreads / P)
+        if (L.key[j] > mine) {
+          before += L.weight[j];
+          ++rank;
+        }
+      if (P == kThreads) {
+        L.before[i] = before;
+        L.rank[i] = rank;
+      } else if (rank) {
+        atomicAdd(&L.before[i], before);
+        atomicAdd(&L.rank[i], rank);
+      }
+    }
+    lds_barrier();
+    if (threadIdx.x < n) {
+      const u64 before = m0 + L.before[threadIdx.x], through = before + L.weight[threadIdx.x];
+      if (by_mass ? through >= Q && before < Q : n0 + L.rank[threadIdx.x] + 1 == Q) {
+        L.ans_mass = through;
+        L.ans_key = L.key[threadIdx.x];
+      }
+    }
+    lds_barrier();
+    if (step < 3) {
+      km = L.ans_mass;
+      lds_barrier();
+    } else if (threadIdx.x == 0) {
+      const u64 key = L.ans_key;
+      a.tokens[r] = (int64_t)key_index(key);
+      a.logprobs[r] = (float)(w.exponent(value_of_key(key)) * 0.69314718055994530942 - log((double)km / w.scale));
+    }
+  }
 }
 
-// The rows whose counters overflowed: a block looks at rows b, b + blocks, ..., a thread
+}  // namespace
+
+// The rows whose counters or lists overflowed: a block looks at rows b, b + blocks, ..., a thread
 // each.
 constexpr u32 kLeftBlocks = 64;
 template <class T>
@@ -1029,14 +1317,12 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(TokenArgs a) {
   for (u64 r0 = blockIdx.x; r0 < a.B; r0 += (u64)kThreads * gridDim.x) {
     const u64 r = r0 + (u64)threadIdx.x * gridDim.x;
     u64 mine = r < a.B && a.tokens[r] == kByValue ? r : ~0ull;
-    for (;;) {
-      __syncthreads();
+    while (__syncthreads_or(mine != ~0ull)) {
       if (threadIdx.x == 0) left = ~0u;
       __syncthreads();
       if (mine != ~0ull) atomicMin(&left, threadIdx.x);
       __syncthreads();
       const u32 t = left;
-      if (t == ~0u) break;
       if (threadIdx.x == t) mine = ~0ull;
       sample_row_by_value<T>(S, a, r0 + (u64)t * gridDim.x);
     }
@@ -1047,6 +1333,22 @@ template <class T, int NV>
 __global__ __launch_bounds__(kThreads) void sample_codes_kernel(TokenArgs a) {
   __shared__ CodeLds S;
   sample_row_by_code<T, NV>(S, a, blockIdx.x);
+}
+
+template <int NV>
+__global__ __launch_bounds__(kThreads) void sample_floats_kernel(TokenArgs a) {
+  __shared__ FloatLds S;
+  sample_row_of_floats<NV>(S, a, blockIdx.x);
+}
+
+static void launch_floats(const TokenArgs& a, hipStream_t s) {
+  const u32 B = (u32)a.B;
+  const u64 vectors = (a.V + 3) / 4;
+  if (vectors <= 4 * kThreads)
+    sample_floats_kernel<4><<<B, kThreads, 0, s>>>(a);
+  else
+    sample_floats_kernel<0><<<B, kThreads, 0, s>>>(a);
+  if (a.V > kListed) sample_left_kernel<float><<<B < kLeftBlocks ? B : kLeftBlocks, kThreads, 0, s>>>(a);
 }
 
 template <class T>
@@ -1066,7 +1368,7 @@ size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
 
 hipError_t launch_sample_tokens(const TokenArgs& a, int dtype, hipStream_t s) {
   if (dtype == PROFK_FP32)
-    sample_values_kernel<float><<<(u32)a.B, kThreads, 0, s>>>(a);
+    launch_floats(a, s);
   else if (dtype == PROFK_FP16)
     launch_codes<Half16>(a, s);
   else
