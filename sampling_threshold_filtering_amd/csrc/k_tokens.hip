@@ -202,10 +202,9 @@ struct Weigher {
     return v == top ? 0.0 : ((double)v - (double)top) * c;  // 0 also where both are +inf
   }
   __device__ __forceinline__ bool present(double y) const { return y >= limit; }  // false for NaN
-  // The weight as an integer: adding 2^52 leaves it, rounded, in the low bits (F <= 50).
-  __device__ __forceinline__ u64 whole(double y, int F) const {
-    const double p = pow2(y, F) + 0x1p52;
-    return __builtin_bit_cast(u64, p) - __builtin_bit_cast(u64, 0x1p52);
+  // A weight times 2^F as an integer: adding 2^52 leaves it, rounded, in the low bits (F <= 50).
+  __device__ __forceinline__ u64 whole(double p) const {
+    return __builtin_bit_cast(u64, p + 0x1p52) - __builtin_bit_cast(u64, 0x1p52);
   }
   __device__ __forceinline__ u64 weight(double y) const { return (u64)rint(pow2(y) * scale); }
   __device__ __forceinline__ u32 bin(double y) const {  // monotone in the value
@@ -1076,8 +1075,10 @@ struct FloatLds {
   u32 rank[kListed];
   u64 scan[kWaves];
   u32 scan_n[kWaves];
-  u32 top, nan, bin, listed, index;
-  u64 minp, total;
+  u64 far_mass[kWave];  // every 64th of the prefixes
+  u32 far_n[kWave];
+  u32 top, nan, index, listed[4];
+  u64 minp;
   u64 ans_mass, ans_key;
 };
 
@@ -1099,15 +1100,13 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   u32 edge_at = threadIdx.x < head ? threadIdx.x : ~0u;
   if (threadIdx.x >= 64 && threadIdx.x - 64 < V - tail) edge_at = tail + threadIdx.x - 64;
   const float edge = edge_at != ~0u ? row[edge_at] : kNone;
-  auto for_each = [&](auto f) {  // f(value, index), once for every entry
-    f(edge, edge_at);
+  auto for_each = [&](auto f) {  // f(four values, the first one's index), each entry once
+    const float e[4] = {edge, kNone, kNone, kNone};
+    f(e, edge_at);
     if (nvec)
       vectors.for_each([&](u32x4 v, u32 j) {
-        const u32 i = head + 4 * j;
-        f(__uint_as_float(v.x), i);
-        f(__uint_as_float(v.y), i + 1);
-        f(__uint_as_float(v.z), i + 2);
-        f(__uint_as_float(v.w), i + 3);
+        const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+        f(x, head + 4 * j);
       });
   };
   for (u32 i = threadIdx.x; i < kFloatBins; i += kThreads) {
@@ -1119,14 +1118,15 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     L.minp = 0;
     L.index = ~0u;
   }
+  if (threadIdx.x < 4) L.listed[threadIdx.x] = 0;
   lds_barrier();
   // 1. the largest value
   {
     float m = kNone;
     bool nan = false;
-    for_each([&](float v, u32) {
-      m = __builtin_fmaxf(m, v);
-      nan |= v != v;
+    for_each([&](const float (&v)[4], u32) {
+      m = __builtin_fmaxf(m, __builtin_fmaxf(__builtin_fmaxf(v[0], v[1]), __builtin_fmaxf(v[2], v[3])));
+      nan |= __builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3]);
     });
     const u32 t = ~wave_min(~ord32(__float_as_uint(m)));
     if (lane_id() == 0) atomicMax(&L.top, t);
@@ -1145,7 +1145,10 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   }
   if (s.t == 0.f) {
     u32 at = ~0u;
-    for_each([&](float v, u32 i) { at = v == top && i < at ? i : at; });
+    for_each([&](const float (&v)[4], u32 i) {
+#pragma unroll
+      for (u32 k = 0; k < 4; ++k) at = v[k] == top && i + k < at ? i + k : at;
+    });
     at = wave_min(at);
     if (lane_id() == 0) atomicMin(&L.index, at);
     lds_barrier();
@@ -1162,27 +1165,37 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   w.top = top;
   w.c = 1.4426950408889634074 / (double)s.t;
   w.scale = (double)(1ull << F);
-  const float reach = (float)F * 0.69314718f * s.t, bins = (float)(kFloatBins - 1) / reach;
+  const float reach_f = (float)F * 0.69314718f * s.t, bins = (float)(kFloatBins - 1) / reach_f;
   // an entry's bin; kFloatBins: absent.  With every setting that makes reach 0, inf or NaN
   // (t at the type's ends), equal entries still share bin 0.
   auto bin_of = [&](float v) -> u32 {
     const float d = v == top ? 0.f : top - v;
-    return d <= reach ? (u32)__builtin_fminf(d * bins, (float)(kFloatBins - 1)) : kFloatBins;
+    return d <= reach_f ? (u32)__builtin_fminf(d * bins, (float)(kFloatBins - 1)) : kFloatBins;
   };
-  auto weight_of = [&](float v) { return w.whole(w.exponent(v), F); };
-  // 2. the histogram
+  auto weight_of = [&](float v) { return w.whole(pow2(w.exponent(v), F)); };
+  // 2. the histogram: four weights at a time, for the 64-bit instructions' latency
   {
     const bool counts = s.k != 0;
+    const double least = (double)s.m * w.scale;
     u64 minp = 0;
-    for_each([&](float v, u32) {
-      const u32 b = bin_of(v);
-      if (b < kFloatBins) {
-        const double y = w.exponent(v);
-        const u64 q = w.whole(y, F);
-        atomicAdd(&L.mass[b], q);
-        if (counts) atomicAdd(&L.n[b], 1u);
-        if (s.m > 0.f && pow2(y) >= (double)s.m) minp += q;
+    for_each([&](const float (&v)[4], u32) {
+      u32 b[4];
+      u64 q[4];
+      bool kept[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        b[k] = bin_of(v[k]);
+        const double p = pow2(w.exponent(v[k]), F);
+        q[k] = w.whole(p);
+        kept[k] = p >= least;
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (b[k] < kFloatBins) {
+          atomicAdd(&L.mass[b[k]], q[k]);
+          if (counts) atomicAdd(&L.n[b[k]], 1u);
+          if (kept[k]) minp += q[k];
+        }
     });
     if (s.m > 0.f) {
       minp = wave_sum(minp);
@@ -1208,11 +1221,15 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
       L.mass[threadIdx.x * kEach + i] = sm - tm + m[i];
       L.n[threadIdx.x * kEach + i] = sn - tn + n[i];
     }
+    if (threadIdx.x % 16 == 15) {
+      L.far_mass[threadIdx.x / 16] = sm;
+      L.far_n[threadIdx.x / 16] = sn;
+    }
     lds_barrier();
-    km = L.mass[kFloatBins - 1];
+    km = L.far_mass[kWave - 1];
   }
   // 3. the questions
-  const u64 minp = L.minp, kn = L.n[kFloatBins - 1];
+  const u64 minp = L.minp, kn = L.far_n[kWave - 1];
   for (int step = 0; step < 4; ++step) {
     bool by_mass = true;
     u64 Q;
@@ -1231,29 +1248,29 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
       Q = (u64)((double)s.u * (double)km) + 1;
       if (Q > km) Q = km;
     }
-    {
-      constexpr u32 kEach = kFloatBins / kThreads;
-#pragma unroll
-      for (u32 i = 0; i < kEach; ++i) {
-        const u32 b = threadIdx.x * kEach + i;
-        const u64 here = by_mass ? L.mass[b] : L.n[b], before = !b ? 0 : by_mass ? L.mass[b - 1] : L.n[b - 1];
-        if (here >= Q && before < Q) L.bin = b;
-      }
-      if (threadIdx.x == 0) L.listed = 0;
-    }
-    lds_barrier();
-    const u32 b = L.bin;
+    // the bin, by every wavefront: first 64 sixty-fourths of the bins, then one of them
+    static_assert(kFloatBins == kWave * kWave, "two steps of 64");
+    const u32 lane = lane_id();
+    u64 reach = __builtin_amdgcn_ballot_w64(by_mass ? L.far_mass[lane] >= Q : L.far_n[lane] >= Q);
+    u32 b = reach ? (u32)__builtin_ctzll(reach) * kWave : kFloatBins - kWave;
+    reach = __builtin_amdgcn_ballot_w64(lane == kWave - 1 || (by_mass ? L.mass[b + lane] >= Q : L.n[b + lane] >= Q));
+    b += (u32)__builtin_ctzll(reach);
     const u64 m0 = b ? L.mass[b - 1] : 0, n0 = b ? L.n[b - 1] : 0;
+    // its entries: near its middle (more than the bin where rounding may tell), then in it
+    const float middle = top - ((float)b + 0.5f) / bins;
+    const float near = 0.51f / bins + (__builtin_fabsf(top) + reach_f) * 0x1p-21f;
     if constexpr (NV == 0)
       if (nvec) vectors.load();
-    for_each([&](float v, u32 i) {
-      if (bin_of(v) == b) {
-        const u32 at = atomicAdd(&L.listed, 1u);
-        if (at < kListed) L.key[at] = make_key(__float_as_uint(v), i);
-      }
+    for_each([&](const float (&v)[4], u32 i) {
+#pragma unroll
+      for (u32 k = 0; k < 4; ++k)
+        if (!(__builtin_fabsf(v[k] - middle) > near) && bin_of(v[k]) == b) {
+          const u32 at = atomicAdd(&L.listed[step], 1u);
+          if (at < kListed) L.key[at] = make_key(__float_as_uint(v[k]), i + k);
+        }
     });
     lds_barrier();
-    const u32 n = L.listed;
+    const u32 n = L.listed[step];
     if (n > kListed) {
       if (threadIdx.x == 0) a.tokens[r] = kByValue;
       return;
