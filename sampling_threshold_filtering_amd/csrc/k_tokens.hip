@@ -16,6 +16,8 @@
 // depend on their order, so LDS atomics and any split of the row give the same bits, and
 // the rounding of a weight (2^-(F+1) of the largest) is far below what a 24-bit u can
 // tell apart.  An entry below 2^-F of the largest counts as absent.
+#include <type_traits>
+
 #include "block_select.h"
 #include "launch.h"
 #include "ops_device.h"
@@ -625,16 +627,16 @@ __device__ __forceinline__ u32 pk_max(u32 a, u32 b) {
   const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
   return __builtin_bit_cast(u32, __builtin_elementwise_max(x, y));
 }
-// The 16-byte vectors of a row, `kBatch` a thread at a time.  NV > 0: all of a thread's NV
-// vectors are loaded at once and stay in registers for the second pass.
-// NV = 0: the next batch is in flight while one is dealt with.
+// The 16-byte vectors of a row, a thread's kBatch in flight while others are dealt with (all
+// loaded at once, the first waits until the last is on its way: 83 us in place of 64 for 512
+// rows of 131072).  NV > 0: a thread's NV vectors stay in registers for later passes.
 typedef u32 u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBatch = 4;
 template <int NV>
 struct RowVectors {
   static constexpr int kHeld = NV ? NV : kBatch;
   const u32x4* vec;
-  u32 nvec, fill;
+  u32 nvec, fill, tid;
   u32x4 held[kHeld];
 
   __device__ __forceinline__ u32x4 at(u32 j) const {  // 32-bit offsets from a scalar base
@@ -643,29 +645,42 @@ struct RowVectors {
   __device__ __forceinline__ u32x4 filled(u32x4 v, u32 j) const {
     return j < nvec ? v : (u32x4){fill, fill, fill, fill};
   }
+  // Each pass works out its own places and loads: kept for the next pass, they would take
+  // more registers than there are.
+  __device__ __forceinline__ void begin() {
+    tid = threadIdx.x;
+    asm volatile("" : "+v"(tid)::"memory");
+  }
   __device__ __forceinline__ void load() {  // of a row of at least one vector
+    begin();
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = at(threadIdx.x + (u32)i * kThreads);
+    for (int i = 0; i < kBatch; ++i) held[i] = at(tid + (u32)i * kThreads);
+  }
+  // What is worked out of the vectors in one pass is not kept for the next.
+  __device__ __forceinline__ void forget() {
+    begin();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) asm volatile("" : "+v"(held[i]));
   }
   template <class F>
   __device__ __forceinline__ void first_batch(F f) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) f(filled(held[i], threadIdx.x + (u32)i * kThreads));
+    for (int i = 0; i < kBatch; ++i) f(filled(held[i], tid + (u32)i * kThreads));
   }
-  template <class F>  // f(the vector, its place)
+  // f(the vector, its place).  LOAD: the pass after load().
+  template <bool LOAD, class F>
   __device__ __forceinline__ void for_each(F f) {
     if constexpr (NV > 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const u32 j = threadIdx.x + (u32)i * kThreads;
-        // what is worked out of a vector in one pass is not kept for the next: registers
-        asm volatile("" : "+v"(held[i]));
+        const u32 j = tid + (u32)i * kThreads;
+        if (LOAD && i + kBatch < NV) held[i + kBatch < NV ? i + kBatch : 0] = at(j + kBatch * kThreads);
         if ((u32)i * kThreads < nvec) f(filled(held[i], j), j);
         __builtin_amdgcn_sched_barrier(0);  // one vector's work at a time: registers
       }
     } else {
-      u32 j = threadIdx.x;
-      for (; j - threadIdx.x + kBatch * kThreads <= nvec; j += kBatch * kThreads) {
+      u32 j = tid;
+      for (; j - tid + kBatch * kThreads <= nvec; j += kBatch * kThreads) {
         u32x4 next[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) next[i] = at(j + (u32)(kBatch + i) * kThreads);
@@ -679,7 +694,7 @@ struct RowVectors {
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i, j += kThreads)
-        if (j - threadIdx.x < nvec) f(filled(held[i], j), j);
+        if (j - tid < nvec) f(filled(held[i], j), j);
     }
   }
 };
@@ -900,7 +915,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
     thr = top > kLowest ? kLowest : s.t > 0.f ? last_code<T>(top, s.t, (float)(F + 1)) : top;
   }
   if (nvec)
-    vectors.for_each([&](u32x4 v, u32) {
+    vectors.template for_each<true>([&](u32x4 v, u32) {
       count(v.x);
       count(v.y);
       count(v.z);
@@ -926,8 +941,11 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
     }
     return;
   }
-  if constexpr (NV == 0)  // the last pass's first vectors, on their way meanwhile
+  if constexpr (NV == 0) {  // the last pass's first vectors, on their way meanwhile
     if (nvec) vectors.load();
+  } else {
+    vectors.forget();
+  }
   // 2. the groups' counts and masses, then the questions
   if (s.t > 0.f) {
     Weigher w;
@@ -1016,7 +1034,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
   if (threadIdx.x < head && (((edge ^ want) & mask) & 0xFFFFu) == 0) match(threadIdx.x);
   if (threadIdx.x < V - tail && ((edge ^ want) & mask) < 0x10000u) match(tail + threadIdx.x);
   if (nvec) {
-    vectors.for_each([&](u32x4 v, u32 at) {
+    vectors.template for_each<NV == 0>([&](u32x4 v, u32 at) {
       const u32 x[4] = {(v.x ^ want) & mask, (v.y ^ want) & mask, (v.z ^ want) & mask, (v.w ^ want) & mask};
       u32 some = 0;
 #pragma unroll
@@ -1067,6 +1085,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
 // than kListed entries is left to the launch that splits bins.
 constexpr u32 kFloatBins = 4096;
 constexpr u32 kListed = 1024;
+constexpr u32 kPowers = 256;
 
 struct FloatLds {
   u64 mass[kFloatBins];
@@ -1075,6 +1094,7 @@ struct FloatLds {
   u32 rank[kListed];
   u64 scan[kWaves];
   u32 scan_n[kWaves];
+  double power[kPowers];  // 2^(j / kPowers)
   u64 far_mass[kWave];  // every 64th of the prefixes
   u32 far_n[kWave];
   u32 top, nan, index, listed[4];
@@ -1100,11 +1120,11 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   u32 edge_at = threadIdx.x < head ? threadIdx.x : ~0u;
   if (threadIdx.x >= 64 && threadIdx.x - 64 < V - tail) edge_at = tail + threadIdx.x - 64;
   const float edge = edge_at != ~0u ? row[edge_at] : kNone;
-  auto for_each = [&](auto f) {  // f(four values, the first one's index), each entry once
+  auto for_each = [&](auto load, auto f) {  // f(four values, the first one's index), each entry once
     const float e[4] = {edge, kNone, kNone, kNone};
     f(e, edge_at);
     if (nvec)
-      vectors.for_each([&](u32x4 v, u32 j) {
+      vectors.template for_each<decltype(load)::value>([&](u32x4 v, u32 j) {
         const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
         f(x, head + 4 * j);
       });
@@ -1119,12 +1139,13 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     L.index = ~0u;
   }
   if (threadIdx.x < 4) L.listed[threadIdx.x] = 0;
+  if (threadIdx.x < kPowers) L.power[threadIdx.x] = 2.0 * pow2((double)threadIdx.x / kPowers - 1.0);
   lds_barrier();
   // 1. the largest value
   {
     float m = kNone;
     bool nan = false;
-    for_each([&](const float (&v)[4], u32) {
+    for_each(std::true_type(), [&](const float (&v)[4], u32) {
       m = __builtin_fmaxf(m, __builtin_fmaxf(__builtin_fmaxf(v[0], v[1]), __builtin_fmaxf(v[2], v[3])));
       nan |= __builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3]);
     });
@@ -1143,21 +1164,7 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     }
     return;
   }
-  if (s.t == 0.f) {
-    u32 at = ~0u;
-    for_each([&](const float (&v)[4], u32 i) {
-#pragma unroll
-      for (u32 k = 0; k < 4; ++k) at = v[k] == top && i + k < at ? i + k : at;
-    });
-    at = wave_min(at);
-    if (lane_id() == 0) atomicMin(&L.index, at);
-    lds_barrier();
-    if (threadIdx.x == 0) {
-      a.tokens[r] = L.index;
-      a.logprobs[r] = 0.f;
-    }
-    return;
-  }
+  const bool greedy = s.t == 0.f;  // the first of the entries equal to the largest
   u32 lg = 0;
   while ((1ull << lg) < a.V) ++lg;
   const int F = 62 - (int)lg < 50 ? 62 - (int)lg : 50;
@@ -1165,37 +1172,61 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   w.top = top;
   w.c = 1.4426950408889634074 / (double)s.t;
   w.scale = (double)(1ull << F);
-  const float reach_f = (float)F * 0.69314718f * s.t, bins = (float)(kFloatBins - 1) / reach_f;
+  const float reach_f = __builtin_fminf((float)F * 0.69314718f * s.t, 3.4e38f);  // of what is present
+  const float bins = greedy ? 0.f : (float)(kFloatBins - 1) / reach_f;
   // an entry's bin; kFloatBins: absent.  With every setting that makes reach 0, inf or NaN
   // (t at the type's ends), equal entries still share bin 0.
-  auto bin_of = [&](float v) -> u32 {
+  auto bin_of = [&](float v, float top) -> u32 {
     const float d = v == top ? 0.f : top - v;
     return d <= reach_f ? (u32)__builtin_fminf(d * bins, (float)(kFloatBins - 1)) : kFloatBins;
   };
-  auto weight_of = [&](float v) { return w.whole(pow2(w.exponent(v), F)); };
-  // 2. the histogram: four weights at a time, for the 64-bit instructions' latency
-  {
+  // An entry's weight times 2^F: y = n + j / 256 + f, 2^(j / 256) from the table and 2^f by
+  // its series to the power 4 (|f ln 2| < 2^-9.5: the next term is below 2^-54).  Half the
+  // 64-bit instructions of pow2, which take twice the time of 32-bit ones and bound the
+  // histogram (65536 entries a CU: 25 us with pow2, 11 us with no weights at all).
+  const double units = greedy ? 0.0 : w.c * kPowers;
+  auto weight_of = [&](float v) -> double {
+    const double y = v == top ? 0.0 : ((double)v - (double)top) * units;
+    const double t = y + scalar(0x1.8p52);  // the nearest integer in the low bits
+    const int i = (int)(u32)__builtin_bit_cast(u64, t);
+    const double x = y - (t - scalar(0x1.8p52)), T = L.power[(u32)i % kPowers];
+    constexpr double k = 0.69314718055994530942 / kPowers;
+    double e = __builtin_fma(x, scalar(k * k * k * k / 24), scalar(k * k * k / 6));
+    e = __builtin_fma(x, e, scalar(k * k / 2));
+    e = __builtin_fma(x, e, scalar(k));
+    const u64 bits = __builtin_bit_cast(u64, __builtin_fma(T, x * e, T));
+    return __builtin_bit_cast(double, bits + ((u64)(u32)((i >> 8) + F) << 52));
+  };
+  static_assert(kPowers == 256, "i >> 8");
+  // 2. the histogram: several weights at a time, for the 64-bit instructions' latency
+  if (!greedy) {
+    constexpr int kTogether = NV == 16 ? 2 : 4;
+    if (NV) vectors.forget();
     const bool counts = s.k != 0;
     const double least = (double)s.m * w.scale;
     u64 minp = 0;
-    for_each([&](const float (&v)[4], u32) {
-      u32 b[4];
-      u64 q[4];
-      bool kept[4];
+    for_each(std::bool_constant<NV == 0>(), [&](const float (&v)[4], u32) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        b[k] = bin_of(v[k]);
-        const double p = pow2(w.exponent(v[k]), F);
-        q[k] = w.whole(p);
-        kept[k] = p >= least;
-      }
+      for (int at = 0; at < 4; at += kTogether) {
+        u32 b[kTogether];
+        u64 q[kTogether];
+        bool kept[kTogether];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (b[k] < kFloatBins) {
-          atomicAdd(&L.mass[b[k]], q[k]);
-          if (counts) atomicAdd(&L.n[b[k]], 1u);
-          if (kept[k]) minp += q[k];
+        for (int k = 0; k < kTogether; ++k) {
+          b[k] = bin_of(v[at + k], top);
+          const double p = weight_of(v[at + k]);
+          q[k] = w.whole(p);
+          kept[k] = p >= least;
         }
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k)
+          if (b[k] < kFloatBins) {
+            atomicAdd(&L.mass[b[k]], q[k]);
+            if (counts) atomicAdd(&L.n[b[k]], 1u);
+            if (kept[k]) minp += q[k];
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     });
     if (s.m > 0.f) {
       minp = wave_sum(minp);
@@ -1203,8 +1234,8 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     }
   }
   lds_barrier();
-  u64 km;  // the mass that is kept
-  {
+  u64 km = 0;  // the mass that is kept
+  if (!greedy) {
     constexpr u32 kEach = kFloatBins / kThreads;
     u64 m[kEach], sm = 0;
     u32 n[kEach], sn = 0;
@@ -1229,11 +1260,13 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     km = L.far_mass[kWave - 1];
   }
   // 3. the questions
-  const u64 minp = L.minp, kn = L.far_n[kWave - 1];
-  for (int step = 0; step < 4; ++step) {
-    bool by_mass = true;
+  const u64 minp = L.minp, kn = greedy ? 0 : L.far_n[kWave - 1];
+  for (int step = greedy ? 3 : 0; step < 4; ++step) {
+    bool by_mass = !greedy;
     u64 Q;
-    if (step == 0) {
+    if (greedy) {
+      Q = 1;
+    } else if (step == 0) {
       if (!s.k || s.k >= kn) continue;
       by_mass = false;
       Q = s.k;
@@ -1248,23 +1281,30 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
       Q = (u64)((double)s.u * (double)km) + 1;
       if (Q > km) Q = km;
     }
-    // the bin, by every wavefront: first 64 sixty-fourths of the bins, then one of them
     static_assert(kFloatBins == kWave * kWave, "two steps of 64");
     const u32 lane = lane_id();
-    u64 reach = __builtin_amdgcn_ballot_w64(by_mass ? L.far_mass[lane] >= Q : L.far_n[lane] >= Q);
-    u32 b = reach ? (u32)__builtin_ctzll(reach) * kWave : kFloatBins - kWave;
-    reach = __builtin_amdgcn_ballot_w64(lane == kWave - 1 || (by_mass ? L.mass[b + lane] >= Q : L.n[b + lane] >= Q));
-    b += (u32)__builtin_ctzll(reach);
-    const u64 m0 = b ? L.mass[b - 1] : 0, n0 = b ? L.n[b - 1] : 0;
+    u32 b = 0;
+    u64 m0 = 0, n0 = 0;
+    if (!greedy) {  // the bin, by every wavefront: first 64 sixty-fourths of the bins, then one of them
+      u64 reach = __builtin_amdgcn_ballot_w64(by_mass ? L.far_mass[lane] >= Q : L.far_n[lane] >= Q);
+      b = reach ? (u32)__builtin_ctzll(reach) * kWave : kFloatBins - kWave;
+      reach = __builtin_amdgcn_ballot_w64(lane == kWave - 1 ||
+                                          (by_mass ? L.mass[b + lane] >= Q : L.n[b + lane] >= Q));
+      b += (u32)__builtin_ctzll(reach);
+      m0 = b ? L.mass[b - 1] : 0;
+      n0 = b ? L.n[b - 1] : 0;
+    }
+    float here = top;  // another for the compiler, which would keep every entry's bin over the loop
+    asm volatile("" : "+v"(here));
     // its entries: near its middle (more than the bin where rounding may tell), then in it
-    const float middle = top - ((float)b + 0.5f) / bins;
-    const float near = 0.51f / bins + (__builtin_fabsf(top) + reach_f) * 0x1p-21f;
-    if constexpr (NV == 0)
-      if (nvec) vectors.load();
-    for_each([&](const float (&v)[4], u32 i) {
+    const float middle = greedy ? top : top - ((float)b + 0.5f) / bins;
+    const float near = greedy ? 0.f : 0.51f / bins + (__builtin_fabsf(top) + reach_f) * 0x1p-21f;
+    vectors.begin();
+    if (NV == 0 && nvec) vectors.load();
+    for_each(std::bool_constant<NV == 0>(), [&](const float (&v)[4], u32 i) {
 #pragma unroll
       for (u32 k = 0; k < 4; ++k)
-        if (!(__builtin_fabsf(v[k] - middle) > near) && bin_of(v[k]) == b) {
+        if (!(__builtin_fabsf(v[k] - middle) > near) && bin_of(v[k], here) == b) {
           const u32 at = atomicAdd(&L.listed[step], 1u);
           if (at < kListed) L.key[at] = make_key(__float_as_uint(v[k]), i + k);
         }
@@ -1276,7 +1316,7 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
       return;
     }
     if (threadIdx.x < n) {
-      L.weight[threadIdx.x] = weight_of(value_of_key(L.key[threadIdx.x]));
+      L.weight[threadIdx.x] = w.whole(weight_of(value_of_key(L.key[threadIdx.x])));
       L.before[threadIdx.x] = 0;
       L.rank[threadIdx.x] = 0;
     }
@@ -1317,7 +1357,9 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     } else if (threadIdx.x == 0) {
       const u64 key = L.ans_key;
       a.tokens[r] = (int64_t)key_index(key);
-      a.logprobs[r] = (float)(w.exponent(value_of_key(key)) * 0.69314718055994530942 - log((double)km / w.scale));
+      a.logprobs[r] = greedy ? 0.f
+                             : (float)(w.exponent(value_of_key(key)) * 0.69314718055994530942 -
+                                       log((double)km / w.scale));
     }
   }
 }
@@ -1363,6 +1405,10 @@ static void launch_floats(const TokenArgs& a, hipStream_t s) {
   const u64 vectors = (a.V + 3) / 4;
   if (vectors <= 4 * kThreads)
     sample_floats_kernel<4><<<B, kThreads, 0, s>>>(a);
+  else if (vectors <= 8 * kThreads)
+    sample_floats_kernel<8><<<B, kThreads, 0, s>>>(a);
+  else if (vectors <= 16 * kThreads)
+    sample_floats_kernel<16><<<B, kThreads, 0, s>>>(a);
   else
     sample_floats_kernel<0><<<B, kThreads, 0, s>>>(a);
   if (a.V > kListed) sample_left_kernel<float><<<B < kLeftBlocks ? B : kLeftBlocks, kThreads, 0, s>>>(a);
@@ -1376,6 +1422,8 @@ static void launch_codes(const TokenArgs& a, hipStream_t s) {
     sample_codes_kernel<T, 4><<<B, kThreads, 0, s>>>(a);
   else if (vectors <= 8 * kThreads)
     sample_codes_kernel<T, 8><<<B, kThreads, 0, s>>>(a);
+  else if (vectors <= 16 * kThreads)
+    sample_codes_kernel<T, 16><<<B, kThreads, 0, s>>>(a);
   else
     sample_codes_kernel<T, 0><<<B, kThreads, 0, s>>>(a);
   if (a.V > 0xFFFFu) sample_left_kernel<T><<<B < kLeftBlocks ? B : kLeftBlocks, kThreads, 0, s>>>(a);
