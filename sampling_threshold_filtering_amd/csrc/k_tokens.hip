@@ -1085,7 +1085,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
 // than kListed entries is left to the launch that splits bins.
 constexpr u32 kFloatBins = 4096;
 constexpr u32 kListed = 1024;
-constexpr u32 kPowers = 256;
+constexpr u32 kPowers = 1024;
 
 struct FloatLds {
   u64 mass[kFloatBins];
@@ -1094,7 +1094,7 @@ struct FloatLds {
   u32 rank[kListed];
   u64 scan[kWaves];
   u32 scan_n[kWaves];
-  double power[kPowers];  // 2^(j / kPowers)
+  double power[kPowers];  // 2^(F + j / kPowers)
   u64 far_mass[kWave];  // every 64th of the prefixes
   u32 far_n[kWave];
   u32 top, nan, index, listed[4];
@@ -1107,6 +1107,9 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   const float* row = reinterpret_cast<const float*>(a.x) + r * a.ld;
   const u32 V = (u32)a.V;
   const RowSettings s = row_settings(a, r);
+  u32 lg = 0;
+  while ((1ull << lg) < a.V) ++lg;
+  const int F = 62 - (int)lg < 50 ? 62 - (int)lg : 50;
   constexpr float kNone = -__builtin_huge_valf();
   u32 head = (u32)((16 - ((uintptr_t)row & 15)) & 15) / 4;
   if (head > V) head = V;
@@ -1139,7 +1142,8 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     L.index = ~0u;
   }
   if (threadIdx.x < 4) L.listed[threadIdx.x] = 0;
-  if (threadIdx.x < kPowers) L.power[threadIdx.x] = 2.0 * pow2((double)threadIdx.x / kPowers - 1.0);
+  static_assert(kPowers == (u32)kThreads, "a power each");
+  L.power[threadIdx.x] = pow2((double)threadIdx.x / kPowers - 1.0, F + 1);
   lds_barrier();
   // 1. the largest value
   {
@@ -1164,45 +1168,47 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     }
     return;
   }
+  if (top == -kNone) {  // entries of +inf share everything
+    if (threadIdx.x == 0) a.tokens[r] = kByValue;
+    return;
+  }
   const bool greedy = s.t == 0.f;  // the first of the entries equal to the largest
-  u32 lg = 0;
-  while ((1ull << lg) < a.V) ++lg;
-  const int F = 62 - (int)lg < 50 ? 62 - (int)lg : 50;
   Weigher w;
   w.top = top;
   w.c = 1.4426950408889634074 / (double)s.t;
   w.scale = (double)(1ull << F);
   const float reach_f = __builtin_fminf((float)F * 0.69314718f * s.t, 3.4e38f);  // of what is present
   const float bins = greedy ? 0.f : (float)(kFloatBins - 1) / reach_f;
-  // an entry's bin; kFloatBins: absent.  With every setting that makes reach 0, inf or NaN
-  // (t at the type's ends), equal entries still share bin 0.
+  // An entry's bin; absent from kFloatBins on.  The conversion saturates and makes 0 of NaN
+  // (the largest value's 0 times infinity, where the temperature is next to 0).
   auto bin_of = [&](float v, float top) -> u32 {
-    const float d = v == top ? 0.f : top - v;
-    return d <= reach_f ? (u32)__builtin_fminf(d * bins, (float)(kFloatBins - 1)) : kFloatBins;
+    u32 b;
+    asm("v_cvt_u32_f32 %0, %1" : "=v"(b) : "v"((top - v) * bins));
+    return b;
   };
-  // An entry's weight times 2^F: y = n + j / 256 + f, 2^(j / 256) from the table and 2^f by
-  // its series to the power 4 (|f ln 2| < 2^-9.5: the next term is below 2^-54).  Half the
-  // 64-bit instructions of pow2, which take twice the time of 32-bit ones and bound the
-  // histogram (65536 entries a CU: 25 us with pow2, 11 us with no weights at all).
+  // An entry's weight times 2^F: y = n + j / 1024 + f, 2^(j / 1024) from the table and 2^f by
+  // its series to the power 3 (|f ln 2| < 2^-11.5: the next term is below 2^-50).  The
+  // histogram is bound by the vector instructions, of which 64-bit ones take twice the time
+  // (65536 entries a CU: 25 us with pow2, 11 us with no weights at all).
   const double units = greedy ? 0.0 : w.c * kPowers;
   auto weight_of = [&](float v) -> double {
-    const double y = v == top ? 0.0 : ((double)v - (double)top) * units;
+    const double y = ((double)v - (double)top) * units;
     const double t = y + scalar(0x1.8p52);  // the nearest integer in the low bits
-    const int i = (int)(u32)__builtin_bit_cast(u64, t);
-    const double x = y - (t - scalar(0x1.8p52)), T = L.power[(u32)i % kPowers];
+    const u32 i = (u32)__builtin_bit_cast(u64, t);
+    const double x = y - (t - scalar(0x1.8p52)), T = L.power[i % kPowers];
     constexpr double k = 0.69314718055994530942 / kPowers;
-    double e = __builtin_fma(x, scalar(k * k * k * k / 24), scalar(k * k * k / 6));
-    e = __builtin_fma(x, e, scalar(k * k / 2));
-    e = __builtin_fma(x, e, scalar(k));
+    const double e = __builtin_fma(x, __builtin_fma(x, scalar(k * k * k / 6), scalar(k * k / 2)), scalar(k));
     const u64 bits = __builtin_bit_cast(u64, __builtin_fma(T, x * e, T));
-    return __builtin_bit_cast(double, bits + ((u64)(u32)((i >> 8) + F) << 52));
+    const u32 high = (u32)(bits >> 32) + ((i & ~(kPowers - 1)) << 10);  // 2^n
+    return __builtin_bit_cast(double, (u64)high << 32 | (u32)bits);
   };
-  static_assert(kPowers == 256, "i >> 8");
+  static_assert(kPowers == 1024, "n is i >> 10, the exponent begins at bit 20");
   // 2. the histogram: several weights at a time, for the 64-bit instructions' latency
   if (!greedy) {
     constexpr int kTogether = NV == 16 ? 2 : 4;
     if (NV) vectors.forget();
     const bool counts = s.k != 0;
+    const bool has_least = s.m > 0.f;
     const double least = (double)s.m * w.scale;
     u64 minp = 0;
     for_each(std::bool_constant<NV == 0>(), [&](const float (&v)[4], u32) {
@@ -1216,14 +1222,17 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
           b[k] = bin_of(v[at + k], top);
           const double p = weight_of(v[at + k]);
           q[k] = w.whole(p);
-          kept[k] = p >= least;
+          kept[k] = has_least && p >= least;
         }
+        // all of them before the first addition, behind which a table read would queue
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) asm volatile("" : "+v"(q[k]));
 #pragma unroll
         for (int k = 0; k < kTogether; ++k)
           if (b[k] < kFloatBins) {
             atomicAdd(&L.mass[b[k]], q[k]);
             if (counts) atomicAdd(&L.n[b[k]], 1u);
-            if (kept[k]) minp += q[k];
+            if (has_least) minp += kept[k] ? q[k] : 0;
           }
         __builtin_amdgcn_sched_barrier(0);
       }
