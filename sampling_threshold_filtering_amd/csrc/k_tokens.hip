@@ -1385,14 +1385,16 @@ __global__ __launch_bounds__(kThreads) void sample_left_kernel(TokenArgs a) {
   for (u64 r0 = blockIdx.x; r0 < a.B; r0 += (u64)kThreads * gridDim.x) {
     const u64 r = r0 + (u64)threadIdx.x * gridDim.x;
     u64 mine = r < a.B && a.tokens[r] == kByValue ? r : ~0ull;
-    while (__syncthreads_or(mine != ~0ull)) {
+    for (;;) {
       if (threadIdx.x == 0) left = ~0u;
-      __syncthreads();
+      lds_barrier();
       if (mine != ~0ull) atomicMin(&left, threadIdx.x);
-      __syncthreads();
+      lds_barrier();
       const u32 t = left;
+      if (t == ~0u) break;
       if (threadIdx.x == t) mine = ~0ull;
       sample_row_by_value<T>(S, a, r0 + (u64)t * gridDim.x);
+      __syncthreads();
     }
   }
 }
