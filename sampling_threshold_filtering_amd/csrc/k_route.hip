@@ -173,8 +173,7 @@ __device__ __forceinline__ u32 ord_of(float v) {
 // A launch of several blocks leaves each block's counts, sums and live rows here for the
 // finishing launch; one block alone writes the outputs itself.
 struct RouteScratch {
-  u32* ticket;   // finishing blocks that have left their part
-  double* part;  // one per finishing block
+  u64* loss;     // the finishing blocks' parts of the loss, and how many there are
   u32* rows;     // blocks
   u32* counts;   // blocks * E
   float* sums;   // blocks * E
@@ -182,9 +181,8 @@ struct RouteScratch {
 
 __host__ __device__ inline RouteScratch route_scratch(char* s, u32 blocks, u32 E) {
   RouteScratch r;
-  r.ticket = (u32*)s;
-  r.part = (double*)(s + 256);
-  r.rows = (u32*)(s + 256 + 8 * kRouteMaxExperts);
+  r.loss = (u64*)s;
+  r.rows = (u32*)(s + 256);
   r.counts = r.rows + blocks;
   r.sums = (float*)(r.counts + (u64)blocks * E);
   return r;
@@ -378,14 +376,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   }
   if (threadIdx.x == 0) {
     sc.rows[blockIdx.x] = s_rows;
-    if (blockIdx.x == 0) *sc.ticket = 0;
+    if (blockIdx.x == 0) *sc.loss = 0;
   }
 }
 
 // The blocks' counts and sums into the outputs.  A finishing block takes 16 experts, its
 // threads 64 slices of the blocks, so that a thread adds 8 of 512, all loaded at once (one
-// block over all experts, 512 each: 121 us).  The last block to leave its part of the loss
-// adds the parts, in a fixed order.
+// block over all experts, 512 each: 121 us).  The last block to add its part of the loss
+// writes it.
 __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs a) {
   constexpr u32 kSlices = kFinishThreads / kFinishExperts;
   constexpr u32 kEach = kRouteMaxBlocks / kSlices;
@@ -448,20 +446,18 @@ __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs 
   if (!a.loss) return;
 #pragma unroll
   for (u32 d = 1; d < kFinishExperts; d <<= 1) part += __shfl_xor(part, d);
-  if (gridDim.x > 1) {
-    u32 last = 0;
-    if (threadIdx.x == 0) {
-      __hip_atomic_store(&sc.part[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = __hip_atomic_fetch_add(sc.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-    }
-    if (!__builtin_amdgcn_readfirstlane(last)) return;
-    // at most 64 finishing blocks
-    part = threadIdx.x < gridDim.x
-               ? __hip_atomic_load(&sc.part[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
-#pragma unroll
-    for (u32 d = 1; d < (u32)kWave; d <<= 1) part += __shfl_xor(part, d);
-  }
-  if (threadIdx.x == 0) *a.loss = balance_of(part, live, a.E, a.k);
+  if (threadIdx.x) return;
+  // sum_e f_e P_e is at most 1: a block adds its part in units of 2^-48, one to the count of
+  // blocks (at most 64) and, for NaN, one to the count of those, with a single 64-bit
+  // addition, whose order does not matter.  (Parts, then a ticket, then the parts read back
+  // were three trips to memory: 0.7 us more.)
+  const double share = live ? part / ((double)live * (double)a.k * (double)live) : 0.0;
+  const u64 mine = (share == share ? (u64)rint(share * 0x1p48) << 14 : 1ull << 7) + 1;
+  const u64 sum = gridDim.x == 1 ? mine
+                                 : mine + __hip_atomic_fetch_add(sc.loss, mine, __ATOMIC_RELAXED,
+                                                                 __HIP_MEMORY_SCOPE_AGENT);
+  if ((sum & 127) == gridDim.x)
+    *a.loss = sum >> 7 & 127 ? __uint_as_float(0x7FC00000u) : (float)((double)a.E * ((double)(sum >> 14) * 0x1p-48));
 }
 
 template <class T, int G, int C, bool QUAD>
@@ -491,10 +487,20 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       }
     }
   }
+  auto slot = [&](u64 t, u32 j) {  // its expert; not below E: none
+    const int64_t e = a.experts[t * a.k + j];
+    return (u64)e < (u64)a.E ? (u32)e : ~0u;
+  };
   const u64 step = (u64)gridDim.x * kGroups;
   for (u64 t0 = (u64)blockIdx.x * kGroups; t0 < a.T; t0 += step) {
     const u64 t = t0 + grp, tr = t < a.T ? t : a.T - 1;
     const bool in = (!a.mask || a.mask[tr]) && t < a.T;
+    u32 first_e = ~0u;
+    float first_d = 0.f;
+    if (a.d_weights && g < a.k) {
+      first_e = slot(tr, g);
+      first_d = a.d_weights[tr * a.k + g];
+    }
     R row;
     row.load(x + tr * a.ld, a.E, g, in);
     row.weigh(in);
@@ -508,37 +514,40 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
     }
     dot = group_reduce<G>(dot, add_f);
     if (a.d_weights) {
-      // the chosen entries: lane g takes slots g, g + G, ...
-      float wsum = 0.f, wd = 0.f;
+      // the chosen entries: lane g takes slots g, g + G, ...; its first one stays in registers
+      const T* xt = x + tr * a.ld;
+      auto weight = [&](u32 e) { return exp_f(to_f32(xt[e]) - row.top) * inv; };
+      const bool first = row.live && first_e < a.E;
+      const float p0 = first ? weight(first_e) : 0.f;
+      float wsum = p0, wd = p0 * first_d;
       if (row.live)
-        for (u32 j = g; j < a.k; j += G) {
-          const int64_t e = a.experts[t * a.k + j];
-          if (e < 0 || e >= (int64_t)a.E) continue;
-          const float p = exp_f(to_f32(x[t * a.ld + e]) - row.top) * inv;
+        for (u32 j = g + G; j < a.k; j += G) {
+          const u32 e = slot(tr, j);
+          if (e >= a.E) continue;
+          const float p = weight(e);
           wsum += p;
-          wd = __builtin_fmaf(p, a.d_weights[t * a.k + j], wd);
+          wd = __builtin_fmaf(p, a.d_weights[tr * a.k + j], wd);
         }
       wsum = group_reduce<G>(wsum, add_f);
       wd = group_reduce<G>(wd, add_f);
       const float r = a.normalize ? 1.f / wsum : 1.f;
-      const float mean = wd * r;
+      const float mean = wd * r, from = a.normalize ? mean : 0.f;
       if (!a.normalize) dot += mean;
+      if (first) atomicAdd(&d[first_e], p0 * r * (first_d - from));
       if (row.live)
-        for (u32 j = g; j < a.k; j += G) {
-          const int64_t e = a.experts[t * a.k + j];
-          if (e < 0 || e >= (int64_t)a.E) continue;
-          const float p = exp_f(to_f32(x[t * a.ld + e]) - row.top) * inv * r;
-          const float dw = a.d_weights[t * a.k + j];
-          atomicAdd(&d[e], p * (a.normalize ? dw - mean : dw));
+        for (u32 j = g + G; j < a.k; j += G) {
+          const u32 e = slot(tr, j);
+          if (e < a.E) atomicAdd(&d[e], weight(e) * r * (a.d_weights[tr * a.k + j] - from));
         }
       wave_lds_sync();
 #pragma unroll
       for (int i = 0; i < C; ++i) out[i] = __builtin_fmaf(row.e[i], f[i] - dot, d[R::index(i, g)]);
       wave_lds_sync();
+      if (first) d[first_e] = 0.f;
       if (row.live)
-        for (u32 j = g; j < a.k; j += G) {
-          const int64_t e = a.experts[t * a.k + j];
-          if (e >= 0 && e < (int64_t)a.E) d[e] = 0.f;
+        for (u32 j = g + G; j < a.k; j += G) {
+          const u32 e = slot(tr, j);
+          if (e < a.E) d[e] = 0.f;
         }
       wave_lds_sync();
     } else {
@@ -630,7 +639,7 @@ hipError_t route_type(const A& a, int dtype, hipStream_t s) {
 
 size_t route_scratch_bytes(u64 T, u32 E) {
   const u64 b = T < kRouteMaxBlocks ? (T ? T : 1) : kRouteMaxBlocks;
-  return 256 + 8 * (size_t)kRouteMaxExperts + b * (4 + 8 * (size_t)E);
+  return 256 + b * (4 + 8 * (size_t)E);
 }
 
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) { return route_type(a, dtype, s); }
