@@ -326,6 +326,7 @@ int profk_read_ceiling(const float* x, int64_t N, int32_t blocks_per_cu, uint64_
 #define PROFK_FP32 0
 #define PROFK_FP16 1
 #define PROFK_BF16 2
+#define PROFK_ROUTE_MAX_EXPERTS 1024
 
 /*
  * profk_sample_tokens: one token per row of logits[B][V] from a given uniform

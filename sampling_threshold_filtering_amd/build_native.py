@@ -2,13 +2,17 @@
 
 Every translation unit is compiled with hipcc for --offload-arch=gfx950 into
 _build/, then linked into sampling_threshold_filtering_amd/libprofk.so.
+_operators.so, the compiled step of operators.py, is host code over it and
+torch's headers (g++).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import resource
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libprofk.so")
+BINDING = os.path.join(HERE, "_operators.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "k_sample.hip", "k_select.hip", "k_filter.hip", "k_refine.hip", "k_sort.hip", "k_batched.hip", "k_merge.hip", "k_probe.hip",
@@ -62,9 +67,25 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     if verbose:
         print(LIB)
     return LIB
+
+
+def _build_binding() -> None:
+    # found without importing torch, which takes its time and is not needed to compile
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "operators_binding.cpp"), "-o", tmp,
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-L", HERE, "-l:libprofk.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -9,6 +9,10 @@ Formulas, ties, empty rows and limits: include/profk.h.  Every call is enqueued 
 current stream of the logits' device and waits for nothing; outputs and scratch come from
 torch's allocator, so calls may be captured into a graph without a first call.
 route_tokens and balance_loss are differentiable where the logits require a gradient.
+
+The checks of arguments, the outputs and the library's call are one compiled step
+(csrc/operators_binding.cpp): a call takes 3 to 60 us on the GPU, and from Python the same
+steps took 9 to 15 us.  There is no other path when it has not been built.
 """
 from __future__ import annotations
 
@@ -17,10 +21,9 @@ from typing import NamedTuple, Optional
 
 import sampling_threshold_filtering_amd as _profk
 
-FP32, FP16, BF16 = 0, 1, 2
-
 
 class Sampling(ctypes.Structure):
+    """profk_sampling"""
     _fields_ = [
         ("temperature", ctypes.c_float), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float),
         ("reserved", ctypes.c_int32), ("top_k", ctypes.c_int64),
@@ -47,70 +50,41 @@ class Balance(NamedTuple):
     k: int
 
 
-_codes = {}
+_module = None
 
 
-def _logits(x, name="logits"):
-    """(torch, x with unit column stride, dtype code, rows, columns, row stride)"""
+def _native():
+    global _module
+    if _module is None:
+        _profk.load_library()
+        import torch  # noqa: F401  (the compiled step uses its libraries)
+        try:
+            from sampling_threshold_filtering_amd import _operators
+        except ImportError as e:
+            raise ImportError("the operators' binding is missing: build it with "
+                              "`python -m sampling_threshold_filtering_amd.build_native`") from e
+        _module = _operators
+    return _module
+
+
+def _check_device(torch, x):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        raise ValueError("logits must be a 2-D float32, float16 or bfloat16 device tensor")
+
+
+def _call(x, fn, *args):
+    """fn(*args, the current stream of x's device); raises ProfkError for a status"""
     import torch
-    if not _codes:
-        _codes.update({torch.float32: FP32, torch.float16: FP16, torch.bfloat16: BF16})
-    code = _codes.get(x.dtype)
-    if code is None or x.dim() != 2 or not x.is_cuda:
-        raise ValueError(f"{name} must be a 2-D float32, float16 or bfloat16 device tensor")
-    n, w = x.shape
-    if w < 1:
-        raise ValueError(f"{name} must have at least one column")
-    if x.stride(1) != 1 and w > 1:
-        x = x.contiguous()
-    ld = x.stride(0)
-    if n <= 1 or w == 1:
-        if w == 1 and n > 1 and ld < 1:
-            x = x.contiguous()
-            ld = 1
-        if ld < w:
-            ld = w
-    elif ld < w:  # broadcast or overlapping rows
-        x = x.contiguous()
-        ld = w
-    return torch, x, code, n, w, ld
-
-
-def _call(torch, x, fn, *args):
-    """fn(*args, the current stream of x's device)"""
+    _check_device(torch, x)
     di = x.get_device()
     if di == _profk._current_device(torch):
-        rc = fn(*args, _profk._raw_stream(torch, di))
+        r = fn(*args, _profk._raw_stream(torch, di))
     else:
         with torch.cuda.device(di):
-            rc = fn(*args, _profk._raw_stream(torch, di))
-    if rc:
-        _profk._check(rc)
-
-
-def _lib():
-    return _profk._lib if _profk._lib is not None else _profk.load_library()
-
-
-def _scratch(torch, need: int, device):
-    """(scratch tensor or None, its address, its bytes) of a scratch query's answer"""
-    if need < 0:
-        _profk._check(need)
-    if need == 0:
-        return None, None, 0
-    s = torch.empty(need, dtype=torch.uint8, device=device)
-    return s, s.data_ptr(), need
-
-
-def _setting(v, name, n, dtype, device):
-    """A sampling setting: (plain value, address of per-row values or None, the tensor held)"""
-    if hasattr(v, "data_ptr"):
-        if v.dim() != 1 or v.shape[0] != n or v.device != device or (v.dtype.is_floating_point != dtype.is_floating_point):
-            raise ValueError(f"{name} must be a number or a 1-D tensor of {n} values on {device}")
-        if v.dtype != dtype or v.stride(0) != 1:
-            v = v.to(dtype).contiguous()
-        return 0, v.data_ptr(), v
-    return v, None, None
+            r = fn(*args, _profk._raw_stream(torch, di))
+    if r.__class__ is int:
+        _profk._check(r)
+    return r
 
 
 def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None):
@@ -123,69 +97,11 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out
     ties to the lower index); its logprob is of that renormalised distribution.  A row with
     no entry above -inf, or with a NaN, gives token -1.  `out=(tokens, logprobs)` reuses
     caller buffers."""
-    torch, x, code, B, V, ld = _logits(logits)
-    dev = x.device
-    if u.dim() != 1 or u.shape[0] != B or u.dtype != torch.float32 or u.device != dev:
-        raise ValueError(f"u must be {B} float32 values on {dev}")
-    if B > 1 and u.stride(0) != 1:
-        u = u.contiguous()
-    t, tp, t_hold = _setting(temperature, "temperature", B, torch.float32, dev)
-    k, kp, k_hold = _setting(top_k, "top_k", B, torch.int64, dev)
-    p, pp, p_hold = _setting(top_p, "top_p", B, torch.float32, dev)
-    m, mp, m_hold = _setting(min_p, "min_p", B, torch.float32, dev)
-    if not (t >= 0 and k >= 0 and 0 <= p <= 1 and 0 <= m <= 1):
-        raise ValueError("need temperature >= 0, top_k >= 0, 0 <= top_p <= 1 and 0 <= min_p <= 1")
-    if out is None:
-        tokens = torch.empty(B, dtype=torch.int64, device=dev)
-        logprobs = torch.empty(B, dtype=torch.float32, device=dev)
-    else:
-        tokens, logprobs = out
-        if (tuple(tokens.shape) != (B,) or tuple(logprobs.shape) != (B,) or tokens.dtype != torch.int64
-                or logprobs.dtype != torch.float32 or tokens.device != dev or logprobs.device != dev
-                or not tokens.is_contiguous() or not logprobs.is_contiguous()):
-            raise ValueError(f"out must be contiguous int64 / float32 tensors of shape ({B},) on {dev}")
-    how = Sampling(t, p, m, 0, min(int(k), 1 << 62), tp, kp, pp, mp)
-    lib = _lib()
-    hold, at, size = _scratch(torch, lib.profk_sample_tokens_scratch(B, V), dev)
-    _call(torch, x, lib.profk_sample_tokens, x.data_ptr(), code, B, V, ld, u.data_ptr(), ctypes.byref(how),
-          tokens.data_ptr(), logprobs.data_ptr(), at, size)
-    return tokens, logprobs
-
-
-def _mask(torch, mask, T, device):
-    """The address of the mask's bytes (or None), and the tensor held"""
-    if mask is None:
-        return None, None
-    if mask.dim() != 1 or mask.shape[0] != T or mask.dtype != torch.bool or mask.device != device:
-        raise ValueError(f"mask must be {T} bool values on {device}")
-    if T > 1 and mask.stride(0) != 1:
-        mask = mask.contiguous()
-    return mask.data_ptr(), mask
-
-
-def _per_slot(t, name, shape, dtype, device):
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}")
-    return t if t.is_contiguous() else t.contiguous()
+    return _call(logits, (_module or _native()).sample, logits, u, temperature, top_k, top_p, min_p, out)
 
 
 def _route(logits, k, normalize, mask, balance):
-    torch, x, code, T, E, ld = _logits(logits)
-    if not 1 <= k <= E:
-        raise ValueError(f"k must be in 1..{E}")
-    dev = x.device
-    mp, m_hold = _mask(torch, mask, T, dev)
-    lib = _lib()
-    hold, at, size = _scratch(torch, lib.profk_route_scratch(T, E), dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    experts = torch.empty((T, k), dtype=torch.int64, device=dev)
-    counts = torch.empty(E, dtype=torch.int64, device=dev)
-    rows = torch.empty((), dtype=torch.int64, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev) if balance else None
-    _call(torch, x, lib.profk_route_tokens, x.data_ptr(), code, T, E, ld, mp, k, 1 if normalize else 0,
-          weights.data_ptr(), experts.data_ptr(), counts.data_ptr(), rows.data_ptr(),
-          loss.data_ptr() if balance else None, at, size)
-    return Routing(weights, experts, counts, rows, loss)
+    return Routing._make(_call(logits, (_module or _native()).route, logits, k, normalize, mask, balance))
 
 
 def route_tokens(logits, k: int, normalize: bool = True, mask=None, balance: bool = False) -> Routing:
@@ -203,59 +119,22 @@ def route_tokens(logits, k: int, normalize: bool = True, mask=None, balance: boo
     return _route(logits, k, normalize, mask, balance)
 
 
-def _loss_scale(torch, d_loss, device):
-    """A loss gradient given as a number or a one-element float32 tensor: (address, factor)"""
-    if hasattr(d_loss, "data_ptr"):
-        if d_loss.numel() != 1 or d_loss.dtype != torch.float32 or d_loss.device != device:
-            raise ValueError(f"d_loss must be a number or one float32 value on {device}")
-        return d_loss.data_ptr(), 1.0
-    return None, float(d_loss)
-
-
 def route_tokens_grad(logits, routing: Routing, d_weights=None, d_loss=None, normalize: bool = True, mask=None):
     """The gradient with respect to the logits (their type, contiguous) of a scalar whose
     gradients are d_weights [T, k] float32 and d_loss (a number or one float32 value) with
     respect to route_tokens' weights and loss; either may be None.  The other arguments are
     those of the call that gave `routing`."""
-    torch, x, code, T, E, ld = _logits(logits)
-    dev = x.device
-    k = routing.experts.shape[1] if routing.experts.dim() == 2 else 0
-    mp, m_hold = _mask(torch, mask, T, dev)
     if d_weights is None and d_loss is None:
-        return torch.zeros((T, E), dtype=x.dtype, device=dev)
-    dwp = ep = cp = rp = dlp = None
-    scale = 0.0
-    if d_weights is not None:
-        d_weights = _per_slot(d_weights, "d_weights", (T, k), torch.float32, dev)
-        experts = _per_slot(routing.experts, "experts", (T, k), torch.int64, dev)
-        dwp, ep = d_weights.data_ptr(), experts.data_ptr()
-    if d_loss is not None:
-        counts = _per_slot(routing.counts, "counts", (E,), torch.int64, dev)
-        rows = _per_slot(routing.rows, "rows", (), torch.int64, dev)
-        cp, rp = counts.data_ptr(), rows.data_ptr()
-        dlp, scale = _loss_scale(torch, d_loss, dev)
-    dx = torch.empty((T, E), dtype=x.dtype, device=dev)
-    _call(torch, x, _lib().profk_route_tokens_grad, x.data_ptr(), code, T, E, ld, mp, k, 1 if normalize else 0, ep,
-          dwp, cp, rp, dlp, scale, dx.data_ptr())
-    return dx
+        import torch
+        _check_device(torch, logits)
+        return torch.zeros(logits.shape, dtype=logits.dtype, device=logits.device)
+    return _call(logits, (_module or _native()).route_grad, logits, routing.experts, routing.counts, routing.rows,
+                 d_weights, d_loss, normalize, mask)
 
 
 def _balance(logits, experts, mask):
-    torch, x, code, T, E, ld = _logits(logits)
-    dev = x.device
-    if experts.dim() != 2 or experts.shape[1] < 1:
-        raise ValueError("experts must be a 2-D int64 tensor with a row per token")
-    k = experts.shape[1]
-    experts = _per_slot(experts, "experts", (T, k), torch.int64, dev)
-    mp, m_hold = _mask(torch, mask, T, dev)
-    lib = _lib()
-    hold, at, size = _scratch(torch, lib.profk_route_scratch(T, E), dev)
-    counts = torch.empty(E, dtype=torch.int64, device=dev)
-    rows = torch.empty((), dtype=torch.int64, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    _call(torch, x, lib.profk_balance_loss, x.data_ptr(), code, T, E, ld, mp, experts.data_ptr(), k,
-          counts.data_ptr(), rows.data_ptr(), loss.data_ptr(), at, size)
-    return Balance(loss, counts, rows, k)
+    loss, counts, rows = _call(logits, (_module or _native()).balance, logits, experts, mask)
+    return Balance(loss, counts, rows, experts.shape[1])
 
 
 def balance_loss(logits, experts, mask=None) -> Balance:
@@ -272,16 +151,8 @@ def balance_loss(logits, experts, mask=None) -> Balance:
 def balance_loss_grad(logits, balance: Balance, d_loss=1.0, mask=None):
     """The gradient with respect to the logits (their type, contiguous) of a scalar whose
     gradient with respect to balance_loss' loss is d_loss (a number or one float32 value)."""
-    torch, x, code, T, E, ld = _logits(logits)
-    dev = x.device
-    mp, m_hold = _mask(torch, mask, T, dev)
-    counts = _per_slot(balance.counts, "counts", (E,), torch.int64, dev)
-    rows = _per_slot(balance.rows, "rows", (), torch.int64, dev)
-    dlp, scale = _loss_scale(torch, d_loss, dev)
-    dx = torch.empty((T, E), dtype=x.dtype, device=dev)
-    _call(torch, x, _lib().profk_balance_loss_grad, x.data_ptr(), code, T, E, ld, mp, balance.k, counts.data_ptr(),
-          rows.data_ptr(), dlp, scale, dx.data_ptr())
-    return dx
+    return _call(logits, (_module or _native()).balance_grad, logits, balance.k, balance.counts, balance.rows, d_loss,
+                 mask)
 
 
 _functions = None
