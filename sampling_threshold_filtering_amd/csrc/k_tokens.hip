@@ -1168,7 +1168,10 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     }
     return;
   }
-  if (top == -kNone) {  // entries of +inf share everything
+  // Entries of +inf share everything.  Short rows, which have no second launch, take the
+  // largest number for it in the differences (one instruction an entry more).
+  constexpr float kMost = 3.40282347e38f;
+  if (NV != 4 && top == -kNone) {
     if (threadIdx.x == 0) a.tokens[r] = kByValue;
     return;
   }
@@ -1190,9 +1193,10 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   // its series to the power 3 (|f ln 2| < 2^-11.5: the next term is below 2^-50).  The
   // histogram is bound by the vector instructions, of which 64-bit ones take twice the time
   // (65536 entries a CU: 25 us with pow2, 11 us with no weights at all).
+  const double top_number = (double)__builtin_fminf(top, kMost);
   const double units = greedy ? 0.0 : w.c * kPowers;
   auto weight_of = [&](float v) -> double {
-    const double y = ((double)v - (double)top) * units;
+    const double y = ((double)(NV == 4 ? __builtin_fminf(v, kMost) : v) - top_number) * units;
     const double t = y + scalar(0x1.8p52);  // the nearest integer in the low bits
     const u32 i = (u32)__builtin_bit_cast(u64, t);
     const double x = y - (t - scalar(0x1.8p52)), T = L.power[i % kPowers];
