@@ -7,15 +7,18 @@
 //   F = the entries of P with w_i >= min_p;  W = mass(F).
 // The token is the first entry of the order whose cumulative mass exceeds u W.  So the
 // whole operator is a few questions of one kind, "where does the running count, or the
-// running mass, of the order first reach Q?", and no row is ever sorted: a histogram over
-// value bins answers a question up to one bin, whose entries are then collected and
-// sorted in LDS (a bin too full for that is split into finer bins by key first).
+// running mass, of the order first reach Q?", and no row is ever sorted: a histogram answers
+// a question up to one bin, whose entries are then looked at.  One workgroup of 1024 threads
+// takes a row, in one of three ways: 16-bit logits by a counter for every value; 32-bit
+// logits by 4096 value bins; rows that overflow either by value bins split as often as it
+// takes (the first part of this file, right for every row).
 //
 // Exactness.  Weights are integers q_i = round(w_i 2^F), with F as large as lets a row's
 // sum fit 63 bits (F = 46 at 2^17 entries), from 64-bit floats.  Integer sums do not
-// depend on their order, so LDS atomics and any split of the row give the same bits, and
-// the rounding of a weight (2^-(F+1) of the largest) is far below what a 24-bit u can
-// tell apart.  An entry below 2^-F of the largest counts as absent.
+// depend on their order, so LDS atomics give the same bits on every run, and the rounding of
+// a weight (2^-(F+1) of the largest) is far below what a 24-bit u can tell apart.  (Counted
+// values are summed in 64-bit floats, sixteen at a time, and rounded to such integers.)  An
+// entry below about 2^-F of the largest counts as absent.
 #include <type_traits>
 
 #include "block_select.h"
@@ -530,13 +533,15 @@ __device__ __forceinline__ void sample_row_by_value(TokLds& L, const TokenArgs& 
 // A row of such logits has few different values, so it is enough to count them: 65536
 // counters of 16 bits fill 128 KB of LDS, an entry costs one LDS addition and no
 // exponential, and the weights are worked out once per value that occurs, not once per
-// entry.  (512 rows of 131072 by value bins, two passes with an exponential and two 64-bit
-// additions per entry: 356 us.)  Codes go down with the value: code(h) = h ^ 0x7FFF for
+// entry.  512 rows of 131072: 59 us, 2.3 TB/s (by value bins, two passes with an exponential
+// and two additions per entry: 356 us).  Of a row's 29 us the counting takes 14, bound by the
+// LDS additions (14 cycles for a wavefront's 64, at random banks), the weights 5, the
+// questions 2, the chosen value's entries 3.  Codes go down with the value: code(h) = h ^ 0x7FFF for
 // h >= 0, else h, so -0 comes right after +0; a positive value's counter is the low half of
 // word code, a negative one's the high half of word code - 0x8000.  A counter that
 // overflows makes the counters' sum differ from the number of entries counted, since each
-// carry takes 65536 or 65535 from it; such a row (it holds 65536 equal entries) is left to
-// a second launch, by value bins.
+// carry takes 65536 or 65535 from it; such a row (it holds 65536 equal entries) goes by
+// value bins, as a last part of the same kernel (a second launch for it took 4 us).
 //
 // Sixteen neighbouring codes (a cell) lie within one binade, so their weights are a geometric
 // series: two exponentials give all of them, and equal largest entries weigh exactly 2^F.  Cells are summed in 64-bit
@@ -562,7 +567,6 @@ struct CodeLds {
   u32 code, j;
 };
 
-constexpr int64_t kByValue = -2;  // a row's token until the second launch
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef short i16x2 __attribute__((ext_vector_type(2)));
@@ -862,7 +866,7 @@ __device__ __forceinline__ void answer_codes(CodeLds& L, const TokenArgs& a, u64
 }
 
 template <class T, int NV>
-__device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& a, u64 r) {
+__device__ __forceinline__ bool sample_row_by_code(CodeLds& L, const TokenArgs& a, u64 r) {
   constexpr u32 kInf = CodeOf<T>::inf;
   constexpr u32 kLowest = 0x8000u | (kInf - 1);  // the lowest number's code
   constexpr u32 kFill = (0x8000u | kInf) * 0x10001u;  // two entries of -inf
@@ -939,7 +943,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
       a.tokens[r] = -1;
       a.logprobs[r] = nan ? __uint_as_float(0x7FC00000u) : -__builtin_huge_valf();
     }
-    return;
+    return true;
   }
   if constexpr (NV == 0) {  // the last pass's first vectors, on their way meanwhile
     if (nvec) vectors.load();
@@ -988,7 +992,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
     }
     lds_barrier();
     // A counter may have overflowed, or entries been counted that are absent.
-    if (NV != 4 && V > 0xFFFFu && L.n[kUnits - 1] != L.counted) {
+    if (NV != 4 && __builtin_expect(V > 0xFFFFu && L.n[kUnits - 1] != L.counted, 0)) {
       u32 n = 0;
       for (u32 i = threadIdx.x; i < kCodeWords / 4; i += kThreads) {
         const uint4 c = reinterpret_cast<const uint4*>(L.cnt)[i];
@@ -1006,8 +1010,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
       const bool lost = total != L.counted;
       lds_barrier();
       if (lost) {
-        if (threadIdx.x == 0) a.tokens[r] = kByValue;
-        return;
+        return false;
       }
     }
     if (threadIdx.x < kWave) answer_codes<T>(L, a, r, s, w, top, last);
@@ -1055,7 +1058,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
       for (u32 i = 0; i < n; ++i) rank += L.match[i] < mine;
       if (rank == j - 1) a.tokens[r] = mine;
     }
-    return;
+    return true;
   }
   // many of them: counts per stretch of the row, then one stretch
   const u32 per = (V + kThreads - 1) / kThreads;
@@ -1071,6 +1074,7 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
         break;
       }
   }
+  return true;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1081,8 +1085,11 @@ __device__ __forceinline__ void sample_row_by_code(CodeLds& L, const TokenArgs& 
 // top-k asks for it), and a question is answered to one bin by the bins' prefix sums and
 // inside it by ranks: each of the bin's entries adds up the weights of those before it.
 // Bins are cut from the 32-bit difference to the largest value, which rounds monotonously.
-// Rows of up to 16384 entries stay in registers between the passes.  A bin of more
-// than kListed entries is left to the launch that splits bins.
+// Rows of up to 65536 entries stay in registers between the passes.  A row with a bin of
+// more than kListed entries, or with +inf, goes by the passes above that split bins.
+// 256 rows of 65536: 42 us a call, 1.6 TB/s (all passes over memory, each entry's weight in
+// 26 vector instructions of 64 bits and its mass and number in two additions: 82 us); of a
+// workgroup's 38 us the first pass takes 8, the histogram 15, a question 4 to 5.
 constexpr u32 kFloatBins = 4096;
 constexpr u32 kListed = 1024;
 constexpr u32 kPowers = 1024;
@@ -1103,7 +1110,7 @@ struct FloatLds {
 };
 
 template <int NV>
-__device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArgs& a, u64 r) {
+__device__ __forceinline__ bool sample_row_of_floats(FloatLds& L, const TokenArgs& a, u64 r) {
   const float* row = reinterpret_cast<const float*>(a.x) + r * a.ld;
   const u32 V = (u32)a.V;
   const RowSettings s = row_settings(a, r);
@@ -1166,15 +1173,9 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
       a.tokens[r] = -1;
       a.logprobs[r] = L.nan ? __uint_as_float(0x7FC00000u) : kNone;
     }
-    return;
+    return true;
   }
-  // Entries of +inf share everything.  Short rows, which have no second launch, take the
-  // largest number for it in the differences (one instruction an entry more).
-  constexpr float kMost = 3.40282347e38f;
-  if (NV != 4 && top == -kNone) {
-    if (threadIdx.x == 0) a.tokens[r] = kByValue;
-    return;
-  }
+  if (__builtin_expect(top == -kNone, 0)) return false;  // entries of +inf share everything
   const bool greedy = s.t == 0.f;  // the first of the entries equal to the largest
   Weigher w;
   w.top = top;
@@ -1193,10 +1194,9 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
   // its series to the power 3 (|f ln 2| < 2^-11.5: the next term is below 2^-50).  The
   // histogram is bound by the vector instructions, of which 64-bit ones take twice the time
   // (65536 entries a CU: 25 us with pow2, 11 us with no weights at all).
-  const double top_number = (double)__builtin_fminf(top, kMost);
   const double units = greedy ? 0.0 : w.c * kPowers;
   auto weight_of = [&](float v) -> double {
-    const double y = ((double)(NV == 4 ? __builtin_fminf(v, kMost) : v) - top_number) * units;
+    const double y = ((double)v - (double)top) * units;
     const double t = y + scalar(0x1.8p52);  // the nearest integer in the low bits
     const u32 i = (u32)__builtin_bit_cast(u64, t);
     const double x = y - (t - scalar(0x1.8p52)), T = L.power[i % kPowers];
@@ -1325,8 +1325,7 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
     lds_barrier();
     const u32 n = L.listed[step];
     if (n > kListed) {
-      if (threadIdx.x == 0) a.tokens[r] = kByValue;
-      return;
+      return false;
     }
     if (threadIdx.x < n) {
       L.weight[threadIdx.x] = w.whole(weight_of(value_of_key(L.key[threadIdx.x])));
@@ -1375,44 +1374,33 @@ __device__ __forceinline__ void sample_row_of_floats(FloatLds& L, const TokenArg
                                        log((double)km / w.scale));
     }
   }
+  return true;
 }
 
 }  // namespace
 
-// The rows whose counters or lists overflowed: a block looks at rows b, b + blocks, ..., a thread
-// each.
-constexpr u32 kLeftBlocks = 64;
-template <class T>
-__global__ __launch_bounds__(kThreads) void sample_left_kernel(TokenArgs a) {
-  __shared__ TokLds S;
-  __shared__ u32 left;
-  for (u64 r0 = blockIdx.x; r0 < a.B; r0 += (u64)kThreads * gridDim.x) {
-    const u64 r = r0 + (u64)threadIdx.x * gridDim.x;
-    u64 mine = r < a.B && a.tokens[r] == kByValue ? r : ~0ull;
-    for (;;) {
-      if (threadIdx.x == 0) left = ~0u;
-      lds_barrier();
-      if (mine != ~0ull) atomicMin(&left, threadIdx.x);
-      lds_barrier();
-      const u32 t = left;
-      if (t == ~0u) break;
-      if (threadIdx.x == t) mine = ~0ull;
-      sample_row_by_value<T>(S, a, r0 + (u64)t * gridDim.x);
-      __syncthreads();
-    }
-  }
-}
-
 template <class T, int NV>
 __global__ __launch_bounds__(kThreads) void sample_codes_kernel(TokenArgs a) {
-  __shared__ CodeLds S;
-  sample_row_by_code<T, NV>(S, a, blockIdx.x);
+  __shared__ union {
+    CodeLds code;
+    TokLds value;
+  } S;
+  if (__builtin_expect(sample_row_by_code<T, NV>(S.code, a, blockIdx.x), 1)) return;
+  if constexpr (NV != 4) {
+    __syncthreads();
+    sample_row_by_value<T>(S.value, a, blockIdx.x);
+  }
 }
 
 template <int NV>
 __global__ __launch_bounds__(kThreads) void sample_floats_kernel(TokenArgs a) {
-  __shared__ FloatLds S;
-  sample_row_of_floats<NV>(S, a, blockIdx.x);
+  __shared__ union {
+    FloatLds bins;
+    TokLds value;
+  } S;
+  if (__builtin_expect(sample_row_of_floats<NV>(S.bins, a, blockIdx.x), 1)) return;
+  __syncthreads();
+  sample_row_by_value<float>(S.value, a, blockIdx.x);
 }
 
 static void launch_floats(const TokenArgs& a, hipStream_t s) {
@@ -1426,7 +1414,6 @@ static void launch_floats(const TokenArgs& a, hipStream_t s) {
     sample_floats_kernel<16><<<B, kThreads, 0, s>>>(a);
   else
     sample_floats_kernel<0><<<B, kThreads, 0, s>>>(a);
-  if (a.V > kListed) sample_left_kernel<float><<<B < kLeftBlocks ? B : kLeftBlocks, kThreads, 0, s>>>(a);
 }
 
 template <class T>
@@ -1441,7 +1428,6 @@ static void launch_codes(const TokenArgs& a, hipStream_t s) {
     sample_codes_kernel<T, 16><<<B, kThreads, 0, s>>>(a);
   else
     sample_codes_kernel<T, 0><<<B, kThreads, 0, s>>>(a);
-  if (a.V > 0xFFFFu) sample_left_kernel<T><<<B < kLeftBlocks ? B : kLeftBlocks, kThreads, 0, s>>>(a);
 }
 
 size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
