@@ -64,15 +64,15 @@ __device__ __forceinline__ float max_f(float a, float b) { return __builtin_fmax
 __device__ __forceinline__ u32 max_u(u32 a, u32 b) { return a > b ? a : b; }
 
 // e^x for x <= 0 to about one unit in the last place: the rounding of x log2(e), which
-// grows with |x|, is made up for by one more multiply-add.  Differences as far apart as the
+// grows with |x|, is made up for by two multiply-adds (x - t ln 2 is what the rounded t left).  Differences as far apart as the
 // type reaches (and -inf) are cut to one whose exponential is 0, and so is NaN: rows that
 // hold one are told apart beforehand.
 __device__ __forceinline__ float exp_f(float x) {
   x = __builtin_fmaxf(x, -150.f);
   const float t = x * 1.44269502f;
-  const float r = __builtin_fmaf(x, 1.44269502f, -t);
+  const float r = __builtin_fmaf(-t, 0.693147182f, x);
   const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, r * 0.693147182f, e);
+  return __builtin_fmaf(e, r, e);
 }
 
 // Four neighbouring entries with one load or store.
@@ -83,7 +83,20 @@ struct alignas(4 * sizeof(T)) Four {
 
 constexpr float kNone = -__builtin_huge_valf();
 
-// One row in registers: C entries per lane, -0 as +0.  QUAD: four neighbours at a time.
+// The largest of three, as one instruction also where the compiler cannot know that none
+// is a signalling NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// Four entries of -inf in the words of a load.
+template <class T> struct NoneWord { static constexpr u32 value = 0xFF800000u; };
+template <> struct NoneWord<Half16> { static constexpr u32 value = 0xFC00FC00u; };
+template <> struct NoneWord<Brain16> { static constexpr u32 value = 0xFF80FF80u; };
+
+// One row in registers: C entries per lane.  QUAD: four neighbours at a time.
 template <int G, int C, bool QUAD>
 struct Row {
   float v[C];
@@ -106,23 +119,33 @@ struct Row {
         q[i / 4] = *reinterpret_cast<const Four<T>*>(x + (at < E ? at : 0u));
       }
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = (in && index(i & ~3, g) < E ? to_f32(q[i / 4].e[i % 4]) : kNone) + 0.f;
+      for (int i = 0; i < C; i += 4) {  // by words: two entries of 16 bits at a time
+        u32 w[sizeof(T)];
+        __builtin_memcpy(w, &q[i / 4], 4 * sizeof(T));
+#pragma unroll
+        for (u32 k = 0; k < sizeof(T); ++k) w[k] = in && index(i, g) < E ? w[k] : NoneWord<T>::value;
+        __builtin_memcpy(&q[i / 4], w, 4 * sizeof(T));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i + k] = to_f32(q[i / 4].e[k]);
+      }
     } else {
       T q[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) q[i] = x[index(i, g) < E ? index(i, g) : 0u];
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = (in && index(i, g) < E ? to_f32(q[i]) : kNone) + 0.f;
+      for (int i = 0; i < C; ++i) v[i] = in && index(i, g) < E ? to_f32(q[i]) : kNone;
     }
   }
   // The largest entry and the exponentials.  A row that holds a NaN has NaN for its top,
   // and every NaN becomes the one that the order ranks first; there, and where the top is
   // +inf, all exponentials are NaN.
   __device__ __forceinline__ void weigh(bool in) {
+    static_assert(C % 2 == 0, "pairs behind the first, and one");
     float m = v[0];
     bool nan = false;
 #pragma unroll
-    for (int i = 1; i < C; ++i) m = max_f(m, v[i]);
+    for (int i = 1; i + 1 < C; i += 2) m = max3(m, v[i], v[i + 1]);
+    m = max_f(m, v[C - 1]);
 #pragma unroll
     for (int i = 0; i < C; i += 2) nan |= __builtin_isunordered(v[i], v[i + 1 < C ? i + 1 : i]);
     top = group_reduce<G>(m, max_f);
@@ -166,7 +189,7 @@ constexpr int key_bits(int entries) {
 
 // Ordered code of a value as a Row holds it.
 __device__ __forceinline__ u32 ord_of(float v) {
-  const u32 b = __float_as_uint(v);
+  const u32 b = __float_as_uint(v + 0.f);  // -0 as +0
   return b ^ ((u32)((int)b >> 31) | 0x80000000u);
 }
 
