@@ -600,19 +600,29 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
 
 namespace {
 
-u32 route_blocks(u64 T, u32 groups) {
-  const u64 b = (T + groups - 1) / groups;
-  return (u32)(b < kRouteMaxBlocks ? (b ? b : 1) : kRouteMaxBlocks);
+// Blocks of a kernel that takes `each` rows a block at a time: no more than are resident at
+// once, as what a block does before and after its rows (the sums over its lanes and
+// wavefronts; the loss's factors) costs as much as a row or two a wavefront, and no more
+// than share the rounds evenly.
+u32 route_blocks(u64 T, u32 each, u32 resident) {
+  const u64 rounds = (T + each - 1) / each;
+  if (rounds <= resident) return rounds ? (u32)rounds : 1;
+  const u64 turns = (rounds + resident - 1) / resident;
+  return (u32)((rounds + turns - 1) / turns);
 }
 
-template <class T, int G, int C, bool QUAD>
-hipError_t route_launch(const RouteArgs& a0, hipStream_t s) {
-  RouteArgs a = a0;
-  a.blocks = route_blocks(a.T, kRouteThreads / G);
-  if (a.balance_only)
-    route_kernel<T, G, C, QUAD, true><<<a.blocks, kRouteThreads, 0, s>>>(a);
-  else
-    route_kernel<T, G, C, QUAD, false><<<a.blocks, kRouteThreads, 0, s>>>(a);
+template <class K>
+u32 resident_blocks(K kernel, int threads) {
+  int each = 0;
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, 0) != hipSuccess || each < 1) each = 1;
+  return (u32)each * (u32)device_cu_count();
+}
+
+template <class T, int G, int C, bool QUAD, bool GIVEN>
+hipError_t route_launch_one(RouteArgs a, hipStream_t s) {
+  static const u32 fit = resident_blocks(route_kernel<T, G, C, QUAD, GIVEN>, kRouteThreads);
+  a.blocks = route_blocks(a.T, kRouteThreads / G, fit < kRouteMaxBlocks ? fit : kRouteMaxBlocks);
+  route_kernel<T, G, C, QUAD, GIVEN><<<a.blocks, kRouteThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.blocks == 1) return e;
   route_finish_kernel<<<(a.E + kFinishExperts - 1) / kFinishExperts, kFinishThreads, 0, s>>>(a);
@@ -620,10 +630,15 @@ hipError_t route_launch(const RouteArgs& a0, hipStream_t s) {
 }
 
 template <class T, int G, int C, bool QUAD>
+hipError_t route_launch(const RouteArgs& a, hipStream_t s) {
+  return a.balance_only ? route_launch_one<T, G, C, QUAD, true>(a, s) : route_launch_one<T, G, C, QUAD, false>(a, s);
+}
+
+template <class T, int G, int C, bool QUAD>
 hipError_t route_launch(const RouteGradArgs& a, hipStream_t s) {
-  const u64 b = (a.T + kGradThreads / G - 1) / (kGradThreads / G);
-  const u64 cap = (u64)device_cu_count() * 8;
-  route_grad_kernel<T, G, C, QUAD><<<(u32)(b < cap ? (b ? b : 1) : cap), kGradThreads, 0, s>>>(a);
+  static const u32 fit = resident_blocks(route_grad_kernel<T, G, C, QUAD>, kGradThreads);
+  const u32 blocks = route_blocks(a.T, kGradThreads / G, fit);
+  route_grad_kernel<T, G, C, QUAD><<<blocks, kGradThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
