@@ -583,6 +583,23 @@ __device__ __forceinline__ u32 pk_counter_words(u32 codes) {
   return w ^ (__builtin_bit_cast(u32, __builtin_bit_cast(u16x2, w) >> 4) & 0x000C000Cu);
 }
 
+// Four times the low or the high 16 bits, as one instruction.
+template <int HIGH>
+__device__ __forceinline__ u32 word_bytes(u32 v) {
+  const u32 two = 2;
+  u32 r;
+  if constexpr (HIGH)
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:WORD_1"
+        : "=v"(r) : "v"(two), "v"(v));
+  else
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:WORD_0"
+        : "=v"(r) : "v"(two), "v"(v));
+  return r;
+}
+__device__ __forceinline__ u32* counter_at(CodeLds& L, u32 bytes) {
+  return reinterpret_cast<u32*>(reinterpret_cast<char*>(L.cnt) + bytes);
+}
+
 template <class T> struct CodeOf;
 template <> struct CodeOf<Half16> { static constexpr u32 inf = 0x7C00; };
 template <> struct CodeOf<Brain16> { static constexpr u32 inf = 0x7F80; };
@@ -633,10 +650,12 @@ __device__ __forceinline__ u32 pk_max(u32 a, u32 b) {
 }
 // The 16-byte vectors of a row, a thread's kBatch in flight while others are dealt with (all
 // loaded at once, the first waits until the last is on its way: 83 us in place of 64 for 512
-// rows of 131072).  NV > 0: a thread's NV vectors stay in registers for later passes.
+// rows of 131072).  NV > 0: a thread's NV vectors stay in registers for later passes.  Places
+// past the row's end hold `fill`: put there once (FILL_ONCE), or in each pass, where the longer
+// lives of the changed registers would make the compiler spill others.
 typedef u32 u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBatch = 4;
-template <int NV>
+template <int NV, bool FILL_ONCE>
 struct RowVectors {
   static constexpr int kHeld = NV ? NV : kBatch;
   const u32x4* vec;
@@ -679,7 +698,12 @@ struct RowVectors {
       for (int i = 0; i < NV; ++i) {
         const u32 j = tid + (u32)i * kThreads;
         if (LOAD && i + kBatch < NV) held[i + kBatch < NV ? i + kBatch : 0] = at(j + kBatch * kThreads);
-        if ((u32)i * kThreads < nvec) f(filled(held[i], j), j);
+        if constexpr (FILL_ONCE) {
+          if (LOAD && (u32)(i + 1) * kThreads > nvec) held[i] = filled(held[i], j);
+          if ((u32)i * kThreads < nvec) f(held[i], j);
+        } else if ((u32)i * kThreads < nvec) {
+          f(filled(held[i], j), j);
+        }
         __builtin_amdgcn_sched_barrier(0);  // one vector's work at a time: registers
       }
     } else {
@@ -879,7 +903,7 @@ __device__ __forceinline__ bool sample_row_by_code(CodeLds& L, const TokenArgs& 
   u32 head = (u32)((16 - ((uintptr_t)row & 15)) & 15) / 2;
   if (head > V) head = V;
   const u32 nvec = (V - head) / 8, tail = head + nvec * 8;
-  RowVectors<NV> vectors;
+  RowVectors<NV, true> vectors;
   vectors.vec = reinterpret_cast<const u32x4*>(row + head);
   vectors.nvec = nvec;
   vectors.fill = kFill;
@@ -900,8 +924,8 @@ __device__ __forceinline__ bool sample_row_by_code(CodeLds& L, const TokenArgs& 
     ends = pk_max(ends, c);
     const u32 at = pk_counter_words(c);
     const bool lo = (c & 0xFFFFu) <= thr, hi = c >> 16 <= thr;
-    if (lo) atomicAdd(&L.cnt[at & 0xFFFFu], (sign & 0xFFFFu) + 1);  // 1 or 2^16
-    if (hi) atomicAdd(&L.cnt[at >> 16], (sign >> 16) + 1);
+    if (lo) atomicAdd(counter_at(L, word_bytes<0>(at)), (sign & 0xFFFFu) + 1);  // 1 or 2^16
+    if (hi) atomicAdd(counter_at(L, word_bytes<1>(at)), (sign >> 16) + 1);
     counted += (u32)__builtin_popcountll(__builtin_amdgcn_ballot_w64(lo)) +
                (u32)__builtin_popcountll(__builtin_amdgcn_ballot_w64(hi));
   };
@@ -1039,10 +1063,8 @@ __device__ __forceinline__ bool sample_row_by_code(CodeLds& L, const TokenArgs& 
   if (nvec) {
     vectors.template for_each<NV == 0>([&](u32x4 v, u32 at) {
       const u32 x[4] = {(v.x ^ want) & mask, (v.y ^ want) & mask, (v.z ^ want) & mask, (v.w ^ want) & mask};
-      u32 some = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) some |= (x[k] - 0x00010001u) & ~x[k] & 0x80008000u;
-      if (some) {
+      const u32 least = pk_min(pk_min(x[0], x[1]), pk_min(x[2], x[3]));
+      if (least < 0x10000u || (least & 0xFFFFu) == 0) {
         const u32 e = head + at * 8;
 #pragma unroll
         for (u32 k = 0; k < 4; ++k) look(x[k], e + 2 * k);
@@ -1121,7 +1143,7 @@ __device__ __forceinline__ bool sample_row_of_floats(FloatLds& L, const TokenArg
   u32 head = (u32)((16 - ((uintptr_t)row & 15)) & 15) / 4;
   if (head > V) head = V;
   const u32 nvec = (V - head) / 4, tail = head + nvec * 4;
-  RowVectors<NV> vectors;
+  RowVectors<NV, false> vectors;
   vectors.vec = reinterpret_cast<const u32x4*>(row + head);
   vectors.nvec = nvec;
   vectors.fill = __float_as_uint(kNone);
