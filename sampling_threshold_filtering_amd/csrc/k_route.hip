@@ -19,6 +19,13 @@
 // same experts for all of its rows, so P_e is summed in its registers; lanes, wavefronts
 // and blocks are then added in a fixed order (no floating-point atomics: the loss has the
 // same bits on every run).
+//
+// 65536 x 256 bf16, k = 8: forward 23 us and 4.5 to join the blocks, backward 20 us;
+// 131072 x 160 bf16, loss alone: forward 17 and 5.7, backward 23 us (3.6 TB/s).  The forward
+// is bound by its vector instructions (93 and 88 % of the cycles): per entry 3 to load and
+// convert, 7 for the exponential and its sum, 4 for a selection key and 2 for each of the k
+// maxima; 16 lanes share a row's log2 G exchanges, which 8 lanes with twice the entries did
+// not make up for (30 us: fewer wavefronts hide less).
 #include "launch.h"
 #include "ops_device.h"
 
@@ -676,7 +683,9 @@ hipError_t route_type(const A& a, int dtype, hipStream_t s) {
 }  // namespace
 
 size_t route_scratch_bytes(u64 T, u32 E) {
-  const u64 b = T < kRouteMaxBlocks ? (T ? T : 1) : kRouteMaxBlocks;
+  constexpr u64 kLeastRows = kRouteThreads / kWave;  // that a block takes at a time
+  const u64 rounds = (T + kLeastRows - 1) / kLeastRows;
+  const u64 b = rounds < kRouteMaxBlocks ? (rounds ? rounds : 1) : kRouteMaxBlocks;
   return 256 + b * (4 + 8 * (size_t)E);
 }
 

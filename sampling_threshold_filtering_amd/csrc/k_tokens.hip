@@ -533,10 +533,11 @@ __device__ __forceinline__ void sample_row_by_value(TokLds& L, const TokenArgs& 
 // A row of such logits has few different values, so it is enough to count them: 65536
 // counters of 16 bits fill 128 KB of LDS, an entry costs one LDS addition and no
 // exponential, and the weights are worked out once per value that occurs, not once per
-// entry.  512 rows of 131072: 59 us, 2.3 TB/s (by value bins, two passes with an exponential
-// and two additions per entry: 356 us).  Of a row's 29 us the counting takes 14, bound by the
-// LDS additions (14 cycles for a wavefront's 64, at random banks), the weights 5, the
-// questions 2, the chosen value's entries 3.  Codes go down with the value: code(h) = h ^ 0x7FFF for
+// entry.  512 rows of 131072: 58 us, 2.3 TB/s (by value bins, two passes with an exponential
+// and two additions per entry: 356 us).  Of a row's 28 us the counting takes 14 to 16, the
+// weights 6, the questions 2, the chosen value's entries 3; over the kernel the vector units
+// are at work 72 % of the cycles and the LDS 30 %, two thirds of that for bank conflicts of
+// the additions.  Codes go down with the value: code(h) = h ^ 0x7FFF for
 // h >= 0, else h, so -0 comes right after +0; a positive value's counter is the low half of
 // word code, a negative one's the high half of word code - 0x8000.  A counter that
 // overflows makes the counters' sum differ from the number of entries counted, since each
@@ -1109,7 +1110,7 @@ __device__ __forceinline__ bool sample_row_by_code(CodeLds& L, const TokenArgs& 
 // Bins are cut from the 32-bit difference to the largest value, which rounds monotonously.
 // Rows of up to 65536 entries stay in registers between the passes.  A row with a bin of
 // more than kListed entries, or with +inf, goes by the passes above that split bins.
-// 256 rows of 65536: 42 us a call, 1.6 TB/s (all passes over memory, each entry's weight in
+// 256 rows of 65536: 39 us a call, 1.7 TB/s (all passes over memory, each entry's weight in
 // 26 vector instructions of 64 bits and its mass and number in two additions: 82 us); of a
 // workgroup's 38 us the first pass takes 8, the histogram 15, a question 4 to 5.
 constexpr u32 kFloatBins = 4096;

@@ -74,6 +74,38 @@ struct Logits {
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType t) const { return at::empty(shape, x.options().dtype(t)); }
 };
 
+// A call's outputs and scratch in one allocation, a tensor each: a tensor of the allocator's
+// takes 0.9 us of the caller's time, one more over the same storage 0.2.  They share no
+// element and no version counter.
+class Together {
+  struct Piece {
+    at::Tensor* to;
+    c10::SmallVector<int64_t, 2> shape;
+    at::ScalarType type;
+    int64_t at;
+  };
+  c10::SmallVector<Piece, 6> pieces;
+  int64_t bytes = 0;
+
+ public:
+  void add(at::Tensor& to, at::IntArrayRef shape, at::ScalarType type) {
+    pieces.push_back({&to, {shape.begin(), shape.end()}, type, bytes});
+    bytes += (c10::multiply_integers(shape) * (int64_t)c10::elementSize(type) + 255) / 256 * 256;
+  }
+  void allocate(const Logits& like) {
+    const at::Tensor all = like.empty({bytes}, at::kByte);
+    for (const Piece& p : pieces) {
+      *p.to = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                       c10::scalarTypeToTypeMeta(p.type));
+      p.to->unsafeGetTensorImpl()->set_sizes_contiguous(p.shape);
+      p.to->unsafeGetTensorImpl()->set_storage_offset(p.at / (int64_t)c10::elementSize(p.type));
+    }
+  }
+};
+
+// Scratch beyond this is an allocation of its own, so that outputs do not keep it.
+constexpr int64_t kScratchWithOutputs = 256 << 10;
+
 // A tensor of one dimension with n values of a type, unit stride; None: undefined.
 at::Tensor vector(PyObject* o, const char* name, const char* what, int64_t n, at::ScalarType t, const Logits& like) {
   if (o == Py_None) return {};
@@ -148,8 +180,10 @@ PyObject* sample(PyObject* const* a) {
     refuse("need temperature >= 0, top_k >= 0, 0 <= top_p <= 1 and 0 <= min_p <= 1");
   at::Tensor tokens, logprobs;
   if (a[6] == Py_None) {
-    tokens = x.empty({x.rows}, at::kLong);
-    logprobs = x.empty({x.rows}, at::kFloat);
+    Together both;
+    both.add(tokens, {x.rows}, at::kLong);
+    both.add(logprobs, {x.rows}, at::kFloat);
+    both.allocate(x);
   } else {
     if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2) refuse("out must be (tokens, logprobs)");
     tokens = tensor(PyTuple_GET_ITEM(a[6], 0), "out[0]");
@@ -183,9 +217,18 @@ PyObject* route(PyObject* const* a) {
   const at::Tensor mask = vector(a[3], "mask", "bool", x.rows, at::kBool, x);
   const int64_t need = profk_route_scratch(x.rows, x.cols);
   if (need < 0) return status(x.cols > PROFK_ROUTE_MAX_EXPERTS ? PROFK_EUNSUPPORTED : need);
-  const at::Tensor scratch = x.empty({need}, at::kByte), weights = x.empty({x.rows, k}, at::kFloat),
-                   experts = x.empty({x.rows, k}, at::kLong), counts = x.empty({x.cols}, at::kLong),
-                   rows = x.empty({}, at::kLong), loss = balance ? x.empty({}, at::kFloat) : at::Tensor();
+  at::Tensor scratch, weights, experts, counts, rows, loss;
+  Together t;
+  t.add(weights, {x.rows, k}, at::kFloat);
+  t.add(experts, {x.rows, k}, at::kLong);
+  t.add(counts, {x.cols}, at::kLong);
+  t.add(rows, {}, at::kLong);
+  if (balance) t.add(loss, {}, at::kFloat);
+  if (need <= kScratchWithOutputs)
+    t.add(scratch, {need}, at::kByte);
+  else
+    scratch = x.empty({need}, at::kByte);
+  t.allocate(x);
   const int rc = profk_route_tokens(x.x.data_ptr(), x.dtype, x.rows, x.cols, x.ld, address<const uint8_t>(mask), k,
                                     normalize, address<float>(weights), address<int64_t>(experts),
                                     address<int64_t>(counts), address<int64_t>(rows), address<float>(loss),
@@ -246,8 +289,16 @@ PyObject* balance(PyObject* const* a) {
                    mask = vector(a[2], "mask", "bool", x.rows, at::kBool, x);
   const int64_t need = profk_route_scratch(x.rows, x.cols);
   if (need < 0) return status(x.cols > PROFK_ROUTE_MAX_EXPERTS ? PROFK_EUNSUPPORTED : need);
-  const at::Tensor scratch = x.empty({need}, at::kByte), counts = x.empty({x.cols}, at::kLong),
-                   rows = x.empty({}, at::kLong), loss = x.empty({}, at::kFloat);
+  at::Tensor scratch, counts, rows, loss;
+  Together t;
+  t.add(counts, {x.cols}, at::kLong);
+  t.add(rows, {}, at::kLong);
+  t.add(loss, {}, at::kFloat);
+  if (need <= kScratchWithOutputs)
+    t.add(scratch, {need}, at::kByte);
+  else
+    scratch = x.empty({need}, at::kByte);
+  t.allocate(x);
   const int rc = profk_balance_loss(x.x.data_ptr(), x.dtype, x.rows, x.cols, x.ld, address<const uint8_t>(mask),
                                     address<const int64_t>(experts), k, address<int64_t>(counts),
                                     address<int64_t>(rows), address<float>(loss), address(scratch), need,
