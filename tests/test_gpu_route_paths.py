@@ -93,6 +93,21 @@ def test_four_at_a_time_and_one_give_the_same_choice(E, dtype):
     check_route(wide[:, 1:E + 1], k, False, d_loss=0.1)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E", [191, 192, 193, 383, 384, 385, 512, 513, 767, 768, 769])
+def test_expert_counts_at_the_limits_of_each_layout(E, dtype):
+    import torch
+    rng = np.random.default_rng(E + 5)
+    T, k = 75, 40
+    x = logits(rng, T, E, dtype)
+    x[3] = 0.0
+    x[4, E // 2:] = float("-inf")
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    say("limits", E, dtype)
+    for normalize in (True, False):
+        check_route(x, k, normalize, d_weights=dw, d_loss=0.4)
+
+
 def test_many_slots_of_one_expert_and_a_long_batch():
     import torch
     T, E, k = 150000, 8, 2
