@@ -651,10 +651,14 @@ hipError_t route_launch(const RouteGradArgs& a, hipStream_t s) {
 
 // Lanes per row and entries per lane: the smallest that hold the row, and the fewest lanes
 // that hold it in 16 entries each (16384 x 384 fp16, forward and backward: 25 us by 32 lanes
-// with 12 entries, 34 by 64 with 8; x 700: 38 by 64 with 12, 43 with 16).
+// with 12 entries, 34 by 64 with 8; x 700: 38 by 64 with 12, 43 with 16).  Up to 64 entries
+// 8 lanes are better where there are rows enough for every CU (131072 x 64 bf16, forward and
+// backward: 31 us in place of 36; 16384 x 64 fp32: 13 in place of 10).
 template <class T, bool QUAD, class A>
 hipError_t route_shape(const A& a, hipStream_t s) {
   if (a.E <= 16) return route_launch<T, 4, 4, QUAD>(a, s);
+  if (a.E <= 32) return route_launch<T, 8, 4, QUAD>(a, s);
+  if (a.E <= 64 && a.T >= 65536) return route_launch<T, 8, 8, QUAD>(a, s);
   if (a.E <= 64) return route_launch<T, 16, 4, QUAD>(a, s);
   if (a.E <= 128) return route_launch<T, 16, 8, QUAD>(a, s);
   if (a.E <= 192) return route_launch<T, 16, 12, QUAD>(a, s);

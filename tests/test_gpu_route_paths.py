@@ -108,6 +108,45 @@ def test_expert_counts_at_the_limits_of_each_layout(E, dtype):
         check_route(x, k, normalize, d_weights=dw, d_loss=0.4)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,k", [(20, 3), (33, 5), (64, 8)])
+def test_long_batches_against_their_parts_and_64_bits(E, k, dtype):
+    """From 65536 tokens on another layout takes the rows: the choice equals that of two
+    shorter batches, and the gradient and the loss the formula's in 64 bits (their error: the
+    exponentials', 4 h and |d| h for the difference, twice for p and a sum over a row's
+    entries, and half a step of the logits' type)."""
+    import torch
+    rng = np.random.default_rng(E)
+    T = 65536 + 77
+    x = logits(rng, T, E, dtype)
+    mask = torch.from_numpy(rng.random(T) < 0.9).cuda()
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    d_loss = 0.01 * T
+    say("long", E, k, dtype)
+    r = stf.route_tokens(x, k, normalize=False, mask=mask, balance=True)
+    g = stf.route_tokens_grad(x, r, dw, d_loss, normalize=False, mask=mask)
+    a = stf.route_tokens(x[:30000], k, normalize=False, mask=mask[:30000])
+    b = stf.route_tokens(x[30000:], k, normalize=False, mask=mask[30000:])
+    assert torch.equal(r.experts, torch.cat([a.experts, b.experts]))
+    assert torch.equal(r.counts, a.counts + b.counts) and int(r.rows) == int(a.rows) + int(b.rows)
+    p = torch.softmax(x.double(), dim=1) * mask.unsqueeze(1)
+    n = int(mask.sum())
+    f = r.counts.double() / (n * k)
+    tol = (64 + 4 * 20) * 2.0 ** -24
+    assert float((x.float().amax(1) - x.float().amin(1)).max()) <= 20
+    w = p.gather(1, r.experts.clamp(min=0)) * (r.experts >= 0)
+    assert ((r.weights.double() - w).abs() <= tol * w).all()
+    loss = float((E * f * p.sum(dim=0) / n).sum())
+    assert abs(float(r.loss) - loss) <= tol * loss
+    d = torch.zeros_like(p).scatter_add_(1, r.experts.clamp(min=0), dw.double() * (r.experts >= 0))
+    want = p * (d - (p * d).sum(1, keepdim=True)) + d_loss * E / n * p * (f - (p * f).sum(1, keepdim=True))
+    big = d.abs().amax(1, keepdim=True)
+    size = 2 * big * p + d_loss * E / n * p * (f + (p * f).sum(1, keepdim=True))
+    half = torch.finfo(x.dtype).eps / 2
+    least = float(torch.finfo(x.dtype).tiny) * 2 * half if x.dtype == torch.float16 else 1e-38
+    assert ((g.double() - want).abs() <= 2 * tol * size + half * (want.abs() + 2 * tol * size) + least).all()
+
+
 def test_many_slots_of_one_expert_and_a_long_batch():
     import torch
     T, E, k = 150000, 8, 2
