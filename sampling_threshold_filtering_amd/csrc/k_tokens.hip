@@ -1127,7 +1127,7 @@ struct FloatLds {
   double power[kPowers];  // 2^(F + j / kPowers)
   u64 far_mass[kWave];  // every 64th of the prefixes
   u32 far_n[kWave];
-  u32 top, nan, index, listed[4];
+  u32 top, nan, listed[4];
   u64 minp;
   u64 ans_mass, ans_key;
 };
@@ -1169,7 +1169,6 @@ __device__ __forceinline__ bool sample_row_of_floats(FloatLds& L, const TokenArg
   if (threadIdx.x == 0) {
     L.top = L.nan = 0;
     L.minp = 0;
-    L.index = ~0u;
   }
   if (threadIdx.x < 4) L.listed[threadIdx.x] = 0;
   static_assert(kPowers == (u32)kThreads, "a power each");
