@@ -549,7 +549,8 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       auto weight = [&](u32 e) { return exp_f(to_f32(xt[e]) - row.top) * inv; };
       const bool first = row.live && first_e < a.E;
       const float p0 = first ? weight(first_e) : 0.f;
-      float wsum = p0, wd = p0 * first_d;
+      const float d0 = first ? first_d : 0.f;  // where there is no expert d_weights may hold anything
+      float wsum = p0, wd = p0 * d0;
       if (row.live)
         for (u32 j = g + G; j < a.k; j += G) {
           const u32 e = slot(tr, j);
@@ -563,7 +564,7 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       const float r = a.normalize ? 1.f / wsum : 1.f;
       const float mean = wd * r, from = a.normalize ? mean : 0.f;
       if (!a.normalize) dot += mean;
-      if (first) atomicAdd(&d[first_e], p0 * r * (first_d - from));
+      if (first) atomicAdd(&d[first_e], p0 * r * (d0 - from));
       if (row.live)
         for (u32 j = g + G; j < a.k; j += G) {
           const u32 e = slot(tr, j);

@@ -1,0 +1,46 @@
+"""The language-model operators at the edges of what their inputs and outputs may be."""
+import numpy as np
+import pytest
+
+import sampling_threshold_filtering_amd as stf
+from tests.test_gpu_route import TYPES, host, logits, say
+from tests.operators_ref import route as route_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,k", [(8, 4), (40, 6), (64, 40), (300, 64)])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_slots_without_an_expert_may_hold_anything(E, k, dtype, normalize):
+    """A live row with fewer than k experts left: what d_weights holds in its empty slots does
+    not reach the gradient, which is that of zeros there, bit for bit."""
+    import torch
+    rng = np.random.default_rng(E + k)
+    T = 130
+    x = logits(rng, T, E, dtype)
+    for t in range(0, T, 2):  # 1 to k - 1 entries left
+        x[t, torch.from_numpy(rng.permutation(E)[1 + (t // 2) % (k - 1):]).cuda()] = float("-inf")
+    r = stf.route_tokens(x, k, normalize=normalize, balance=True)
+    empty = r.experts < 0
+    assert empty[::2].any(dim=1).all() and not empty[1::2].any()
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    zeros = dw.masked_fill(empty, 0.0)
+    want = stf.route_tokens_grad(x, r, zeros, 0.3, normalize=normalize)
+    assert torch.isfinite(want).all()
+    for junk in (float("nan"), float("inf"), float("-inf")):
+        say("empty slots", E, k, dtype, normalize, junk)
+        got = stf.route_tokens_grad(x, r, dw.masked_fill(empty, junk), 0.3, normalize=normalize)
+        assert torch.equal(got, want)
+    y = x.detach().requires_grad_()
+    q = stf.route_tokens(y, k, normalize=normalize, balance=True)
+    torch.autograd.backward([q.weights, q.loss], [dw.masked_fill(empty, float("nan")),
+                                                  torch.tensor(0.3, device="cuda")])
+    assert torch.equal(y.grad, want)
+    ref = route_ref(host(x), k, normalize, None, zeros.cpu().numpy(), 0.0)["d_logits"]
+    g = stf.route_tokens_grad(x, r, dw.masked_fill(empty, float("nan")), None, normalize=normalize)
+    # the exponential's and the sums' error (64 + 4 |d|) h with |d| < 20, twice, of terms of at most 2 max |d_weights|
+    big = 2 * np.abs(zeros.cpu().numpy()).max(axis=1, keepdims=True)
+    half = torch.finfo(x.dtype).eps / 2
+    bound = 2 * (64 + 4 * 20) * 2.0 ** -24 * big + half * np.abs(ref) + float(torch.finfo(x.dtype).tiny)
+    assert np.all(np.abs(host(g) - ref) <= bound)
