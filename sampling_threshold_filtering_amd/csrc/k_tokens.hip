@@ -1109,7 +1109,8 @@ __device__ __forceinline__ bool sample_row_by_code(CodeLds& L, const TokenArgs& 
 // inside it by ranks: each of the bin's entries adds up the weights of those before it.
 // Bins are cut from the 32-bit difference to the largest value, which rounds monotonously.
 // Rows of up to 65536 entries stay in registers between the passes.  A row with a bin of
-// more than kListed entries, or with +inf, goes by the passes above that split bins.
+// more than kListed entries, with +inf, or of a temperature next to the type's largest, goes
+// by the passes above that split bins.
 // 256 rows of 65536: 39 us a call, 1.7 TB/s (all passes over memory, each entry's weight in
 // 26 vector instructions of 64 bits and its mass and number in two additions: 82 us); of a
 // workgroup's 38 us the first pass takes 8, the histogram 15, a question 4 to 5.
@@ -1203,7 +1204,9 @@ __device__ __forceinline__ bool sample_row_of_floats(FloatLds& L, const TokenArg
   w.top = top;
   w.c = 1.4426950408889634074 / (double)s.t;
   w.scale = (double)(1ull << F);
-  const float reach_f = __builtin_fminf((float)F * 0.69314718f * s.t, 3.4e38f);  // of what is present
+  const float reach_f = (float)F * 0.69314718f * s.t;  // of what is present
+  // From temperatures of about 1e37 on, differences that are still present pass 32-bit floats.
+  if (__builtin_expect(!(reach_f <= 3.4e38f), 0)) return false;
   const float bins = greedy ? 0.f : (float)(kFloatBins - 1) / reach_f;
   // An entry's bin; absent from kFloatBins on.  The conversion saturates and makes 0 of NaN
   // (the largest value's 0 times infinity, where the temperature is next to 0).

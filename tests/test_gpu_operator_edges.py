@@ -4,6 +4,7 @@ import pytest
 
 import sampling_threshold_filtering_amd as stf
 from tests.test_gpu_route import TYPES, host, logits, say
+from tests.test_gpu_tokens import check
 from tests.operators_ref import route as route_ref
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,25 @@ def test_slots_without_an_expert_may_hold_anything(E, k, dtype, normalize):
     half = torch.finfo(x.dtype).eps / 2
     bound = 2 * (64 + 4 * 20) * 2.0 ** -24 * big + half * np.abs(ref) + float(torch.finfo(x.dtype).tiny)
     assert np.all(np.abs(host(g) - ref) <= bound)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [700, 20000, 70001])
+def test_temperatures_next_to_the_largest_number(V, dtype):
+    """Differences of logits that pass 32-bit floats and yet count, at temperatures up to
+    infinity (where all finite entries weigh the same), beside masked entries."""
+    import torch
+    rng = np.random.default_rng(V + 17)
+    most = float(torch.finfo(getattr(torch, dtype)).max)
+    x = np.clip(rng.standard_normal((4, V)) * (most / 3), -most, most)
+    x[0, ::2] = -np.inf
+    x[1, :5] = [most, -most, 0.0, most, -most]
+    x[2, 1:] = np.where(rng.random(V - 1) < 0.5, -most, -np.inf)
+    x = torch.from_numpy(x).to("cuda", dtype=getattr(torch, dtype))
+    assert not torch.isposinf(x).any()
+    for t in (1e36, 9e36, 1.2e37, 1e38, 3.4e38, float("inf")):
+        say("temperature", t, V, dtype)
+        check(x, rng.random(4), t=t)
+        check(x, rng.random(4), t=t, k=300, p=0.7, m=0.01)
+    rows = np.array([1e38, 1.0, np.inf, 3e38], np.float32)  # a setting per row
+    check(x, rng.random(4), t=rows, p=0.9)
