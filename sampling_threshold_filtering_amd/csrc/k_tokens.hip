@@ -1457,14 +1457,31 @@ static void launch_codes(const TokenArgs& a, hipStream_t s) {
 
 size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
 
+// A workgroup a row, and a grid has fewer than 2^32 threads: longer batches go in parts.
 hipError_t launch_sample_tokens(const TokenArgs& a, int dtype, hipStream_t s) {
-  if (dtype == PROFK_FP32)
-    launch_floats(a, s);
-  else if (dtype == PROFK_FP16)
-    launch_codes<Half16>(a, s);
-  else
-    launch_codes<Brain16>(a, s);
-  return hipGetLastError();
+  constexpr u64 kMostRows = (1ull << 32) / kThreads - 1;
+  const u64 size = dtype == PROFK_FP32 ? 4 : 2;
+  for (u64 r = 0; r < a.B; r += kMostRows) {
+    TokenArgs part = a;
+    part.B = a.B - r < kMostRows ? a.B - r : kMostRows;
+    part.x = reinterpret_cast<const char*>(a.x) + r * a.ld * size;
+    part.u += r;
+    if (a.t_row) part.t_row += r;
+    if (a.p_row) part.p_row += r;
+    if (a.m_row) part.m_row += r;
+    if (a.k_row) part.k_row += r;
+    part.tokens += r;
+    part.logprobs += r;
+    if (dtype == PROFK_FP32)
+      launch_floats(part, s);
+    else if (dtype == PROFK_FP16)
+      launch_codes<Half16>(part, s);
+    else
+      launch_codes<Brain16>(part, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace profk

@@ -67,3 +67,28 @@ def test_temperatures_next_to_the_largest_number(V, dtype):
         check(x, rng.random(4), t=t, k=300, p=0.7, m=0.01)
     rows = np.array([1e38, 1.0, np.inf, 3e38], np.float32)  # a setting per row
     check(x, rng.random(4), t=rows, p=0.9)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_more_rows_than_one_grid_holds(dtype):
+    """A workgroup of 1024 threads a row and fewer than 2^32 threads a grid: 2^22 - 1 rows."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    most = (1 << 22) - 1
+    B, V = most + 70, 6
+    x = torch.randn((B, V), generator=gen, device="cuda").to(getattr(torch, dtype))
+    u = torch.rand(B, generator=gen, device="cuda")
+    t = torch.rand(B, generator=gen, device="cuda") * 2
+    k = torch.randint(0, V + 1, (B,), generator=gen, device="cuda")
+    p = torch.rand(B, generator=gen, device="cuda") * 0.5 + 0.5
+    m = torch.rand(B, generator=gen, device="cuda") * 0.1
+    say("rows", B, dtype)
+    tok, lp = stf.sample_tokens(x, u, t, k, p, m)
+    for a, b in ((0, 50), (most // 2, most // 2 + 50), (most - 60, most + 70)):
+        s = slice(a, b)
+        want = stf.sample_tokens(x[s], u[s], t[s], k[s], p[s], m[s])
+        assert torch.equal(tok[s], want[0]) and torch.equal(lp[s], want[1])
+        check(x[s], u[s].cpu().numpy(), *(v[s].cpu().numpy() for v in (t, k, p, m)), got=(tok[s], lp[s]))
+    tok, lp = stf.sample_tokens(x, u, temperature=0.0)
+    assert torch.equal(tok, x.float().sort(dim=1, descending=True, stable=True)[1][:, 0]) and (lp == 0).all()
