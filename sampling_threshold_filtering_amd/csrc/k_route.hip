@@ -16,9 +16,10 @@
 // so that a row's maximum and sums are log2 G lane exchanges and 64 / G rows share every
 // instruction.  A lane takes its entries four neighbours at a time where rows allow it (one
 // load of 16 or 8 bytes each), else lane g takes entries g, g + G, ...  A lane keeps the
-// same experts for all of its rows, so P_e is summed in its registers; lanes, wavefronts
-// and blocks are then added in a fixed order (no floating-point atomics: the loss has the
-// same bits on every run).
+// same experts for all of its rows, so P_e is summed in its registers, in 32 bits for at
+// most four rows; the wavefronts' sums of those and the blocks' are then added in 64 bits, in
+// a fixed order (no floating-point atomics: the loss has the same bits on every run).  Summed
+// in 32 bits to the end, the error grew with the batch: 3e-6 of P_e at 128 rows a lane.
 //
 // 65536 x 256 bf16, k = 8: forward 23 us and 4.5 to join the blocks, backward 20 us;
 // 131072 x 160 bf16, loss alone: forward 17 and 5.7, backward 23 us (3.6 TB/s).  The forward
@@ -39,6 +40,7 @@ constexpr u32 kRouteMaxBlocks = 512;
 constexpr int kGradThreads = 256;
 constexpr int kFinishThreads = 1024;
 constexpr u32 kFinishExperts = 16;
+constexpr u32 kTurnsInRegisters = 4;  // rows a lane sums in 32 bits
 
 // Sum / maximum over the G lanes of a group; every lane gets the result.  Within 16 lanes
 // the partner is a mirrored one, which holds the same partial result as the one across.
@@ -204,17 +206,17 @@ __device__ __forceinline__ u32 ord_of(float v) {
 // finishing launch; one block alone writes the outputs itself.
 struct RouteScratch {
   u64* loss;     // the finishing blocks' parts of the loss, and how many there are
-  u32* rows;     // blocks
+  double* sums;  // blocks * E
   u32* counts;   // blocks * E
-  float* sums;   // blocks * E
+  u32* rows;     // blocks
 };
 
 __host__ __device__ inline RouteScratch route_scratch(char* s, u32 blocks, u32 E) {
   RouteScratch r;
   r.loss = (u64*)s;
-  r.rows = (u32*)(s + 256);
-  r.counts = r.rows + blocks;
-  r.sums = (float*)(r.counts + (u64)blocks * E);
+  r.sums = (double*)(s + 256);
+  r.counts = (u32*)(r.sums + (u64)blocks * E);
+  r.rows = r.counts + (u64)blocks * E;
   return r;
 }
 
@@ -346,6 +348,24 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   u32 rows = 0;
   const u64 step = (u64)gridDim.x * kGroups;
   const bool balance = GIVEN || a.loss;
+  // The block's sums so far, of expert threadIdx.x: a wavefront's groups by lane exchanges,
+  // its wavefronts in 64 bits.
+  static_assert(G * C <= kRouteThreads, "a thread per expert");
+  double total = 0;
+  auto join = [&]() {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float v = sum[i];
+#pragma unroll
+      for (int d = G; d < kWave; d <<= 1) v += __shfl_xor(v, d);
+      if (lane_id() < G) s_sum[threadIdx.x / kWave][Row<G, C, QUAD>::index(i, g)] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.E)
+#pragma unroll
+      for (int w = 0; w < kRouteWaves; ++w) total += (double)s_sum[w][threadIdx.x];
+  };
+  u32 turn = 0;
   for (u64 t0 = (u64)blockIdx.x * kGroups; t0 < a.T; t0 += step) {
     const u64 t = t0 + grp, tr = t < a.T ? t : a.T - 1;
     const bool in = (!a.mask || a.mask[tr]) && t < a.T;
@@ -368,25 +388,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     } else {
       choose<T, G, C, QUAD>(a, row, x + tr * a.ld, t, g, inv, s_cnt);
     }
-  }
-  // the block's sums: the wavefront's groups, then its wavefronts
+    if (balance && ++turn == kTurnsInRegisters && t0 + step < a.T) {  // the same for the whole block
+      join();
+      __syncthreads();
+      turn = 0;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    float v = sum[i];
-#pragma unroll
-    for (int d = G; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-    if (lane_id() < G) s_sum[threadIdx.x / kWave][Row<G, C, QUAD>::index(i, g)] = v;
+      for (int i = 0; i < C; ++i) sum[i] = 0.f;
+    }
   }
   if (rows) atomicAdd(&s_rows, rows);
-  __syncthreads();
+  join();
   if (gridDim.x == 1) {
     double part = 0;
-    for (u32 e = threadIdx.x; e < a.E; e += kRouteThreads) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kRouteWaves; ++w) v += s_sum[w][e];
-      a.counts[e] = (int64_t)s_cnt[e];
-      part += (double)s_cnt[e] * (double)v;
+    if (threadIdx.x < a.E) {
+      a.counts[threadIdx.x] = (int64_t)s_cnt[threadIdx.x];
+      part = (double)s_cnt[threadIdx.x] * total;
     }
     __shared__ double s_part[kRouteWaves];
     part = block_sum<kRouteWaves>(part, s_part);
@@ -397,12 +413,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     return;
   }
   const RouteScratch sc = route_scratch(a.scratch, gridDim.x, a.E);
-  for (u32 e = threadIdx.x; e < a.E; e += kRouteThreads) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) v += s_sum[w][e];
-    sc.counts[(u64)blockIdx.x * a.E + e] = s_cnt[e];
-    sc.sums[(u64)blockIdx.x * a.E + e] = v;
+  if (threadIdx.x < a.E) {
+    const u64 at = (u64)blockIdx.x * a.E + threadIdx.x;
+    sc.counts[at] = s_cnt[threadIdx.x];
+    sc.sums[at] = total;
   }
   if (threadIdx.x == 0) {
     sc.rows[blockIdx.x] = s_rows;
@@ -426,21 +440,21 @@ __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs 
   const u32 el = threadIdx.x % kFinishExperts, sl = threadIdx.x / kFinishExperts, wid = threadIdx.x / kWave;
   const u32 e = blockIdx.x * kFinishExperts + el;
   u32 cs[kEach];
-  float ps[kEach];
+  double ps[kEach];
   u32 rows = threadIdx.x < a.blocks ? sc.rows[threadIdx.x] : 0;
 #pragma unroll
   for (u32 i = 0; i < kEach; ++i) {
     const u32 b = sl + i * kSlices;
     const bool some = e < a.E && b < a.blocks;
     cs[i] = some ? sc.counts[(u64)b * a.E + e] : 0;
-    ps[i] = some && a.loss ? sc.sums[(u64)b * a.E + e] : 0.f;
+    ps[i] = some && a.loss ? sc.sums[(u64)b * a.E + e] : 0.0;
   }
   u32 c = 0;  // at most T k < 2^37 slots in all; a thread's and a wavefront's are of 8 and 32 blocks
   double p = 0;
 #pragma unroll
   for (u32 i = 0; i < kEach; ++i) {
     c += cs[i];
-    p += (double)ps[i];
+    p += ps[i];
   }
 #pragma unroll
   for (u32 d = kFinishExperts; d < (u32)kWave; d <<= 1) {
@@ -695,7 +709,7 @@ size_t route_scratch_bytes(u64 T, u32 E) {
   constexpr u64 kLeastRows = kRouteThreads / kWave;  // that a block takes at a time
   const u64 rounds = (T + kLeastRows - 1) / kLeastRows;
   const u64 b = rounds < kRouteMaxBlocks ? (rounds ? rounds : 1) : kRouteMaxBlocks;
-  return 256 + b * (4 + 8 * (size_t)E);
+  return 256 + b * (4 + 12 * (size_t)E);
 }
 
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) { return route_type(a, dtype, s); }

@@ -92,3 +92,23 @@ def test_more_rows_than_one_grid_holds(dtype):
         check(x[s], u[s].cpu().numpy(), *(v[s].cpu().numpy() for v in (t, k, p, m)), got=(tok[s], lp[s]))
     tok, lp = stf.sample_tokens(x, u, temperature=0.0)
     assert torch.equal(tok, x.float().sort(dim=1, descending=True, stable=True)[1][:, 0]) and (lp == 0).all()
+
+
+@pytest.mark.parametrize("E,T", [(4, 1 << 25), (60, 1 << 22), (256, 1 << 21), (1024, 1 << 19)])
+def test_long_batches_sum_probabilities_as_well_as_short_ones(E, T):
+    """Equal rows that all choose one expert: the loss is E p_e whatever the batch's length.
+    In units of h = 2^-24: one row's p is rounded once; of a long batch four rows are summed in
+    32 bits, off by at most 1 + 2 + 3 + 4 of 4 p, and up to sixteen groups of a wavefront in
+    four exchanges; each loss is rounded once: 1 + 2.5 + 4 + 2."""
+    import torch
+    for seed in range(10):
+        gen = torch.Generator()
+        gen.manual_seed(seed)
+        row = (torch.randn((1, E), generator=gen) * 1.5).to("cuda", dtype=torch.bfloat16)
+        e = int(torch.randint(0, E, (1,), generator=gen))
+        choice = torch.full((1, 1), e, dtype=torch.int64, device="cuda")
+        one = stf.balance_loss(row, choice)
+        many = stf.balance_loss(row.expand(T, E).contiguous(), choice.expand(T, 1).contiguous())
+        say("long sums", E, T, seed, float(one.loss), float(many.loss))
+        assert int(many.rows) == T and int(many.counts[e]) == T and int(many.counts.sum()) == T
+        assert abs(float(many.loss) - float(one.loss)) <= 9.5 * 2.0 ** -24 * float(one.loss)
