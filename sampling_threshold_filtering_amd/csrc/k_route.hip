@@ -41,6 +41,8 @@ constexpr int kGradThreads = 256;
 constexpr int kFinishThreads = 1024;
 constexpr u32 kFinishExperts = 16;
 constexpr u32 kTurnsInRegisters = 4;  // rows a lane sums in 32 bits
+constexpr u32 kMostFinishing = kRouteMaxExperts / kFinishExperts;
+constexpr size_t kRouteScratchHead = 256 + 8 * kMostFinishing;
 
 // Sum / maximum over the G lanes of a group; every lane gets the result.  Within 16 lanes
 // the partner is a mirrored one, which holds the same partial result as the one across.
@@ -206,6 +208,7 @@ __device__ __forceinline__ u32 ord_of(float v) {
 // finishing launch; one block alone writes the outputs itself.
 struct RouteScratch {
   u64* loss;     // the finishing blocks' parts of the loss, and how many there are
+  double* parts; // small ones of them, a place per finishing block
   double* sums;  // blocks * E
   u32* counts;   // blocks * E
   u32* rows;     // blocks
@@ -214,7 +217,8 @@ struct RouteScratch {
 __host__ __device__ inline RouteScratch route_scratch(char* s, u32 blocks, u32 E) {
   RouteScratch r;
   r.loss = (u64*)s;
-  r.sums = (double*)(s + 256);
+  r.parts = (double*)(s + 256);
+  r.sums = (double*)(s + kRouteScratchHead);
   r.counts = (u32*)(r.sums + (u64)blocks * E);
   r.rows = r.counts + (u64)blocks * E;
   return r;
@@ -422,6 +426,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     sc.rows[blockIdx.x] = s_rows;
     if (blockIdx.x == 0) *sc.loss = 0;
   }
+  if (blockIdx.x == 0 && threadIdx.x < kMostFinishing) sc.parts[threadIdx.x] = 0;
 }
 
 // The blocks' counts and sums into the outputs.  A finishing block takes 16 experts, its
@@ -491,17 +496,36 @@ __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs 
 #pragma unroll
   for (u32 d = 1; d < kFinishExperts; d <<= 1) part += __shfl_xor(part, d);
   if (threadIdx.x) return;
+  const double share = live ? part / ((double)live * (double)a.k * (double)live) : 0.0;
+  if (gridDim.x == 1) {
+    *a.loss = (float)((double)a.E * share);
+    return;
+  }
   // sum_e f_e P_e is at most 1: a block adds its part in units of 2^-48, one to the count of
   // blocks (at most 64) and, for NaN, one to the count of those, with a single 64-bit
   // addition, whose order does not matter.  (Parts, then a ticket, then the parts read back
-  // were three trips to memory: 0.7 us more.)
-  const double share = live ? part / ((double)live * (double)a.k * (double)live) : 0.0;
+  // were three trips to memory: 0.7 us more.)  Those units are too coarse for a sum below
+  // kSmall, as of a choice that the probabilities do not favour; all parts of such a sum are
+  // below it, and such a part is stored as it is beforehand, for the last block to add up in
+  // their order.
+  constexpr double kSmall = 0x1p-18;  // 64 roundings to 2^-49 are 2^-25 of it
+  if (share > 0 && share < kSmall) {
+    __hip_atomic_store(&sc.parts[blockIdx.x], share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __threadfence();
+  }
   const u64 mine = (share == share ? (u64)rint(share * 0x1p48) << 14 : 1ull << 7) + 1;
-  const u64 sum = gridDim.x == 1 ? mine
-                                 : mine + __hip_atomic_fetch_add(sc.loss, mine, __ATOMIC_RELAXED,
-                                                                 __HIP_MEMORY_SCOPE_AGENT);
-  if ((sum & 127) == gridDim.x)
-    *a.loss = sum >> 7 & 127 ? __uint_as_float(0x7FC00000u) : (float)((double)a.E * ((double)(sum >> 14) * 0x1p-48));
+  const u64 sum = mine + __hip_atomic_fetch_add(sc.loss, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if ((sum & 127) != gridDim.x) return;
+  double all = (double)(sum >> 14) * 0x1p-48;
+  if (sum >> 7 & 127) {
+    all = __builtin_nan("");
+  } else if (all < kSmall) {
+    __threadfence();
+    all = 0;
+    for (u32 b = 0; b < gridDim.x; ++b)
+      all += __hip_atomic_load(&sc.parts[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  *a.loss = (float)((double)a.E * all);
 }
 
 template <class T, int G, int C, bool QUAD>
@@ -709,7 +733,7 @@ size_t route_scratch_bytes(u64 T, u32 E) {
   constexpr u64 kLeastRows = kRouteThreads / kWave;  // that a block takes at a time
   const u64 rounds = (T + kLeastRows - 1) / kLeastRows;
   const u64 b = rounds < kRouteMaxBlocks ? (rounds ? rounds : 1) : kRouteMaxBlocks;
-  return 256 + b * (4 + 12 * (size_t)E);
+  return kRouteScratchHead + b * (4 + 12 * (size_t)E);
 }
 
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) { return route_type(a, dtype, s); }

@@ -112,3 +112,51 @@ def test_long_batches_sum_probabilities_as_well_as_short_ones(E, T):
         say("long sums", E, T, seed, float(one.loss), float(many.loss))
         assert int(many.rows) == T and int(many.counts[e]) == T and int(many.counts.sum()) == T
         assert abs(float(many.loss) - float(one.loss)) <= 9.5 * 2.0 ** -24 * float(one.loss)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("E", [12, 64, 200, 1000])
+@pytest.mark.parametrize("T", [10, 300, 70001])
+def test_small_losses_are_as_exact_as_others(T, E, dtype):
+    """A choice made elsewhere of experts whose probabilities are small: from one block and from
+    many, the loss is off by no more than its probabilities are (and by no more than the
+    smallest 32-bit numbers, below which they are 0)."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T + E)
+    for gap in (4.0, 10.0, 14.0, 23.0, 35.0, 60.0, 80.0):
+        x = torch.rand((T, E), generator=gen, device="cuda")
+        x[:, 0] = gap
+        x = x.to(getattr(torch, dtype))
+        experts = torch.randint(1, E, (T, 2), generator=gen, device="cuda")
+        for some in (1.0, 0.01):  # many dropped slots make it smaller still
+            e = experts.masked_fill(torch.rand((T, 2), generator=gen, device="cuda") > some, -1)
+            b = stf.balance_loss(x, e)
+            p = torch.softmax(x.double(), dim=1)
+            f = b.counts.double() / (T * 2)
+            want = float((E * f * p.mean(dim=0)).sum())
+            assert torch.equal(b.counts, torch.bincount(e[e >= 0], minlength=E))
+            say("small loss", T, E, dtype, gap, some, float(b.loss), want)
+            # the weights' own error, and that of a long batch's sums
+            assert abs(float(b.loss) - want) <= (64 + 4 * (gap + 1) + 10) * 2.0 ** -24 * want + E * 1.2e-38
+            assert torch.equal(stf.balance_loss(x, e).loss, b.loss)  # the same bits
+
+
+def test_a_loss_that_is_small_in_all_blocks_but_one():
+    """Experts of one finishing block hold nearly everything, the others next to nothing."""
+    import torch
+    T, E = 5000, 320
+    for gap in (0.0, 20.0, 40.0):
+        for hot in (0, 100, 319):
+            x = torch.zeros((T, E), device="cuda")
+            x[:, hot] = gap
+            e = (torch.arange(T, device="cuda") % E).unsqueeze(1)
+            b = stf.balance_loss(x, e)
+            p = torch.softmax(x.double(), dim=1)
+            want = float((E * b.counts.double() / T * p.mean(dim=0)).sum())
+            say("one large part", gap, hot)
+            assert abs(float(b.loss) - want) <= (64 + 4 * gap + 10) * 2.0 ** -24 * want
+            without = e.masked_fill(e == hot, -1)
+            b = stf.balance_loss(x, without)
+            want = float((E * b.counts.double() / T * p.mean(dim=0)).sum())
+            assert abs(float(b.loss) - want) <= (64 + 4 * gap + 10) * 2.0 ** -24 * want
