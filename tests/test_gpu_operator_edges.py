@@ -160,3 +160,84 @@ def test_a_loss_that_is_small_in_all_blocks_but_one():
             b = stf.balance_loss(x, without)
             want = float((E * b.counts.double() / T * p.mean(dim=0)).sum())
             assert abs(float(b.loss) - want) <= (64 + 4 * gap + 10) * 2.0 ** -24 * want
+
+
+def results(dtype="float32", T=4000, E=100, V=9000):
+    """A result of every operator, by name, and the functions that make them again."""
+    import torch
+    rng = np.random.default_rng(77)
+    x, l = logits(rng, T, E, dtype), logits(rng, 40, V, dtype)
+    u = torch.from_numpy(rng.random(40).astype(np.float32)).cuda()
+
+    def make():
+        r = stf.route_tokens(x, 4, balance=True)
+        b = stf.balance_loss(x, r.experts)
+        t = stf.sample_tokens(l, u, 0.9, 0, 0.95)
+        return {"weights": r.weights, "experts": r.experts, "counts": r.counts, "rows": r.rows, "loss": r.loss,
+                "balance loss": b.loss, "balance counts": b.counts, "balance rows": b.rows, "tokens": t[0],
+                "logprobs": t[1], "gradient": stf.route_tokens_grad(x, r, r.weights, 0.1),
+                "balance gradient": stf.balance_loss_grad(x, b)}
+    return make
+
+
+def test_outputs_have_storages_of_their_own():
+    """Kept or saved, an output takes no other output and no scratch along."""
+    import torch
+    out = results()()
+    for name, t in out.items():
+        assert t.untyped_storage().nbytes() == t.numel() * t.element_size() and t.storage_offset() == 0, name
+    assert len({t.untyped_storage().data_ptr() for t in out.values()}) == len(out)
+    before = torch.cuda.memory_allocated()
+    x = torch.zeros((20000, 64), device="cuda")
+    made = torch.cuda.memory_allocated()
+    losses = [stf.route_tokens(x, 8, balance=True).loss for _ in range(20)]
+    assert torch.cuda.memory_allocated() - made <= 20 * 512  # the allocator's least block each
+    del losses, x
+    assert torch.cuda.memory_allocated() <= before
+
+
+def test_results_are_saved_copied_and_resized_like_any_tensor():
+    import copy
+    import io
+
+    import torch
+    make = results(T=50, E=20, V=300)
+    out = make()
+    for value in (out, tuple(out.values()), stf.route_tokens(torch.randn((30, 10), device="cuda"), 2, balance=True)._asdict(),
+                  stf.sample_tokens(torch.randn((3, 50), device="cuda"), torch.rand(3, device="cuda"))):
+        f = io.BytesIO()
+        torch.save(value, f)
+        f.seek(0)
+        back = torch.load(f, weights_only=True)
+        pairs = [(value[k], back[k]) for k in value] if isinstance(value, dict) else list(zip(value, back))
+        assert all(torch.equal(a, b) and a.dtype == b.dtype for a, b in pairs)
+        same = copy.deepcopy(value)
+        pairs = [(value[k], same[k]) for k in value] if isinstance(value, dict) else list(zip(value, same))
+        assert all(torch.equal(a, b) for a, b in pairs)
+    want = {k: t.clone() for k, t in out.items()}
+    for k in out:  # grown and overwritten, it leaves the others alone
+        out[k].resize_(out[k].numel() + 100).fill_(7)
+        del want[k]
+        assert all(torch.equal(out[j], want[j]) for j in want), k
+
+
+def test_outputs_used_on_other_streams_and_under_inference_mode():
+    import torch
+    make = results(dtype="bfloat16")
+    want = make()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            got = make()
+            again = make()  # its scratch and outputs come behind the first call's
+        torch.cuda.current_stream().wait_stream(s)
+        for t in got.values():
+            t.record_stream(torch.cuda.current_stream())
+        assert all(torch.equal(got[k], want[k]) and torch.equal(again[k], want[k]) for k in want)
+        del got, again
+    with torch.inference_mode():
+        got = make()
+        assert all(t.is_inference() for t in got.values())
+        assert all(torch.equal(got[k], want[k]) for k in want)
+    assert not any(t.is_inference() or t.requires_grad for t in want.values())
