@@ -52,6 +52,12 @@ double number(PyObject* o, const char* name) {
   return v;
 }
 
+// Forward-mode derivatives would be lost without a word.
+void no_tangent(const at::Tensor& t, const char* name) {
+  if (t.defined() && t._fw_grad(/*level=*/0).defined())
+    refuse(std::string(name) + " has a forward-mode tangent, and this operator has no forward-mode derivative: detach it");
+}
+
 void* stream_of(PyObject* o) { return PyLong_AsVoidPtr(o); }
 
 // torch's device allocator, as its own tensors have it; it allocates on the current device,
@@ -201,6 +207,7 @@ PyObject* sample(PyObject* const* a) {
 // route(logits, k, normalize, mask, balance, stream)
 PyObject* route(PyObject* const* a) {
   const Logits x(a[0]);
+  no_tangent(x.x, "logits");
   const int64_t k = integer(a[1], "k");
   if (k < 1 || k > x.cols) refuse("k must be in 1.." + std::to_string(x.cols));
   const bool normalize = PyObject_IsTrue(a[2]), balance = PyObject_IsTrue(a[4]);
@@ -230,12 +237,14 @@ struct LossScale {
     value = THPVariable_Unpack(o);
     if (value.numel() != 1 || value.scalar_type() != at::kFloat || value.device() != like.x.device())
       refuse("d_loss must be a number or one float32 value on " + like.x.device().str());
+    no_tangent(value, "d_loss");
   }
 };
 
 // route_grad(logits, experts, counts, rows, d_weights, d_loss, normalize, mask, stream)
 PyObject* route_grad(PyObject* const* a) {
   const Logits x(a[0]);
+  no_tangent(x.x, "logits");
   const at::Tensor& choice = tensor(a[1], "experts");
   const int64_t k = choice.dim() == 2 ? choice.size(1) : 0;
   const at::Tensor mask = vector(a[7], "mask", "bool", x.rows, at::kBool, x);
@@ -243,6 +252,7 @@ PyObject* route_grad(PyObject* const* a) {
   double factor = 0;
   if (a[4] != Py_None) {
     d_weights = shaped(a[4], "d_weights", {x.rows, k}, at::kFloat, x);
+    no_tangent(d_weights, "d_weights");
     experts = shaped(a[1], "experts", {x.rows, k}, at::kLong, x);
   }
   if (a[5] != Py_None) {
@@ -264,6 +274,7 @@ PyObject* route_grad(PyObject* const* a) {
 // balance(logits, experts, mask, stream)
 PyObject* balance(PyObject* const* a) {
   const Logits x(a[0]);
+  no_tangent(x.x, "logits");
   const at::Tensor& choice = tensor(a[1], "experts");
   if (choice.dim() != 2 || choice.size(1) < 1) refuse("experts must be a 2-D int64 tensor with a row per token");
   const int64_t k = choice.size(1);
@@ -283,6 +294,7 @@ PyObject* balance(PyObject* const* a) {
 // balance_grad(logits, k, counts, rows, d_loss, mask, stream)
 PyObject* balance_grad(PyObject* const* a) {
   const Logits x(a[0]);
+  no_tangent(x.x, "logits");
   const at::Tensor mask = vector(a[5], "mask", "bool", x.rows, at::kBool, x),
                    counts = shaped(a[2], "counts", {x.cols}, at::kLong, x),
                    rows = shaped(a[3], "rows", {}, at::kLong, x);

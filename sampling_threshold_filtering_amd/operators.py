@@ -8,7 +8,9 @@
 Formulas, ties, empty rows and limits: include/profk.h.  Every call is enqueued on the
 current stream of the logits' device and waits for nothing; outputs and scratch come from
 torch's allocator, so calls may be captured into a graph without a first call.
-route_tokens and balance_loss are differentiable where the logits require a gradient.
+route_tokens and balance_loss are differentiable (backward, once) where the logits require a
+gradient; a forward-mode tangent is refused.  sample_tokens' results and the gradients by name
+are constants to autograd.
 
 The checks of arguments, the outputs and the library's call are one compiled step
 (csrc/operators_binding.cpp): a call takes 3 to 60 us on the GPU, and from Python the same
@@ -97,8 +99,8 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out
     B values.  temperature 0 is greedy; top_k 0, top_p 1 and min_p 0 are off.  The token is
     the quantile u of what is left, counted from the likeliest down (u = 0: the likeliest;
     ties to the lower index); its logprob is of that renormalised distribution.  A row with
-    no entry above -inf, or with a NaN, gives token -1.  `out=(tokens, logprobs)` reuses
-    caller buffers."""
+    no entry above -inf, or with a NaN, gives token -1.  The log-probabilities are constants:
+    no gradient reaches the logits.  `out=(tokens, logprobs)` reuses caller buffers."""
     return _call(logits, (_module or _native()).sample, logits, u, temperature, top_k, top_p, min_p, out)
 
 

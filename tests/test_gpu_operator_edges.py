@@ -241,3 +241,31 @@ def test_outputs_used_on_other_streams_and_under_inference_mode():
         assert all(t.is_inference() for t in got.values())
         assert all(torch.equal(got[k], want[k]) for k in want)
     assert not any(t.is_inference() or t.requires_grad for t in want.values())
+
+
+def test_forward_mode_tangents_are_refused():
+    """They would be lost without a word; sampling's results are constants and stay so."""
+    import torch
+    import torch.autograd.forward_ad as forward
+    x, d = torch.randn((4, 8), device="cuda"), torch.randn((4, 8), device="cuda")
+    r = stf.route_tokens(x, 2, balance=True)
+    b = stf.balance_loss(x, r.experts)
+    dw = torch.randn((4, 2), device="cuda")
+    with forward.dual_level():
+        y = forward.make_dual(x, d)
+        w = forward.make_dual(dw, torch.ones_like(dw))
+        s = forward.make_dual(torch.tensor(2.0, device="cuda"), torch.tensor(1.0, device="cuda"))
+        for call in (lambda: stf.route_tokens(y, 2), lambda: stf.route_tokens(y, 2, balance=True),
+                     lambda: stf.balance_loss(y, r.experts), lambda: stf.route_tokens_grad(y, r, dw, 0.5),
+                     lambda: stf.route_tokens_grad(x, r, w), lambda: stf.route_tokens_grad(x, r, None, s),
+                     lambda: stf.balance_loss_grad(y, b), lambda: stf.balance_loss_grad(x, b, s)):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+        for call in (lambda v: stf.route_tokens(v, 2, balance=True), lambda v: stf.balance_loss(v, r.experts)):
+            with pytest.raises((ValueError, RuntimeError, NotImplementedError)):
+                call(forward.make_dual(x.detach().requires_grad_(), d))
+        assert torch.equal(stf.route_tokens(y.detach(), 2, balance=True).weights, r.weights)
+        tok, lp = stf.sample_tokens(y, torch.rand(4, device="cuda"))
+        assert forward.unpack_dual(lp).tangent is None
+    tok, lp = stf.sample_tokens(x.clone().requires_grad_(), torch.rand(4, device="cuda"))
+    assert not lp.requires_grad
