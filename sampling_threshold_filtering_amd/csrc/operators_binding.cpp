@@ -52,6 +52,15 @@ double number(PyObject* o, const char* name) {
   return v;
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be true or false");
+  }
+  return v;
+}
+
 // Forward-mode derivatives would be lost without a word.
 void no_tangent(const at::Tensor& t, const char* name) {
   if (t.defined() && t._fw_grad(/*level=*/0).defined())
@@ -210,7 +219,7 @@ PyObject* route(PyObject* const* a) {
   no_tangent(x.x, "logits");
   const int64_t k = integer(a[1], "k");
   if (k < 1 || k > x.cols) refuse("k must be in 1.." + std::to_string(x.cols));
-  const bool normalize = PyObject_IsTrue(a[2]), balance = PyObject_IsTrue(a[4]);
+  const bool normalize = truth(a[2], "normalize"), balance = truth(a[4], "balance");
   const at::Tensor mask = vector(a[3], "mask", "bool", x.rows, at::kBool, x);
   const int64_t need = profk_route_scratch(x.rows, x.cols);
   if (need < 0) return status(x.cols > PROFK_ROUTE_MAX_EXPERTS ? PROFK_EUNSUPPORTED : need);
@@ -248,6 +257,7 @@ PyObject* route_grad(PyObject* const* a) {
   const at::Tensor& choice = tensor(a[1], "experts");
   const int64_t k = choice.dim() == 2 ? choice.size(1) : 0;
   const at::Tensor mask = vector(a[7], "mask", "bool", x.rows, at::kBool, x);
+  const bool normalize = truth(a[6], "normalize");
   at::Tensor experts, d_weights, counts, rows, d_loss;
   double factor = 0;
   if (a[4] != Py_None) {
@@ -264,7 +274,7 @@ PyObject* route_grad(PyObject* const* a) {
   }
   const at::Tensor dx = x.empty({x.rows, x.cols}, x.x.scalar_type());
   const int rc = profk_route_tokens_grad(x.x.data_ptr(), x.dtype, x.rows, x.cols, x.ld, address<const uint8_t>(mask), k,
-                                         PyObject_IsTrue(a[6]), address<const int64_t>(experts),
+                                         normalize, address<const int64_t>(experts),
                                          address<const float>(d_weights), address<const int64_t>(counts),
                                          address<const int64_t>(rows), address<const float>(d_loss), (float)factor,
                                          dx.data_ptr(), stream_of(a[8]));

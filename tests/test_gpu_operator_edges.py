@@ -269,3 +269,15 @@ def test_forward_mode_tangents_are_refused():
         assert forward.unpack_dual(lp).tangent is None
     tok, lp = stf.sample_tokens(x.clone().requires_grad_(), torch.rand(4, device="cuda"))
     assert not lp.requires_grad
+
+
+def test_flags_that_are_neither_true_nor_false_are_refused():
+    import torch
+    x = torch.randn((4, 8), device="cuda")
+    r = stf.route_tokens(x, 2)
+    for bad in (torch.zeros(2), np.zeros(2)):
+        for call in (lambda: stf.route_tokens(x, 2, normalize=bad), lambda: stf.route_tokens(x, 2, balance=bad),
+                     lambda: stf.route_tokens_grad(x, r, r.weights, normalize=bad)):
+            with pytest.raises(ValueError, match="true or false"):
+                call()
+    assert torch.equal(stf.route_tokens(x, 2, normalize=np.bool_(True)).weights, r.weights)
