@@ -3,13 +3,15 @@
 Every translation unit is compiled with hipcc for --offload-arch=gfx950 into
 _build/, then linked into sampling_threshold_filtering_amd/libprofk.so.
 _operators.so, the compiled step of operators.py, is host code over it and
-torch's headers (g++).
+torch's headers (g++, or hipcc where there is none).  Where there is no torch
+for ROCm it is left out: the library needs none.
 """
 from __future__ import annotations
 
 import importlib.util
 import os
 import resource
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -73,11 +75,25 @@ def build(verbose: bool = False) -> str:
     return LIB
 
 
+def _torch_folder():
+    """Of an installed torch for ROCm, or None; found without importing it, which takes its time
+    and is not needed to compile."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    folder = os.path.dirname(spec.origin)
+    return folder if os.path.exists(os.path.join(folder, "lib", "libtorch_hip.so")) else None
+
+
 def _build_binding() -> None:
-    # found without importing torch, which takes its time and is not needed to compile
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch = _torch_folder()
+    if torch is None:
+        if os.path.exists(BINDING):  # of another library and torch than these
+            os.remove(BINDING)
+        print("no torch for ROCm: the language-model operators' binding is left out")
+        return
     tmp = BINDING + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or HIPCC, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
            "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "operators_binding.cpp"), "-o", tmp,
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10",
