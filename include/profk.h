@@ -361,7 +361,9 @@ typedef struct profk_sampling {
   const float* row_min_p;
 } profk_sampling;
 
-int64_t profk_sample_tokens_scratch(int64_t B, int64_t V); /* bytes, or PROFK_EINVAL */
+/* 0, or PROFK_EINVAL: sampling uses no scratch.  The query and the two arguments below are
+ * reserved; scratch may be NULL. */
+int64_t profk_sample_tokens_scratch(int64_t B, int64_t V);
 
 int profk_sample_tokens(const void* logits, int32_t dtype, int64_t B, int64_t V, int64_t ld, const float* u,
                         const profk_sampling* how, int64_t* out_tokens, float* out_logprobs, void* scratch,

@@ -1455,8 +1455,6 @@ static void launch_codes(const TokenArgs& a, hipStream_t s) {
     sample_codes_kernel<T, 0><<<B, kThreads, 0, s>>>(a);
 }
 
-size_t sample_tokens_scratch_bytes(u64, u64) { return 0; }
-
 // A workgroup a row, and a grid has fewer than 2^32 threads: longer batches go in parts.
 hipError_t launch_sample_tokens(const TokenArgs& a, int dtype, hipStream_t s) {
   constexpr u64 kMostRows = (1ull << 32) / kThreads - 1;

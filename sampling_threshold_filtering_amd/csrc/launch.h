@@ -293,9 +293,7 @@ struct TokenArgs {
   const int64_t* k_row;
   int64_t* tokens;
   float* logprobs;
-  char* scratch;
 };
-size_t sample_tokens_scratch_bytes(u64 B, u64 V);
 hipError_t launch_sample_tokens(const TokenArgs& a, int dtype, hipStream_t s);
 
 // Routing tokens to experts and the balance loss (k_route.hip).

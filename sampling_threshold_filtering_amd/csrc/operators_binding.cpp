@@ -130,7 +130,7 @@ at::Tensor shaped(PyObject* o, const char* name, at::IntArrayRef shape, at::Scal
   return v.is_contiguous() ? v : v.contiguous();
 }
 
-template <class T = void>
+template <class T>
 T* address(const at::Tensor& t) {
   return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
 }
@@ -201,15 +201,11 @@ PyObject* sample(PyObject* const* a) {
       refuse("out must be contiguous int64 / float32 tensors of shape " + shape_text(shape) + " on " +
              x.x.device().str());
   }
-  const int64_t need = profk_sample_tokens_scratch(x.rows, x.cols);
-  at::Tensor scratch;
-  if (need > 0) scratch = x.empty({need}, at::kByte);
   const profk_sampling how = {(float)t.value,         (float)p.value,           (float)m.value,
                               0,                      k.whole,                  address<const float>(t.rows),
                               address<const int64_t>(k.rows), address<const float>(p.rows), address<const float>(m.rows)};
   const int rc = profk_sample_tokens(x.x.data_ptr(), x.dtype, x.rows, x.cols, x.ld, address<const float>(u), &how,
-                                     address<int64_t>(tokens), address<float>(logprobs), address(scratch),
-                                     need > 0 ? need : 0, stream_of(a[7]));
+                                     address<int64_t>(tokens), address<float>(logprobs), nullptr, 0, stream_of(a[7]));
   return rc ? status(rc) : result({tokens, logprobs});
 }
 
