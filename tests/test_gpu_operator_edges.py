@@ -281,3 +281,64 @@ def test_flags_that_are_neither_true_nor_false_are_refused():
             with pytest.raises(ValueError, match="true or false"):
                 call()
     assert torch.equal(stf.route_tokens(x, 2, normalize=np.bool_(True)).weights, r.weights)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("T,E,k", [(300001, 16, 16), (150001, 30, 9), (70001, 60, 20), (70003, 160, 6), (70001, 256, 17),
+                                   (65537, 300, 40), (40001, 700, 64), (40003, 1024, 3)])
+def test_several_rows_a_group(T, E, k, normalize, dtype):
+    """Batches of which every group of lanes takes several rows, slots beyond its lanes' first
+    among them: what one row left in registers and shared memory must not reach the next.
+    Against the formulas in 64 bits; tolerances as in test_gpu_route."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E + k)
+    x = torch.randn((T, E), generator=gen, device="cuda") * 1.5 + torch.randn(E, generator=gen, device="cuda") * 0.7
+    x[::7, 1::3] = float("-inf")   # rows with fewer entries, some with fewer than k
+    x[5::1000, 1:] = float("-inf")
+    x[6::1000] = float("-inf")
+    x = x.to(getattr(torch, dtype))
+    mask = torch.rand(T, generator=gen, device="cuda") < 0.9
+    dw = torch.randn((T, k), generator=gen, device="cuda")
+    d_loss = 0.01 * T
+    say("several rows", T, E, k, normalize, dtype)
+    r = stf.route_tokens(x, k, normalize=normalize, mask=mask, balance=True)
+    g = stf.route_tokens_grad(x, r, dw, d_loss, normalize=normalize, mask=mask).double()
+    val, at = x.float().sort(dim=1, descending=True, stable=True)
+    val, at = val[:, :k], at[:, :k]
+    live = mask & (val[:, 0] > float("-inf"))
+    taken = (val > float("-inf")) & live.unsqueeze(1)
+    assert torch.equal(r.experts, at.masked_fill(~taken, -1)) and int(r.rows) == int(live.sum())
+    assert torch.equal(r.counts, torch.bincount(at[taken], minlength=E))
+    p = torch.softmax(x.double(), dim=1).masked_fill(~live.unsqueeze(1), 0.0)
+    w = p.gather(1, at) * taken
+    if normalize:
+        w = w / w.sum(dim=1, keepdim=True).clamp(min=1e-300)
+    spread = float((val[:, :1].clamp(min=-1e30) - x.float()).masked_fill(torch.isinf(x.float()), 0.0).max())
+    assert spread <= 25
+    tol = (64 + 4 * 25) * 2.0 ** -24
+    assert ((r.weights.double() - w).abs() <= tol * w).all()
+    n = int(live.sum())
+    f = r.counts.double() / (n * k)
+    loss = float((E * f * p.sum(dim=0) / n).sum())
+    assert abs(float(r.loss) - loss) <= (tol + 10 * 2.0 ** -24) * loss
+    d = dw.double() * taken
+    if normalize:
+        want = torch.zeros_like(p).scatter_add_(1, at, w * (d - (w * d).sum(1, keepdim=True)))
+        weight = torch.maximum(p, torch.zeros_like(p).scatter_add_(1, at, w))
+    else:
+        want = torch.zeros_like(p).scatter_add_(1, at, d)
+        want = p * (want - (p * want).sum(1, keepdim=True))
+        weight = p
+    pf = (p * f).sum(1, keepdim=True)
+    want += d_loss * E / n * p * (f - pf)
+    size = 2 * d.abs().amax(1, keepdim=True) * weight + d_loss * E / n * p * (f + pf)
+    half = torch.finfo(x.dtype).eps / 2
+    assert ((g - want).abs() <= 2 * tol * size + half * (want.abs() + 2 * tol * size) + 1e-38).all()
+    e = torch.where(torch.rand((T, k), generator=gen, device="cuda") < 0.05, torch.full_like(at, E), at)
+    b = stf.balance_loss(x, e, mask=mask)
+    assert int(b.rows) == n and torch.equal(b.counts, torch.bincount(e[(e < E) & live.unsqueeze(1)], minlength=E))
+    f = b.counts.double() / (n * k)
+    loss = float((E * f * p.sum(dim=0) / n).sum())
+    assert abs(float(b.loss) - loss) <= (tol + 10 * 2.0 ** -24) * loss
