@@ -19,6 +19,7 @@ steps took 9 to 15 us.  There is no other path when it has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import sampling_threshold_filtering_amd as _profk
@@ -52,11 +53,12 @@ class Balance(NamedTuple):
     k: int
 
 
-_module = _torch = None  # set together, at first use
+# set together, at first use; the last two are looked up once (0.1 us each time)
+_module = _torch = _stream = _device = None
 
 
 def _native():
-    global _module, _torch
+    global _module, _torch, _stream, _device
     if _module is None:
         _profk.load_library()
         import torch  # the compiled step uses its libraries
@@ -66,6 +68,8 @@ def _native():
             raise ImportError("the operators' binding is missing: build it with "
                               "`python -m sampling_threshold_filtering_amd.build_native`") from e
         _torch = torch
+        _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or functools.partial(_profk._raw_stream, torch)
+        _device = getattr(torch._C, "_cuda_getDevice", None) or functools.partial(_profk._current_device, torch)
         _module = _operators
     return _module
 
@@ -81,11 +85,11 @@ def _call(x, fn, *args):
     if not (isinstance(x, torch.Tensor) and x.is_cuda):
         _check_device(torch, x)
     di = x.get_device()
-    if di == _profk._current_device(torch):
-        r = fn(*args, _profk._raw_stream(torch, di))
+    if di == _device():
+        r = fn(*args, _stream(di))
     else:
         with torch.cuda.device(di):
-            r = fn(*args, _profk._raw_stream(torch, di))
+            r = fn(*args, _stream(di))
     if r.__class__ is int:
         _profk._check(r)
     return r
