@@ -343,8 +343,8 @@ int profk_read_ceiling(const float* x, int64_t N, int32_t blocks_per_cu, uint64_
  * holds a NaN gives token -1 and logprob NaN; a row with no entry above -inf
  * gives token -1 and logprob -inf.  Weights are held as integers, in units of
  * 2^-F of the largest, F = min(50, 62 - ceil(log2 V)): the token does not
- * depend on how the work is split, and an entry below 2^-F of the largest
- * counts as absent.
+ * depend on how the work is split, an entry below 2^-F of the largest counts as
+ * absent, and a border is off by at most V 2^-(F+1) of the largest weight.
  *   u             device, B floats
  *   how           settings: each row_* pointer (device, B values) where not NULL,
  *                 else the plain field for every row

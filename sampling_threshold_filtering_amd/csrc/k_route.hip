@@ -21,9 +21,9 @@
 // a fixed order (no floating-point atomics: the loss has the same bits on every run).  Summed
 // in 32 bits to the end, the error grew with the batch: 3e-6 of P_e at 128 rows a lane.
 //
-// 65536 x 256 bf16, k = 8: forward 23 us and 4.5 to join the blocks, backward 20 us;
-// 131072 x 160 bf16, loss alone: forward 17 and 5.7, backward 23 us (3.6 TB/s).  The forward
-// is bound by its vector instructions (93 and 88 % of the cycles): per entry 3 to load and
+// 65536 x 256 bf16, k = 8: forward 24 us and 4.7 to join the blocks, backward 21 us;
+// 131072 x 160 bf16, loss alone: forward 17 and 4.7, backward 24 us (3.5 TB/s).  The forward
+// is bound by its vector instructions (90 % of the cycles in both): per entry 3 to load and
 // convert, 7 for the exponential and its sum, 4 for a selection key and 2 for each of the k
 // maxima; 16 lanes share a row's log2 G exchanges, which 8 lanes with twice the entries did
 // not make up for (30 us: fewer wavefronts hide less).
@@ -75,9 +75,9 @@ __device__ __forceinline__ float max_f(float a, float b) { return __builtin_fmax
 __device__ __forceinline__ u32 max_u(u32 a, u32 b) { return a > b ? a : b; }
 
 // e^x for x <= 0 to about one unit in the last place: the rounding of x log2(e), which
-// grows with |x|, is made up for by two multiply-adds (x - t ln 2 is what the rounded t left).  Differences as far apart as the
-// type reaches (and -inf) are cut to one whose exponential is 0, and so is NaN: rows that
-// hold one are told apart beforehand.
+// grows with |x|, is made up for by two multiply-adds (x - t ln 2 is what the rounded t
+// left).  Differences as far apart as the type reaches (and -inf) are cut to one whose
+// exponential is 0, and so is NaN: rows that hold one are told apart beforehand.
 __device__ __forceinline__ float exp_f(float x) {
   x = __builtin_fmaxf(x, -150.f);
   const float t = x * 1.44269502f;
@@ -691,8 +691,10 @@ hipError_t route_launch(const RouteGradArgs& a, hipStream_t s) {
 // Lanes per row and entries per lane: the smallest that hold the row, and the fewest lanes
 // that hold it in 16 entries each (16384 x 384 fp16, forward and backward: 25 us by 32 lanes
 // with 12 entries, 34 by 64 with 8; x 700: 38 by 64 with 12, 43 with 16).  Up to 64 entries
-// 8 lanes are better where there are rows enough for every CU (131072 x 64 bf16, forward and
-// backward: 31 us in place of 36; 16384 x 64 fp32: 13 in place of 10).
+// 8 lanes are better for long batches, whose blocks of 128 rows reach every CU: 131072 x 64
+// bf16, forward with the loss and backward in one graph, 33 us by 8 lanes and 40 by 16; 65536
+// rows 22.9 and 24.9, 32768 rows 15.4 and 18.1, 16384 rows 14.1 and 13.1 (fp32 the same way).
+// The bound is a constant on the safe side of 256 CUs' 32768 rows.
 template <class T, bool QUAD, class A>
 hipError_t route_shape(const A& a, hipStream_t s) {
   if (a.E <= 16) return route_launch<T, 4, 4, QUAD>(a, s);

@@ -13,12 +13,14 @@
 // logits by 4096 value bins; rows that overflow either by value bins split as often as it
 // takes (the first part of this file, right for every row).
 //
-// Exactness.  Weights are integers q_i = round(w_i 2^F), with F as large as lets a row's
-// sum fit 63 bits (F = 46 at 2^17 entries), from 64-bit floats.  Integer sums do not
-// depend on their order, so LDS atomics give the same bits on every run, and the rounding of
-// a weight (2^-(F+1) of the largest) is far below what a 24-bit u can tell apart.  (Counted
-// values are summed in 64-bit floats, sixteen at a time, and rounded to such integers.)  An
-// entry below about 2^-F of the largest counts as absent.
+// Exactness.  Weights are integers q_i = round(w_i 2^F), with F = min(50, 62 - ceil(log2 V))
+// as large as lets a row's sum fit 63 bits (50 up to 4096 entries, 45 at 2^17, 38 at 2^24),
+// from 64-bit floats.  Integer sums do not depend on their order, so LDS atomics give the same
+// bits on every run.  A row's V roundings move a border by at most V 2^-(F+1) of the largest
+// weight: 2^-29 at 2^17 entries and 2^-27 at 2^18, below the 2^-24 steps of u, but 2^-23 at
+// 2^20 and 2^-15 at 2^24, so in rows that long a draw next to a border may fall on its other
+// side.  (Counted values are summed in 64-bit floats, sixteen at a time, and rounded to such
+// integers.)  An entry below about 2^-F of the largest counts as absent.
 #include <type_traits>
 
 #include "block_select.h"
@@ -536,7 +538,7 @@ __device__ __forceinline__ void sample_row_by_value(TokLds& L, const TokenArgs& 
 // entry.  512 rows of 131072: 58 us, 2.3 TB/s (by value bins, two passes with an exponential
 // and two additions per entry: 356 us).  Of a row's 28 us the counting takes 14 to 16, the
 // weights 6, the questions 2, the chosen value's entries 3; over the kernel the vector units
-// are at work 72 % of the cycles and the LDS 30 %, two thirds of that for bank conflicts of
+// are at work 67 % of the cycles and the LDS 30 %, two thirds of that for bank conflicts of
 // the additions.  Codes go down with the value: code(h) = h ^ 0x7FFF for
 // h >= 0, else h, so -0 comes right after +0; a positive value's counter is the low half of
 // word code, a negative one's the high half of word code - 0x8000.  A counter that
