@@ -384,7 +384,7 @@ int profk_sample_tokens(const void* logits, int32_t dtype, int64_t B, int64_t V,
  *                 E * sum_e f_e P_e, f_e = counts_e / (n k), P_e = sum_t p_te / n
  *                 (0 when n = 0)
  *   Limits: E <= 1024, k <= 64, T < 2^31 (PROFK_EUNSUPPORTED); k <= E.
- *   The loss has the same bits on every run.
+ *   Probabilities below 2^-126 count as 0.  The loss has the same bits on every run.
  */
 int64_t profk_route_scratch(int64_t T, int64_t E); /* bytes, or PROFK_EINVAL */
 

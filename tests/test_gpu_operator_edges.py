@@ -342,3 +342,40 @@ def test_several_rows_a_group(T, E, k, normalize, dtype):
     f = b.counts.double() / (n * k)
     loss = float((E * f * p.sum(dim=0) / n).sum())
     assert abs(float(b.loss) - loss) <= (tol + 10 * 2.0 ** -24) * loss
+
+
+FIRST_CALL = """
+import sys
+sys.path.insert(0, {root!r})
+import torch, sampling_threshold_filtering_amd as stf
+x = torch.randn(3000, 500, device="cuda").half()
+dw, l, u = torch.randn(3000, 4, device="cuda"), torch.randn(3, 50000, device="cuda"), torch.rand(3, device="cuda")
+torch.cuda.synchronize()
+def step():
+    r = stf.route_tokens(x, 4, balance=True)
+    b = stf.balance_loss(x, r.experts)
+    return tuple(r) + (stf.route_tokens_grad(x, r, dw, 0.1), b.loss, stf.balance_loss_grad(x, b)) + \\
+        stf.sample_tokens(l, u, 0.8, 30, 0.9)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = step()
+for i in range(4):
+    x.copy_(torch.randn(3000, 500, device="cuda"))
+    l.copy_(torch.randn(3, 50000, device="cuda"))
+    want = step()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+    del want
+print("the same")
+"""
+
+
+def test_captured_without_a_call_before():
+    """The first calls of a process, inside a captured graph."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root)], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and r.stdout.strip().endswith("the same"), r.stderr[-2000:]
