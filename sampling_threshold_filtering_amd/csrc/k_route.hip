@@ -584,7 +584,10 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
     if (a.d_weights) {
       // the chosen entries: lane g takes slots g, g + G, ...; its first one stays in registers
       const T* xt = x + tr * a.ld;
-      auto weight = [&](u32 e) { return exp_f(to_f32(xt[e]) - row.top) * inv; };
+      // A normalised weight is of the exponentials themselves: the only one of its row is 1, and
+      // its gradient 0, exactly.
+      const float unit = a.normalize ? 1.f : inv;
+      auto weight = [&](u32 e) { return exp_f(to_f32(xt[e]) - row.top) * unit; };
       const bool first = row.live && first_e < a.E;
       const float p0 = first ? weight(first_e) : 0.f;
       const float d0 = first ? first_d : 0.f;  // where there is no expert d_weights may hold anything

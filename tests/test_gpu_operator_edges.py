@@ -379,3 +379,30 @@ def test_captured_without_a_call_before():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root)], capture_output=True, text=True, timeout=100)
     assert r.returncode == 0 and r.stdout.strip().endswith("the same"), r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E", [4, 13, 60, 138, 300, 1000])
+def test_the_only_weight_of_a_row_has_no_gradient(E, dtype):
+    """Normalised, a single chosen expert's weight is 1 whatever the logits are: its part of the
+    gradient is 0 exactly, and the loss's part, often far smaller than d_weights, keeps all of
+    its digits."""
+    import torch
+    rng = np.random.default_rng(E + 900)
+    T = 500
+    x = logits(rng, T, E, dtype)
+    dw = torch.from_numpy(rng.standard_normal((T, 1)).astype(np.float32)).cuda()
+    r = stf.route_tokens(x, 1, normalize=True, balance=True)
+    assert (r.weights == 1).all()
+    say("one weight", E, dtype)
+    for scale in (1.0, 1e10):
+        assert (stf.route_tokens_grad(x, r, dw * scale, None) == 0).all()
+        assert torch.equal(stf.route_tokens_grad(x, r, dw * scale, 1e-4), stf.route_tokens_grad(x, r, None, 1e-4))
+    k = min(E, 40)  # more slots, one live expert
+    y = torch.full_like(x, float("-inf"))
+    at = torch.from_numpy(rng.integers(0, E, T)).cuda()
+    y[torch.arange(T, device="cuda"), at] = x[:, 0]
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    r = stf.route_tokens(y, k, normalize=True)
+    assert (r.weights[:, 0] == 1).all() and (r.weights[:, 1:] == 0).all()
+    assert (stf.route_tokens_grad(y, r, dw, None) == 0).all()
