@@ -421,6 +421,92 @@ int profk_balance_loss_grad(const void* logits, int32_t dtype, int64_t T, int64_
                             int64_t k, const int64_t* counts, const int64_t* rows, const float* d_loss,
                             float d_loss_scale, void* out_d_logits, void* stream);
 
+/*
+ * Losses over given tokens.  Logits as above, V <= 2^24, T < 2^31
+ * (PROFK_EUNSUPPORTED); temperature in [2^-20, 2^20].  A row is live when its
+ * mask byte is nonzero (mask NULL: every row) and its token is in [0, V); other
+ * rows have log-probability 0, count nowhere and get gradient 0, whatever they
+ * hold.  For a live row
+ *   lp = x_token / temperature - ln sum_j exp(x_j / temperature)
+ * A token whose logit is -inf (so too in a row of -inf alone) has lp = -inf; it
+ * adds nothing to a loss and its row gets gradient 0 from one.  A row that holds
+ * a NaN or +inf has lp = NaN.  Probabilities below 2^-126 count as 0.  Sums over
+ * rows are in 64 bits and have the same bits on every run.  Gradients are of the
+ * logits' type, T*V contiguous, rounded once.  `scratch` as above, of at least
+ * profk_token_loss_scratch's size.
+ */
+int64_t profk_token_loss_scratch(int64_t T, int64_t V); /* bytes, or PROFK_EINVAL */
+
+/*
+ * profk_token_logprobs: lp of T rows (out_logprobs, device, T floats), and its
+ * gradient: of a scalar whose gradients with respect to lp are
+ * d_logprobs[t] * *d_scale * scale (d_scale: device, 1 float, or NULL: 1).
+ * A row of d_logprobs 0, or without a finite lp of its token (-inf), gets 0.
+ */
+int profk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
+                         const uint8_t* mask, float temperature, float* out_logprobs, void* scratch,
+                         int64_t scratch_bytes, void* stream);
+
+int profk_token_logprobs_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                              const int64_t* tokens, const uint8_t* mask, float temperature, const float* d_logprobs,
+                              const float* d_scale, float scale, void* out_d_logits, void* scratch,
+                              int64_t scratch_bytes, void* stream);
+
+/*
+ * profk_policy_loss: with ratio r = exp(lp - old), advantage A and q = ref - lp,
+ *   loss = sum over live rows of w (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                                   + kl_weight (e^q - 1 - q))
+ * w = weights[t], or 1 / (the number of live rows) where weights is NULL; ref
+ * NULL: no such term.  In the same pass, where out_d_logits is not NULL, the
+ * gradient of *d_loss * d_loss_scale * loss (d_loss: device, 1 float, or NULL: 1);
+ * where r A is clipped the first term has none.
+ *   out_loss, out_kl   device, 1 float each: the loss, and the sum of w (e^q - 1 - q)
+ *   out_clipped        device, 1 int64: the live rows whose first term is clipped
+ *   out_rows           device, 1 int64: the live rows
+ *   out_logprobs       device, T floats
+ */
+typedef struct profk_policy {
+  const float *old_logprobs, *advantages;  /* device, T each */
+  const float *ref_logprobs, *weights;     /* device, T each, or NULL */
+  float clip_low, clip_high, kl_weight;    /* each at least 0 */
+  int32_t reserved;
+} profk_policy;
+
+int profk_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
+                      const uint8_t* mask, float temperature, const profk_policy* how, float* out_loss, float* out_kl,
+                      int64_t* out_clipped, int64_t* out_rows, float* out_logprobs, const float* d_loss,
+                      float d_loss_scale, void* out_d_logits, void* scratch, int64_t scratch_bytes, void* stream);
+
+/*
+ * profk_preference_loss: sequence s is rows offsets[s] .. offsets[s + 1], s < 2 *
+ * pairs; sequence i is the preferred one of pair i, sequence pairs + i the other.
+ * With D_s the sum (`average`: the mean, 0 of none) over the sequence's live rows
+ * of lp - ref (ref_logprobs NULL: of lp),
+ *   z_i = beta (D_i - D_{pairs + i}) - margin
+ *   loss = mean over pairs of -(1 - smoothing) ln sigmoid(z) - smoothing ln sigmoid(-z)
+ * Offsets that decrease count as the largest before them, and as T beyond T; rows
+ * outside every sequence take no part.
+ *   out_loss              device, 1 float
+ *   out_margins           device, pairs floats: z
+ *   out_sequence_logprobs device, 2 * pairs floats: the sum (mean) of lp
+ *   out_rows              device, 1 int64: the live rows of all sequences
+ *   out_logprobs          device, T floats
+ *   out_coefficients      device, T floats: dloss / dlp, which
+ *                         profk_token_logprobs_grad takes as d_logprobs
+ */
+typedef struct profk_preference {
+  const int64_t* offsets;     /* device, 2 * pairs + 1 */
+  const float* ref_logprobs;  /* device, T, or NULL */
+  int64_t pairs;              /* at least 1, below 2^30 */
+  float beta, smoothing, margin;
+  int32_t average;
+} profk_preference;
+
+int profk_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
+                          const uint8_t* mask, float temperature, const profk_preference* how, float* out_loss,
+                          float* out_margins, float* out_sequence_logprobs, int64_t* out_rows, float* out_logprobs,
+                          float* out_coefficients, void* scratch, int64_t scratch_bytes, void* stream);
+
 /* Message for a status code (thread-local detail for PROFK_EHIP). */
 const char* profk_strerror(int code);
 

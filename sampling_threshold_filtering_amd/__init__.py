@@ -16,6 +16,10 @@ Language-model operators (operators.py), rows of logits turned into a choice:
   sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None)
   route_tokens(logits, k, normalize=True, mask=None, balance=False) and route_tokens_grad
   balance_loss(logits, experts, mask=None) and balance_loss_grad
+and the losses that train a policy on the tokens it drew:
+  token_logprobs(logits, tokens, mask=None, temperature=1.0) and token_logprobs_grad
+  policy_loss(logits, tokens, old_logprobs, advantages, ...) and policy_loss_and_grad
+  preference_loss(logits, tokens, offsets, ...) and preference_loss_grad
 """
 from __future__ import annotations
 
@@ -42,7 +46,9 @@ EXPORTED = ("profk_topk", "profk_topk_ex", "profk_topk_approx", "profk_topk_appr
             "profk_stage_sample", "profk_stage_threshold", "profk_stage_batched_sample", "profk_stage_filter",
             "profk_read_ceiling", "profk_strerror", "profk_release",
             "profk_sample_tokens_scratch", "profk_sample_tokens", "profk_route_scratch", "profk_route_tokens",
-            "profk_route_tokens_grad", "profk_balance_loss", "profk_balance_loss_grad")
+            "profk_route_tokens_grad", "profk_balance_loss", "profk_balance_loss_grad",
+            "profk_token_loss_scratch", "profk_token_logprobs", "profk_token_logprobs_grad", "profk_policy_loss",
+            "profk_preference_loss")
 
 
 class Options(ctypes.Structure):
@@ -139,8 +145,17 @@ def load_library():
                                             vp, vp]
     lib.profk_balance_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, vp]
     lib.profk_balance_loss_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, ctypes.c_float, vp, vp]
+    f32 = ctypes.c_float
+    rows = [vp, i32, i64, i64, i64, vp, vp, f32]  # logits and their layout, tokens, mask, temperature
+    lib.profk_token_loss_scratch.argtypes = [i64, i64]
+    lib.profk_token_loss_scratch.restype = i64
+    lib.profk_token_logprobs.argtypes = rows + [vp, vp, i64, vp]
+    lib.profk_token_logprobs_grad.argtypes = rows + [vp, vp, f32, vp, vp, i64, vp]
+    lib.profk_policy_loss.argtypes = rows + [vp, vp, vp, vp, vp, vp, vp, f32, vp, vp, i64, vp]
+    lib.profk_preference_loss.argtypes = rows + [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]
     for name in ("profk_sample_tokens", "profk_route_tokens", "profk_route_tokens_grad", "profk_balance_loss",
-                 "profk_balance_loss_grad"):
+                 "profk_balance_loss_grad", "profk_token_logprobs", "profk_token_logprobs_grad", "profk_policy_loss",
+                 "profk_preference_loss"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("profk_sample_tokens_scratch", "profk_route_scratch"):
         getattr(lib, name).restype = i64
@@ -453,5 +468,6 @@ def release():
     load_library().profk_release()
 
 
-from .operators import (Balance, Routing, balance_loss, balance_loss_grad, route_tokens,  # noqa: E402
-                        route_tokens_grad, sample_tokens)
+from .operators import (Balance, PolicyLoss, PreferenceLoss, Routing, balance_loss, balance_loss_grad,  # noqa: E402
+                        policy_loss, policy_loss_and_grad, preference_loss, preference_loss_grad, route_tokens,
+                        route_tokens_grad, sample_tokens, token_logprobs, token_logprobs_grad)

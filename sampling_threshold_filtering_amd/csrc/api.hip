@@ -1108,6 +1108,29 @@ int check_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t
   return PROFK_OK;
 }
 
+// What the losses over given tokens have in common.
+int vocab_args(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
+               const uint8_t* mask, float temperature, void* scratch, int64_t scratch_bytes, VocabArgs* a) {
+  if (!known_dtype(dtype) || T < 0 || V < 1 || ld < V) return PROFK_EINVAL;
+  if (!(temperature >= 0x1p-20f && temperature <= 0x1p20f)) return PROFK_EINVAL;
+  if (V > kTokMaxV || T > kOpMaxRows) return PROFK_EUNSUPPORTED;
+  if (T && (!logits || !tokens)) return PROFK_EINVAL;
+  const int rc = check_scratch(scratch, scratch_bytes, (int64_t)vocab_scratch_bytes((u64)T));
+  if (rc) return rc;
+  a->x = logits;
+  a->T = (u64)T;
+  a->V = (u64)V;
+  a->ld = (u64)ld;
+  a->tokens = tokens;
+  a->mask = mask;
+  a->inverse_temperature = 1.0 / (double)temperature;
+  const double exponent = 1.4426950408889634 / (double)temperature;
+  a->exponent_hi = (float)exponent;
+  a->exponent_lo = (float)(exponent - (double)a->exponent_hi);
+  a->scratch = (char*)scratch;
+  return PROFK_OK;
+}
+
 }  // namespace
 }  // namespace profk
 
@@ -1516,6 +1539,104 @@ int profk_balance_loss_grad(const void* logits, int32_t dtype, int64_t T, int64_
   if (!counts || !rows) return PROFK_EINVAL;
   return profk_route_tokens_grad(logits, dtype, T, E, ld, mask, k, 0, nullptr, nullptr, counts, rows, d_loss,
                                  d_loss_scale, out_d_logits, stream);
+}
+
+int64_t profk_token_loss_scratch(int64_t T, int64_t V) {
+  if (T < 0 || V < 1 || V > kTokMaxV || T > kOpMaxRows) return PROFK_EINVAL;
+  return (int64_t)vocab_scratch_bytes((u64)T);
+}
+
+int profk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
+                         const uint8_t* mask, float temperature, float* out_logprobs, void* scratch,
+                         int64_t scratch_bytes, void* stream) {
+  VocabArgs a{};
+  const int rc = vocab_args(logits, dtype, T, V, ld, tokens, mask, temperature, scratch, scratch_bytes, &a);
+  if (rc) return rc;
+  if (T == 0) return PROFK_OK;
+  if (!out_logprobs) return PROFK_EINVAL;
+  a.logprobs = out_logprobs;
+  HIPCHK(launch_vocab(a, dtype, (hipStream_t)stream), "launch token log-probabilities");
+  return PROFK_OK;
+}
+
+int profk_token_logprobs_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                              const int64_t* tokens, const uint8_t* mask, float temperature, const float* d_logprobs,
+                              const float* d_scale, float scale, void* out_d_logits, void* scratch,
+                              int64_t scratch_bytes, void* stream) {
+  VocabArgs a{};
+  const int rc = vocab_args(logits, dtype, T, V, ld, tokens, mask, temperature, scratch, scratch_bytes, &a);
+  if (rc) return rc;
+  if (T == 0) return PROFK_OK;
+  if (!d_logprobs || !out_d_logits) return PROFK_EINVAL;
+  a.given = d_logprobs;
+  a.d_loss = d_scale;
+  a.d_loss_scale = scale;
+  a.d_x = out_d_logits;
+  HIPCHK(launch_vocab(a, dtype, (hipStream_t)stream), "launch token log-probabilities' gradient");
+  return PROFK_OK;
+}
+
+int profk_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
+                      const uint8_t* mask, float temperature, const profk_policy* how, float* out_loss, float* out_kl,
+                      int64_t* out_clipped, int64_t* out_rows, float* out_logprobs, const float* d_loss,
+                      float d_loss_scale, void* out_d_logits, void* scratch, int64_t scratch_bytes, void* stream) {
+  VocabArgs a{};
+  const int rc = vocab_args(logits, dtype, T, V, ld, tokens, mask, temperature, scratch, scratch_bytes, &a);
+  if (rc) return rc;
+  if (!how || !out_loss || !out_kl || !out_clipped || !out_rows) return PROFK_EINVAL;
+  if (T && (!how->old_logprobs || !how->advantages || !out_logprobs)) return PROFK_EINVAL;
+  if (!(how->clip_low >= 0.f) || !(how->clip_high >= 0.f) || !(how->kl_weight >= 0.f) || std::isinf(how->kl_weight))
+    return PROFK_EINVAL;
+  a.policy = true;
+  a.old = how->old_logprobs;
+  a.advantages = how->advantages;
+  a.ref = how->ref_logprobs;
+  a.weights = how->weights;
+  a.clip_low = 1.f - how->clip_low;
+  a.clip_high = 1.f + how->clip_high;
+  a.kl_weight = how->kl_weight;
+  a.loss = out_loss;
+  a.kl = out_kl;
+  a.clipped = out_clipped;
+  a.rows = out_rows;
+  a.logprobs = out_logprobs;
+  a.d_loss = d_loss;
+  a.d_loss_scale = d_loss_scale;
+  a.d_x = out_d_logits;
+  HIPCHK(launch_vocab(a, dtype, (hipStream_t)stream), "launch policy loss");
+  return PROFK_OK;
+}
+
+int profk_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
+                          const uint8_t* mask, float temperature, const profk_preference* how, float* out_loss,
+                          float* out_margins, float* out_sequence_logprobs, int64_t* out_rows, float* out_logprobs,
+                          float* out_coefficients, void* scratch, int64_t scratch_bytes, void* stream) {
+  PairArgs p{};
+  const int rc = vocab_args(logits, dtype, T, V, ld, tokens, mask, temperature, scratch, scratch_bytes, &p.v);
+  if (rc) return rc;
+  if (!how || how->pairs < 1 || !how->offsets || !out_loss || !out_margins || !out_sequence_logprobs || !out_rows)
+    return PROFK_EINVAL;
+  if (how->pairs >= (int64_t(1) << 30)) return PROFK_EUNSUPPORTED;
+  if (T && (!out_logprobs || !out_coefficients)) return PROFK_EINVAL;
+  if (!std::isfinite(how->beta) || !std::isfinite(how->margin) || !(how->smoothing >= 0.f && how->smoothing <= 1.f))
+    return PROFK_EINVAL;
+  p.v.pairs = true;
+  p.v.logprobs = out_logprobs;
+  HIPCHK(launch_vocab(p.v, dtype, (hipStream_t)stream), "launch token log-probabilities");
+  p.v.ref = how->ref_logprobs;
+  p.v.loss = out_loss;
+  p.v.rows = out_rows;
+  p.offsets = how->offsets;
+  p.pairs = (u64)how->pairs;
+  p.beta = (double)how->beta;
+  p.smoothing = (double)how->smoothing;
+  p.margin = (double)how->margin;
+  p.average = how->average != 0;
+  p.margins = out_margins;
+  p.sequence_logprobs = out_sequence_logprobs;
+  p.coefficients = out_coefficients;
+  HIPCHK(launch_pairs(p, (hipStream_t)stream), "launch preference loss");
+  return PROFK_OK;
 }
 
 const char* profk_strerror(int code) {

@@ -44,22 +44,6 @@ constexpr u32 kTurnsInRegisters = 4;  // rows a lane sums in 32 bits
 constexpr u32 kMostFinishing = kRouteMaxExperts / kFinishExperts;
 constexpr size_t kRouteScratchHead = 256 + 8 * kMostFinishing;
 
-// Sum / maximum over the G lanes of a group; every lane gets the result.  Within 16 lanes
-// the partner is a mirrored one, which holds the same partial result as the one across.
-template <int CTRL, class V>
-__device__ __forceinline__ V dpp(V v) {
-  return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
-}
-template <int G, class V, class F>
-__device__ __forceinline__ V group_reduce(V v, F f) {
-  if constexpr (G > 1) v = f(v, dpp<0xB1>(v));    // quad_perm [1,0,3,2]
-  if constexpr (G > 2) v = f(v, dpp<0x4E>(v));    // quad_perm [2,3,0,1]
-  if constexpr (G > 4) v = f(v, dpp<0x141>(v));   // row_half_mirror
-  if constexpr (G > 8) v = f(v, dpp<0x140>(v));   // row_mirror
-  if constexpr (G > 16) v = f(v, __shfl_xor(v, 16));
-  if constexpr (G > 32) v = f(v, __shfl_xor(v, 32));
-  return v;
-}
 template <int G>
 __device__ __forceinline__ u64 group_reduce64(u64 v) {  // the maximum
 #pragma unroll
@@ -70,8 +54,6 @@ __device__ __forceinline__ u64 group_reduce64(u64 v) {  // the maximum
   return v;
 }
 
-__device__ __forceinline__ float add_f(float a, float b) { return a + b; }
-__device__ __forceinline__ float max_f(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ u32 max_u(u32 a, u32 b) { return a > b ? a : b; }
 
 // e^x for x <= 0 to about one unit in the last place: the rounding of x log2(e), which
@@ -91,21 +73,6 @@ template <class T>
 struct alignas(4 * sizeof(T)) Four {
   T e[4];
 };
-
-constexpr float kNone = -__builtin_huge_valf();
-
-// The largest of three, as one instruction also where the compiler cannot know that none
-// is a signalling NaN.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
-
-// Four entries of -inf in the words of a load.
-template <class T> struct NoneWord { static constexpr u32 value = 0xFF800000u; };
-template <> struct NoneWord<Half16> { static constexpr u32 value = 0xFC00FC00u; };
-template <> struct NoneWord<Brain16> { static constexpr u32 value = 0xFF80FF80u; };
 
 // One row in registers: C entries per lane.  QUAD: four neighbours at a time.
 template <int G, int C, bool QUAD>

@@ -102,13 +102,6 @@ __device__ __forceinline__ V wave_min(V v) {
   return of_lane(wave_scan(v, (V)~(V)0, [](V x, V y) { return x < y ? x : y; }), kWave - 1);
 }
 
-// A barrier that waits for LDS accesses alone: loads from memory stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // The value of the lane across in a quad: quad_perm [1,0,3,2] or [2,3,0,1].
 template <int CTRL>
 __device__ __forceinline__ u32 quad_xor(u32 v) {

@@ -333,6 +333,43 @@ size_t route_scratch_bytes(u64 T, u32 E);
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s);
 
+// The log-probabilities of given tokens and the losses over them (k_vocab.hip).
+struct VocabArgs {
+  const void* x;  // logits, row t at x + t * ld entries
+  u64 T, V, ld;
+  const int64_t* tokens;       // T
+  const unsigned char* mask;   // nonzero: the row takes part; or nullptr
+  double inverse_temperature;
+  float exponent_hi, exponent_lo;  // log2(e) / temperature
+  // each row's coefficient of the gradient, or nullptr
+  const float* given;
+  bool policy;                 // the policy loss
+  const float *old, *advantages, *ref, *weights;  // T each; the last two may be nullptr
+  float clip_low, clip_high;   // the ratio's borders
+  float kl_weight;
+  const float* d_loss;         // 1, or nullptr
+  float d_loss_scale;
+  float* logprobs;             // T, or nullptr
+  bool pairs;                  // launch_pairs follows: the log-probabilities go to scratch in 64 bits too
+  float *loss, *kl;            // 1 each: with the policy loss
+  int64_t *clipped, *rows;
+  void* d_x;                   // T * V, contiguous, of the logits' type, or nullptr: no gradient
+  char* scratch;               // vocab_scratch_bytes
+  u32 count_blocks;            // set by launch_vocab
+};
+// The preference loss over the log-probabilities that launch_vocab left in scratch.
+struct PairArgs {
+  VocabArgs v;
+  const int64_t* offsets;      // 2 * pairs + 1
+  u64 pairs;
+  double beta, smoothing, margin;
+  bool average;
+  float *margins, *sequence_logprobs, *coefficients;  // pairs, 2 * pairs, T
+};
+size_t vocab_scratch_bytes(u64 T);
+hipError_t launch_vocab(VocabArgs a, int dtype, hipStream_t s);
+hipError_t launch_pairs(const PairArgs& a, hipStream_t s);
+
 hipError_t launch_sort_and_write(u64* buf0, u64* buf1, u32* hist, u32 k, const float* row, u64 N, float* out_vals,
                                  int64_t* out_idx, RowCtl* ctl, AttemptRecord* rec, hipStream_t s);
 u64 sort_hist_words(u64 k);

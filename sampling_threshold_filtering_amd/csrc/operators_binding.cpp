@@ -13,6 +13,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
+
 #include "profk.h"
 
 namespace {
@@ -313,6 +315,122 @@ PyObject* balance_grad(PyObject* const* a) {
   return rc ? status(rc) : THPVariable_Wrap(dx);
 }
 
+float temperature_of(PyObject* o) {
+  const double t = number(o, "temperature");
+  if (!(t >= 0x1p-20 && t <= 0x1p20)) refuse("temperature must be within 2^-20 .. 2^20");
+  return (float)t;
+}
+
+// What the losses over given tokens have in common: one token per row, the mask, scratch.
+struct TokenRows {
+  Logits x;
+  at::Tensor tokens, mask;
+  float temperature;
+  int64_t need;
+  TokenRows(PyObject* logits, PyObject* tok, PyObject* m, PyObject* temp) : x(logits) {
+    no_tangent(x.x, "logits");
+    if (tok == Py_None) refuse("tokens must be a tensor");
+    tokens = vector(tok, "tokens", "int64", x.rows, at::kLong, x);
+    mask = vector(m, "mask", "bool", x.rows, at::kBool, x);
+    temperature = temperature_of(temp);
+    need = profk_token_loss_scratch(x.rows, x.cols);
+  }
+  at::Tensor row_values(PyObject* o, const char* name, bool needed) const {
+    if (needed && o == Py_None) refuse(std::string(name) + " must be a tensor");
+    const at::Tensor v = vector(o, name, "float32", x.rows, at::kFloat, x);
+    no_tangent(v, name);
+    return v;
+  }
+};
+
+// token_logprobs(logits, tokens, mask, temperature, stream)
+PyObject* token_logprobs(PyObject* const* a) {
+  const TokenRows r(a[0], a[1], a[2], a[3]);
+  if (r.need < 0) return status(PROFK_EUNSUPPORTED);
+  const Scratch scratch(r.x, r.need);
+  const at::Tensor logprobs = r.x.empty({r.x.rows}, at::kFloat);
+  const int rc = profk_token_logprobs(r.x.x.data_ptr(), r.x.dtype, r.x.rows, r.x.cols, r.x.ld,
+                                      address<const int64_t>(r.tokens), address<const uint8_t>(r.mask), r.temperature,
+                                      address<float>(logprobs), scratch.get(), scratch.bytes, stream_of(a[4]));
+  return rc ? status(rc) : THPVariable_Wrap(logprobs);
+}
+
+// token_logprobs_grad(logits, tokens, d_logprobs, d_loss, mask, temperature, stream)
+PyObject* token_logprobs_grad(PyObject* const* a) {
+  const TokenRows r(a[0], a[1], a[4], a[5]);
+  if (r.need < 0) return status(PROFK_EUNSUPPORTED);
+  const at::Tensor d = r.row_values(a[2], "d_logprobs", true);
+  const LossScale s(a[3], r.x);
+  const Scratch scratch(r.x, r.need);
+  const at::Tensor dx = r.x.empty({r.x.rows, r.x.cols}, r.x.x.scalar_type());
+  const int rc = profk_token_logprobs_grad(
+      r.x.x.data_ptr(), r.x.dtype, r.x.rows, r.x.cols, r.x.ld, address<const int64_t>(r.tokens),
+      address<const uint8_t>(r.mask), r.temperature, address<const float>(d), address<const float>(s.value),
+      (float)s.factor, dx.data_ptr(), scratch.get(), scratch.bytes, stream_of(a[6]));
+  return rc ? status(rc) : THPVariable_Wrap(dx);
+}
+
+// policy(logits, tokens, old, advantages, ref, weights, mask, clip_low, clip_high, kl_weight, temperature, d_loss,
+// stream); d_loss None: no gradient
+PyObject* policy(PyObject* const* a) {
+  const TokenRows r(a[0], a[1], a[6], a[10]);
+  if (r.need < 0) return status(PROFK_EUNSUPPORTED);
+  const at::Tensor old = r.row_values(a[2], "old_logprobs", true), adv = r.row_values(a[3], "advantages", true),
+                   ref = r.row_values(a[4], "ref_logprobs", false), weights = r.row_values(a[5], "weights", false);
+  const double low = number(a[7], "clip_low"), high = number(a[8], "clip_high"), kl = number(a[9], "kl_weight");
+  if (!(low >= 0 && high >= 0 && kl >= 0 && kl < 3e38)) refuse("need clip_low >= 0, clip_high >= 0 and a finite kl_weight >= 0");
+  if (kl > 0 && !ref.defined()) refuse("a kl_weight needs ref_logprobs");
+  const bool grad = a[11] != Py_None;
+  at::Tensor d_loss, dx;
+  double factor = 1;
+  if (grad) {
+    const LossScale s(a[11], r.x);
+    d_loss = s.value;
+    factor = s.factor;
+    dx = r.x.empty({r.x.rows, r.x.cols}, r.x.x.scalar_type());
+  }
+  const Scratch scratch(r.x, r.need);
+  const at::Tensor loss = r.x.empty({}, at::kFloat), logprobs = r.x.empty({r.x.rows}, at::kFloat),
+                   gap = r.x.empty({}, at::kFloat), clipped = r.x.empty({}, at::kLong), rows = r.x.empty({}, at::kLong);
+  const profk_policy how = {address<const float>(old),     address<const float>(adv), address<const float>(ref),
+                            address<const float>(weights), (float)low,                (float)high,
+                            (float)kl,                     0};
+  const int rc = profk_policy_loss(
+      r.x.x.data_ptr(), r.x.dtype, r.x.rows, r.x.cols, r.x.ld, address<const int64_t>(r.tokens),
+      address<const uint8_t>(r.mask), r.temperature, &how, address<float>(loss), address<float>(gap),
+      address<int64_t>(clipped), address<int64_t>(rows), address<float>(logprobs), address<const float>(d_loss),
+      (float)factor, address<void>(dx), scratch.get(), scratch.bytes, stream_of(a[12]));
+  return rc ? status(rc) : result({loss, logprobs, gap, clipped, rows, dx});
+}
+
+// preference(logits, tokens, offsets, ref, mask, beta, smoothing, margin, average, temperature, stream)
+PyObject* preference(PyObject* const* a) {
+  const TokenRows r(a[0], a[1], a[4], a[9]);
+  if (r.need < 0) return status(PROFK_EUNSUPPORTED);
+  at::Tensor offsets = tensor(a[2], "offsets");
+  if (offsets.dim() != 1 || offsets.size(0) < 3 || offsets.size(0) % 2 == 0 || offsets.scalar_type() != at::kLong ||
+      offsets.device() != r.x.x.device())
+    refuse("offsets must be 2 * pairs + 1 int64 values on " + r.x.x.device().str());
+  offsets = offsets.contiguous();
+  const int64_t pairs = offsets.size(0) / 2;
+  const at::Tensor ref = r.row_values(a[3], "ref_logprobs", false);
+  const double beta = number(a[5], "beta"), smoothing = number(a[6], "smoothing"), margin = number(a[7], "margin");
+  if (!(std::abs(beta) < 3e38 && std::abs(margin) < 3e38 && smoothing >= 0 && smoothing <= 1))
+    refuse("need a finite beta and margin and 0 <= smoothing <= 1");
+  const profk_preference how = {address<const int64_t>(offsets), address<const float>(ref), pairs,         (float)beta,
+                                (float)smoothing,                (float)margin,             truth(a[8], "average")};
+  const Scratch scratch(r.x, r.need);
+  const at::Tensor loss = r.x.empty({}, at::kFloat), margins = r.x.empty({pairs}, at::kFloat),
+                   sums = r.x.empty({2 * pairs}, at::kFloat), rows = r.x.empty({}, at::kLong),
+                   logprobs = r.x.empty({r.x.rows}, at::kFloat), coefficients = r.x.empty({r.x.rows}, at::kFloat);
+  const int rc = profk_preference_loss(
+      r.x.x.data_ptr(), r.x.dtype, r.x.rows, r.x.cols, r.x.ld, address<const int64_t>(r.tokens),
+      address<const uint8_t>(r.mask), r.temperature, &how, address<float>(loss), address<float>(margins),
+      address<float>(sums), address<int64_t>(rows), address<float>(logprobs), address<float>(coefficients),
+      scratch.get(), scratch.bytes, stream_of(a[10]));
+  return rc ? status(rc) : result({loss, margins, sums, rows, logprobs, coefficients});
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -336,7 +454,10 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<sample, 8>("sample"),       method<route, 6>("route"),
                          method<route_grad, 9>("route_grad"), method<balance, 4>("balance"),
-                         method<balance_grad, 7>("balance_grad"), {nullptr, nullptr, 0, nullptr}};
+                         method<balance_grad, 7>("balance_grad"),
+                         method<token_logprobs, 5>("token_logprobs"),
+                         method<token_logprobs_grad, 7>("token_logprobs_grad"), method<policy, 13>("policy"),
+                         method<preference, 11>("preference"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operators", nullptr, -1, methods};
 

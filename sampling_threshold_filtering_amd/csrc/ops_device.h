@@ -1,5 +1,5 @@
-// Reading logits of any of the three types, shared by the language-model operators
-// (k_tokens.hip, k_route.hip).
+// Reading logits of any of the three types, and what else the language-model operators
+// share (k_tokens.hip, k_route.hip, k_vocab.hip).
 #pragma once
 
 #include "profk_device.h"
@@ -27,5 +27,46 @@ __device__ __forceinline__ void from_f32(float v, Brain16& out) {
   const __bf16 b = (__bf16)v;  // one instruction on gfx950
   __builtin_memcpy(&out.bits, &b, 2);
 }
+
+constexpr float kNone = -__builtin_huge_valf();
+
+// The largest of three, as one instruction also where the compiler cannot know that none
+// is a signalling NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// Entries of -inf in the words of a load.
+template <class T> struct NoneWord { static constexpr u32 value = 0xFF800000u; };
+template <> struct NoneWord<Half16> { static constexpr u32 value = 0xFC00FC00u; };
+template <> struct NoneWord<Brain16> { static constexpr u32 value = 0xFF80FF80u; };
+
+// A barrier that waits for LDS accesses alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Sum / maximum over the G lanes of a group; every lane gets the result.  Within 16 lanes
+// the partner is a mirrored one, which holds the same partial result as the one across.
+template <int CTRL, class V>
+__device__ __forceinline__ V dpp(V v) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+template <int G, class V, class F>
+__device__ __forceinline__ V group_reduce(V v, F f) {
+  if constexpr (G > 1) v = f(v, dpp<0xB1>(v));    // quad_perm [1,0,3,2]
+  if constexpr (G > 2) v = f(v, dpp<0x4E>(v));    // quad_perm [2,3,0,1]
+  if constexpr (G > 4) v = f(v, dpp<0x141>(v));   // row_half_mirror
+  if constexpr (G > 8) v = f(v, dpp<0x140>(v));   // row_mirror
+  if constexpr (G > 16) v = f(v, __shfl_xor(v, 16));
+  if constexpr (G > 32) v = f(v, __shfl_xor(v, 32));
+  return v;
+}
+__device__ __forceinline__ float add_f(float a, float b) { return a + b; }
+__device__ __forceinline__ float max_f(float a, float b) { return __builtin_fmaxf(a, b); }
 
 }  // namespace profk

@@ -3,14 +3,17 @@
   sample_tokens      a token per row: temperature, top-k, top-p, min-p, given uniform numbers
   route_tokens       the k experts of a token, gate weights, per-expert counts, balance loss
   balance_loss       the balance loss and counts of a choice made elsewhere
+  token_logprobs     the log-probabilities of given tokens
+  policy_loss        the clipped policy loss of drawn tokens, with a KL term
+  preference_loss    the loss of pairs of sequences, by their log ratios to a reference
   *_grad             their gradients with respect to the logits
 
 Formulas, ties, empty rows and limits: include/profk.h.  Every call is enqueued on the
 current stream of the logits' device and waits for nothing; outputs and scratch come from
 torch's allocator, so calls may be captured into a graph without a first call.
-route_tokens and balance_loss are differentiable (backward, once) where the logits require a
-gradient; a forward-mode tangent is refused.  sample_tokens' results and the gradients by name
-are constants to autograd.
+All but sample_tokens are differentiable (backward, once) with respect to the logits, where
+those require a gradient; a forward-mode tangent is refused.  Their other inputs, sample_tokens'
+results and the gradients by name are constants to autograd.
 
 The checks of arguments, the outputs and the library's call are one compiled step
 (csrc/operators_binding.cpp): a call takes 3 to 60 us on the GPU, and from Python the same
@@ -35,6 +38,23 @@ class Sampling(ctypes.Structure):
     ]
 
 
+class PolicySettings(ctypes.Structure):
+    """profk_policy"""
+    _fields_ = [
+        ("old_logprobs", ctypes.c_void_p), ("advantages", ctypes.c_void_p), ("ref_logprobs", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p), ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+        ("kl_weight", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+class PreferenceSettings(ctypes.Structure):
+    """profk_preference"""
+    _fields_ = [
+        ("offsets", ctypes.c_void_p), ("ref_logprobs", ctypes.c_void_p), ("pairs", ctypes.c_int64),
+        ("beta", ctypes.c_float), ("smoothing", ctypes.c_float), ("margin", ctypes.c_float), ("average", ctypes.c_int32),
+    ]
+
+
 class Routing(NamedTuple):
     """weights [T, k] float32, experts [T, k] int64 (-1: none), counts [E] int64, rows int64
     (the live rows), loss float32 or None."""
@@ -51,6 +71,27 @@ class Balance(NamedTuple):
     counts: object
     rows: object
     k: int
+
+
+class PolicyLoss(NamedTuple):
+    """loss float32, logprobs [T] float32, kl float32 (the weighted sum of e^q - 1 - q), clipped
+    int64 (live rows whose ratio is clipped), rows int64 (the live rows)."""
+    loss: object
+    logprobs: object
+    kl: object
+    clipped: object
+    rows: object
+
+
+class PreferenceLoss(NamedTuple):
+    """loss float32, margins [pairs] float32, sequence_logprobs [2 * pairs] float32, rows int64
+    (the live rows), logprobs [T] float32, coefficients [T] float32 (dloss / dlogprobs)."""
+    loss: object
+    margins: object
+    sequence_logprobs: object
+    rows: object
+    logprobs: object
+    coefficients: object
 
 
 # set together, at first use; the last two are looked up once (0.1 us each time)
@@ -164,6 +205,92 @@ def balance_loss_grad(logits, balance: Balance, d_loss=1.0, mask=None):
                  mask)
 
 
+def token_logprobs(logits, tokens, mask=None, temperature=1.0):
+    """The log-probability [T] float32 of each row's token (tokens [T] int64) under the softmax
+    of logits [T, V] / temperature (fp32, fp16 or bf16; rows may be strided).  Rows whose `mask`
+    ([T] bool) is False or whose token is outside [0, V) give 0; a token whose logit is -inf
+    gives -inf, a row with a NaN or +inf NaN.  Differentiable with respect to the logits."""
+    if logits.requires_grad:
+        import torch
+        if torch.is_grad_enabled():
+            return _loss_functions().logprobs(logits, tokens, mask, temperature)
+    return _call(logits, (_module or _native()).token_logprobs, logits, tokens, mask, temperature)
+
+
+def token_logprobs_grad(logits, tokens, d_logprobs, mask=None, temperature=1.0, d_loss=1.0):
+    """The gradient with respect to the logits (their type, contiguous) of a scalar whose
+    gradients with respect to token_logprobs' result are d_loss (a number or one float32 value)
+    times d_logprobs [T] float32.  A row of d_logprobs 0 and one whose token has logit -inf get
+    0.  One pass over the logits; the forward pass need not have run."""
+    return _call(logits, (_module or _native()).token_logprobs_grad, logits, tokens, d_logprobs, d_loss, mask, temperature)
+
+
+def _policy(logits, tokens, old_logprobs, advantages, ref_logprobs, weights, mask, clip_low, clip_high, kl_weight,
+            temperature, d_loss):
+    return _call(logits, (_module or _native()).policy, logits, tokens, old_logprobs, advantages, ref_logprobs, weights,
+                 mask, clip_low, clip_high, kl_weight, temperature, d_loss)
+
+
+def policy_loss(logits, tokens, old_logprobs, advantages, ref_logprobs=None, weights=None, mask=None, clip_low=0.2,
+                clip_high=0.2, kl_weight=0.0, temperature=1.0) -> PolicyLoss:
+    """The clipped policy loss of tokens [T] int64 that a policy of log-probabilities
+    old_logprobs drew, under logits [T, V] / temperature: a PolicyLoss.  With r = exp(logprob -
+    old), advantage A and q = ref - logprob, its loss is the sum over live rows of
+      weight (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_weight (e^q - 1 - q))
+    with weights [T], or 1 / (the number of live rows) without them; no last term without
+    ref_logprobs.  The values per row are float32.  Rows whose `mask` ([T] bool) is False or
+    whose token is outside [0, V) take no part; a token whose logit is -inf adds nothing.  Only
+    loss is differentiable, and only with respect to the logits."""
+    if logits.requires_grad:
+        import torch
+        if torch.is_grad_enabled():
+            return _loss_functions().policy(logits, tokens, old_logprobs, advantages, ref_logprobs, weights, mask,
+                                            clip_low, clip_high, kl_weight, temperature)
+    return PolicyLoss(*_policy(logits, tokens, old_logprobs, advantages, ref_logprobs, weights, mask, clip_low,
+                               clip_high, kl_weight, temperature, None)[:5])
+
+
+def policy_loss_and_grad(logits, tokens, old_logprobs, advantages, ref_logprobs=None, weights=None, mask=None,
+                         clip_low=0.2, clip_high=0.2, kl_weight=0.0, temperature=1.0, d_loss=1.0):
+    """(policy_loss of the same arguments, its gradient with respect to the logits) in one pass:
+    the gradient (the logits' type, contiguous) of a scalar whose gradient with respect to the
+    loss is d_loss, a number or one float32 value."""
+    if d_loss is None:
+        raise ValueError("d_loss must be a number or one float32 value")
+    r = _policy(logits, tokens, old_logprobs, advantages, ref_logprobs, weights, mask, clip_low, clip_high, kl_weight,
+                temperature, d_loss)
+    return PolicyLoss(*r[:5]), r[5]
+
+
+def _preference(logits, tokens, offsets, ref_logprobs, mask, beta, smoothing, margin, average, temperature):
+    return PreferenceLoss(*_call(logits, (_module or _native()).preference, logits, tokens, offsets, ref_logprobs, mask,
+                                 beta, smoothing, margin, average, temperature))
+
+
+def preference_loss(logits, tokens, offsets, ref_logprobs=None, mask=None, beta=0.1, smoothing=0.0, margin=0.0,
+                    average=False, temperature=1.0) -> PreferenceLoss:
+    """The loss of pairs of sequences, the first preferred: a PreferenceLoss.  Sequence s is rows
+    offsets[s] .. offsets[s + 1] of logits [T, V] and tokens [T] (offsets [2 * pairs + 1] int64 on
+    the device); pair i is sequences i and pairs + i.  With D the sum over a sequence's live rows
+    of logprob - ref_logprobs [T] (`average`: the mean), z = beta (D_i - D_{pairs + i}) - margin
+    and loss = mean of -(1 - smoothing) ln sigmoid(z) - smoothing ln sigmoid(-z).  Rows whose
+    `mask` ([T] bool) is False or whose token is outside [0, V) take no part; a token whose logit
+    is -inf adds nothing.  Only loss is differentiable, and only with respect to the logits."""
+    if logits.requires_grad:
+        import torch
+        if torch.is_grad_enabled():
+            return _loss_functions().preference(logits, tokens, offsets, ref_logprobs, mask, beta, smoothing, margin,
+                                                average, temperature)
+    return _preference(logits, tokens, offsets, ref_logprobs, mask, beta, smoothing, margin, average, temperature)
+
+
+def preference_loss_grad(logits, tokens, preference: PreferenceLoss, d_loss=1.0, mask=None, temperature=1.0):
+    """The gradient with respect to the logits (their type, contiguous) of a scalar whose
+    gradient with respect to preference_loss' loss is d_loss (a number or one float32 value).
+    The other arguments are those of the call that gave `preference`."""
+    return token_logprobs_grad(logits, tokens, preference.coefficients, mask, temperature, d_loss)
+
+
 _functions = None
 
 
@@ -222,3 +349,77 @@ def _route_function():
 
     _functions = Functions
     return _functions
+
+
+_losses = None
+
+
+def _loss_functions():
+    """As _route_function, of the losses over given tokens."""
+    global _losses
+    if _losses is not None:
+        return _losses
+    import torch
+
+    class LogprobsFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, tokens, mask, temperature):
+            ctx.save_for_backward(logits, tokens, mask)
+            ctx.temperature = temperature
+            return _call(logits, (_module or _native()).token_logprobs, logits, tokens, mask, temperature)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, d_logprobs):
+            logits, tokens, mask = ctx.saved_tensors
+            return token_logprobs_grad(logits, tokens, d_logprobs, mask, ctx.temperature), None, None, None
+
+    class PolicyFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, tokens, old, advantages, ref, weights, mask, *settings):
+            ctx.save_for_backward(logits, tokens, old, advantages, ref, weights, mask)
+            ctx.settings = settings
+            r = _policy(logits, tokens, old, advantages, ref, weights, mask, *settings, None)[:5]
+            ctx.mark_non_differentiable(*r[1:])
+            ctx.set_materialize_grads(False)
+            return r
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, d_loss, *constants):
+            if d_loss is None:
+                return (None,) * 11
+            # the loss again, beside the gradient: one pass over the logits either way
+            return (_policy(*ctx.saved_tensors, *ctx.settings, d_loss)[5],) + (None,) * 10
+
+    class PreferenceFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, tokens, offsets, ref, mask, *settings):
+            r = _preference(logits, tokens, offsets, ref, mask, *settings)
+            ctx.save_for_backward(logits, tokens, mask, r.coefficients)
+            ctx.temperature = settings[-1]
+            ctx.mark_non_differentiable(*r[1:])
+            ctx.set_materialize_grads(False)
+            return tuple(r)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, d_loss, *constants):
+            if d_loss is None:
+                return (None,) * 10
+            logits, tokens, mask, coefficients = ctx.saved_tensors
+            return (token_logprobs_grad(logits, tokens, coefficients, mask, ctx.temperature, d_loss),) + (None,) * 9
+
+    class Functions:
+        logprobs = staticmethod(LogprobsFunction.apply)
+
+        @staticmethod
+        def policy(*args):
+            return PolicyLoss(*PolicyFunction.apply(*args))
+
+        @staticmethod
+        def preference(*args):
+            return PreferenceLoss(*PreferenceFunction.apply(*args))
+
+    _losses = Functions
+    return _losses
