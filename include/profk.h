@@ -409,6 +409,44 @@ int profk_route_tokens_grad(const void* logits, int32_t dtype, int64_t T, int64_
                             void* out_d_logits, void* stream);
 
 /*
+ * profk_route_scored: routing by scores.  s = softmax(row) (PROFK_SOFTMAX) or
+ * s_e = 1 / (1 + exp(-l_e)) (PROFK_SIGMOID); the choice score is c = s + bias.
+ * An expert whose logit or bias is -inf is never chosen.  The experts are in
+ * `groups` equal groups of neighbours, a group's score the sum of its
+ * `group_best` (1 or 2) largest choice scores; of the top_groups best groups the
+ * first k experts by choice score are chosen.  Ties go to the lower index, NaN
+ * first; scores are compared as 64-bit arithmetic gives them.  The gate weights
+ * are scale * s, with `normalize` scale * s over the chosen ones' sum (0 where
+ * that is 0).  Live rows, empty slots, counts, rows, scratch and limits as for
+ * profk_route_tokens; loss = E * sum_e f_e P_e with P the mean of s / sum_e s.
+ * Limits: groups <= 64 (PROFK_EUNSUPPORTED).
+ *
+ * profk_route_scored_grad: as profk_route_tokens_grad (bias and groups only
+ * steer the choice and have no gradient).
+ */
+#define PROFK_SOFTMAX 0
+#define PROFK_SIGMOID 1
+#define PROFK_ROUTE_MAX_GROUPS 64
+
+typedef struct profk_scoring {
+  int32_t scores;                          /* PROFK_SOFTMAX or PROFK_SIGMOID */
+  int32_t groups, top_groups, group_best;  /* E a multiple of groups; 1 <= top_groups <= groups */
+  float scale;                             /* finite */
+  int32_t normalize;
+  const float* bias;                       /* device, E, or NULL */
+} profk_scoring;
+
+int profk_route_scored(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                       int64_t k, const profk_scoring* how, float* out_weights, int64_t* out_experts,
+                       int64_t* out_counts, int64_t* out_rows, float* out_loss, void* scratch, int64_t scratch_bytes,
+                       void* stream);
+
+int profk_route_scored_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                            int64_t k, int32_t normalize, int32_t scores, float scale, const int64_t* experts,
+                            const float* d_weights, const int64_t* counts, const int64_t* rows, const float* d_loss,
+                            float d_loss_scale, void* out_d_logits, void* stream);
+
+/*
  * profk_balance_loss / profk_balance_loss_grad: the same loss, counts and
  * gradient for a choice made elsewhere (experts, T*k int64; entries outside
  * [0, E) are dropped slots: not counted, and n k stays the divisor).

@@ -14,7 +14,8 @@ Functions mirror include/profk.h:
 
 Language-model operators (operators.py), rows of logits turned into a choice:
   sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None)
-  route_tokens(logits, k, normalize=True, mask=None, balance=False) and route_tokens_grad
+  route_tokens(logits, k, normalize=True, mask=None, balance=False) and route_tokens_grad,
+    also by sigmoid scores, with a bias for balance, groups of experts and a scale
   balance_loss(logits, experts, mask=None) and balance_loss_grad
 and the losses that train a policy on the tokens it drew:
   token_logprobs(logits, tokens, mask=None, temperature=1.0) and token_logprobs_grad
@@ -47,7 +48,7 @@ EXPORTED = ("profk_topk", "profk_topk_ex", "profk_topk_approx", "profk_topk_appr
             "profk_read_ceiling", "profk_strerror", "profk_release",
             "profk_sample_tokens_scratch", "profk_sample_tokens", "profk_route_scratch", "profk_route_tokens",
             "profk_route_tokens_grad", "profk_balance_loss", "profk_balance_loss_grad",
-            "profk_token_loss_scratch", "profk_token_logprobs", "profk_token_logprobs_grad", "profk_policy_loss",
+            "profk_route_scored", "profk_route_scored_grad", "profk_token_loss_scratch", "profk_token_logprobs", "profk_token_logprobs_grad", "profk_policy_loss",
             "profk_preference_loss")
 
 
@@ -146,6 +147,8 @@ def load_library():
     lib.profk_balance_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, vp]
     lib.profk_balance_loss_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, ctypes.c_float, vp, vp]
     f32 = ctypes.c_float
+    lib.profk_route_scored.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.profk_route_scored_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, i32, i32, f32, vp, vp, vp, vp, vp, f32, vp, vp]
     rows = [vp, i32, i64, i64, i64, vp, vp, f32]  # logits and their layout, tokens, mask, temperature
     lib.profk_token_loss_scratch.argtypes = [i64, i64]
     lib.profk_token_loss_scratch.restype = i64
@@ -155,7 +158,7 @@ def load_library():
     lib.profk_preference_loss.argtypes = rows + [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]
     for name in ("profk_sample_tokens", "profk_route_tokens", "profk_route_tokens_grad", "profk_balance_loss",
                  "profk_balance_loss_grad", "profk_token_logprobs", "profk_token_logprobs_grad", "profk_policy_loss",
-                 "profk_preference_loss"):
+                 "profk_preference_loss", "profk_route_scored", "profk_route_scored_grad"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("profk_sample_tokens_scratch", "profk_route_scratch"):
         getattr(lib, name).restype = i64

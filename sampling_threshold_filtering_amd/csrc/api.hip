@@ -1481,6 +1481,43 @@ int profk_route_tokens(const void* logits, int32_t dtype, int64_t T, int64_t E, 
   return PROFK_OK;
 }
 
+int profk_route_scored(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                       int64_t k, const profk_scoring* how, float* out_weights, int64_t* out_experts,
+                       int64_t* out_counts, int64_t* out_rows, float* out_loss, void* scratch, int64_t scratch_bytes,
+                       void* stream) {
+  int rc = check_route(logits, dtype, T, E, ld, k);
+  if (rc) return rc;
+  if (k > E || (T && (!out_weights || !out_experts)) || !out_counts || !out_rows || !how) return PROFK_EINVAL;
+  if ((how->scores != PROFK_SOFTMAX && how->scores != PROFK_SIGMOID) || !std::isfinite(how->scale)) return PROFK_EINVAL;
+  if (how->groups < 1 || E % how->groups || how->top_groups < 1 || how->top_groups > how->groups) return PROFK_EINVAL;
+  if (how->group_best != 1 && how->group_best != 2) return PROFK_EINVAL;
+  if (how->groups > (int32_t)kRouteMaxGroups) return PROFK_EUNSUPPORTED;
+  rc = check_scratch(scratch, scratch_bytes, (int64_t)route_scratch_bytes((u64)T, (u32)E));
+  if (rc) return rc;
+  RouteArgs a{};
+  a.x = logits;
+  a.T = (u64)T;
+  a.ld = (u64)ld;
+  a.E = (u32)E;
+  a.k = (u32)k;
+  a.mask = mask;
+  a.normalize = how->normalize != 0;
+  a.weights = out_weights;
+  a.experts = out_experts;
+  a.counts = out_counts;
+  a.rows = out_rows;
+  a.loss = out_loss;
+  a.scratch = (char*)scratch;
+  a.sigmoid = how->scores == PROFK_SIGMOID;
+  a.groups = (u32)how->groups;
+  a.top_groups = (u32)how->top_groups;
+  a.group_best = (u32)how->group_best;
+  a.scale = how->scale;
+  a.bias = how->bias;
+  HIPCHK(launch_scored(a, dtype, (hipStream_t)stream), "launch routing by scores");
+  return PROFK_OK;
+}
+
 int profk_balance_loss(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
                        const int64_t* experts, int64_t k, int64_t* out_counts, int64_t* out_rows, float* out_loss,
                        void* scratch, int64_t scratch_bytes, void* stream) {
@@ -1506,12 +1543,13 @@ int profk_balance_loss(const void* logits, int32_t dtype, int64_t T, int64_t E, 
   return PROFK_OK;
 }
 
-int profk_route_tokens_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
-                            int64_t k, int32_t normalize, const int64_t* experts, const float* d_weights,
-                            const int64_t* counts, const int64_t* rows, const float* d_loss, float d_loss_scale,
-                            void* out_d_logits, void* stream) {
+int profk_route_scored_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                            int64_t k, int32_t normalize, int32_t scores, float scale, const int64_t* experts,
+                            const float* d_weights, const int64_t* counts, const int64_t* rows, const float* d_loss,
+                            float d_loss_scale, void* out_d_logits, void* stream) {
   const int rc = check_route(logits, dtype, T, E, ld, k);
   if (rc) return rc;
+  if ((scores != PROFK_SOFTMAX && scores != PROFK_SIGMOID) || !std::isfinite(scale)) return PROFK_EINVAL;
   if (T == 0) return PROFK_OK;
   if (!out_d_logits || (d_weights && !experts) || (counts && !rows) || (!counts && !d_weights)) return PROFK_EINVAL;
   RouteGradArgs a{};
@@ -1529,8 +1567,18 @@ int profk_route_tokens_grad(const void* logits, int32_t dtype, int64_t T, int64_
   a.d_loss = d_loss;
   a.d_loss_scale = d_loss_scale;
   a.d_x = out_d_logits;
+  a.sigmoid = scores == PROFK_SIGMOID;
+  a.scale = scale;
   HIPCHK(launch_route_grad(a, dtype, (hipStream_t)stream), "launch route gradient");
   return PROFK_OK;
+}
+
+int profk_route_tokens_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,
+                            int64_t k, int32_t normalize, const int64_t* experts, const float* d_weights,
+                            const int64_t* counts, const int64_t* rows, const float* d_loss, float d_loss_scale,
+                            void* out_d_logits, void* stream) {
+  return profk_route_scored_grad(logits, dtype, T, E, ld, mask, k, normalize, PROFK_SOFTMAX, 1.f, experts, d_weights,
+                                 counts, rows, d_loss, d_loss_scale, out_d_logits, stream);
 }
 
 int profk_balance_loss_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld, const uint8_t* mask,

@@ -11,6 +11,10 @@
 //   weights:              dl_te = p_te (d_te - sum_j p_tj d_tj), d scattered to the row
 //   normalised weights:   dl_te = w_te (d_te - sum_j w_tj d_tj) at the chosen, else 0
 //     (they are the softmax over the chosen entries alone)
+// Of sigmoid scores s (k_scored.hip), p_t = s_t / sum s_t, and w_t = s_t / sum of the chosen ones:
+//   loss:                 dl_te = (g E / n) p_te (1 - s_te) (f_e - sum_j p_tj f_j)
+//   weights:              dl_te = s_te (1 - s_te) d_te
+//   normalised weights:   dl_te = w_te (1 - s_te) (d_te - sum_j w_tj d_tj) at the chosen, else 0
 //
 // Layout.  A group of G lanes takes a row and holds C entries of it per lane in registers,
 // so that a row's maximum and sums are log2 G lane exchanges and 64 / G rows share every
@@ -27,8 +31,7 @@
 // convert, 7 for the exponential and its sum, 4 for a selection key and 2 for each of the k
 // maxima; 16 lanes share a row's log2 G exchanges, which 8 lanes with twice the entries did
 // not make up for (30 us: fewer wavefronts hide less).
-#include "launch.h"
-#include "ops_device.h"
+#include "route_device.h"
 
 namespace profk {
 
@@ -36,13 +39,8 @@ namespace {
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / kWave;
-constexpr u32 kRouteMaxBlocks = 512;
 constexpr int kGradThreads = 256;
 constexpr int kFinishThreads = 1024;
-constexpr u32 kFinishExperts = 16;
-constexpr u32 kTurnsInRegisters = 4;  // rows a lane sums in 32 bits
-constexpr u32 kMostFinishing = kRouteMaxExperts / kFinishExperts;
-constexpr size_t kRouteScratchHead = 256 + 8 * kMostFinishing;
 
 template <int G>
 __device__ __forceinline__ u64 group_reduce64(u64 v) {  // the maximum
@@ -54,158 +52,10 @@ __device__ __forceinline__ u64 group_reduce64(u64 v) {  // the maximum
   return v;
 }
 
-__device__ __forceinline__ u32 max_u(u32 a, u32 b) { return a > b ? a : b; }
-
-// e^x for x <= 0 to about one unit in the last place: the rounding of x log2(e), which
-// grows with |x|, is made up for by two multiply-adds (x - t ln 2 is what the rounded t
-// left).  Differences as far apart as the type reaches (and -inf) are cut to one whose
-// exponential is 0, and so is NaN: rows that hold one are told apart beforehand.
-__device__ __forceinline__ float exp_f(float x) {
-  x = __builtin_fmaxf(x, -150.f);
-  const float t = x * 1.44269502f;
-  const float r = __builtin_fmaf(-t, 0.693147182f, x);
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, r, e);
-}
-
-// Four neighbouring entries with one load or store.
-template <class T>
-struct alignas(4 * sizeof(T)) Four {
-  T e[4];
-};
-
-// One row in registers: C entries per lane.  QUAD: four neighbours at a time.
-template <int G, int C, bool QUAD>
-struct Row {
-  float v[C];
-  float e[C];  // exp(v - top)
-  bool live;
-  float top;
-
-  static __device__ __forceinline__ u32 index(int i, u32 g) {
-    return QUAD ? (u32)(i / 4 * G) * 4 + (u32)(i % 4) + g * 4 : (u32)i * G + g;
-  }
-  // All loads go out before the first is used: places past the row's end read its start,
-  // rows past the last (x of a row that exists) are read and not taken.
-  template <class T>
-  __device__ __forceinline__ void load(const T* x, u32 E, u32 g, bool in) {
-    if constexpr (QUAD) {
-      Four<T> q[C / 4];
-#pragma unroll
-      for (int i = 0; i < C; i += 4) {  // E is a multiple of 4
-        const u32 at = index(i, g);
-        q[i / 4] = *reinterpret_cast<const Four<T>*>(x + (at < E ? at : 0u));
-      }
-#pragma unroll
-      for (int i = 0; i < C; i += 4) {  // by words: two entries of 16 bits at a time
-        u32 w[sizeof(T)];
-        __builtin_memcpy(w, &q[i / 4], 4 * sizeof(T));
-#pragma unroll
-        for (u32 k = 0; k < sizeof(T); ++k) w[k] = in && index(i, g) < E ? w[k] : NoneWord<T>::value;
-        __builtin_memcpy(&q[i / 4], w, 4 * sizeof(T));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[i + k] = to_f32(q[i / 4].e[k]);
-      }
-    } else {
-      T q[C];
-#pragma unroll
-      for (int i = 0; i < C; ++i) q[i] = x[index(i, g) < E ? index(i, g) : 0u];
-#pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = in && index(i, g) < E ? to_f32(q[i]) : kNone;
-    }
-  }
-  // The largest entry and the exponentials.  A row that holds a NaN has NaN for its top,
-  // and every NaN becomes the one that the order ranks first; there, and where the top is
-  // +inf, all exponentials are NaN.
-  __device__ __forceinline__ void weigh(bool in) {
-    static_assert(C % 2 == 0, "pairs behind the first, and one");
-    float m = v[0];
-    bool nan = false;
-#pragma unroll
-    for (int i = 1; i + 1 < C; i += 2) m = max3(m, v[i], v[i + 1]);
-    m = max_f(m, v[C - 1]);
-#pragma unroll
-    for (int i = 0; i < C; i += 2) nan |= __builtin_isunordered(v[i], v[i + 1 < C ? i + 1 : i]);
-    top = group_reduce<G>(m, max_f);
-    live = in && !(top == kNone);
-    const float base = live ? top : 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) e[i] = exp_f(v[i] - base);  // entries of -inf: 0
-    if (__builtin_expect(__ballot(nan || top == __builtin_huge_valf()) != 0, 0)) {
-      const float first = __uint_as_float(0x7FFFFFFFu);
-      if (group_reduce<G>((u32)nan, max_u)) {
-        top = first;
-        live = true;
-      }
-      if (!(top < __builtin_huge_valf())) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-          v[i] = v[i] != v[i] ? first : v[i];
-          e[i] = first;
-        }
-      }
-    }
-  }
-  // 1 / the row's sum; 0 for a row that is not live
-  __device__ __forceinline__ float inverse() const {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) s += e[i];
-    s = group_reduce<G>(s, add_f);
-    return live ? 1.f / s : 0.f;
-  }
-};
-
-// Selection keys of 32 bits: the value's ordered code with its low bits replaced by the
-// entry's complement, so that the largest key is the first entry by value, then lower
-// index, wherever the bits that are left tell the values apart.
-constexpr int key_bits(int entries) {
-  int b = 0;
-  while ((1 << b) < entries) ++b;
-  return b;
-}
-
 // Ordered code of a value as a Row holds it.
 __device__ __forceinline__ u32 ord_of(float v) {
   const u32 b = __float_as_uint(v + 0.f);  // -0 as +0
   return b ^ ((u32)((int)b >> 31) | 0x80000000u);
-}
-
-// A launch of several blocks leaves each block's counts, sums and live rows here for the
-// finishing launch; one block alone writes the outputs itself.
-struct RouteScratch {
-  u64* loss;     // the finishing blocks' parts of the loss, and how many there are
-  double* parts; // small ones of them, a place per finishing block
-  double* sums;  // blocks * E
-  u32* counts;   // blocks * E
-  u32* rows;     // blocks
-};
-
-__host__ __device__ inline RouteScratch route_scratch(char* s, u32 blocks, u32 E) {
-  RouteScratch r;
-  r.loss = (u64*)s;
-  r.parts = (double*)(s + 256);
-  r.sums = (double*)(s + kRouteScratchHead);
-  r.counts = (u32*)(r.sums + (u64)blocks * E);
-  r.rows = r.counts + (u64)blocks * E;
-  return r;
-}
-
-// Sum of one double per thread over the block, in a fixed order; thread 0 has it.
-template <int WAVES>
-__device__ __forceinline__ double block_sum(double v, double* wave_tot) {
-#pragma unroll
-  for (int d = kWave / 2; d; d >>= 1) v += __shfl_down(v, d);
-  if (lane_id() == 0) wave_tot[threadIdx.x / kWave] = v;
-  __syncthreads();
-  double s = 0;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) s += wave_tot[w];
-  return s;
-}
-
-__device__ __forceinline__ float balance_of(double total, u64 rows, u32 E, u32 k) {
-  return rows ? (float)((double)E * total / ((double)rows * (double)k * (double)rows)) : 0.f;
 }
 
 }  // namespace
@@ -495,7 +345,8 @@ __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs 
   *a.loss = (float)((double)a.E * all);
 }
 
-template <class T, int G, int C, bool QUAD>
+// SIGMOID: of sigmoid scores; p are their shares of the row's sum.
+template <class T, int G, int C, bool QUAD, bool SIGMOID>
 __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs a) {
   using R = Row<G, C, QUAD>;
   constexpr int kGroups = kGradThreads / G;
@@ -534,11 +385,15 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
     float first_d = 0.f;
     if (a.d_weights && g < a.k) {
       first_e = slot(tr, g);
-      first_d = a.d_weights[tr * a.k + g];
+      first_d = a.d_weights[tr * a.k + g] * a.scale;
     }
     R row;
     row.load(x + tr * a.ld, a.E, g, in);
-    row.weigh(in);
+    float falling[SIGMOID ? C : 1];  // 1 - score
+    if constexpr (SIGMOID)
+      row.score(in, falling);
+    else
+      row.weigh(in);
     const float inv = row.inverse();
     float out[C];
     float dot = 0.f;
@@ -554,7 +409,10 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       // A normalised weight is of the exponentials themselves: the only one of its row is 1, and
       // its gradient 0, exactly.
       const float unit = a.normalize ? 1.f : inv;
-      auto weight = [&](u32 e) { return exp_f(to_f32(xt[e]) - row.top) * unit; };
+      auto weight = [&](u32 e) {
+        if constexpr (SIGMOID) return sigmoid_of(to_f32(xt[e])).up;
+        return exp_f(to_f32(xt[e]) - row.top) * unit;
+      };
       const bool first = row.live && first_e < a.E;
       const float p0 = first ? weight(first_e) : 0.f;
       const float d0 = first ? first_d : 0.f;  // where there is no expert d_weights may hold anything
@@ -565,22 +423,28 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
           if (e >= a.E) continue;
           const float p = weight(e);
           wsum += p;
-          wd = __builtin_fmaf(p, a.d_weights[tr * a.k + j], wd);
+          wd = __builtin_fmaf(p, a.d_weights[tr * a.k + j] * a.scale, wd);
         }
       wsum = group_reduce<G>(wsum, add_f);
       wd = group_reduce<G>(wd, add_f);
-      const float r = a.normalize ? 1.f / wsum : 1.f;
+      const float r = !a.normalize ? 1.f : wsum == 0.f ? 0.f : 1.f / wsum;  // 0: all far below the row's top
       const float mean = wd * r, from = a.normalize ? mean : 0.f;
-      if (!a.normalize) dot += mean;
-      if (first) atomicAdd(&d[first_e], p0 * r * (d0 - from));
+      if (!a.normalize && !SIGMOID) dot += mean;
+      // the only one of a row has weight 1 and gradient 0, exactly, also where its exponential is not 1
+      const u64 firsts = __ballot(first) >> (lane_id() / G * G) & (~0ull >> (kWave - G));
+      const bool lone = a.normalize && a.k <= (u32)G && __popcll(firsts) == 1;
+      if (first && !lone) atomicAdd(&d[first_e], p0 * r * (d0 - from));
       if (row.live)
         for (u32 j = g + G; j < a.k; j += G) {
           const u32 e = slot(tr, j);
-          if (e < a.E) atomicAdd(&d[e], weight(e) * r * (a.d_weights[tr * a.k + j] - from));
+          if (e < a.E) atomicAdd(&d[e], weight(e) * r * (a.d_weights[tr * a.k + j] * a.scale - from));
         }
       wave_lds_sync();
 #pragma unroll
-      for (int i = 0; i < C; ++i) out[i] = __builtin_fmaf(row.e[i], f[i] - dot, d[R::index(i, g)]);
+      for (int i = 0; i < C; ++i) {
+        out[i] = __builtin_fmaf(row.e[i], f[i] - dot, d[R::index(i, g)]);
+        if constexpr (SIGMOID) out[i] *= falling[i];
+      }
       wave_lds_sync();
       if (first) d[first_e] = 0.f;
       if (row.live)
@@ -591,7 +455,10 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       wave_lds_sync();
     } else {
 #pragma unroll
-      for (int i = 0; i < C; ++i) out[i] = row.e[i] * (f[i] - dot);
+      for (int i = 0; i < C; ++i) {
+        out[i] = row.e[i] * (f[i] - dot);
+        if constexpr (SIGMOID) out[i] *= falling[i];
+      }
     }
     if (t >= a.T) continue;  // no lane exchange below
     T* to = dx + t * a.E;
@@ -614,25 +481,12 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
   }
 }
 
+hipError_t launch_route_finish(const RouteArgs& a, hipStream_t s) {
+  route_finish_kernel<<<(a.E + kFinishExperts - 1) / kFinishExperts, kFinishThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 namespace {
-
-// Blocks of a kernel that takes `each` rows a block at a time: no more than are resident at
-// once, as what a block does before and after its rows (the sums over its lanes and
-// wavefronts; the loss's factors) costs as much as a row or two a wavefront, and no more
-// than share the rounds evenly.
-u32 route_blocks(u64 T, u32 each, u32 resident) {
-  const u64 rounds = (T + each - 1) / each;
-  if (rounds <= resident) return rounds ? (u32)rounds : 1;
-  const u64 turns = (rounds + resident - 1) / resident;
-  return (u32)((rounds + turns - 1) / turns);
-}
-
-template <class K>
-u32 resident_blocks(K kernel, int threads) {
-  int each = 0;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, 0) != hipSuccess || each < 1) each = 1;
-  return (u32)each * (u32)device_cu_count();
-}
 
 template <class T, int G, int C, bool QUAD, bool GIVEN>
 hipError_t route_launch_one(RouteArgs a, hipStream_t s) {
@@ -640,75 +494,39 @@ hipError_t route_launch_one(RouteArgs a, hipStream_t s) {
   a.blocks = route_blocks(a.T, kRouteThreads / G, fit < kRouteMaxBlocks ? fit : kRouteMaxBlocks);
   route_kernel<T, G, C, QUAD, GIVEN><<<a.blocks, kRouteThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.blocks == 1) return e;
-  route_finish_kernel<<<(a.E + kFinishExperts - 1) / kFinishExperts, kFinishThreads, 0, s>>>(a);
-  return hipGetLastError();
+  return e != hipSuccess || a.blocks == 1 ? e : launch_route_finish(a, s);
 }
 
-template <class T, int G, int C, bool QUAD>
-hipError_t route_launch(const RouteArgs& a, hipStream_t s) {
-  return a.balance_only ? route_launch_one<T, G, C, QUAD, true>(a, s) : route_launch_one<T, G, C, QUAD, false>(a, s);
-}
+struct Forward {
+  template <class T, int G, int C, bool QUAD>
+  static hipError_t launch(const RouteArgs& a, hipStream_t s) {
+    return a.balance_only ? route_launch_one<T, G, C, QUAD, true>(a, s) : route_launch_one<T, G, C, QUAD, false>(a, s);
+  }
+};
 
-template <class T, int G, int C, bool QUAD>
-hipError_t route_launch(const RouteGradArgs& a, hipStream_t s) {
-  static const u32 fit = resident_blocks(route_grad_kernel<T, G, C, QUAD>, kGradThreads);
-  const u32 blocks = route_blocks(a.T, kGradThreads / G, fit);
-  route_grad_kernel<T, G, C, QUAD><<<blocks, kGradThreads, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-// Lanes per row and entries per lane: the smallest that hold the row, and the fewest lanes
-// that hold it in 16 entries each (16384 x 384 fp16, forward and backward: 25 us by 32 lanes
-// with 12 entries, 34 by 64 with 8; x 700: 38 by 64 with 12, 43 with 16).  Up to 64 entries
-// 8 lanes are better for long batches, whose blocks of 128 rows reach every CU: 131072 x 64
-// bf16, forward with the loss and backward in one graph, 33 us by 8 lanes and 40 by 16; 65536
-// rows 22.9 and 24.9, 32768 rows 15.4 and 18.1, 16384 rows 14.1 and 13.1 (fp32 the same way).
-// The bound is a constant on the safe side of 256 CUs' 32768 rows.
-template <class T, bool QUAD, class A>
-hipError_t route_shape(const A& a, hipStream_t s) {
-  if (a.E <= 16) return route_launch<T, 4, 4, QUAD>(a, s);
-  if (a.E <= 32) return route_launch<T, 8, 4, QUAD>(a, s);
-  if (a.E <= 64 && a.T >= 65536) return route_launch<T, 8, 8, QUAD>(a, s);
-  if (a.E <= 64) return route_launch<T, 16, 4, QUAD>(a, s);
-  if (a.E <= 128) return route_launch<T, 16, 8, QUAD>(a, s);
-  if (a.E <= 192) return route_launch<T, 16, 12, QUAD>(a, s);
-  if (a.E <= 256) return route_launch<T, 16, 16, QUAD>(a, s);
-  if (a.E <= 384) return route_launch<T, 32, 12, QUAD>(a, s);
-  if (a.E <= 512) return route_launch<T, 32, 16, QUAD>(a, s);
-  if (a.E <= 768) return route_launch<T, 64, 12, QUAD>(a, s);
-  return route_launch<T, 64, 16, QUAD>(a, s);
-}
-
-inline const void* written(const RouteArgs&) { return nullptr; }
-inline const void* written(const RouteGradArgs& a) { return a.d_x; }
-
-// Four entries at a time where every row starts at a multiple of four entries' bytes and
-// ends with a whole four.
-template <class T, class A>
-hipError_t route_rows(const A& a, hipStream_t s) {
-  const uintptr_t bases = (uintptr_t)a.x | (uintptr_t)written(a);
-  if (a.E % 4 == 0 && a.ld % 4 == 0 && bases % (4 * sizeof(T)) == 0) return route_shape<T, true>(a, s);
-  return route_shape<T, false>(a, s);
-}
-
-template <class A>
-hipError_t route_type(const A& a, int dtype, hipStream_t s) {
-  if (dtype == PROFK_FP32) return route_rows<float>(a, s);
-  if (dtype == PROFK_FP16) return route_rows<Half16>(a, s);
-  return route_rows<Brain16>(a, s);
-}
+struct Gradient {
+  template <class T, int G, int C, bool QUAD, bool SIGMOID>
+  static hipError_t launch_one(const RouteGradArgs& a, hipStream_t s) {
+    static const u32 fit = resident_blocks(route_grad_kernel<T, G, C, QUAD, SIGMOID>, kGradThreads);
+    const u32 blocks = route_blocks(a.T, kGradThreads / G, fit);
+    route_grad_kernel<T, G, C, QUAD, SIGMOID><<<blocks, kGradThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  template <class T, int G, int C, bool QUAD>
+  static hipError_t launch(const RouteGradArgs& a, hipStream_t s) {
+    return a.sigmoid ? launch_one<T, G, C, QUAD, true>(a, s) : launch_one<T, G, C, QUAD, false>(a, s);
+  }
+};
 
 }  // namespace
 
 size_t route_scratch_bytes(u64 T, u32 E) {
-  constexpr u64 kLeastRows = kRouteThreads / kWave;  // that a block takes at a time
   const u64 rounds = (T + kLeastRows - 1) / kLeastRows;
   const u64 b = rounds < kRouteMaxBlocks ? (rounds ? rounds : 1) : kRouteMaxBlocks;
   return kRouteScratchHead + b * (4 + 12 * (size_t)E);
 }
 
-hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) { return route_type(a, dtype, s); }
-hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s) { return route_type(a, dtype, s); }
+hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) { return route_type<Forward>(a, dtype, s); }
+hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s) { return route_type<Gradient>(a, dtype, s); }
 
 }  // namespace profk

@@ -15,7 +15,6 @@
 //   preference: D = sum (or mean) over a sequence's live rows of lp - ref,
 //     z = beta (D_chosen - D_rejected) - margin, l = (1 - h) softplus(-z) + h softplus(z),
 //     dl/dz = sigmoid(z) - (1 - h);  c_t = +-beta dl/dz / pairs (/ the sequence's live rows)
-#include "launch.h"
 #include "ops_device.h"
 
 namespace profk {
@@ -542,17 +541,10 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
 
 namespace {
 
-template <class K>
-u32 vocab_resident(K kernel, int threads) {
-  int each = 0;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, 0) != hipSuccess || each < 1) each = 1;
-  return (u32)each * (u32)device_cu_count();
-}
-
 template <class T, int TEAM, int N, bool GRAD, bool MULTI>
 hipError_t vocab_launch(const VocabArgs& a, hipStream_t s) {
   constexpr int kBlock = TEAM < 256 ? 256 : TEAM, kTeams = kBlock / TEAM;
-  static const u32 fit = vocab_resident(vocab_kernel<T, TEAM, N, GRAD, MULTI>, kBlock);
+  static const u32 fit = resident_blocks(vocab_kernel<T, TEAM, N, GRAD, MULTI>, kBlock);
   const u64 rounds = (a.T + kTeams - 1) / kTeams;
   u64 blocks = rounds < fit ? rounds : fit;
   if (blocks > kVocabMaxBlocks) blocks = kVocabMaxBlocks;

@@ -312,6 +312,12 @@ struct RouteArgs {
   float* loss;                 // 1, or nullptr
   char* scratch;               // route_scratch_bytes
   u32 blocks;                  // set by launch_route
+  // routing by scores (k_scored.hip)
+  bool sigmoid;                // of each logit alone, else the row's softmax
+  u32 groups, top_groups;      // equal groups of neighbours, and how many of them are kept
+  u32 group_best;              // 1 or 2: a group's score is the sum of so many of its choice scores
+  float scale;                 // of the gate weights
+  const float* bias;           // E, or nullptr
 };
 struct RouteGradArgs {
   const void* x;
@@ -326,11 +332,16 @@ struct RouteGradArgs {
   const float* d_loss;         // 1, or nullptr
   float d_loss_scale;
   void* d_x;                   // T * E, contiguous, of the logits' type
+  bool sigmoid;
+  float scale;                 // of the gate weights
 };
+constexpr u32 kRouteMaxGroups = 64;
 constexpr u32 kRouteMaxExperts = 1024;
 constexpr u32 kRouteMaxK = 64;
 size_t route_scratch_bytes(u64 T, u32 E);
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
+hipError_t launch_route_finish(const RouteArgs& a, hipStream_t s);  // the blocks' counts and sums into the outputs
+hipError_t launch_scored(const RouteArgs& a, int dtype, hipStream_t s);
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s);
 
 // The log-probabilities of given tokens and the losses over them (k_vocab.hip).

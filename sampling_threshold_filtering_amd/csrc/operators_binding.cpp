@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <cstring>
 
 #include "profk.h"
 
@@ -154,6 +155,21 @@ PyObject* result(std::initializer_list<at::Tensor> out) {
 
 PyObject* status(int64_t rc) { return PyLong_FromLongLong(rc); }
 
+int32_t scores_of(PyObject* o) {
+  const char* text = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
+  if (!text) PyErr_Clear();
+  if (text && !std::strcmp(text, "softmax")) return PROFK_SOFTMAX;
+  if (text && !std::strcmp(text, "sigmoid")) return PROFK_SIGMOID;
+  refuse("scores must be \"softmax\" or \"sigmoid\"");
+  return 0;
+}
+
+float finite(PyObject* o, const char* name) {
+  const double v = number(o, name);
+  if (!(std::abs(v) < 3e38)) refuse(std::string(name) + " must be finite");
+  return (float)v;
+}
+
 // A sampling setting: a number for all rows, or a tensor of one value per row.
 struct Setting {
   at::Tensor rows;
@@ -248,7 +264,7 @@ struct LossScale {
   }
 };
 
-// route_grad(logits, experts, counts, rows, d_weights, d_loss, normalize, mask, stream)
+// route_grad(logits, experts, counts, rows, d_weights, d_loss, normalize, mask, scores, scale, stream)
 PyObject* route_grad(PyObject* const* a) {
   const Logits x(a[0]);
   no_tangent(x.x, "logits");
@@ -256,6 +272,8 @@ PyObject* route_grad(PyObject* const* a) {
   const int64_t k = choice.dim() == 2 ? choice.size(1) : 0;
   const at::Tensor mask = vector(a[7], "mask", "bool", x.rows, at::kBool, x);
   const bool normalize = truth(a[6], "normalize");
+  const int32_t scores = scores_of(a[8]);
+  const float scale = finite(a[9], "scale");
   at::Tensor experts, d_weights, counts, rows, d_loss;
   double factor = 0;
   if (a[4] != Py_None) {
@@ -271,12 +289,45 @@ PyObject* route_grad(PyObject* const* a) {
     factor = s.factor;
   }
   const at::Tensor dx = x.empty({x.rows, x.cols}, x.x.scalar_type());
-  const int rc = profk_route_tokens_grad(x.x.data_ptr(), x.dtype, x.rows, x.cols, x.ld, address<const uint8_t>(mask), k,
-                                         normalize, address<const int64_t>(experts),
+  const int rc = profk_route_scored_grad(x.x.data_ptr(), x.dtype, x.rows, x.cols, x.ld, address<const uint8_t>(mask), k,
+                                         normalize, scores, scale, address<const int64_t>(experts),
                                          address<const float>(d_weights), address<const int64_t>(counts),
                                          address<const int64_t>(rows), address<const float>(d_loss), (float)factor,
-                                         dx.data_ptr(), stream_of(a[8]));
+                                         dx.data_ptr(), stream_of(a[10]));
   return rc ? status(rc) : THPVariable_Wrap(dx);
+}
+
+// scored(logits, k, normalize, mask, balance, scores, bias, groups, top_groups, group_best, scale, stream)
+PyObject* scored(PyObject* const* a) {
+  const Logits x(a[0]);
+  no_tangent(x.x, "logits");
+  const int64_t k = integer(a[1], "k");
+  if (k < 1 || k > x.cols) refuse("k must be in 1.." + std::to_string(x.cols));
+  const bool normalize = truth(a[2], "normalize"), balance = truth(a[4], "balance");
+  const at::Tensor mask = vector(a[3], "mask", "bool", x.rows, at::kBool, x),
+                   bias = vector(a[6], "bias", "float32", x.cols, at::kFloat, x);
+  no_tangent(bias, "bias");
+  const int64_t groups = integer(a[7], "groups"), top = a[8] == Py_None ? groups : integer(a[8], "top_groups"),
+                best = integer(a[9], "group_best");
+  if (groups < 1 || x.cols % groups) refuse("groups must divide the " + std::to_string(x.cols) + " experts");
+  if (top < 1 || top > groups) refuse("top_groups must be in 1.." + std::to_string(groups));
+  if (best != 1 && best != 2) refuse("group_best must be 1 or 2");
+  const int32_t scores = scores_of(a[5]);
+  const float scale = finite(a[10], "scale");
+  const int64_t need = profk_route_scratch(x.rows, x.cols);
+  if (need < 0) return status(x.cols > PROFK_ROUTE_MAX_EXPERTS ? PROFK_EUNSUPPORTED : need);
+  if (groups > PROFK_ROUTE_MAX_GROUPS) return status(PROFK_EUNSUPPORTED);
+  const Scratch scratch(x, need);
+  const at::Tensor weights = x.empty({x.rows, k}, at::kFloat), experts = x.empty({x.rows, k}, at::kLong),
+                   counts = x.empty({x.cols}, at::kLong), rows = x.empty({}, at::kLong),
+                   loss = balance ? x.empty({}, at::kFloat) : at::Tensor();
+  const profk_scoring how = {scores, (int32_t)groups, (int32_t)top, (int32_t)best, scale, normalize,
+                             address<const float>(bias)};
+  const int rc = profk_route_scored(x.x.data_ptr(), x.dtype, x.rows, x.cols, x.ld, address<const uint8_t>(mask), k,
+                                    &how, address<float>(weights), address<int64_t>(experts),
+                                    address<int64_t>(counts), address<int64_t>(rows), address<float>(loss),
+                                    scratch.get(), scratch.bytes, stream_of(a[11]));
+  return rc ? status(rc) : result({weights, experts, counts, rows, loss});
 }
 
 // balance(logits, experts, mask, stream)
@@ -452,8 +503,8 @@ PyMethodDef method(const char* name) {
   return {name, (PyCFunction)(void (*)(void))call<F, N>, METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<sample, 8>("sample"),       method<route, 6>("route"),
-                         method<route_grad, 9>("route_grad"), method<balance, 4>("balance"),
+PyMethodDef methods[] = {method<sample, 8>("sample"),       method<route, 6>("route"), method<scored, 12>("scored"),
+                         method<route_grad, 11>("route_grad"), method<balance, 4>("balance"),
                          method<balance_grad, 7>("balance_grad"),
                          method<token_logprobs, 5>("token_logprobs"),
                          method<token_logprobs_grad, 7>("token_logprobs_grad"), method<policy, 13>("policy"),

@@ -2,6 +2,7 @@
 // share (k_tokens.hip, k_route.hip, k_vocab.hip).
 #pragma once
 
+#include "launch.h"
 #include "profk_device.h"
 
 namespace profk {
@@ -68,5 +69,13 @@ __device__ __forceinline__ V group_reduce(V v, F f) {
 }
 __device__ __forceinline__ float add_f(float a, float b) { return a + b; }
 __device__ __forceinline__ float max_f(float a, float b) { return __builtin_fmaxf(a, b); }
+
+// Blocks of a kernel that the device holds at once.
+template <class K>
+u32 resident_blocks(K kernel, int threads) {
+  int each = 0;
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, 0) != hipSuccess || each < 1) each = 1;
+  return (u32)each * (u32)device_cu_count();
+}
 
 }  // namespace profk

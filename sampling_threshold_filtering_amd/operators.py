@@ -38,6 +38,14 @@ class Sampling(ctypes.Structure):
     ]
 
 
+class ScoringSettings(ctypes.Structure):
+    """profk_scoring"""
+    _fields_ = [
+        ("scores", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+        ("group_best", ctypes.c_int32), ("scale", ctypes.c_float), ("normalize", ctypes.c_int32), ("bias", ctypes.c_void_p),
+    ]
+
+
 class PolicySettings(ctypes.Structure):
     """profk_policy"""
     _fields_ = [
@@ -149,27 +157,43 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out
     return _call(logits, (_module or _native()).sample, logits, u, temperature, top_k, top_p, min_p, out)
 
 
-def _route(logits, k, normalize, mask, balance):
+def _route(logits, k, normalize, mask, balance, scores, bias, groups, top_groups, group_best, scale):
+    module = _module or _native()
     # (Routing._make does this too, in 0.3 us more)
-    return tuple.__new__(Routing, _call(logits, (_module or _native()).route, logits, k, normalize, mask, balance))
+    if scores == "softmax" and bias is None and scale == 1.0 and (top_groups is None or top_groups == groups) \
+            and groups == 1 and group_best in (1, 2):
+        return tuple.__new__(Routing, _call(logits, module.route, logits, k, normalize, mask, balance))
+    return tuple.__new__(Routing, _call(logits, module.scored, logits, k, normalize, mask, balance, scores, bias, groups,
+                                        top_groups, group_best, scale))
 
 
-def route_tokens(logits, k: int, normalize: bool = True, mask=None, balance: bool = False) -> Routing:
+def route_tokens(logits, k: int, normalize: bool = True, mask=None, balance: bool = False, scores: str = "softmax",
+                 bias=None, groups: int = 1, top_groups: Optional[int] = None, group_best: int = 2,
+                 scale: float = 1.0) -> Routing:
     """The k experts of each token from router logits [T, E] (fp32, fp16 or bf16; rows may be
     strided): a Routing.  Experts by logit, descending, ties to the lower index; gate weights
     are the softmax's, divided by the chosen ones' sum with `normalize`.  Tokens whose `mask`
     ([T] bool) is False, and rows of -inf alone, get expert -1 and weight 0 and count nowhere;
     a logit of -inf is never chosen.  With `balance`, loss = E sum_e f_e P_e with f_e the share
     of slots that expert e got and P_e its mean probability.  weights and loss are
-    differentiable with respect to the logits (the choice and the counts are constants)."""
+    differentiable with respect to the logits (the choice and the counts are constants).
+
+    Routing by scores: `scores` "sigmoid" takes s = sigmoid(logit) in place of the softmax (its
+    probability is then s / sum s).  The choice is by s + `bias` ([E] float32, a constant), ties
+    to the lower index.  With `top_groups` of `groups` (equal groups of neighbours), a group's
+    score is the sum of its `group_best` (1 or 2) largest of those, and only the best groups'
+    experts are chosen from.  The gate weights are s, with `normalize` over the chosen ones' sum,
+    times `scale`; the bias is not among them.  An expert of bias -inf is never chosen."""
     if logits.requires_grad:
         import torch
         if torch.is_grad_enabled():
-            return _route_function().route(logits, k, normalize, mask, balance)
-    return _route(logits, k, normalize, mask, balance)
+            return _route_function().route(logits, k, normalize, mask, balance, scores, bias, groups, top_groups,
+                                           group_best, scale)
+    return _route(logits, k, normalize, mask, balance, scores, bias, groups, top_groups, group_best, scale)
 
 
-def route_tokens_grad(logits, routing: Routing, d_weights=None, d_loss=None, normalize: bool = True, mask=None):
+def route_tokens_grad(logits, routing: Routing, d_weights=None, d_loss=None, normalize: bool = True, mask=None,
+                      scores: str = "softmax", scale: float = 1.0):
     """The gradient with respect to the logits (their type, contiguous) of a scalar whose
     gradients are d_weights [T, k] float32 and d_loss (a number or one float32 value) with
     respect to route_tokens' weights and loss; either may be None.  The other arguments are
@@ -179,7 +203,7 @@ def route_tokens_grad(logits, routing: Routing, d_weights=None, d_loss=None, nor
         _check_device(torch, logits)
         return torch.zeros(logits.shape, dtype=logits.dtype, device=logits.device)
     return _call(logits, (_module or _native()).route_grad, logits, routing.experts, routing.counts, routing.rows,
-                 d_weights, d_loss, normalize, mask)
+                 d_weights, d_loss, normalize, mask, scores, scale)
 
 
 def _balance(logits, experts, mask):
@@ -303,10 +327,10 @@ def _route_function():
 
     class RouteFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, logits, k, normalize, mask, balance):
-            r = _route(logits, k, normalize, mask, balance)
+        def forward(ctx, logits, k, normalize, mask, balance, scores, bias, groups, top_groups, group_best, scale):
+            r = _route(logits, k, normalize, mask, balance, scores, bias, groups, top_groups, group_best, scale)
             ctx.save_for_backward(logits, mask, r.experts, r.counts, r.rows)
-            ctx.normalize = normalize
+            ctx.normalize, ctx.scores, ctx.scale = normalize, scores, scale
             ctx.mark_non_differentiable(r.experts, r.counts, r.rows)
             ctx.set_materialize_grads(False)
             return tuple(r)
@@ -316,9 +340,9 @@ def _route_function():
         def backward(ctx, d_weights, d_experts, d_counts, d_rows, d_loss):
             logits, mask, experts, counts, rows = ctx.saved_tensors
             if d_weights is None and d_loss is None:
-                return None, None, None, None, None
+                return (None,) * 11
             r = Routing(None, experts, counts, rows, None)
-            return route_tokens_grad(logits, r, d_weights, d_loss, ctx.normalize, mask), None, None, None, None
+            return (route_tokens_grad(logits, r, d_weights, d_loss, ctx.normalize, mask, ctx.scores, ctx.scale),) + (None,) * 10
 
     class BalanceFunction(torch.autograd.Function):
         @staticmethod
@@ -340,8 +364,8 @@ def _route_function():
 
     class Functions:
         @staticmethod
-        def route(logits, k, normalize, mask, balance):
-            return Routing(*RouteFunction.apply(logits, k, normalize, mask, balance))
+        def route(*args):
+            return Routing(*RouteFunction.apply(*args))
 
         @staticmethod
         def balance(logits, experts, mask):

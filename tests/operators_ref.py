@@ -94,3 +94,69 @@ def route(x, k, normalize, mask=None, d_weights=None, d_loss=0.0):
                 grad[t] += p[t] * (g - p[t] @ g)
     loss, counts, n, lgrad = balance(p, live, experts, k)
     return dict(weights=weights, experts=experts, counts=counts, rows=n, loss=loss, d_logits=grad + d_loss * lgrad, p=p)
+
+
+def scored(x, k, how, mask=None, d_weights=None, d_loss=0.0):
+    """Routing by scores: dict as route's, with score, p, falling (of the score, for its own
+    logit) and ok (rows whose choice no distance below 1e-14 decides, but for equal entries)."""
+    x = np.asarray(x, np.float64)
+    T, E = x.shape
+    sigmoid, bias, groups = how["scores"] == "sigmoid", how.get("bias"), how.get("groups", 1)
+    top, best, scale = how.get("top_groups") or groups, how.get("group_best", 2), how.get("scale", 1.0)
+    normalize = how.get("normalize", True)
+    p, live = softmax(x, mask)
+    with np.errstate(over="ignore"):
+        up, down = 1 / (1 + np.exp(-x)), 1 / (1 + np.exp(x))
+    score = np.where(live[:, None], up, 0.0) if sigmoid else p
+    falling = down if sigmoid else np.ones_like(x)
+    if sigmoid:
+        total = score.sum(axis=1, keepdims=True)
+        p = np.divide(score, total, out=np.zeros_like(score), where=total != 0)
+    experts, weights, grad = np.full((T, k), -1, np.int64), np.zeros((T, k)), np.zeros((T, E))
+    ok = np.ones(T, bool)
+
+    def rank(values):
+        """Order by value, NaN first, then index; whether every step down is a clear one or none."""
+        key = np.where(np.isnan(values), np.inf, values)
+        order = np.argsort(-key, kind="stable")
+        with np.errstate(invalid="ignore"):
+            gaps = -np.diff(key[order])
+            return order, ~((gaps > 0) & (gaps < 1e-14))
+
+    for t in np.flatnonzero(live):
+        c = score[t] + (bias if bias is not None else 0.0)
+        c = np.where((x[t] == -np.inf) | (c == -np.inf), -np.inf, c)
+        if top < groups:
+            value = np.full(groups, -np.inf)
+            for g in range(groups):
+                m = c[g * (E // groups):(g + 1) * (E // groups)]
+                m = m[rank(m)[0]][:best]
+                m = m[~(m == -np.inf)]
+                if m.size:
+                    value[g] = m.sum()
+            order, clear = rank(value)
+            ok[t] &= clear[top - 1] or value[order[top]] == -np.inf
+            for g in order[top:]:
+                c[g * (E // groups):(g + 1) * (E // groups)] = -np.inf
+        order, clear = rank(c)
+        ok[t] &= bool(clear[:k].all())
+        order = order[:k]
+        order = order[~(c[order] == -np.inf)]
+        experts[t, :order.size] = order
+        w = score[t][order]
+        if normalize:
+            w = w / w.sum() if w.sum() != 0 else np.zeros_like(w)
+        weights[t, :order.size] = scale * w
+        if d_weights is not None:
+            d = scale * np.asarray(d_weights[t, :order.size], np.float64)
+            if normalize:
+                grad[t][order] += w * (d - w @ d)
+            elif sigmoid:
+                grad[t][order] += w * d
+            else:
+                g = np.zeros(E)
+                g[order] = d
+                grad[t] += p[t] * (g - p[t] @ g)
+    loss, counts, n, lgrad = balance(p, live, experts, k)
+    return dict(weights=weights, experts=experts, counts=counts, rows=n, loss=loss, score=score, p=p, falling=falling,
+                ok=ok, d_logits=(grad + d_loss * lgrad) * falling)
