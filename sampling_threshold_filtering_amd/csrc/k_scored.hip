@@ -36,16 +36,49 @@ __device__ __forceinline__ double of_code(u64 u) {
   if (u == ~0ull) return __builtin_nan("");
   return __builtin_bit_cast(double, u >> 63 ? u ^ 1ull << 63 : ~u);
 }
-__device__ __forceinline__ u64 wave_max(u64 v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const u64 o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
-  return v;
+__device__ __forceinline__ u32 wave_max(u32 v) { return wave_reduce_u32(v, max_u); }
+__device__ __forceinline__ u64 wave_max(u64 v) {  // the upper halves, then the lower ones of those that have it
+  const u32 high = wave_max((u32)(v >> 32));
+  return (u64)high << 32 | wave_max((u32)(v >> 32) == high ? (u32)v : 0u);
 }
 __device__ __forceinline__ u32 wave_min(u32 v) {
-  return ~wave_reduce_u32(~v, [](u32 a, u32 b) { return a > b ? a : b; });
+  return ~wave_max(~v);
+}
+
+// A constant in scalar registers, made where it is used: held in vector registers over the rows'
+// loop, the few dozen of the 64-bit choice took a third of the loop's.
+__device__ __forceinline__ double in_scalar(double v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+__device__ __forceinline__ u32 in_scalar(u32 v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// e^x: x = n ln 2 + f with |f| <= ln 2 / 2, the Taylor series of e^f to the power 13 (the next
+// term is below 2^-57), scaled by 2^n.  NaN stays.
+__device__ __forceinline__ double exp_64(double x) {
+  const double y = __builtin_fmin(__builtin_fmax(x, in_scalar(-800.0)), in_scalar(800.0));
+  const double n = rint(y * in_scalar(1.4426950408889634));
+  // ln 2 in two parts, the first with room for n's bits
+  double f = __builtin_fma(-n, in_scalar(0x1.62e42fefap-1), y);
+  f = __builtin_fma(-n, in_scalar(0x1.cf79abc9e3b3ap-40), f);
+  double p = in_scalar(1.0 / 6227020800.0);
+  p = __builtin_fma(p, f, in_scalar(1.0 / 479001600));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 39916800));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 3628800));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 362880));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 40320));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 5040));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 720));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 120));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 24));
+  p = __builtin_fma(p, f, in_scalar(1.0 / 6));
+  p = __builtin_fma(p, f, 0.5);
+  p = __builtin_fma(p, f, 1.0);
+  p = __builtin_fma(p, f, 1.0);
+  return x != x ? x : __builtin_ldexp(p, (int)n);
 }
 
 // What the wavefront's rows need of the choice: the keys in LDS, row by row.
@@ -57,121 +90,136 @@ struct Choice {
   static constexpr u32 kMostGroups = G * C < (int)kRouteMaxGroups ? G * C : kRouteMaxGroups;
 };
 
+// A row's values in LDS, by entry.
+template <bool QUAD, int G, int C, class V>
+__device__ __forceinline__ void to_lds(V* row, u32 g, const V (&v)[C]) {
+  if constexpr (QUAD) {
+#pragma unroll
+    for (int i = 0; i < C; i += 4)
+      *reinterpret_cast<Four<V>*>(row + Row<G, C, QUAD>::index(i, g)) = Four<V>{{v[i], v[i + 1], v[i + 2], v[i + 3]}};
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) row[Row<G, C, QUAD>::index(i, g)] = v[i];
+  }
+}
+template <bool QUAD, int G, int C, class V>
+__device__ __forceinline__ void from_lds(const V* row, u32 g, V (&v)[C]) {
+  if constexpr (QUAD) {
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+      const Four<V> q = *reinterpret_cast<const Four<V>*>(row + Row<G, C, QUAD>::index(i, g));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i + k] = q.e[k];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = row[Row<G, C, QUAD>::index(i, g)];
+  }
+}
+
 }  // namespace
 
-// One row by the whole wavefront in 64 bits: lane j gets slot j's expert, or ~0.
-template <class T, int E64>
-__device__ __forceinline__ u32 choose_exactly(const RouteArgs& a, const T* x) {
-  const u32 lane = lane_id();
-  double l[E64];
-  double top = -__builtin_huge_val();
-#pragma unroll
-  for (int i = 0; i < E64; ++i) {
-    const u32 e = i * kWave + lane;
-    l[i] = e < a.E ? (double)to_f32(x[e]) : -__builtin_huge_val();
-    top = l[i] > top || l[i] != l[i] ? l[i] : top;
-  }
-  u64 code[E64];
-  if (!a.sigmoid) {
-    // (a NaN or +inf makes every score NaN)
+// One row by the whole wavefront in 64 bits: lane j gets slot j's expert, or ~0.  `codes` has
+// room for E.  No array of it lives in registers: the rows that come here are few, and the
+// others' loop keeps its registers.
+template <class T>
+__device__ __forceinline__ u32 choose_exactly(const RouteArgs& a, const T* x, u64* codes) {
+  const u32 lane = lane_id(), E = in_scalar(a.E);
+  if (!a.sigmoid) {  // a NaN or +inf makes every score NaN
+    double top = -__builtin_huge_val(), sum = 0;
+#pragma unroll 1
+    for (u32 e = lane; e < E; e += kWave) {
+      const double l = (double)to_f32(x[e]);
+      top = l > top || l != l ? l : top;
+    }
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
       const double o = __shfl_xor(top, d);
       top = o > top || o != o ? o : top;
     }
-    double sum = 0;
-#pragma unroll
-    for (int i = 0; i < E64; ++i) sum += exp(l[i] - top);
+#pragma unroll 1
+    for (u32 e = lane; e < E; e += kWave) {
+      const double p = exp_64((double)to_f32(x[e]) - top);
+      codes[e] = __builtin_bit_cast(u64, p);
+      sum += p;
+    }
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
-#pragma unroll
-    for (int i = 0; i < E64; ++i) code[i] = __builtin_bit_cast(u64, exp(l[i] - top) / sum);
-  } else {
-#pragma unroll
-    for (int i = 0; i < E64; ++i) code[i] = __builtin_bit_cast(u64, 1.0 / (1.0 + exp(-l[i])));
+#pragma unroll 1
+    for (u32 e = lane; e < E; e += kWave) codes[e] = __builtin_bit_cast(u64, __builtin_bit_cast(double, codes[e]) / sum);
   }
-#pragma unroll
-  for (int i = 0; i < E64; ++i) {
-    const u32 e = i * kWave + lane;
-    const double b = a.bias && e < a.E ? (double)a.bias[e] : 0.0;
-    const double c = __builtin_bit_cast(double, code[i]) + b;
-    code[i] = e >= a.E || l[i] == -__builtin_huge_val() || c == -__builtin_huge_val() ? 0 : code_of(c);
+#pragma unroll 1
+  for (u32 e = lane; e < E; e += kWave) {
+    const double l = (double)to_f32(x[e]);
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp_64(-l)) : __builtin_bit_cast(double, codes[e]);
+    const double c = a.bias ? s + (double)a.bias[e] : s;
+    codes[e] = l == -__builtin_huge_val() || c == -__builtin_huge_val() ? 0 : code_of(c);
   }
-  const u32 size = a.E / a.groups;
+  wave_lds_sync();
   if (a.top_groups < a.groups) {
+    const u32 size = E / in_scalar(a.groups);
     u64 mine = 0;  // lane g: group g's score
+#pragma unroll 1
     for (u32 g = 0; g < a.groups; ++g) {
-      u64 first = 0;
-#pragma unroll
-      for (int i = 0; i < E64; ++i) {
-        const u32 e = i * kWave + lane;
-        if (e / size == g && code[i] > first) first = code[i];
+      u64 first = 0, second = 0;
+#pragma unroll 1
+      for (u32 j = lane; j < size; j += kWave) {
+        const u64 c = codes[g * size + j], low = c < first ? c : first;
+        second = low > second ? low : second;
+        first = c > first ? c : first;
       }
-      first = wave_max(first);
-      u64 score = first;
-      if (a.group_best == 2 && first) {
-        u32 at = ~0u;
-#pragma unroll
-        for (int i = 0; i < E64; ++i) {
-          const u32 e = i * kWave + lane;
-          if (e / size == g && code[i] == first && e < at) at = e;
-        }
-        at = wave_min(at);
-        u64 second = 0;
-#pragma unroll
-        for (int i = 0; i < E64; ++i) {
-          const u32 e = i * kWave + lane;
-          if (e / size == g && e != at && code[i] > second) second = code[i];
-        }
-        second = wave_max(second);
-        if (second) score = code_of(of_code(first) + of_code(second));
-      }
-      if (lane == g) mine = score;
+      const u64 top = wave_max(first);
+      const u64 holders = __ballot(first == top);
+      second = holders & (holders - 1) ? top : wave_max(first == top ? second : first);
+      first = a.group_best == 2 && second ? code_of(of_code(top) + of_code(second)) : top;
+      if (lane == g) mine = first;
     }
     u32 before = 0;
+#pragma unroll 1
     for (u32 g = 0; g < a.groups; ++g) {
       const u64 o = __shfl(mine, (int)g);
       before += o > mine || (o == mine && g < lane);
     }
     const u64 kept = __ballot(lane < a.groups && before < a.top_groups);
-#pragma unroll
-    for (int i = 0; i < E64; ++i) {
-      const u32 e = i * kWave + lane;
-      if (e < a.E && !(kept >> (e / size) & 1)) code[i] = 0;
-    }
+#pragma unroll 1
+    for (u32 e = lane; e < E; e += kWave)
+      if (!(kept >> (e / size) & 1)) codes[e] = 0;
+    wave_lds_sync();
   }
   u32 slot = ~0u;
   static_assert(kRouteMaxK <= kWave, "a lane per slot");
+#pragma unroll 1
   for (u32 j = 0; j < a.k; ++j) {
     u64 first = 0;
-#pragma unroll
-    for (int i = 0; i < E64; ++i) first = code[i] > first ? code[i] : first;
-    first = wave_max(first);
     u32 at = ~0u;
-    if (first) {
-#pragma unroll
-      for (int i = 0; i < E64; ++i) {
-        const u32 e = i * kWave + lane;
-        if (code[i] == first && e < at) at = e;
+#pragma unroll 1
+    for (u32 e = lane; e < E; e += kWave) {
+      const u64 c = codes[e];
+      if (c > first) {
+        first = c;
+        at = e;
       }
-      at = wave_min(at);
-#pragma unroll
-      for (int i = 0; i < E64; ++i)
-        if (i * kWave + lane == at) code[i] = 0;
     }
+    const u64 top = wave_max(first);
+    if (!top) break;
+    at = wave_min(first == top ? at : ~0u);
     if (lane == j) slot = at;
+    if (lane == at % kWave) codes[at] = 0;
+    wave_lds_sync();
   }
   return slot;
 }
 
 template <class T, int G, int C, bool QUAD, bool SIGMOID>
-__global__ __launch_bounds__(kScoredThreads) void scored_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) {
   using R = Row<G, C, QUAD>;
   using K = Choice<G, C>;
   constexpr int kGroups = kScoredThreads / G, kRows = kWave / G;  // rows of a block, of a wavefront
-  __shared__ u32 s_key[kScoredWaves][kRows][G * C];
+  // the rows' keys and, for the rows chosen in 64 bits, one row's codes
+  __shared__ alignas(16) u32 s_key[kScoredWaves][kRows > 1 ? kRows : 2][G * C];
   __shared__ u32 s_group[kScoredWaves][kRows][K::kMostGroups];
   __shared__ u32 s_cnt[G * C];
+  __shared__ alignas(16) float s_base[G * C];  // the biases in units from the lowest; -inf: none
   __shared__ float s_sum[kScoredWaves][G * C];
   __shared__ u32 s_rows;
   __shared__ double s_part[kScoredWaves];
@@ -179,38 +227,37 @@ __global__ __launch_bounds__(kScoredThreads) void scored_kernel(RouteArgs a) {
   const u32 g = threadIdx.x % G, grp = threadIdx.x / G, wave = threadIdx.x / kWave, row_of_wave = lane_id() / G;
   for (u32 e = threadIdx.x; e < G * C; e += kScoredThreads) s_cnt[e] = 0;
   if (threadIdx.x == 0) s_rows = 0;
-  __syncthreads();
   u32* key_row = s_key[wave][row_of_wave];
   u32* group_row = s_group[wave][row_of_wave];
   const T* x = reinterpret_cast<const T*>(a.x);
-  // The biases in units from the lowest; entries without one (-inf) get none.
   float low = a.bias ? __builtin_huge_valf() : 0.f, high = a.bias ? -__builtin_huge_valf() : 0.f;
   bool odd = false;  // a bias that the keys cannot hold
-  float base[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const u32 e = R::index(i, g);
-    base[i] = e >= a.E ? kNone : a.bias ? a.bias[e] : 0.f;
-    odd |= base[i] != base[i] || base[i] == __builtin_huge_valf();
-    if (base[i] > kNone && base[i] < __builtin_huge_valf()) {
-      low = __builtin_fminf(low, base[i]);
-      high = __builtin_fmaxf(high, base[i]);
+#pragma unroll 1
+  for (u32 e = lane_id(); e < a.E; e += kWave) {
+    const float b = a.bias ? a.bias[e] : 0.f;
+    odd |= b != b || b == __builtin_huge_valf();
+    if (b > kNone && b < __builtin_huge_valf()) {
+      low = __builtin_fminf(low, b);
+      high = __builtin_fmaxf(high, b);
     }
   }
-  low = -group_reduce<G>(-low, max_f);
-  high = group_reduce<G>(high, max_f);
+  low = -group_reduce<kWave>(-low, max_f);
+  high = group_reduce<kWave>(high, max_f);
   if (!(low <= high)) low = high = 0.f;
-  odd = group_reduce<G>((u32)odd, max_u) != 0;
+  odd = __ballot(odd) != 0;
   // a unit: the range of c over 2^kUnits, less room for roundings at both ends
   const float unit = (float)(((double)(1u << K::kUnits) - 64.0) / ((double)high - (double)low + 1.0));
-#pragma unroll
-  for (int i = 0; i < C; ++i)
-    base[i] = base[i] == kNone ? kNone : (float)(((double)base[i] - (double)low) * (double)unit + 32.0);
+  for (u32 e = threadIdx.x; e < G * C; e += kScoredThreads) {
+    const float b = e >= a.E ? kNone : a.bias ? a.bias[e] : 0.f;
+    s_base[e] = b == kNone ? kNone : (float)(((double)b - (double)low) * (double)unit + 32.0);
+  }
+  __syncthreads();
   const u32 size = a.E / a.groups;
   const bool grouped = a.top_groups < a.groups;
   const u32 best = a.group_best < size ? a.group_best : size;
-  u32 lanes = 1;  // per group of experts
-  while (lanes * 2 * a.groups <= (u32)G) lanes *= 2;
+  u32 lanes_log = 0;  // lanes per group of experts
+  while ((2u << lanes_log) * a.groups <= (u32)G) ++lanes_log;
+  const u32 lanes = 1u << lanes_log, part = g & (lanes - 1);
 
   float sum[C];
 #pragma unroll
@@ -242,15 +289,23 @@ __global__ __launch_bounds__(kScoredThreads) void scored_kernel(RouteArgs a) {
     const T* xt = x + tr * a.ld;
     R row;
     row.load(xt, a.E, g, in);
+    // entries of -inf, a bit each: the logits themselves do not stay in registers
+    u32 none = 0;
+    float least_logit = row.v[0];
+#pragma unroll
+    for (int i = 1; i < C; ++i) least_logit = __builtin_fminf(least_logit, row.v[i]);
+    const bool nones = __ballot(least_logit == kNone) != 0;
+    if (nones) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) none |= (u32)(row.v[i] == kNone) << i;
+    }
     bool nan = false;
     if constexpr (SIGMOID) {
-      float unused[1];
-      row.score(in, unused);
+      row.score(in, nan);
     } else {
       row.weigh(in);
+      nan = !(row.top < __builtin_huge_valf());
     }
-#pragma unroll
-    for (int i = 0; i < C; ++i) nan |= row.e[i] != row.e[i];
     const float inv = row.inverse();
     if (a.loss) {
 #pragma unroll
@@ -260,107 +315,156 @@ __global__ __launch_bounds__(kScoredThreads) void scored_kernel(RouteArgs a) {
     // keys
     u32 key[C];
     const float per = SIGMOID ? unit : unit * inv;
+    float base[C];
+    from_lds<QUAD, G, C>(s_base, g, base);
+    if (nones) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) base[i] = none >> i & 1 ? kNone : base[i];
+    }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const u32 e = R::index(i, g);
-      const float u = __builtin_fmaf(row.e[i], per, base[i]);
-      key[i] = row.v[i] > kNone && base[i] > kNone ? (u32)u << K::kBits | (K::kLow - e) : K::kLow - e;
+      const float u = __builtin_fmaf(row.e[i], per, base[i]);  // of an entry that is none -inf: converts to 0
+      key[i] = (u32)__builtin_fmaxf(u, 0.f) << K::kBits | (K::kLow - R::index(i, g));
     }
-    // How far two keys may be off each other, in units.  A sigmoid is off by 3.5 h of 1 at most (h =
-    // 2^-24), which is 3.5 units at most; a probability by (32 + 2 |d|) h of itself, below 64 h of
-    // the row's largest; the product's and the bias's rounding by half a unit each, the cut by one.
-    const u32 near = SIGMOID ? 12 : 5 + (u32)(__builtin_fminf(unit * inv, 0x1p24f) * 0x1p-17f);
+    auto same = [&](u32 m, u32 n) {  // the entries of two keys
+      const u32 e = K::kLow - (m & K::kLow), f = K::kLow - (n & K::kLow);
+      return to_f32(xt[e]) == to_f32(xt[f]) && (!a.bias || a.bias[e] == a.bias[f]);
+    };
+    // How far two keys may be off each other, in units.  A sigmoid is off by 5 h of 1 at most (h =
+    // 2^-24: half of its exponential's 4 h, the sum's h, the reciprocal's 2 h), which is 5 units at
+    // most; a probability by (32 + 2 |d|) h of itself, below 64 h of the row's largest; the product's
+    // and the bias's rounding by half a unit each, the cut by one.
+    const u32 near = SIGMOID ? 15 : 5 + (u32)(__builtin_fminf(unit * inv, 0x1p24f) * 0x1p-17f);
+    const u32 close = near << K::kBits | K::kLow;  // in keys
     bool unsure = odd || group_reduce<G>((u32)nan, max_u) != 0;
     if (grouped) {
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (R::index(i, g) < a.E) key_row[R::index(i, g)] = key[i];
+      to_lds<QUAD, G, C>(key_row, g, key);
       wave_lds_sync();
-      for (u32 q = g / lanes; q < a.groups; q += (u32)G / lanes) {
+      // A lane's groups: their two largest keys, then their scores: one key, or a sum of two values.
+      for (u32 q = g >> lanes_log; q < a.groups; q += (u32)G >> lanes_log) {
         u32 first = 0, second = 0;
-        for (u32 j = g % lanes; j < size; j += lanes) {
-          const u32 u = key_row[q * size + j] >> K::kBits;
+        auto take = [&](u32 u) {
           second = max_u(second, first < u ? first : u);
           first = max_u(first, u);
+        };
+        if (QUAD && size % 4 == 0) {
+          for (u32 j = part * 4; j < size; j += lanes * 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(key_row + q * size + j);
+            take(u.x);
+            take(u.y);
+            take(u.z);
+            take(u.w);
+          }
+        } else {
+#pragma unroll 4
+          for (u32 j = part; j < size; j += lanes) take(key_row[q * size + j]);
         }
         for (u32 d = 1; d < lanes; d <<= 1) {
           const u32 f = __shfl_xor(first, (int)d), s = __shfl_xor(second, (int)d);
           second = max_u(max_u(second, s), first < f ? first : f);
           first = max_u(first, f);
         }
+        if (first <= K::kLow) first = 0;
         if (best == 2) {
-          unsure |= first && !second;  // one score against sums of two
-          first += second;
+          unsure |= first && second <= K::kLow;  // one score against sums of two
+          first = (first >> K::kBits) + (second >> K::kBits);
         }
-        if (g % lanes == 0) group_row[q] = first;
+        if (part == 0) group_row[q] = first;
       }
       wave_lds_sync();
       u32 least = ~0u, most = 0;  // of the groups kept, of those left out
-      for (u32 q = g / lanes; q < a.groups; q += (u32)G / lanes) {
+      u32 kept = 0, turn_of = 1;  // a bit for each of the lane's groups
+      for (u32 q = g >> lanes_log; q < a.groups; q += (u32)G >> lanes_log, turn_of <<= 1) {
         const u32 own = group_row[q];
         u32 before = 0;
+#pragma unroll 4
         for (u32 h = 0; h < a.groups; ++h) {
           const u32 o = group_row[h];
           before += o > own || (o == own && h < q);
         }
         if (before < a.top_groups) {
           least = least < own ? least : own;
+          kept |= turn_of;
         } else {
           most = max_u(most, own);
-          for (u32 j = g % lanes; j < size; j += lanes) key_row[q * size + j] = K::kLow - (q * size + j);
         }
       }
       least = ~group_reduce<G>(~least, max_u);
       most = group_reduce<G>(most, max_u);
-      unsure |= most && least - most <= 2 * near;
+      if (best == 2) {
+        unsure |= most && least - most <= 2 * near;
+      } else if (most && least - most <= close) {
+        // Groups of the same best logit and bias are told apart by their index in any arithmetic: so
+        // are these if whatever may be the best of a group at the border is the same as theirs.
+        turn_of = 1;
+        for (u32 q = g >> lanes_log; q < a.groups; q += (u32)G >> lanes_log, turn_of <<= 1) {
+          const u32 own = group_row[q];
+          if (!own || (kept & turn_of ? own - most : least - own) > close) continue;
+          for (u32 j = part; j < size; j += lanes) {
+            const u32 u = key_row[q * size + j];
+            unsure |= u > K::kLow && (u > most || most - u <= 2 * close) && !same(u, most);
+          }
+        }
+      }
+      turn_of = 1;
+      for (u32 q = g >> lanes_log; q < a.groups; q += (u32)G >> lanes_log, turn_of <<= 1)
+        if (!(kept & turn_of))
+          for (u32 j = part; j < size; j += lanes) key_row[q * size + j] = K::kLow - (q * size + j);
       wave_lds_sync();
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (R::index(i, g) < a.E) key[i] = key_row[R::index(i, g)];
+      from_lds<QUAD, G, C>(key_row, g, key);
       wave_lds_sync();
     }
-    // the first k keys, and the next
-    u32 m = 0;
-    auto next_key = [&]() {
+    // the first k keys, and the next: lane g holds slots g, g + G, ... of them
+    bool closes = false;
+    u32 m = key[0], mine = 0;
+#pragma unroll
+    for (int i = 1; i < C; ++i) m = max_u(m, key[i]);
+    m = group_reduce<G>(m, max_u);
+    for (u32 j = 0;; ++j) {
+      if (g == j % G) mine = m;
+      if (a.k > (u32)G && (j % G == G - 1 || j + 1 == a.k) && g <= j % G) key_row[j / G * G + g] = mine;
+      if (j + 1 == a.E) break;
       u32 d = 0;
 #pragma unroll
       for (int i = 0; i < C; ++i) d = max_u(d, key[i] - m);
-      return m + group_reduce<G>(d, max_u);
-    };
-    for (u32 j = 0; j <= a.k && j < a.E; ++j) {
-      const u32 n = next_key();
-      if (j && n > K::kLow && (m >> K::kBits) - (n >> K::kBits) <= near) {
-        const u32 e = K::kLow - (m & K::kLow), f = K::kLow - (n & K::kLow);
-        unsure |= to_f32(xt[e]) != to_f32(xt[f]) || (a.bias && a.bias[e] != a.bias[f]);
-      }
+      const u32 n = m + group_reduce<G>(d, max_u);
+      closes |= n > K::kLow && m - n <= close;
+      if (j + 1 == a.k) break;
       m = n;
-      if (g == 0 && j < a.k) key_row[j] = n > K::kLow ? K::kLow - (n & K::kLow) : ~0u;
+    }
+    wave_lds_sync();
+    if (__builtin_expect(__ballot(closes) != 0, 0)) {
+      // neighbours of the same logit and bias are told apart by their index in any arithmetic
+      u32 last = 0;
+      for (u32 j = 0;; ++j) {
+        u32 d = 0;
+#pragma unroll
+        for (int i = 0; i < C; ++i) d = max_u(d, key[i] - last);
+        const u32 n = last + group_reduce<G>(d, max_u);
+        if (n <= K::kLow || !closes) break;
+        unsure |= j && last - n <= close && !same(last, n);
+        if (j == a.k || j + 1 == a.E) break;
+        last = n;
+      }
     }
     unsure = group_reduce<G>((u32)unsure, max_u) && row.live;
-    wave_lds_sync();
-    for (u64 left = __ballot(unsure && g == 0); left; left &= left - 1) {
-      const u32 from = (u32)__builtin_ctzll(left) / G;
-      const u32 slot = choose_exactly<T, (G * C + kWave - 1) / kWave>(a, x + (t0 + wave * kRows + from) * a.ld);
-      if (lane_id() < a.k) s_key[wave][from][lane_id()] = slot;
-      wave_lds_sync();
-    }
+    auto weight_of = [&](float v, float top, float inverse) {
+      if constexpr (SIGMOID) return sigmoid_of(v).up;
+      if (!(top < __builtin_huge_valf())) return top - top;  // of +inf or NaN: NaN
+      const float w = exp_f(v - top);
+      return a.normalize ? w : w * inverse;
+    };
+    auto share_of = [&](float w, float chosen) { return chosen == 0.f ? 0.f : w / chosen * a.scale; };
     // lane g takes slots g, g + G, ...
-    if (here) {
+    if (here && !unsure) {
       const u64 at = t * a.k;
       float chosen = 0.f, w = 0.f;
       for (u32 j = g; j < a.k; j += G) {
-        const u32 e = key_row[j];
-        const bool some = row.live && e < a.E;
+        const u32 n = a.k > (u32)G ? key_row[j] : mine, e = K::kLow - (n & K::kLow);
+        const bool some = row.live && n > K::kLow;
         w = 0.f;
         if (some) {
-          const float v = to_f32(xt[e]);
-          if constexpr (SIGMOID) {
-            w = sigmoid_of(v).up;
-          } else {
-            w = exp_f(v - row.top);
-            if (!(row.top < __builtin_huge_valf())) w = row.top - row.top;  // of +inf or NaN: NaN
-            if (!a.normalize) w *= inv;
-          }
+          w = weight_of(to_f32(xt[e]), row.top, inv);
           atomicAdd(&s_cnt[e], 1u);
         }
         chosen += w;
@@ -369,15 +473,32 @@ __global__ __launch_bounds__(kScoredThreads) void scored_kernel(RouteArgs a) {
       }
       if (a.normalize) {
         chosen = group_reduce<G>(chosen, add_f);
-        const float r = chosen == 0.f ? 0.f : 1.f;
         if (a.k <= (u32)G) {
-          if (g < a.k) a.weights[at + g] = r != 0.f ? w / chosen * a.scale : 0.f;
+          if (g < a.k) a.weights[at + g] = share_of(w, chosen);
         } else {
-          for (u32 j = g; j < a.k; j += G) a.weights[at + j] = r != 0.f ? a.weights[at + j] / chosen * a.scale : 0.f;
+          for (u32 j = g; j < a.k; j += G) a.weights[at + j] = share_of(a.weights[at + j], chosen);
         }
       }
     }
     wave_lds_sync();
+    for (u64 left = __ballot(unsure && g == 0); left; left &= left - 1) {
+      const u32 from = (u32)__builtin_ctzll(left);  // the row's first lane
+      const u64 r = t0 + wave * kRows + from / G;
+      const float top = __shfl(row.top, (int)from), inverse = __shfl(inv, (int)from);
+      const u32 e = choose_exactly(a, x + r * a.ld, reinterpret_cast<u64*>(s_key[wave][0]));
+      const bool slot = lane_id() < a.k, some = slot && e < a.E;
+      float w = 0.f;
+      if (some) {
+        w = weight_of(to_f32(x[r * a.ld + e]), top, inverse);
+        atomicAdd(&s_cnt[e], 1u);
+      }
+      const float chosen = group_reduce<kWave>(w, add_f);
+      if (slot) {
+        a.experts[r * a.k + lane_id()] = some ? (int64_t)e : -1;
+        a.weights[r * a.k + lane_id()] = a.normalize ? share_of(w, chosen) : w * a.scale;
+      }
+      wave_lds_sync();
+    }
     if (a.loss && ++turn == kTurnsInRegisters && t0 + step < a.T) {  // the same for the whole block
       join();
       __syncthreads();

@@ -120,6 +120,34 @@ struct Row {
       }
     }
   }
+  // Sigmoid scores for e, to (4 e + 3) / (1 + e) units of 2^-24 of themselves, e = exp(-v); nan:
+  // this lane has one.  Differences from 0 beyond 88 count as 88.
+  __device__ __forceinline__ void score(bool in, bool& nan) {
+    static_assert(C % 2 == 0, "pairs behind the first, and one");
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i + 1 < C; i += 2) m = max3(m, v[i], v[i + 1]);
+    m = max_f(m, v[C - 1]);
+#pragma unroll
+    for (int i = 0; i < C; i += 2) nan |= __builtin_isunordered(v[i], v[i + 1]);
+    live = in && !(group_reduce<G>(m, max_f) == kNone);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const float x = __builtin_amdgcn_fmed3f(v[i], -88.f, 150.f), y = x * -1.44269502f;
+      const float r = __builtin_fmaf(y, -0.693147182f, -x);  // what the rounding of y left
+      const float t = __builtin_amdgcn_exp2f(y);
+      e[i] = __builtin_amdgcn_rcpf(__builtin_fmaf(t, r, t) + 1.f);
+    }
+    if (!in) {  // rows that are not live hold -inf
+#pragma unroll
+      for (int i = 0; i < C; ++i) e[i] = 0.f;
+    }
+    if (__builtin_expect(__ballot(nan) != 0, 0)) {
+      if (group_reduce<G>((u32)nan, max_u)) live = in;
+#pragma unroll
+      for (int i = 0; i < C; ++i) e[i] = v[i] != v[i] ? v[i] : e[i];
+    }
+  }
   // The same with sigmoid scores for e: 0 in a row that is not live; top is not set.  falling,
   // where the caller has room for it: 1 - e.
   template <int N>
