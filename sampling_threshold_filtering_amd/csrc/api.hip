@@ -1683,7 +1683,7 @@ int profk_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t 
   p.margins = out_margins;
   p.sequence_logprobs = out_sequence_logprobs;
   p.coefficients = out_coefficients;
-  HIPCHK(launch_pairs(p, (hipStream_t)stream), "launch preference loss");
+  HIPCHK(launch_pairs(p, dtype, (hipStream_t)stream), "launch preference loss");
   return PROFK_OK;
 }
 

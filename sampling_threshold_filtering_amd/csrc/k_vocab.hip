@@ -21,30 +21,49 @@ namespace profk {
 
 namespace {
 
-constexpr u32 kVocabMaxBlocks = 2048;
-constexpr u32 kCountBlocks = 64;
 constexpr int kCountThreads = 1024;
+constexpr u32 kCountBlocks = 64;  // a lane per part of the count
+constexpr u64 kChunk = 1024;      // rows whose terms one wavefront adds up
 constexpr int kPairThreads = 256;
 constexpr u32 kPairBlocks = 1024;
+constexpr u32 kSlices = 64;       // most parts of a row: a lane each
+constexpr u64 kSplitRows = 512;   // most rows that are split
 
-// What the blocks leave for the last of them.
-struct BlockTerms {
+// A row's part of the policy loss, or a chunk's, or a block of pairs'.
+struct Terms {
   double loss, kl;
-  u64 clipped;
+  u64 count;  // clipped rows, or live ones
 };
+// Of a slice of a row that is split.
+struct Part {
+  float top, rest;
+};
+
+// All of it is written before it is read within a call.
 struct VocabScratch {
-  u32* ticket;
-  u32* live;          // kCountBlocks parts of the number of live rows
-  BlockTerms* terms;  // kVocabMaxBlocks
-  double* lp;         // T, for the preference loss
+  u32* last;      // a ticket for the chunks (or the pairs' blocks)
+  u32* live;      // kCountBlocks parts of the number of live rows
+  u32* tickets;   // for the rows of each chunk
+  Terms* chunks;  // of each chunk (or of each of kPairBlocks blocks)
+  Terms* rows;    // T, with the policy loss
+  double* lp;     // T, with the preference loss
+  Part* parts;    // T * kSlices, where rows are split
 };
-constexpr size_t kVocabHead = 512;
-__host__ __device__ inline VocabScratch vocab_scratch(char* s) {
+__host__ __device__ inline u64 vocab_chunks(u64 T) { return (T + kChunk - 1) / kChunk; }
+__host__ __device__ inline VocabScratch vocab_scratch(char* s, u64 T) {
   VocabScratch v;
-  v.ticket = (u32*)s;
+  v.last = (u32*)s;
   v.live = (u32*)(s + 128);
-  v.terms = (BlockTerms*)(s + kVocabHead);
-  v.lp = (double*)(s + kVocabHead + kVocabMaxBlocks * sizeof(BlockTerms));
+  s += 512;
+  const u64 chunks = vocab_chunks(T);
+  v.chunks = (Terms*)s;
+  s += sizeof(Terms) * (chunks > kPairBlocks ? chunks : kPairBlocks);
+  v.rows = (Terms*)s;
+  v.lp = (double*)s;
+  s += sizeof(Terms) * T;
+  v.tickets = (u32*)s;
+  s += 8 * (chunks / 2 + 1);
+  v.parts = (Part*)s;
   return v;
 }
 
@@ -163,7 +182,7 @@ __device__ __forceinline__ float kl_of(float q) {
 
 struct RowTerms {
   double loss = 0, kl = 0;
-  u32 clipped = 0;
+  bool clipped = false;
   float c = 0;  // dloss / dlp, d_loss among it
 };
 
@@ -220,76 +239,189 @@ __device__ __forceinline__ double ld_double(const double* p) { return __builtin_
 
 }  // namespace
 
-// The live rows, in kCountBlocks parts at most, and the ticket at 0.
+// The live rows, in kCountBlocks parts at most, and the tickets at 0.
 __global__ __launch_bounds__(kCountThreads) void vocab_count_kernel(VocabArgs a) {
   __shared__ u32 s_n[kCountThreads / kWave];
-  const VocabScratch sc = vocab_scratch(a.scratch);
+  const VocabScratch sc = vocab_scratch(a.scratch, a.T);
   u32 n = 0;
   for (u64 t = (u64)blockIdx.x * kCountThreads + threadIdx.x; t < a.T; t += (u64)gridDim.x * kCountThreads)
     n += row_live(a, t);
   n = block_total<kCountThreads / kWave>(n, s_n);
   if (threadIdx.x == 0) {
     sc.live[blockIdx.x] = n;
-    if (blockIdx.x == 0) *sc.ticket = 0;
+    if (blockIdx.x == 0) *sc.last = 0;
+  }
+  for (u64 i = (u64)blockIdx.x * kCountThreads + threadIdx.x; i < vocab_chunks(a.T); i += (u64)gridDim.x * kCountThreads)
+    sc.tickets[i] = 0;
+}
+
+// Adds up the policy's terms, in a fixed order: a chunk's by the wavefront that ends its last
+// row, the chunks' by the one that ends the last chunk.  By all lanes of a row's first wavefront.
+__device__ __forceinline__ void add_terms(const VocabArgs& a, const VocabScratch& sc, u64 t, const RowTerms& o, u32 live) {
+  const u32 lane = lane_id();
+  auto store = [&](Terms* to, double loss, double kl, u64 count) {
+    st_double(&to->loss, loss);
+    st_double(&to->kl, kl);
+    st_agent(&to->count, count);
+    drain_memory_ops();
+  };
+  auto total = [&](const Terms* from, u64 n) {
+    Terms s = {0, 0, 0};
+#pragma unroll 4
+    for (u64 i = lane; i < n; i += kWave) {
+      s.loss += ld_double(&from[i].loss);
+      s.kl += ld_double(&from[i].kl);
+      s.count += ld_agent(&from[i].count);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      s.loss += __shfl_xor(s.loss, d);
+      s.kl += __shfl_xor(s.kl, d);
+      s.count += __shfl_xor(s.count, d);
+    }
+    return s;
+  };
+  const u64 chunk = t / kChunk, first = chunk * kChunk, rows = a.T - first < kChunk ? a.T - first : kChunk;
+  u32 before = 0;
+  if (lane == 0) {
+    store(sc.rows + t, o.loss, o.kl, o.clipped);
+    before = __hip_atomic_fetch_add(sc.tickets + chunk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if ((u64)__builtin_amdgcn_readfirstlane(before) + 1 < rows) return;
+  Terms s = total(sc.rows + first, rows);
+  const u64 chunks = vocab_chunks(a.T);
+  if (chunks > 1) {
+    if (lane == 0) {
+      store(sc.chunks + chunk, s.loss, s.kl, s.count);
+      before = __hip_atomic_fetch_add(sc.last, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if ((u64)__builtin_amdgcn_readfirstlane(before) + 1 < chunks) return;
+    s = total(sc.chunks, chunks);
+  }
+  if (lane == 0) {
+    *a.loss = (float)s.loss;
+    *a.kl = (float)s.kl;
+    *a.clipped = (int64_t)s.count;
+    *a.rows = (int64_t)live;
   }
 }
 
-// A team of TEAM threads takes a row, N vectors of it per thread in registers; of a longer row
-// (MULTI) that many at a time, the last of them staying for the gradient.
-template <class T, int TEAM, int N, bool GRAD, bool MULTI>
-__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void vocab_kernel(VocabArgs a) {
+// WHOLE: a team takes a row.  PART: a block takes a slice of a row, and leaves its sums; one block
+// more counts the live rows.  JOIN: a block takes a slice of a row again, with the row's sums from
+// all its parts; with the policy loss one block more per row deals with its terms (without a
+// gradient, that one alone).
+enum { kWhole, kPart, kJoin };
+
+// A team of TEAM threads with N vectors per thread in registers; of more (MULTI) that many at a
+// time, the last of them staying for the gradient.
+template <class T, int TEAM, int N, bool GRAD, bool MULTI, int MODE>
+__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void vocab_kernel(VocabArgs a) {
   constexpr int kBlock = TEAM < 256 ? 256 : TEAM, kTeams = kBlock / TEAM, kTeamWaves = TEAM / kWave;
-  constexpr int kBlockWaves = kBlock / kWave;
   constexpr u32 W = 16 / sizeof(T);
-  __shared__ float s_top[2][kBlockWaves], s_rest[2][kBlockWaves], s_token[2][kTeams];
-  __shared__ double s_d[kBlockWaves];
-  __shared__ u32 s_n[kBlockWaves], s_last;
-  const VocabScratch sc = vocab_scratch(a.scratch);
+  __shared__ float s_top[kBlock / kWave], s_rest[kBlock / kWave], s_token[kTeams];
+  __shared__ u32 s_n[kBlock / kWave];
+  const VocabScratch sc = vocab_scratch(a.scratch, a.T);
   const u32 wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const u32 team = wave / kTeamWaves, tid = threadIdx.x % TEAM, base = wave % kTeamWaves * kWave;
+  const u32 team = wave / kTeamWaves, tid = threadIdx.x % TEAM, base = wave % kTeamWaves * kWave, lane = lane_id();
   const Exponent ex = {a.exponent_hi, a.exponent_lo};
-    u32 n = 0;
-  if (a.policy)
-    for (u32 i = 0; i < a.count_blocks; ++i) n += sc.live[i];
-  const double share = n ? 1.0 / (double)n : 0.0;
-  const double d_loss = GRAD ? (double)(a.d_loss ? *a.d_loss : 1.f) * (double)a.d_loss_scale : 0.0;
-  RowTerms sum;
-  u32 turn = 0;
-  for (u64 t = (u64)blockIdx.x * kTeams + team; t < a.T; t += (u64)gridDim.x * kTeams) {
-    const T* x = reinterpret_cast<const T*>(a.x) + t * a.ld;
-    T* dx = GRAD ? reinterpret_cast<T*>(a.d_x) + t * a.V : nullptr;
-    // vectors between the 16-byte boundaries of what is written, or of what is read
-    u32 head = (u32)(-(uintptr_t)(GRAD ? (const T*)dx : x) & 15) / (u32)sizeof(T);
-    if (head > a.V) head = (u32)a.V;
-    const u32 nvec = (u32)(a.V - head) / W;
-    const u32 edges = (u32)a.V - nvec * W, mine = tid < head ? tid : nvec * W + tid;  // entry of this thread's edge
-    const T* xv = x + head;
-    T* dv = GRAD ? dx + head : nullptr;
-    const u32 segments = MULTI ? (nvec + TEAM * N - 1) / (TEAM * N) : 1;
-    auto store = [&](u32 j, const Words& w) {
-      __builtin_nontemporal_store(w, reinterpret_cast<Words*>(dv + (u64)j * W));
-    };
-    auto zero_row = [&]() {
-      for (u32 j = tid; j < nvec; j += TEAM) store(j, Words{0, 0, 0, 0});
-      T z;
-      from_f32(0.f, z);
-      if (tid < edges) dx[mine] = z;
-    };
-    if (!row_live(a, t) || (GRAD && a.given && a.given[t] == 0.f)) {
-      if (GRAD) zero_row();
+  constexpr bool kSliced = MODE == kPart || (MODE == kJoin && GRAD);  // else a block (or a team) to a row
+  const u32 per = kSliced ? a.slices + (MODE == kJoin && a.policy) : 1;
+  const u32 slice = kSliced ? blockIdx.x % per : 0;
+  const u64 t = kSliced ? blockIdx.x / per : a.row0 + (u64)blockIdx.x * kTeams + team;
+  // this block's are the row's terms and its log-probability
+  const bool own_terms = MODE == kWhole || (MODE == kJoin && slice + 1 == per);
+  const bool own_grad = GRAD && (MODE != kJoin || slice < a.slices);
+  if constexpr (MODE == kPart) {
+    if (t == a.T) {
+      u32 n = 0;
+      for (u64 r = tid; r < a.T; r += kBlock) n += row_live(a, r);
+      n = block_total<kBlock / kWave>(n, s_n);
       if (tid == 0) {
-        if (a.logprobs) a.logprobs[t] = 0.f;
-        if (a.pairs) sc.lp[t] = 0;
+        *sc.live = n;
+        *sc.last = 0;
+        *sc.tickets = 0;  // no more rows than a chunk
       }
-      continue;
     }
-    const u32 token = (u32)a.tokens[t];
-    // the token's vector, if it is in one: slot of which thread's, and the entry in it
-    const u32 in_vec = token - head;
-    const bool in_vecs = token >= head && in_vec < nvec * W;
-    const u32 slot = in_vec / W / TEAM, owner = in_vec / W % TEAM, place = in_vec % W;
-    const bool own_wave = in_vecs && owner / kWave * kWave == base;
-    float edge = kNone, x_token = kNone;
+  }
+  if (t >= a.T) return;  // no barrier below joins teams of a wavefront each
+  const T* x = reinterpret_cast<const T*>(a.x) + t * a.ld;
+  T* dx = GRAD ? reinterpret_cast<T*>(a.d_x) + t * a.V : nullptr;
+  // vectors between the 16-byte boundaries of what is written, or of what is read
+  u32 head = (u32)(-(uintptr_t)(GRAD ? (const T*)dx : x) & 15) / (u32)sizeof(T);
+  if (head > a.V) head = (u32)a.V;
+  const u32 all = (u32)(a.V - head) / W;
+  // this slice's vectors; the entries outside all vectors are the first slice's
+  const u32 each = kSliced ? (all + a.slices - 1) / a.slices : all;
+  const u32 from = slice * each < all ? slice * each : all, nvec = each < all - from ? each : all - from;
+  const u32 edges = slice ? 0 : (u32)a.V - all * W, mine = tid < head ? tid : all * W + tid;  // this thread's edge
+  const char* xv = reinterpret_cast<const char*>(x + head) + (u64)from * 16;
+  char* dv = GRAD ? reinterpret_cast<char*>(dx + head) + (u64)from * 16 : nullptr;
+  const u32 off = tid * 16;
+  u32 first = 0;  // the segment's first vector
+  // Vectors of this wavefront in the segment; of the last of them, whether this lane has one.
+  auto count = [&]() {
+    const u32 left = nvec > first + base ? (nvec - first - base + TEAM - 1) / TEAM : 0;
+    return (int)(left < N ? left : N);
+  };
+  auto has = [&](int i) { return first + i * TEAM + tid < nvec; };
+  auto store = [&](int i, const Words& w) {
+    __builtin_nontemporal_store(w, reinterpret_cast<Words*>(dv + (u64)(first + i * TEAM) * 16 + off));
+  };
+  auto zero_row = [&]() {
+    for (u32 j = tid; j < nvec; j += TEAM) __builtin_nontemporal_store(Words{0, 0, 0, 0}, reinterpret_cast<Words*>(dv + (u64)j * 16));
+    T z;
+    from_f32(0.f, z);
+    if (tid < edges) dx[mine] = z;
+  };
+  auto n_of = [&]() {  // the live rows of all
+    return wave_reduce_u32(lane < a.count_blocks ? sc.live[lane] : 0, [](u32 p, u32 q) { return p + q; });
+  };
+  const bool live = row_live(a, t);
+  if (!live || (GRAD && a.given && a.given[t] == 0.f)) {
+    if (own_grad) zero_row();
+    if (tid == 0 && own_terms) {
+      if (a.logprobs) a.logprobs[t] = 0.f;
+      if (a.pairs) sc.lp[t] = 0;
+    }
+    if (a.policy && own_terms && base == 0) add_terms(a, sc, t, RowTerms(), n_of());
+    return;
+  }
+  const u32 token = (u32)a.tokens[t];
+  // the token's vector, if it is in one of this slice: slot of which thread's, and the entry in it
+  const u32 in_vec = token - head - from * W;
+  const bool in_vecs = token >= head + from * W && in_vec < nvec * W;
+  const u32 slot = in_vec / W / TEAM, owner = in_vec / W % TEAM, place = in_vec % W;
+  const bool own_wave = in_vecs && owner / kWave * kWave == base;
+  Words v[N];
+  auto load = [&]() {
+    const int n = count();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i >= n) continue;
+      if (i + 1 == n) v[i] = Words{NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value};
+      if (i + 1 < n || has(i))
+        v[i] = __builtin_nontemporal_load(
+            reinterpret_cast<const typename AnyWords<T>::type*>(xv + (u64)(first + i * TEAM) * 16 + off));
+    }
+  };
+  auto slot_of = [&]() { return own_wave && slot >= first / TEAM && slot < first / TEAM + N ? (int)(slot - first / TEAM) : -1; };
+  const u32 segments = MULTI && nvec > TEAM * N ? (nvec + TEAM * N - 1) / (TEAM * N) : 1;
+  float edge = kNone;
+  RowSums row;
+  if constexpr (MODE == kJoin) {
+    first = (segments - 1) * (TEAM * N);
+    if (own_grad) load();
+    if (tid < edges && mine != token) edge = to_f32(x[mine]);
+    const Part p = lane < a.slices ? sc.parts[t * a.slices + lane] : Part{kLowest, 0.f};
+    row.top = group_reduce<kWave>(p.top, max_f);
+    row.rest = group_reduce<kWave>(p.rest * ex.of<T>(p.top - row.top), add_f);
+    row.token = to_f32(x[token]);
+    const int at = slot_of();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (own_grad && i == at && tid == owner) set_entry<T>(v[i], place, none_entry<T>());
+  } else {
+    float x_token = kNone;
     if (tid < edges) {
       edge = to_f32(x[mine]);
       if (mine == token) {
@@ -298,26 +430,14 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void vocab_kernel(VocabArg
       }
     }
     float top = edge > kLowest ? edge : kLowest, rest[4] = {0.f, 0.f, 0.f, 0.f};
-    Words v[N];
-    u32 first = 0;  // the first vector of the segment
-    auto load = [&]() {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const u32 j = first + i * TEAM + tid;
-        if (first + i * TEAM + base >= nvec) continue;
-        v[i] = Words{NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value};
-        if (j < nvec) v[i] = __builtin_nontemporal_load(reinterpret_cast<const typename AnyWords<T>::type*>(xv + (u64)j * W));
-      }
-    };
-    auto slot_of = [&]() { return own_wave && slot >= first / TEAM && slot < first / TEAM + N ? (int)(slot - first / TEAM) : -1; };
     for (u32 seg = 0; seg < segments; ++seg) {
       first = seg * TEAM * N;
       load();
-      const int at = slot_of();
+      const int at = slot_of(), n = count();
       const float before = top;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (first + i * TEAM + base >= nvec) continue;
+        if (i >= n) continue;
         if (i == at && tid == owner) {
           x_token = to_f32(get_entry<T>(v[i], place));
           set_entry<T>(v[i], place, none_entry<T>());
@@ -332,51 +452,51 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void vocab_kernel(VocabArg
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (first + i * TEAM + base >= nvec) continue;
+        if (i >= n) continue;
 #pragma unroll
         for (u32 k = 0; k < W; ++k) rest[k % 4] += ex.of<T>(entry<T>(v[i], k) - top);
       }
     }
     rest[0] += ex.of<T>(edge - top);
     // over the lanes, then over the team's wavefronts
-    RowSums row;
     row.top = group_reduce<kWave>(top, max_f);
     row.rest = group_reduce<kWave>((rest[0] + rest[1] + (rest[2] + rest[3])) * ex.of<T>(top - row.top), add_f);
     if constexpr (kTeamWaves == 1) {
-      const u32 lane = in_vecs ? owner : (token < head ? token : token - nvec * W);
-      row.token = __uint_as_float((u32)__builtin_amdgcn_readlane((int)__float_as_uint(x_token), (int)lane));
+      const u32 l = in_vecs ? owner : (token < head ? token : token - all * W);
+      row.token = __uint_as_float((u32)__builtin_amdgcn_readlane((int)__float_as_uint(x_token), (int)l));
     } else {
-      const u32 b = turn++ & 1;  // written again only behind the next row's barrier
-      if (tid % kWave == 0) {
-        s_top[b][wave] = row.top;
-        s_rest[b][wave] = row.rest;
+      if (lane == 0) {
+        s_top[wave] = row.top;
+        s_rest[wave] = row.rest;
       }
-      if (in_vecs ? tid == owner : (tid < edges && mine == token)) s_token[b][team] = x_token;
+      if (in_vecs ? tid == owner : (tid < edges && mine == token)) s_token[team] = x_token;
       lds_barrier();
-      const u32 from = team * kTeamWaves + tid % kTeamWaves;
-      const float m = s_top[b][from], s = s_rest[b][from];
+      const float m = s_top[tid % kTeamWaves], s = s_rest[tid % kTeamWaves];
       row.top = group_reduce<kTeamWaves>(m, max_f);
       row.rest = group_reduce<kTeamWaves>(s * ex.of<T>(m - row.top), add_f);
-      row.token = s_token[b][team];
+      row.token = s_token[team];  // (nobody's, in a slice that does not hold it)
     }
-    if (row.token > row.top) {
-      row.rest *= ex.of<T>(row.top - row.token);
-      row.top = row.token;
+    if constexpr (MODE == kPart) {
+      if (tid == 0) sc.parts[t * a.slices + slice] = Part{row.top, row.rest};
+      return;
     }
-    const RowEnd end = end_of(a, row);
-    const RowTerms o = terms_of(a, t, end, d_loss, share);
-    sum.loss += o.loss;
-    sum.kl += o.kl;
-    sum.clipped += o.clipped;
-    if (tid == 0) {
-      if (a.logprobs) a.logprobs[t] = (float)end.lp;
-      if (a.pairs) sc.lp[t] = end.lp;
-    }
-    if constexpr (GRAD) {
-      if (o.c == 0.f || end.absent) {
-        zero_row();
-        continue;
-      }
+  }
+  if (row.token > row.top) {
+    row.rest *= ex.of<T>(row.top - row.token);
+    row.top = row.token;
+  }
+  const u32 n = a.policy ? n_of() : 0;
+  const double d_loss = GRAD ? (double)(a.d_loss ? *a.d_loss : 1.f) * (double)a.d_loss_scale : 0.0;
+  const RowEnd end = end_of(a, row);
+  const RowTerms o = terms_of(a, t, end, d_loss, n ? 1.0 / (double)n : 0.0);
+  if (tid == 0 && own_terms) {
+    if (a.logprobs) a.logprobs[t] = (float)end.lp;
+    if (a.pairs) sc.lp[t] = end.lp;
+  }
+  if (own_grad) {
+    if (o.c == 0.f || end.absent) {
+      zero_row();
+    } else {
       const float c = (float)((double)o.c * a.inverse_temperature);
       const float scale = -c / end.total;
       T at_token;
@@ -391,11 +511,10 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void vocab_kernel(VocabArg
           first = seg * TEAM * N;
           load();
         }
-        const int at = slot_of();
+        const int at = slot_of(), cnt = count();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const u32 j = first + i * TEAM + tid;
-          if (first + i * TEAM + base >= nvec) continue;
+          if (i >= cnt) continue;
           Words w;
 #pragma unroll
           for (u32 k = 0; k < 4; ++k) {
@@ -408,93 +527,132 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void vocab_kernel(VocabArg
             w[k] = bits;
           }
           if (i == at && tid == owner) set_entry<T>(w, place, at_token);
-          if (j < nvec) store(j, w);
+          if (i + 1 < cnt || has(i)) store(i, w);
         }
       }
     }
   }
-  if (!a.policy) return;
-  // the block's terms, then the blocks' by the last one to end: sums in a fixed order
-  if (tid) sum = RowTerms();
-  sum.loss = block_total<kBlockWaves>(sum.loss, s_d);
-  sum.kl = block_total<kBlockWaves>(sum.kl, s_d);
-  sum.clipped = block_total<kBlockWaves>(sum.clipped, s_n);
-  if (threadIdx.x == 0) {
-    BlockTerms* o = sc.terms + blockIdx.x;
-    st_double(&o->loss, sum.loss);
-    st_double(&o->kl, sum.kl);
-    st_agent(&o->clipped, (u64)sum.clipped);
-    drain_memory_ops();
-    s_last = __hip_atomic_fetch_add(sc.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == gridDim.x;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  double loss = 0, kl = 0, clipped = 0;  // counts below 2^53
-  for (u32 i = threadIdx.x; i < gridDim.x; i += kBlock) {
-    loss += ld_double(&sc.terms[i].loss);
-    kl += ld_double(&sc.terms[i].kl);
-    clipped += (double)ld_agent(&sc.terms[i].clipped);
-  }
-  loss = block_total<kBlockWaves>(loss, s_d);
-  kl = block_total<kBlockWaves>(kl, s_d);
-  clipped = block_total<kBlockWaves>(clipped, s_d);
-  if (threadIdx.x == 0) {
-    *a.loss = (float)loss;
-    *a.kl = (float)kl;
-    *a.clipped = (int64_t)clipped;
-    *a.rows = (int64_t)n;
-  }
+  if (a.policy && own_terms && base == 0) add_terms(a, sc, t, o, n);
+}
+
+// The policy loss of no rows.
+__global__ void vocab_empty_kernel(VocabArgs a) {
+  *a.loss = *a.kl = 0.f;
+  *a.clipped = *a.rows = 0;
+}
+
+__device__ __forceinline__ float logit_of(const PairArgs& a, u64 t) {
+  const u64 at = t * a.v.ld + (u64)a.v.tokens[t];
+  if (a.dtype == PROFK_FP32) return reinterpret_cast<const float*>(a.v.x)[at];
+  if (a.dtype == PROFK_FP16) return to_f32(reinterpret_cast<const Half16*>(a.v.x)[at]);
+  return to_f32(reinterpret_cast<const Brain16*>(a.v.x)[at]);
 }
 
 // The pairs' losses, and every row's coefficient.  A block takes a pair at a time.
 __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   constexpr int kWaves = kPairThreads / kWave;
-  __shared__ double s_d[kWaves];
-  __shared__ u64 s_n[kWaves];
+  __shared__ double s_d[kWaves], s_own[2][kWaves], s_ref[2][kWaves];
+  __shared__ u64 s_n[kWaves], s_live[2][kWaves];
+  __shared__ int64_t s_rise[4][kWaves];
   __shared__ u32 s_last;
-  const VocabScratch sc = vocab_scratch(a.v.scratch);
-  // offsets as far as they rise, within [0, T]: an offset below an earlier one counts as that
-  auto offset = [&](u64 i) {
-    int64_t m = 0;
-    for (u64 k = threadIdx.x; k <= i; k += kPairThreads) m = a.offsets[k] > m ? a.offsets[k] : m;
-#pragma unroll
-    for (int d = kWave / 2; d; d >>= 1) {
-      const int64_t o = __shfl_xor(m, d);
-      m = o > m ? o : m;
+  const VocabScratch sc = vocab_scratch(a.v.scratch, a.v.T);
+  const Exponent ex = {a.v.exponent_hi, a.v.exponent_lo};
+  // A live row's log-probability; of rows that are split, from their parts.
+  auto lp_of = [&](u64 t) {
+    if (!a.v.slices) return sc.lp[t];
+    RowSums row = {kLowest, 0.f, logit_of(a, t)};
+    for (u32 i = 0; i < a.v.slices; ++i) row.top = max_f(row.top, sc.parts[t * a.v.slices + i].top);
+    for (u32 i = 0; i < a.v.slices; ++i) {
+      const Part p = sc.parts[t * a.v.slices + i];
+      row.rest += p.rest * ex.of<float>(p.top - row.top);
     }
-    if (lane_id() == 0) s_n[threadIdx.x / kWave] = (u64)m;
-    lds_barrier();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) m = (int64_t)s_n[w] > m ? (int64_t)s_n[w] : m;
-    lds_barrier();
-    return (u64)m < a.v.T ? (u64)m : a.v.T;
+    if (row.token > row.top) {
+      row.rest *= ex.of<float>(row.top - row.token);
+      row.top = row.token;
+    }
+    return end_of(a.v, row).lp;
+  };
+  // Rows that no sequence takes.
+  auto outside = [&](u64 t) {
+    a.coefficients[t] = 0.f;
+    if (a.v.slices) a.v.logprobs[t] = row_live(a.v, t) ? (float)lp_of(t) : 0.f;
   };
   double total = 0;
   u64 rows = 0;
   for (u64 p = blockIdx.x; p < a.pairs; p += gridDim.x) {
-    u64 start[2], end[2], live[2];
-    double ratio[2];
+    // Offsets as far as they rise, within [0, T]: one below an earlier one counts as that.
+    int64_t rise[4] = {0, 0, 0, 0};
+    const u64 at[4] = {p, p + 1, p + a.pairs, p + a.pairs + 1};
+    for (u64 k = threadIdx.x; k <= at[3]; k += kPairThreads) {
+      const int64_t o = a.offsets[k];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) rise[h] = k <= at[h] && o > rise[h] ? o : rise[h];
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+      for (int d = kWave / 2; d; d >>= 1) {
+        const int64_t o = __shfl_xor(rise[h], d);
+        rise[h] = o > rise[h] ? o : rise[h];
+      }
+      if (lane_id() == 0) s_rise[h][threadIdx.x / kWave] = rise[h];
+    }
+    lds_barrier();
+    u64 start[2], end[2], live[2] = {0, 0};
+    double own[2] = {0, 0}, ref[2] = {0, 0}, ratio[2];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) rise[h] = s_rise[h][w] > rise[h] ? s_rise[h][w] : rise[h];
+      const u64 r = (u64)rise[h] < a.v.T ? (u64)rise[h] : a.v.T;
+      if (h & 1)
+        end[h / 2] = r;
+      else
+        start[h / 2] = r;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      for (u64 t = start[h] + threadIdx.x; t < end[h]; t += kPairThreads) {
+        if (!row_live(a.v, t)) {
+          if (a.v.slices) a.v.logprobs[t] = 0.f;
+          continue;
+        }
+        ++live[h];
+        const double lp = lp_of(t);
+        if (a.v.slices) a.v.logprobs[t] = (float)lp;
+        if (lp == -__builtin_huge_val()) continue;  // a token of weight 0 adds nothing
+        own[h] += lp;
+        if (a.v.ref) ref[h] += (double)a.v.ref[t];
+      }
+#pragma unroll
+    for (int d = kWave / 2; d; d >>= 1)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        own[h] += __shfl_xor(own[h], d);
+        ref[h] += __shfl_xor(ref[h], d);
+        live[h] += __shfl_xor(live[h], d);
+      }
+    if (lane_id() == 0)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s_own[h][threadIdx.x / kWave] = own[h];
+        s_ref[h][threadIdx.x / kWave] = ref[h];
+        s_live[h][threadIdx.x / kWave] = live[h];
+      }
+    lds_barrier();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const u64 s = p + h * a.pairs;
-      start[h] = offset(s);
-      end[h] = offset(s + 1);
-      double own = 0, ref = 0;
-      u64 n = 0;
-      for (u64 t = start[h] + threadIdx.x; t < end[h]; t += kPairThreads) {
-        if (!row_live(a.v, t)) continue;
-        ++n;
-        const double lp = sc.lp[t];
-        if (lp == -__builtin_huge_val()) continue;  // a token of weight 0 adds nothing
-        own += lp;
-        if (a.v.ref) ref += (double)a.v.ref[t];
+      own[h] = ref[h] = 0;
+      live[h] = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        own[h] += s_own[h][w];
+        ref[h] += s_ref[h][w];
+        live[h] += s_live[h][w];
       }
-      own = block_total<kWaves>(own, s_d);
-      ref = block_total<kWaves>(ref, s_d);
-      live[h] = block_total<kWaves>(n, s_n);
       const double mean = a.average && live[h] ? 1.0 / (double)live[h] : 1.0;
-      ratio[h] = (own - ref) * mean;
-      if (threadIdx.x == 0) a.sequence_logprobs[s] = (float)(own * mean);
+      ratio[h] = (own[h] - ref[h]) * mean;
+      if (threadIdx.x == 0) a.sequence_logprobs[p + h * a.pairs] = (float)(own[h] * mean);
       rows += live[h];
     }
     const double z = a.beta * (ratio[0] - ratio[1]) - a.margin;
@@ -513,23 +671,23 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
         a.coefficients[t] = row_live(a.v, t) ? c : 0.f;
     }
     if (p == 0)
-      for (u64 t = threadIdx.x; t < start[0]; t += kPairThreads) a.coefficients[t] = 0.f;
+      for (u64 t = threadIdx.x; t < start[0]; t += kPairThreads) outside(t);
     if (p == a.pairs - 1)
-      for (u64 t = end[1] + threadIdx.x; t < a.v.T; t += kPairThreads) a.coefficients[t] = 0.f;
+      for (u64 t = end[1] + threadIdx.x; t < a.v.T; t += kPairThreads) outside(t);
   }
   if (threadIdx.x == 0) {
-    st_double(&sc.terms[blockIdx.x].loss, total);
-    st_agent(&sc.terms[blockIdx.x].clipped, rows);
+    st_double(&sc.chunks[blockIdx.x].loss, total);
+    st_agent(&sc.chunks[blockIdx.x].count, rows);
     drain_memory_ops();
-    s_last = __hip_atomic_fetch_add(sc.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == gridDim.x;
+    s_last = __hip_atomic_fetch_add(sc.last, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == gridDim.x;
   }
   __syncthreads();
   if (!s_last) return;
   double loss = 0;
   u64 n = 0;
   for (u32 i = threadIdx.x; i < gridDim.x; i += kPairThreads) {
-    loss += ld_double(&sc.terms[i].loss);
-    n += ld_agent(&sc.terms[i].clipped);
+    loss += ld_double(&sc.chunks[i].loss);
+    n += ld_agent(&sc.chunks[i].count);
   }
   loss = block_total<kWaves>(loss, s_d);
   n = block_total<kWaves>(n, s_n);
@@ -542,15 +700,16 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
 namespace {
 
 template <class T, int TEAM, int N, bool GRAD, bool MULTI>
-hipError_t vocab_launch(const VocabArgs& a, hipStream_t s) {
+hipError_t vocab_launch(VocabArgs a, hipStream_t s) {
   constexpr int kBlock = TEAM < 256 ? 256 : TEAM, kTeams = kBlock / TEAM;
-  static const u32 fit = resident_blocks(vocab_kernel<T, TEAM, N, GRAD, MULTI>, kBlock);
-  const u64 rounds = (a.T + kTeams - 1) / kTeams;
-  u64 blocks = rounds < fit ? rounds : fit;
-  if (blocks > kVocabMaxBlocks) blocks = kVocabMaxBlocks;
-  if (!blocks) blocks = 1;
-  vocab_kernel<T, TEAM, N, GRAD, MULTI><<<(u32)blocks, kBlock, 0, s>>>(a);
-  return hipGetLastError();
+  constexpr u64 kMost = ((1ull << 32) / kBlock - 1) * kTeams;  // rows of a launch, which has fewer than 2^32 threads
+  for (a.row0 = 0; a.row0 < a.T; a.row0 += kMost) {
+    const u64 rows = a.T - a.row0 < kMost ? a.T - a.row0 : kMost;
+    vocab_kernel<T, TEAM, N, GRAD, MULTI, kWhole><<<(u32)((rows + kTeams - 1) / kTeams), kBlock, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <class T, bool GRAD>
@@ -564,30 +723,67 @@ hipError_t vocab_shape(const VocabArgs& a, hipStream_t s) {
   return vocab_launch<T, 1024, 16, GRAD, true>(a, s);
 }
 
+constexpr int kSliceThreads = 256, kSliceVectors = 8;
+
 template <class T>
-hipError_t vocab_grad(const VocabArgs& a, hipStream_t s) {
+hipError_t vocab_split(const VocabArgs& a, hipStream_t s) {
+  vocab_kernel<T, kSliceThreads, kSliceVectors, false, true, kPart>
+      <<<(u32)a.T * a.slices + 1, kSliceThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.pairs) return e;
+  if (a.d_x)
+    vocab_kernel<T, kSliceThreads, kSliceVectors, true, true, kJoin>
+        <<<(u32)a.T * (a.slices + (a.policy ? 1 : 0)), kSliceThreads, 0, s>>>(a);
+  else
+    vocab_kernel<T, kSliceThreads, kSliceVectors, false, true, kJoin><<<(u32)a.T, kSliceThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t vocab_type(const VocabArgs& a, hipStream_t s) {
+  if (a.slices) return vocab_split<T>(a, s);
   return a.d_x ? vocab_shape<T, true>(a, s) : vocab_shape<T, false>(a, s);
 }
 
 }  // namespace
 
-size_t vocab_scratch_bytes(u64 T) { return kVocabHead + kVocabMaxBlocks * sizeof(BlockTerms) + 8 * T; }
+size_t vocab_scratch_bytes(u64 T) {
+  const VocabScratch v = vocab_scratch(nullptr, T);
+  return (size_t)(uintptr_t)v.parts + sizeof(Part) * kSlices * (T < kSplitRows ? T : kSplitRows);
+}
+
+u32 vocab_slices(const VocabArgs& a, int dtype) {
+  const u64 bytes = a.V * (dtype == PROFK_FP32 ? 4 : 2);
+  if (a.T > kSplitRows || bytes < (a.policy || a.pairs || a.d_x ? 32768 : 131072)) return 0;
+  const u64 s = (bytes + 16383) / 16384;
+  return (u32)(s < kSlices ? s : kSlices);
+}
 
 hipError_t launch_vocab(VocabArgs a, int dtype, hipStream_t s) {
-  if (a.policy || a.pairs) {
-    const u64 rounds = (a.T + kCountThreads * 4 - 1) / (kCountThreads * 4);
-    a.count_blocks = rounds < 1 ? 1 : rounds < kCountBlocks ? (u32)rounds : kCountBlocks;
+  if (!a.T) {
+    if (a.policy)
+      vocab_empty_kernel<<<1, 1, 0, s>>>(a);
+    else if (a.pairs)
+      vocab_count_kernel<<<1, kCountThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  a.slices = vocab_slices(a, dtype);
+  a.count_blocks = 1;
+  if ((a.policy || a.pairs) && !a.slices) {
+    const u64 rounds = (a.T + kCountThreads - 1) / kCountThreads;
+    a.count_blocks = rounds < kCountBlocks ? (u32)rounds : kCountBlocks;
     vocab_count_kernel<<<a.count_blocks, kCountThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!a.T && !a.policy) return hipSuccess;
-  if (dtype == PROFK_FP32) return vocab_grad<float>(a, s);
-  if (dtype == PROFK_FP16) return vocab_grad<Half16>(a, s);
-  return vocab_grad<Brain16>(a, s);
+  if (dtype == PROFK_FP32) return vocab_type<float>(a, s);
+  if (dtype == PROFK_FP16) return vocab_type<Half16>(a, s);
+  return vocab_type<Brain16>(a, s);
 }
 
-hipError_t launch_pairs(const PairArgs& a, hipStream_t s) {
+hipError_t launch_pairs(PairArgs a, int dtype, hipStream_t s) {
+  a.dtype = dtype;
+  a.v.slices = a.v.T ? vocab_slices(a.v, dtype) : 0;
   pair_kernel<<<a.pairs < kPairBlocks ? (u32)a.pairs : kPairBlocks, kPairThreads, 0, s>>>(a);
   return hipGetLastError();
 }

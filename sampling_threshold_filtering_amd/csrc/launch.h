@@ -366,7 +366,8 @@ struct VocabArgs {
   int64_t *clipped, *rows;
   void* d_x;                   // T * V, contiguous, of the logits' type, or nullptr: no gradient
   char* scratch;               // vocab_scratch_bytes
-  u32 count_blocks;            // set by launch_vocab
+  u32 count_blocks, slices;    // set by launch_vocab; slices of a row, 0: none
+  u64 row0;                    // the launch's first row
 };
 // The preference loss over the log-probabilities that launch_vocab left in scratch.
 struct PairArgs {
@@ -375,11 +376,12 @@ struct PairArgs {
   u64 pairs;
   double beta, smoothing, margin;
   bool average;
+  int dtype;                   // set by launch_pairs
   float *margins, *sequence_logprobs, *coefficients;  // pairs, 2 * pairs, T
 };
 size_t vocab_scratch_bytes(u64 T);
 hipError_t launch_vocab(VocabArgs a, int dtype, hipStream_t s);
-hipError_t launch_pairs(const PairArgs& a, hipStream_t s);
+hipError_t launch_pairs(PairArgs a, int dtype, hipStream_t s);
 
 hipError_t launch_sort_and_write(u64* buf0, u64* buf1, u32* hist, u32 k, const float* row, u64 N, float* out_vals,
                                  int64_t* out_idx, RowCtl* ctl, AttemptRecord* rec, hipStream_t s);
