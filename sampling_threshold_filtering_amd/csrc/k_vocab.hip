@@ -24,7 +24,7 @@ namespace {
 constexpr int kCountThreads = 1024;
 constexpr u32 kCountBlocks = 64;  // a lane per part of the count
 constexpr u64 kChunk = 1024;      // rows whose terms one wavefront adds up
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 512;
 constexpr u32 kPairBlocks = 1024;
 constexpr u32 kSlices = 64;       // most parts of a row: a lane each
 constexpr u64 kSplitRows = 512;   // most rows that are split
@@ -217,7 +217,8 @@ __device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, u64 t, const Ro
 
 __device__ __forceinline__ bool row_live(const VocabArgs& a, u64 t) {
   const int64_t k = a.tokens[t];
-  return (!a.mask || a.mask[t]) && k >= 0 && (u64)k < a.V;
+  const unsigned char m = a.mask ? a.mask[t] : 1;  // both loads at once
+  return m & (u32)((u64)k < a.V) ? true : false;
 }
 
 // Sum of one value per thread over the block, in a fixed order; every thread has it.
@@ -358,12 +359,13 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
   char* dv = GRAD ? reinterpret_cast<char*>(dx + head) + (u64)from * 16 : nullptr;
   const u32 off = tid * 16;
   u32 first = 0;  // the segment's first vector
-  // Vectors of this wavefront in the segment; of the last of them, whether this lane has one.
-  auto count = [&]() {
-    const u32 left = nvec > first + base ? (nvec - first - base + TEAM - 1) / TEAM : 0;
+  // Vectors of this wavefront in the segment that begins at f; of the last of them, whether this
+  // lane has one.
+  auto count = [&](u32 f) {
+    const u32 left = nvec > f + base ? (nvec - f - base + TEAM - 1) / TEAM : 0;
     return (int)(left < N ? left : N);
   };
-  auto has = [&](int i) { return first + i * TEAM + tid < nvec; };
+  auto has = [&](u32 f, int i) { return f + i * TEAM + tid < nvec; };
   auto store = [&](int i, const Words& w) {
     __builtin_nontemporal_store(w, reinterpret_cast<Words*>(dv + (u64)(first + i * TEAM) * 16 + off));
   };
@@ -393,16 +395,17 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
   const u32 slot = in_vec / W / TEAM, owner = in_vec / W % TEAM, place = in_vec % W;
   const bool own_wave = in_vecs && owner / kWave * kWave == base;
   Words v[N];
+  auto load_one = [&](u32 f, int i, int n) {
+    if (i + 1 == n) v[i] = Words{NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value};
+    if (i + 1 < n || has(f, i))
+      v[i] = __builtin_nontemporal_load(
+          reinterpret_cast<const typename AnyWords<T>::type*>(xv + (u64)(f + i * TEAM) * 16 + off));
+  };
   auto load = [&]() {
-    const int n = count();
+    const int n = count(first);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i >= n) continue;
-      if (i + 1 == n) v[i] = Words{NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value, NoneWord<T>::value};
-      if (i + 1 < n || has(i))
-        v[i] = __builtin_nontemporal_load(
-            reinterpret_cast<const typename AnyWords<T>::type*>(xv + (u64)(first + i * TEAM) * 16 + off));
-    }
+    for (int i = 0; i < N; ++i)
+      if (i < n) load_one(first, i, n);
   };
   auto slot_of = [&]() { return own_wave && slot >= first / TEAM && slot < first / TEAM + N ? (int)(slot - first / TEAM) : -1; };
   const u32 segments = MULTI && nvec > TEAM * N ? (nvec + TEAM * N - 1) / (TEAM * N) : 1;
@@ -430,10 +433,10 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
       }
     }
     float top = edge > kLowest ? edge : kLowest, rest[4] = {0.f, 0.f, 0.f, 0.f};
+    load();
     for (u32 seg = 0; seg < segments; ++seg) {
       first = seg * TEAM * N;
-      load();
-      const int at = slot_of(), n = count();
+      const int at = slot_of(), n = count(first), next = seg + 1 < segments ? count(first + TEAM * N) : 0;
       const float before = top;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -455,6 +458,8 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
         if (i >= n) continue;
 #pragma unroll
         for (u32 k = 0; k < W; ++k) rest[k % 4] += ex.of<T>(entry<T>(v[i], k) - top);
+        // its place for the next segment's, on its way while the others are dealt with
+        if (MULTI && i < next) load_one(first + TEAM * N, i, next);
       }
     }
     rest[0] += ex.of<T>(edge - top);
@@ -511,7 +516,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
           first = seg * TEAM * N;
           load();
         }
-        const int at = slot_of(), cnt = count();
+        const int at = slot_of(), cnt = count(first);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           if (i >= cnt) continue;
@@ -527,7 +532,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
             w[k] = bits;
           }
           if (i == at && tid == owner) set_entry<T>(w, place, at_token);
-          if (i + 1 < cnt || has(i)) store(i, w);
+          if (i + 1 < cnt || has(first, i)) store(i, w);
         }
       }
     }
@@ -553,13 +558,14 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   constexpr int kWaves = kPairThreads / kWave;
   __shared__ double s_d[kWaves], s_own[2][kWaves], s_ref[2][kWaves];
   __shared__ u64 s_n[kWaves], s_live[2][kWaves];
-  __shared__ int64_t s_rise[4][kWaves];
+  __shared__ u32 s_rise[4][kWaves];
   __shared__ u32 s_last;
   const VocabScratch sc = vocab_scratch(a.v.scratch, a.v.T);
   const Exponent ex = {a.v.exponent_hi, a.v.exponent_lo};
   // A live row's log-probability; of rows that are split, from their parts.
-  auto lp_of = [&](u64 t) {
+  auto lp_of = [&](u64 t, bool here) {
     if (!a.v.slices) return sc.lp[t];
+    if (!here) return 0.0;
     RowSums row = {kLowest, 0.f, logit_of(a, t)};
     for (u32 i = 0; i < a.v.slices; ++i) row.top = max_f(row.top, sc.parts[t * a.v.slices + i].top);
     for (u32 i = 0; i < a.v.slices; ++i) {
@@ -575,26 +581,23 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   // Rows that no sequence takes.
   auto outside = [&](u64 t) {
     a.coefficients[t] = 0.f;
-    if (a.v.slices) a.v.logprobs[t] = row_live(a.v, t) ? (float)lp_of(t) : 0.f;
+    if (a.v.slices) a.v.logprobs[t] = (float)lp_of(t, row_live(a.v, t));
   };
   double total = 0;
   u64 rows = 0;
   for (u64 p = blockIdx.x; p < a.pairs; p += gridDim.x) {
-    // Offsets as far as they rise, within [0, T]: one below an earlier one counts as that.
-    int64_t rise[4] = {0, 0, 0, 0};
+    // Offsets as far as they rise, within [0, T] (T < 2^31): one below an earlier one counts as that.
+    u32 rise[4] = {0, 0, 0, 0};
     const u64 at[4] = {p, p + 1, p + a.pairs, p + a.pairs + 1};
     for (u64 k = threadIdx.x; k <= at[3]; k += kPairThreads) {
       const int64_t o = a.offsets[k];
+      const u32 within = o < 0 ? 0 : (u64)o < a.v.T ? (u32)o : (u32)a.v.T;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) rise[h] = k <= at[h] && o > rise[h] ? o : rise[h];
+      for (int h = 0; h < 4; ++h) rise[h] = k <= at[h] && within > rise[h] ? within : rise[h];
     }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-#pragma unroll
-      for (int d = kWave / 2; d; d >>= 1) {
-        const int64_t o = __shfl_xor(rise[h], d);
-        rise[h] = o > rise[h] ? o : rise[h];
-      }
+      rise[h] = wave_reduce_u32(rise[h], [](u32 x, u32 y) { return x > y ? x : y; });
       if (lane_id() == 0) s_rise[h][threadIdx.x / kWave] = rise[h];
     }
     lds_barrier();
@@ -604,26 +607,29 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
     for (int h = 0; h < 4; ++h) {
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) rise[h] = s_rise[h][w] > rise[h] ? s_rise[h][w] : rise[h];
-      const u64 r = (u64)rise[h] < a.v.T ? (u64)rise[h] : a.v.T;
       if (h & 1)
-        end[h / 2] = r;
+        end[h / 2] = rise[h];
       else
-        start[h / 2] = r;
+        start[h / 2] = rise[h];
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      for (u64 t = start[h] + threadIdx.x; t < end[h]; t += kPairThreads) {
-        if (!row_live(a.v, t)) {
-          if (a.v.slices) a.v.logprobs[t] = 0.f;
-          continue;
-        }
-        ++live[h];
-        const double lp = lp_of(t);
-        if (a.v.slices) a.v.logprobs[t] = (float)lp;
-        if (lp == -__builtin_huge_val()) continue;  // a token of weight 0 adds nothing
-        own[h] += lp;
-        if (a.v.ref) ref[h] += (double)a.v.ref[t];
-      }
+    // the rows of both, all of a row's loads at once
+    const u64 first = end[0] - start[0], both = first + (end[1] - start[1]);
+    auto row_of = [&](u64 i) { return i < first ? start[0] + i : start[1] + (i - first); };
+    for (u64 i = threadIdx.x; i < both; i += kPairThreads) {
+      const u64 t = row_of(i);
+      const int h = i >= first;
+      const bool here = row_live(a.v, t);
+      const float r = a.v.ref ? a.v.ref[t] : 0.f;
+      const double lp = lp_of(t, here);
+      if (a.v.slices) a.v.logprobs[t] = here ? (float)lp : 0.f;
+      const bool counts = here && lp != -__builtin_huge_val();  // a token of weight 0 adds nothing
+      live[0] += here && !h;
+      live[1] += here && h;
+      own[0] += counts && !h ? lp : 0.0;
+      own[1] += counts && h ? lp : 0.0;
+      ref[0] += counts && !h ? (double)r : 0.0;
+      ref[1] += counts && h ? (double)r : 0.0;
+    }
 #pragma unroll
     for (int d = kWave / 2; d; d >>= 1)
 #pragma unroll
@@ -663,12 +669,13 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
     total += z == z ? keep * up + a.smoothing * down : z;
     if (threadIdx.x == 0) a.margins[p] = (float)z;
     const double slope = a.beta / (double)a.pairs * (a.smoothing * sigmoid - keep * other);
+    float c[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const double mean = a.average && live[h] ? 1.0 / (double)live[h] : 1.0;
-      const float c = (float)((h ? -slope : slope) * mean);
-      for (u64 t = start[h] + threadIdx.x; t < end[h]; t += kPairThreads)
-        a.coefficients[t] = row_live(a.v, t) ? c : 0.f;
+    for (int h = 0; h < 2; ++h)
+      c[h] = (float)((h ? -slope : slope) * (a.average && live[h] ? 1.0 / (double)live[h] : 1.0));
+    for (u64 i = threadIdx.x; i < both; i += kPairThreads) {
+      const u64 t = row_of(i);
+      a.coefficients[t] = row_live(a.v, t) ? c[i >= first] : 0.f;
     }
     if (p == 0)
       for (u64 t = threadIdx.x; t < start[0]; t += kPairThreads) outside(t);
@@ -719,6 +726,7 @@ hipError_t vocab_shape(const VocabArgs& a, hipStream_t s) {
   if (bytes <= 64 * 16 * 16) return vocab_launch<T, 64, 16, GRAD, false>(a, s);
   if (bytes <= 256 * 16 * 16) return vocab_launch<T, 256, 16, GRAD, false>(a, s);
   if (bytes <= 512 * 16 * 16) return vocab_launch<T, 512, 16, GRAD, false>(a, s);
+  if constexpr (!GRAD) return vocab_launch<T, 256, 16, GRAD, true>(a, s);
   if (bytes <= 1024 * 16 * 16) return vocab_launch<T, 1024, 16, GRAD, false>(a, s);
   return vocab_launch<T, 1024, 16, GRAD, true>(a, s);
 }
