@@ -390,10 +390,12 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
     R row;
     row.load(x + tr * a.ld, a.E, g, in);
     float falling[SIGMOID ? C : 1];  // 1 - score
-    if constexpr (SIGMOID)
-      row.score(in, falling);
-    else
+    if constexpr (SIGMOID) {
+      bool nan = false;
+      row.score(in, nan, falling);
+    } else {
       row.weigh(in);
+    }
     const float inv = row.inverse();
     float out[C];
     float dot = 0.f;

@@ -10,10 +10,10 @@
 //
 // The choice goes by keys of 32 bits, as in k_route.hip: c in units of (its possible range) /
 // 2^24, from the lowest bias up, above the entry's complement.  A unit is a few times the
-// error of c in 32 bits, so where two neighbours among the first k + 1 keys, or the worst
-// group kept and the best left out, are within that error of each other, the wavefront
-// chooses again in 64 bits; two entries of the same logit and bias are told apart by their
-// index in any arithmetic and do not need it.  A fixed point rather than the float's own bits:
+// error of c in 32 bits, so where two neighbours among the first k + 1 keys are within that
+// error of each other, the wavefront ranks those that may be among the first k in 64 bits, a
+// lane each; and where the worst group kept and the best left out are, it chooses the whole row
+// again in 64 bits.  A fixed point rather than the float's own bits:
 // its low bits are what the index leaves of a float's 24 (at 256 experts 15, too few for one
 // row in 30; the fixed point's 24 leave one row in 600).
 #include "route_device.h"
@@ -48,10 +48,6 @@ __device__ __forceinline__ u32 wave_min(u32 v) {
 // A constant in scalar registers, made where it is used: held in vector registers over the rows'
 // loop, the few dozen of the 64-bit choice took a third of the loop's.
 __device__ __forceinline__ double in_scalar(double v) {
-  asm volatile("" : "+s"(v));
-  return v;
-}
-__device__ __forceinline__ u32 in_scalar(u32 v) {
   asm volatile("" : "+s"(v));
   return v;
 }
@@ -119,60 +115,89 @@ __device__ __forceinline__ void from_lds(const V* row, u32 g, V (&v)[C]) {
 
 }  // namespace
 
+// The kernel's arguments, read again: held in scalar registers over the rows' loop, those that
+// only the 64-bit choice needs would drive others out of them.
+__device__ __forceinline__ const RouteArgs& arguments_again() {
+  typedef const __attribute__((address_space(4))) RouteArgs* Constant;
+  Constant p = (Constant)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const RouteArgs*)p;
+}
+
+// The sum of a row's softmax in 64 bits, by the whole wavefront; top is the row's largest logit
+// (NaN or +inf make every score NaN).
+template <class T>
+__device__ __forceinline__ double softmax_sum(const RouteArgs& a, const T* x, float top) {
+  double sum = 0;
+#pragma unroll 1
+  for (u32 e = lane_id(); e < a.E; e += kWave) sum += exp_64((double)to_f32(x[e]) - (double)top);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
+  return sum;
+}
+
+// The code of the choice score of an entry of logit l and bias b; 0: none.
+__device__ __forceinline__ u64 choice_code(const RouteArgs& a, float l, float b, float top, double sum) {
+  const double s = a.sigmoid ? 1.0 / (1.0 + exp_64(-(double)l)) : exp_64((double)l - (double)top) / sum;
+  const double c = a.bias ? s + (double)b : s;
+  return l == kNone || c == -__builtin_huge_val() ? 0 : code_of(c);
+}
+
+// The first keys of a row, `n` of them and among them its k experts, in the order of 64 bits:
+// lane j has the j-th key's expert and gets its rank.
+template <class T>
+__device__ __forceinline__ u32 rank_exactly(const RouteArgs& a, u64 row, u32 n, u32 e, float top) {
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ld;
+  const bool mine = lane_id() < n;
+  const float l = mine ? to_f32(x[e]) : kNone, b = mine && a.bias ? a.bias[e] : 0.f;
+  const u64 code = choice_code(a, l, b, top, a.sigmoid ? 1.0 : softmax_sum(a, x, top));
+  u32 rank = 0;
+#pragma unroll 1
+  for (u32 j = 0; j < n; ++j) {
+    const u64 o = (u64)(u32)__builtin_amdgcn_readlane((int)(code >> 32), (int)j) << 32 |
+                  (u32)__builtin_amdgcn_readlane((int)code, (int)j);
+    const u32 f = (u32)__builtin_amdgcn_readlane((int)e, (int)j);
+    rank += o > code || (o == code && f < e);
+  }
+  return rank;
+}
+
+// The code of group q's score, by the whole wavefront.
+template <class T>
+__device__ __forceinline__ u64 group_code(const RouteArgs& a, const T* x, u32 q, u32 size, float top, double sum) {
+  u64 first = 0, second = 0;
+#pragma unroll 1
+  for (u32 j = lane_id(); j < size; j += kWave) {
+    const u32 e = q * size + j;
+    const u64 c = choice_code(a, to_f32(x[e]), a.bias ? a.bias[e] : 0.f, top, sum), low = c < first ? c : first;
+    second = low > second ? low : second;
+    first = c > first ? c : first;
+  }
+  const u64 best = wave_max(first);
+  if (a.group_best != 2) return best;
+  const u64 holders = __ballot(first == best);
+  second = holders & (holders - 1) ? best : wave_max(first == best ? second : first);
+  return second ? code_of(of_code(best) + of_code(second)) : best;
+}
+
 // One row by the whole wavefront in 64 bits: lane j gets slot j's expert, or ~0.  `codes` has
 // room for E.  No array of it lives in registers: the rows that come here are few, and the
 // others' loop keeps its registers.
 template <class T>
-__device__ __forceinline__ u32 choose_exactly(const RouteArgs& a, const T* x, u64* codes) {
-  const u32 lane = lane_id(), E = in_scalar(a.E);
-  if (!a.sigmoid) {  // a NaN or +inf makes every score NaN
-    double top = -__builtin_huge_val(), sum = 0;
+__device__ __forceinline__ u32 choose_exactly(const RouteArgs& a, u64 row, float top, u64* codes) {
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ld;
+  const u32 lane = lane_id(), E = a.E;
+  const double sum = a.sigmoid ? 1.0 : softmax_sum(a, x, top);
 #pragma unroll 1
-    for (u32 e = lane; e < E; e += kWave) {
-      const double l = (double)to_f32(x[e]);
-      top = l > top || l != l ? l : top;
-    }
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const double o = __shfl_xor(top, d);
-      top = o > top || o != o ? o : top;
-    }
-#pragma unroll 1
-    for (u32 e = lane; e < E; e += kWave) {
-      const double p = exp_64((double)to_f32(x[e]) - top);
-      codes[e] = __builtin_bit_cast(u64, p);
-      sum += p;
-    }
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
-#pragma unroll 1
-    for (u32 e = lane; e < E; e += kWave) codes[e] = __builtin_bit_cast(u64, __builtin_bit_cast(double, codes[e]) / sum);
-  }
-#pragma unroll 1
-  for (u32 e = lane; e < E; e += kWave) {
-    const double l = (double)to_f32(x[e]);
-    const double s = a.sigmoid ? 1.0 / (1.0 + exp_64(-l)) : __builtin_bit_cast(double, codes[e]);
-    const double c = a.bias ? s + (double)a.bias[e] : s;
-    codes[e] = l == -__builtin_huge_val() || c == -__builtin_huge_val() ? 0 : code_of(c);
-  }
+  for (u32 e = lane; e < E; e += kWave) codes[e] = choice_code(a, to_f32(x[e]), a.bias ? a.bias[e] : 0.f, top, sum);
   wave_lds_sync();
   if (a.top_groups < a.groups) {
-    const u32 size = E / in_scalar(a.groups);
+    const u32 size = E / a.groups;
     u64 mine = 0;  // lane g: group g's score
 #pragma unroll 1
     for (u32 g = 0; g < a.groups; ++g) {
-      u64 first = 0, second = 0;
-#pragma unroll 1
-      for (u32 j = lane; j < size; j += kWave) {
-        const u64 c = codes[g * size + j], low = c < first ? c : first;
-        second = low > second ? low : second;
-        first = c > first ? c : first;
-      }
-      const u64 top = wave_max(first);
-      const u64 holders = __ballot(first == top);
-      second = holders & (holders - 1) ? top : wave_max(first == top ? second : first);
-      first = a.group_best == 2 && second ? code_of(of_code(top) + of_code(second)) : top;
-      if (lane == g) mine = first;
+      const u64 c = group_code(a, x, g, size, top, sum);
+      if (lane == g) mine = c;
     }
     u32 before = 0;
 #pragma unroll 1
@@ -211,7 +236,8 @@ __device__ __forceinline__ u32 choose_exactly(const RouteArgs& a, const T* x, u6
 }
 
 template <class T, int G, int C, bool QUAD, bool SIGMOID>
-__global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs args) {
+  const RouteArgs& a = args;  // up to the rows' loop
   using R = Row<G, C, QUAD>;
   using K = Choice<G, C>;
   constexpr int kGroups = kScoredThreads / G, kRows = kWave / G;  // rows of a block, of a wavefront
@@ -220,7 +246,8 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
   __shared__ u32 s_group[kScoredWaves][kRows][K::kMostGroups];
   __shared__ u32 s_cnt[G * C];
   __shared__ alignas(16) float s_base[G * C];  // the biases in units from the lowest; -inf: none
-  __shared__ float s_sum[kScoredWaves][G * C];
+  // each lane's sums of probabilities, four experts together; while they are joined, the wavefront's
+  __shared__ alignas(16) float s_sum[kScoredWaves][kWave * C];
   __shared__ u32 s_rows;
   __shared__ double s_part[kScoredWaves];
   static_assert(G * C <= 2 * kScoredThreads, "two experts a thread");
@@ -230,6 +257,18 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
   u32* key_row = s_key[wave][row_of_wave];
   u32* group_row = s_group[wave][row_of_wave];
   const T* x = reinterpret_cast<const T*>(a.x);
+  const u64 step = (u64)gridDim.x * kGroups;
+  // A row's loads go out a turn ahead: with four wavefronts a SIMD the others do not cover them.
+  typename R::template Raw<T> raw;
+  bool masked = true;
+  auto fetch = [&](u64 t0) {
+    const RouteArgs& a = arguments_again();
+    const u64 t = t0 + grp, tr = t < a.T ? t : a.T - 1;
+    masked = a.mask && !a.mask[tr];
+    R::fetch(reinterpret_cast<const T*>(a.x) + tr * a.ld, a.E, g, raw);
+  };
+  u64 t0 = (u64)blockIdx.x * kGroups;
+  if (t0 < a.T) fetch(t0);
   float low = a.bias ? __builtin_huge_valf() : 0.f, high = a.bias ? -__builtin_huge_valf() : 0.f;
   bool odd = false;  // a bias that the keys cannot hold
 #pragma unroll 1
@@ -259,36 +298,48 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
   while ((2u << lanes_log) * a.groups <= (u32)G) ++lanes_log;
   const u32 lanes = 1u << lanes_log, part = g & (lanes - 1);
 
-  float sum[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) sum[i] = 0.f;
   u32 rows = 0;
-  const u64 step = (u64)gridDim.x * kGroups;
+  // The lane's sums live in LDS: in registers they would take 16 of 128, and the row's choice spill.
+  Four<float>* sums = reinterpret_cast<Four<float>*>(s_sum[wave]) + lane_id();
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) sums[i * kWave] = Four<float>{{0.f, 0.f, 0.f, 0.f}};
+  };
+  clear();
   double total[2] = {0, 0};  // of experts threadIdx.x and threadIdx.x + kScoredThreads
   auto join = [&]() {
+    float v[C];
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+      const Four<float> q = sums[i / 4 * kWave];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i + k] = q.e[k];
+    }
+    wave_lds_sync();
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      float v = sum[i];
 #pragma unroll
-      for (int d = G; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-      if (lane_id() < G) s_sum[wave][R::index(i, g)] = v;
+      for (int d = G; d < kWave; d <<= 1) v[i] += __shfl_xor(v[i], d);
+      if (lane_id() < G) s_sum[wave][R::index(i, g)] = v[i];
     }
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const u32 e = threadIdx.x + h * kScoredThreads;
-      if (e < a.E)
+      if (e < arguments_again().E)
 #pragma unroll
         for (int w = 0; w < kScoredWaves; ++w) total[h] += (double)s_sum[w][e];
     }
   };
   u32 turn = 0;
-  for (u64 t0 = (u64)blockIdx.x * kGroups; t0 < a.T; t0 += step) {
-    const u64 t = t0 + grp, tr = t < a.T ? t : a.T - 1;
-    const bool in = (!a.mask || a.mask[tr]) && t < a.T, here = t < a.T;
-    const T* xt = x + tr * a.ld;
+  for (; t0 < arguments_again().T; t0 += step) {
+    const RouteArgs& a = arguments_again();
+    const u64 t = t0 + grp;
+    const bool here = t < a.T, in = here && !masked;
+    const T* xt = x + (here ? t : a.T - 1) * a.ld;
     R row;
-    row.load(xt, a.E, g, in);
+    row.take(raw, a.E, g, in);
+    if (t0 + step < a.T) fetch(t0 + step);
     // entries of -inf, a bit each: the logits themselves do not stay in registers
     u32 none = 0;
     float least_logit = row.v[0];
@@ -301,7 +352,8 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
     }
     bool nan = false;
     if constexpr (SIGMOID) {
-      row.score(in, nan);
+      float unused[1];
+      row.score(in, nan, unused);
     } else {
       row.weigh(in);
       nan = !(row.top < __builtin_huge_valf());
@@ -309,13 +361,19 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
     const float inv = row.inverse();
     if (a.loss) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) sum[i] = __builtin_fmaf(row.e[i], inv, sum[i]);
+      for (int i = 0; i < C; i += 4) {
+        Four<float> q = sums[i / 4 * kWave];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q.e[k] = __builtin_fmaf(row.e[i + k], inv, q.e[k]);
+        sums[i / 4 * kWave] = q;
+      }
     }
     rows += row.live && g == 0;
     // keys
     u32 key[C];
     const float per = SIGMOID ? unit : unit * inv;
     float base[C];
+    const u32 low = opaque_u32(K::kLow - R::index(0, g));  // of entry 0; here, so that 16 of them do not stay in registers
     from_lds<QUAD, G, C>(s_base, g, base);
     if (nones) {
 #pragma unroll
@@ -324,9 +382,10 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const float u = __builtin_fmaf(row.e[i], per, base[i]);  // of an entry that is none -inf: converts to 0
-      key[i] = (u32)__builtin_fmaxf(u, 0.f) << K::kBits | (K::kLow - R::index(i, g));
+      key[i] = (u32)__builtin_fmaxf(u, 0.f) << K::kBits | (low - R::index(i, 0));
     }
     auto same = [&](u32 m, u32 n) {  // the entries of two keys
+      const RouteArgs& a = arguments_again();
       const u32 e = K::kLow - (m & K::kLow), f = K::kLow - (n & K::kLow);
       return to_f32(xt[e]) == to_f32(xt[f]) && (!a.bias || a.bias[e] == a.bias[f]);
     };
@@ -338,6 +397,7 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
     const u32 close = near << K::kBits | K::kLow;  // in keys
     bool unsure = odd || group_reduce<G>((u32)nan, max_u) != 0;
     if (grouped) {
+      const RouteArgs& a = arguments_again();
       to_lds<QUAD, G, C>(key_row, g, key);
       wave_lds_sync();
       // A lane's groups: their two largest keys, then their scores: one key, or a sum of two values.
@@ -391,19 +451,61 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
       }
       least = ~group_reduce<G>(~least, max_u);
       most = group_reduce<G>(most, max_u);
-      if (best == 2) {
-        unsure |= most && least - most <= 2 * near;
-      } else if (most && least - most <= close) {
-        // Groups of the same best logit and bias are told apart by their index in any arithmetic: so
-        // are these if whatever may be the best of a group at the border is the same as theirs.
+      // Groups whose order against the border rounding may have changed.
+      const u32 margin = best == 2 ? 2 * near : close;
+      bool border = most && least - most <= margin && row.live && !unsure;
+      if (best == 1 && border) {
+        // Of the same best logit and bias they are told apart by their index in any arithmetic: so are
+        // these if whatever may be the best of one of them is the same.
+        border = false;
         turn_of = 1;
         for (u32 q = g >> lanes_log; q < a.groups; q += (u32)G >> lanes_log, turn_of <<= 1) {
           const u32 own = group_row[q];
-          if (!own || (kept & turn_of ? own - most : least - own) > close) continue;
+          if (!own || (kept & turn_of ? own - most : least - own) > margin) continue;
           for (u32 j = part; j < size; j += lanes) {
             const u32 u = key_row[q * size + j];
-            unsure |= u > K::kLow && (u > most || most - u <= 2 * close) && !same(u, most);
+            border |= u > K::kLow && (u > most || most - u <= 2 * margin) && !same(u, most);
           }
+        }
+      }
+      border = group_reduce<G>((u32)border, max_u) != 0;
+      for (u64 left = __ballot(border && g == 0); left; left &= left - 1) {
+        // as many of them are kept as were, by their scores in 64 bits; lane f has the f-th of them
+        const RouteArgs& b = arguments_again();
+        const u32 from = (u32)__builtin_ctzll(left), lane = lane_id(), per = (u32)G >> lanes_log;
+        const bool own_row = lane / G == from / G;
+        const T* xr = reinterpret_cast<const T*>(b.x) + (t0 + wave * kRows + from / G) * b.ld;
+        const float top = __shfl(row.top, (int)from);
+        const double sum = b.sigmoid ? 1.0 : softmax_sum(b, xr, top);
+        u64 code = 0;
+        u32 group = 0, count = 0, keep = 0;
+        turn_of = 1;
+        for (u32 q0 = 0; q0 < b.groups; q0 += per, turn_of <<= 1) {
+          const u32 q = q0 + (g >> lanes_log), own = q < b.groups ? group_row[q] : 0;
+          const bool was = kept & turn_of;
+          for (u64 near_ones = __ballot(own_row && part == 0 && own && (was ? own - most : least - own) <= margin); near_ones;
+               near_ones &= near_ones - 1) {
+            const u32 l = (u32)__builtin_ctzll(near_ones), it = q0 + ((l - from) >> lanes_log);
+            const u64 c = group_code(b, xr, it, size, top, sum);
+            if (lane == count) {
+              code = c;
+              group = it;
+            }
+            ++count;
+            keep += (u32)__builtin_amdgcn_readlane((int)was, (int)l) != 0;
+          }
+        }
+        u32 rank = 0;
+        for (u32 f = 0; f < count; ++f) {
+          const u64 o = (u64)(u32)__builtin_amdgcn_readlane((int)(code >> 32), (int)f) << 32 |
+                        (u32)__builtin_amdgcn_readlane((int)code, (int)f);
+          rank += o > code || (o == code && f < lane);  // (lane f's group comes before lane f + 1's)
+        }
+        for (u32 f = 0; f < count; ++f) {
+          const u32 it = (u32)__builtin_amdgcn_readlane((int)group, (int)f);
+          const u32 bit = 1u << it / per;
+          if (own_row && it % per == g >> lanes_log)
+            kept = (u32)__builtin_amdgcn_readlane((int)rank, (int)f) < keep ? kept | bit : kept & ~bit;
         }
       }
       turn_of = 1;
@@ -420,43 +522,70 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
 #pragma unroll
     for (int i = 1; i < C; ++i) m = max_u(m, key[i]);
     m = group_reduce<G>(m, max_u);
+    const u32 slots = arguments_again().k, last_slot = slots - 1, experts = arguments_again().E;
     for (u32 j = 0;; ++j) {
       if (g == j % G) mine = m;
-      if (a.k > (u32)G && (j % G == G - 1 || j + 1 == a.k) && g <= j % G) key_row[j / G * G + g] = mine;
-      if (j + 1 == a.E) break;
+      if (j % G == G - 1 || j == last_slot) {
+        if (slots > (u32)G && g <= j % G) key_row[j / G * G + g] = mine;
+      }
+      if (j + 1 == experts) break;
       u32 d = 0;
 #pragma unroll
       for (int i = 0; i < C; ++i) d = max_u(d, key[i] - m);
       const u32 n = m + group_reduce<G>(d, max_u);
       closes |= n > K::kLow && m - n <= close;
-      if (j + 1 == a.k) break;
+      if (j == last_slot) break;
       m = n;
     }
     wave_lds_sync();
+    unsure = group_reduce<G>((u32)unsure, max_u) && row.live;
+    closes = closes && !unsure && row.live;
     if (__builtin_expect(__ballot(closes) != 0, 0)) {
-      // neighbours of the same logit and bias are told apart by their index in any arithmetic
-      u32 last = 0;
-      for (u32 j = 0;; ++j) {
+      // Whatever may be among the first k: the keys down to as far below the k-th as two may be off
+      // each other.  The wavefront ranks them in 64 bits, a lane each.
+      u32 last = 0, border = 0, some = 0;
+      bool differ = false;  // neighbours of the same logit and bias go by their index in any arithmetic
+      for (u32 j = 0; j < (u32)kWave && j < experts; ++j) {
         u32 d = 0;
 #pragma unroll
         for (int i = 0; i < C; ++i) d = max_u(d, key[i] - last);
         const u32 n = last + group_reduce<G>(d, max_u);
-        if (n <= K::kLow || !closes) break;
-        unsure |= j && last - n <= close && !same(last, n);
-        if (j == a.k || j + 1 == a.E) break;
+        const bool takes = closes && some == j && n > K::kLow && (j <= last_slot || border - n <= close);
+        if (__ballot(takes) == 0) break;
+        if (!takes) continue;
+        differ |= j && last - n <= close && !same(last, n);
+        if (g == 0) key_row[j] = n;
+        if (j == last_slot) border = n;
         last = n;
+        some = j + 1;
       }
+      closes = closes && differ;
+      if (some == (u32)kWave && experts > (u32)kWave) unsure = closes;  // more than there are lanes
+      wave_lds_sync();
+      for (u64 left = __ballot(closes && !unsure && g == 0); left; left &= left - 1) {
+        const RouteArgs& b = arguments_again();
+        const u32 from = (u32)__builtin_ctzll(left);  // the row's first lane
+        const u32 count = (u32)__builtin_amdgcn_readlane((int)some, (int)from), lane = lane_id();
+        u32* keys = s_key[wave][from / G];
+        const u32 n = lane < count ? keys[lane] : 0;
+        const u32 rank = rank_exactly<T>(b, t0 + wave * kRows + from / G, count, K::kLow - (n & K::kLow),
+                                         __shfl(row.top, (int)from));
+        wave_lds_sync();
+        if (lane < count && rank < b.k) keys[rank] = n;
+      }
+      wave_lds_sync();
+      if (closes && !unsure && slots <= (u32)G && g < some && g < slots) mine = key_row[g];
     }
-    unsure = group_reduce<G>((u32)unsure, max_u) && row.live;
-    auto weight_of = [&](float v, float top, float inverse) {
+    auto weight_of = [](const RouteArgs& a, float v, float top, float inverse) {
       if constexpr (SIGMOID) return sigmoid_of(v).up;
       if (!(top < __builtin_huge_valf())) return top - top;  // of +inf or NaN: NaN
       const float w = exp_f(v - top);
       return a.normalize ? w : w * inverse;
     };
-    auto share_of = [&](float w, float chosen) { return chosen == 0.f ? 0.f : w / chosen * a.scale; };
+    auto share_of = [](const RouteArgs& a, float w, float chosen) { return chosen == 0.f ? 0.f : w / chosen * a.scale; };
     // lane g takes slots g, g + G, ...
     if (here && !unsure) {
+      const RouteArgs& a = arguments_again();
       const u64 at = t * a.k;
       float chosen = 0.f, w = 0.f;
       for (u32 j = g; j < a.k; j += G) {
@@ -464,7 +593,7 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
         const bool some = row.live && n > K::kLow;
         w = 0.f;
         if (some) {
-          w = weight_of(to_f32(xt[e]), row.top, inv);
+          w = weight_of(a, to_f32(xt[e]), row.top, inv);
           atomicAdd(&s_cnt[e], 1u);
         }
         chosen += w;
@@ -474,65 +603,66 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs a) 
       if (a.normalize) {
         chosen = group_reduce<G>(chosen, add_f);
         if (a.k <= (u32)G) {
-          if (g < a.k) a.weights[at + g] = share_of(w, chosen);
+          if (g < a.k) a.weights[at + g] = share_of(a, w, chosen);
         } else {
-          for (u32 j = g; j < a.k; j += G) a.weights[at + j] = share_of(a.weights[at + j], chosen);
+          for (u32 j = g; j < a.k; j += G) a.weights[at + j] = share_of(a, a.weights[at + j], chosen);
         }
       }
     }
     wave_lds_sync();
     for (u64 left = __ballot(unsure && g == 0); left; left &= left - 1) {
+      const RouteArgs& b = arguments_again();
       const u32 from = (u32)__builtin_ctzll(left);  // the row's first lane
       const u64 r = t0 + wave * kRows + from / G;
       const float top = __shfl(row.top, (int)from), inverse = __shfl(inv, (int)from);
-      const u32 e = choose_exactly(a, x + r * a.ld, reinterpret_cast<u64*>(s_key[wave][0]));
-      const bool slot = lane_id() < a.k, some = slot && e < a.E;
+      const u32 e = choose_exactly<T>(b, r, top, reinterpret_cast<u64*>(s_key[wave][0]));
+      const bool slot = lane_id() < b.k, some = slot && e < b.E;
       float w = 0.f;
       if (some) {
-        w = weight_of(to_f32(x[r * a.ld + e]), top, inverse);
+        w = weight_of(b, to_f32(reinterpret_cast<const T*>(b.x)[r * b.ld + e]), top, inverse);
         atomicAdd(&s_cnt[e], 1u);
       }
       const float chosen = group_reduce<kWave>(w, add_f);
       if (slot) {
-        a.experts[r * a.k + lane_id()] = some ? (int64_t)e : -1;
-        a.weights[r * a.k + lane_id()] = a.normalize ? share_of(w, chosen) : w * a.scale;
+        b.experts[r * b.k + lane_id()] = some ? (int64_t)e : -1;
+        b.weights[r * b.k + lane_id()] = b.normalize ? share_of(b, w, chosen) : w * b.scale;
       }
       wave_lds_sync();
     }
-    if (a.loss && ++turn == kTurnsInRegisters && t0 + step < a.T) {  // the same for the whole block
+    if (arguments_again().loss && ++turn == kTurnsInRegisters && t0 + step < arguments_again().T) {  // the same for the whole block
       join();
       __syncthreads();
       turn = 0;
-#pragma unroll
-      for (int i = 0; i < C; ++i) sum[i] = 0.f;
+      clear();
     }
   }
   if (rows) atomicAdd(&s_rows, rows);
   join();
+  const RouteArgs& z = arguments_again();
   if (gridDim.x == 1) {
     double part = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const u32 e = threadIdx.x + h * kScoredThreads;
-      if (e < a.E) {
-        a.counts[e] = (int64_t)s_cnt[e];
+      if (e < z.E) {
+        z.counts[e] = (int64_t)s_cnt[e];
         part += (double)s_cnt[e] * total[h];
       }
     }
     part = block_sum<kScoredWaves>(part, s_part);
     if (threadIdx.x == 0) {
-      *a.rows = (int64_t)s_rows;
-      if (a.loss) *a.loss = balance_of(part, s_rows, a.E, a.k);
+      *z.rows = (int64_t)s_rows;
+      if (z.loss) *z.loss = balance_of(part, s_rows, z.E, z.k);
     }
     return;
   }
-  const RouteScratch sc = route_scratch(a.scratch, gridDim.x, a.E);
+  const RouteScratch sc = route_scratch(z.scratch, gridDim.x, z.E);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const u32 e = threadIdx.x + h * kScoredThreads;
-    if (e < a.E) {
-      sc.counts[(u64)blockIdx.x * a.E + e] = s_cnt[e];
-      sc.sums[(u64)blockIdx.x * a.E + e] = total[h];
+    if (e < z.E) {
+      sc.counts[(u64)blockIdx.x * z.E + e] = s_cnt[e];
+      sc.sums[(u64)blockIdx.x * z.E + e] = total[h];
     }
   }
   if (threadIdx.x == 0) {

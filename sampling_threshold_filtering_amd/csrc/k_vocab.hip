@@ -726,9 +726,12 @@ hipError_t vocab_shape(const VocabArgs& a, hipStream_t s) {
   if (bytes <= 64 * 16 * 16) return vocab_launch<T, 64, 16, GRAD, false>(a, s);
   if (bytes <= 256 * 16 * 16) return vocab_launch<T, 256, 16, GRAD, false>(a, s);
   if (bytes <= 512 * 16 * 16) return vocab_launch<T, 512, 16, GRAD, false>(a, s);
-  if constexpr (!GRAD) return vocab_launch<T, 256, 16, GRAD, true>(a, s);
-  if (bytes <= 1024 * 16 * 16) return vocab_launch<T, 1024, 16, GRAD, false>(a, s);
-  return vocab_launch<T, 1024, 16, GRAD, true>(a, s);
+  if constexpr (GRAD) {
+    if (bytes <= 1024 * 16 * 16) return vocab_launch<T, 1024, 16, true, false>(a, s);
+    return vocab_launch<T, 1024, 16, true, true>(a, s);
+  } else {
+    return vocab_launch<T, 256, 16, false, true>(a, s);
+  }
 }
 
 constexpr int kSliceThreads = 256, kSliceVectors = 8;

@@ -59,34 +59,51 @@ struct Row {
   static __device__ __forceinline__ u32 index(int i, u32 g) {
     return QUAD ? (u32)(i / 4 * G) * 4 + (u32)(i % 4) + g * 4 : (u32)i * G + g;
   }
+  // What a lane's loads of a row bring.
+  template <class T>
+  struct Raw {
+    Four<T> q[QUAD ? C / 4 : 1];
+    T s[QUAD ? 1 : C];
+  };
   // All loads go out before the first is used: places past the row's end read its start,
   // rows past the last (x of a row that exists) are read and not taken.
   template <class T>
-  __device__ __forceinline__ void load(const T* x, u32 E, u32 g, bool in) {
+  static __device__ __forceinline__ void fetch(const T* x, u32 E, u32 g, Raw<T>& raw) {
     if constexpr (QUAD) {
-      Four<T> q[C / 4];
 #pragma unroll
       for (int i = 0; i < C; i += 4) {  // E is a multiple of 4
         const u32 at = index(i, g);
-        q[i / 4] = *reinterpret_cast<const Four<T>*>(x + (at < E ? at : 0u));
-      }
-#pragma unroll
-      for (int i = 0; i < C; i += 4) {  // by words: two entries of 16 bits at a time
-        u32 w[sizeof(T)];
-        __builtin_memcpy(w, &q[i / 4], 4 * sizeof(T));
-#pragma unroll
-        for (u32 k = 0; k < sizeof(T); ++k) w[k] = in && index(i, g) < E ? w[k] : NoneWord<T>::value;
-        __builtin_memcpy(&q[i / 4], w, 4 * sizeof(T));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[i + k] = to_f32(q[i / 4].e[k]);
+        raw.q[i / 4] = *reinterpret_cast<const Four<T>*>(x + (at < E ? at : 0u));
       }
     } else {
-      T q[C];
 #pragma unroll
-      for (int i = 0; i < C; ++i) q[i] = x[index(i, g) < E ? index(i, g) : 0u];
-#pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = in && index(i, g) < E ? to_f32(q[i]) : kNone;
+      for (int i = 0; i < C; ++i) raw.s[i] = x[index(i, g) < E ? index(i, g) : 0u];
     }
+  }
+  template <class T>
+  __device__ __forceinline__ void take(const Raw<T>& raw, u32 E, u32 g, bool in) {
+    if constexpr (QUAD) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4) {  // by words: two entries of 16 bits at a time
+        Four<T> q = raw.q[i / 4];
+        u32 w[sizeof(T)];
+        __builtin_memcpy(w, &q, 4 * sizeof(T));
+#pragma unroll
+        for (u32 k = 0; k < sizeof(T); ++k) w[k] = in && index(i, g) < E ? w[k] : NoneWord<T>::value;
+        __builtin_memcpy(&q, w, 4 * sizeof(T));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i + k] = to_f32(q.e[k]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = in && index(i, g) < E ? to_f32(raw.s[i]) : kNone;
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ void load(const T* x, u32 E, u32 g, bool in) {
+    Raw<T> raw;
+    fetch(x, E, g, raw);
+    take(raw, E, g, in);
   }
   // The largest entry and the exponentials.  A row that holds a NaN has NaN for its top,
   // and every NaN becomes the one that the order ranks first; there, and where the top is
@@ -120,9 +137,12 @@ struct Row {
       }
     }
   }
-  // Sigmoid scores for e, to (4 e + 3) / (1 + e) units of 2^-24 of themselves, e = exp(-v); nan:
-  // this lane has one.  Differences from 0 beyond 88 count as 88.
-  __device__ __forceinline__ void score(bool in, bool& nan) {
+  // Sigmoid scores for e, and falling = 1 - e where the caller has room for it, each to 8 units of
+  // 2^-24 of itself; top is not set.  nan: this lane has one.  e is 0 in a row that does not take
+  // part, and for logits up to -87.4 (the reciprocal's result is flushed; beyond -88 differences do
+  // not count, so that nothing overflows on the way).
+  template <int N>
+  __device__ __forceinline__ void score(bool in, bool& nan, float (&falling)[N]) {
     static_assert(C % 2 == 0, "pairs behind the first, and one");
     float m = v[0];
 #pragma unroll
@@ -135,8 +155,9 @@ struct Row {
     for (int i = 0; i < C; ++i) {
       const float x = __builtin_amdgcn_fmed3f(v[i], -88.f, 150.f), y = x * -1.44269502f;
       const float r = __builtin_fmaf(y, -0.693147182f, -x);  // what the rounding of y left
-      const float t = __builtin_amdgcn_exp2f(y);
-      e[i] = __builtin_amdgcn_rcpf(__builtin_fmaf(t, r, t) + 1.f);
+      const float t = __builtin_amdgcn_exp2f(y), u = __builtin_fmaf(t, r, t);
+      e[i] = __builtin_amdgcn_rcpf(u + 1.f);
+      if constexpr (N == C) falling[i] = u * e[i];
     }
     if (!in) {  // rows that are not live hold -inf
 #pragma unroll
@@ -145,22 +166,10 @@ struct Row {
     if (__builtin_expect(__ballot(nan) != 0, 0)) {
       if (group_reduce<G>((u32)nan, max_u)) live = in;
 #pragma unroll
-      for (int i = 0; i < C; ++i) e[i] = v[i] != v[i] ? v[i] : e[i];
-    }
-  }
-  // The same with sigmoid scores for e: 0 in a row that is not live; top is not set.  falling,
-  // where the caller has room for it: 1 - e.
-  template <int N>
-  __device__ __forceinline__ void score(bool in, float (&falling)[N]) {
-    bool some = false;
-#pragma unroll
-    for (int i = 0; i < C; ++i) some |= !(v[i] == kNone);
-    live = group_reduce<G>((u32)some, max_u) && in;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const Sigmoid s = sigmoid_of(v[i]);
-      e[i] = live ? s.up : 0.f;
-      if constexpr (N == C) falling[i] = s.down;
+      for (int i = 0; i < C; ++i) {
+        e[i] = v[i] != v[i] ? v[i] : e[i];
+        if constexpr (N == C) falling[i] = v[i] != v[i] ? v[i] : falling[i];
+      }
     }
   }
   // 1 / the row's sum; 0 for a row that is not live, or all of whose scores are 0
