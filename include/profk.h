@@ -482,11 +482,11 @@ int64_t profk_token_loss_scratch(int64_t T, int64_t V); /* bytes, or PROFK_EINVA
  * A row of d_logprobs 0, or without a finite lp of its token (-inf), gets 0.
  */
 int profk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
-                         const uint8_t* mask, float temperature, float* out_logprobs, void* scratch,
+                         const uint8_t* mask, double temperature, float* out_logprobs, void* scratch,
                          int64_t scratch_bytes, void* stream);
 
 int profk_token_logprobs_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
-                              const int64_t* tokens, const uint8_t* mask, float temperature, const float* d_logprobs,
+                              const int64_t* tokens, const uint8_t* mask, double temperature, const float* d_logprobs,
                               const float* d_scale, float scale, void* out_d_logits, void* scratch,
                               int64_t scratch_bytes, void* stream);
 
@@ -506,12 +506,11 @@ int profk_token_logprobs_grad(const void* logits, int32_t dtype, int64_t T, int6
 typedef struct profk_policy {
   const float *old_logprobs, *advantages;  /* device, T each */
   const float *ref_logprobs, *weights;     /* device, T each, or NULL */
-  float clip_low, clip_high, kl_weight;    /* each at least 0 */
-  int32_t reserved;
+  double clip_low, clip_high, kl_weight;   /* each at least 0 */
 } profk_policy;
 
 int profk_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
-                      const uint8_t* mask, float temperature, const profk_policy* how, float* out_loss, float* out_kl,
+                      const uint8_t* mask, double temperature, const profk_policy* how, float* out_loss, float* out_kl,
                       int64_t* out_clipped, int64_t* out_rows, float* out_logprobs, const float* d_loss,
                       float d_loss_scale, void* out_d_logits, void* scratch, int64_t scratch_bytes, void* stream);
 
@@ -536,12 +535,12 @@ typedef struct profk_preference {
   const int64_t* offsets;     /* device, 2 * pairs + 1 */
   const float* ref_logprobs;  /* device, T, or NULL */
   int64_t pairs;              /* at least 1, below 2^30 */
-  float beta, smoothing, margin;
-  int32_t average;
+  double beta, smoothing, margin;
+  int32_t average, reserved;
 } profk_preference;
 
 int profk_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
-                          const uint8_t* mask, float temperature, const profk_preference* how, float* out_loss,
+                          const uint8_t* mask, double temperature, const profk_preference* how, float* out_loss,
                           float* out_margins, float* out_sequence_logprobs, int64_t* out_rows, float* out_logprobs,
                           float* out_coefficients, void* scratch, int64_t scratch_bytes, void* stream);
 

@@ -149,7 +149,7 @@ def load_library():
     f32 = ctypes.c_float
     lib.profk_route_scored.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
     lib.profk_route_scored_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, i32, i32, f32, vp, vp, vp, vp, vp, f32, vp, vp]
-    rows = [vp, i32, i64, i64, i64, vp, vp, f32]  # logits and their layout, tokens, mask, temperature
+    rows = [vp, i32, i64, i64, i64, vp, vp, f64]  # logits and their layout, tokens, mask, temperature
     lib.profk_token_loss_scratch.argtypes = [i64, i64]
     lib.profk_token_loss_scratch.restype = i64
     lib.profk_token_logprobs.argtypes = rows + [vp, vp, i64, vp]

@@ -1110,9 +1110,9 @@ int check_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t
 
 // What the losses over given tokens have in common.
 int vocab_args(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
-               const uint8_t* mask, float temperature, void* scratch, int64_t scratch_bytes, VocabArgs* a) {
+               const uint8_t* mask, double temperature, void* scratch, int64_t scratch_bytes, VocabArgs* a) {
   if (!known_dtype(dtype) || T < 0 || V < 1 || ld < V) return PROFK_EINVAL;
-  if (!(temperature >= 0x1p-20f && temperature <= 0x1p20f)) return PROFK_EINVAL;
+  if (!(temperature >= 0x1p-20 && temperature <= 0x1p20)) return PROFK_EINVAL;
   if (V > kTokMaxV || T > kOpMaxRows) return PROFK_EUNSUPPORTED;
   if (T && (!logits || !tokens)) return PROFK_EINVAL;
   const int rc = check_scratch(scratch, scratch_bytes, (int64_t)vocab_scratch_bytes((u64)T));
@@ -1123,9 +1123,10 @@ int vocab_args(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t 
   a->ld = (u64)ld;
   a->tokens = tokens;
   a->mask = mask;
-  a->inverse_temperature = 1.0 / (double)temperature;
-  const double exponent = 1.4426950408889634 / (double)temperature;
+  a->inverse_temperature = 1.0 / temperature;
+  const double exponent = 1.4426950408889634 / temperature;
   a->exponent_hi = (float)exponent;
+  if ((double)a->exponent_hi >= exponent) a->exponent_hi = std::nextafterf(a->exponent_hi, 0.f);  // the rest above 0
   a->exponent_lo = (float)(exponent - (double)a->exponent_hi);
   a->scratch = (char*)scratch;
   return PROFK_OK;
@@ -1595,7 +1596,7 @@ int64_t profk_token_loss_scratch(int64_t T, int64_t V) {
 }
 
 int profk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
-                         const uint8_t* mask, float temperature, float* out_logprobs, void* scratch,
+                         const uint8_t* mask, double temperature, float* out_logprobs, void* scratch,
                          int64_t scratch_bytes, void* stream) {
   VocabArgs a{};
   const int rc = vocab_args(logits, dtype, T, V, ld, tokens, mask, temperature, scratch, scratch_bytes, &a);
@@ -1608,7 +1609,7 @@ int profk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V
 }
 
 int profk_token_logprobs_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
-                              const int64_t* tokens, const uint8_t* mask, float temperature, const float* d_logprobs,
+                              const int64_t* tokens, const uint8_t* mask, double temperature, const float* d_logprobs,
                               const float* d_scale, float scale, void* out_d_logits, void* scratch,
                               int64_t scratch_bytes, void* stream) {
   VocabArgs a{};
@@ -1625,7 +1626,7 @@ int profk_token_logprobs_grad(const void* logits, int32_t dtype, int64_t T, int6
 }
 
 int profk_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
-                      const uint8_t* mask, float temperature, const profk_policy* how, float* out_loss, float* out_kl,
+                      const uint8_t* mask, double temperature, const profk_policy* how, float* out_loss, float* out_kl,
                       int64_t* out_clipped, int64_t* out_rows, float* out_logprobs, const float* d_loss,
                       float d_loss_scale, void* out_d_logits, void* scratch, int64_t scratch_bytes, void* stream) {
   VocabArgs a{};
@@ -1633,15 +1634,15 @@ int profk_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, i
   if (rc) return rc;
   if (!how || !out_loss || !out_kl || !out_clipped || !out_rows) return PROFK_EINVAL;
   if (T && (!how->old_logprobs || !how->advantages || !out_logprobs)) return PROFK_EINVAL;
-  if (!(how->clip_low >= 0.f) || !(how->clip_high >= 0.f) || !(how->kl_weight >= 0.f) || std::isinf(how->kl_weight))
+  if (!(how->clip_low >= 0) || !(how->clip_high >= 0) || !(how->kl_weight >= 0) || std::isinf(how->kl_weight))
     return PROFK_EINVAL;
   a.policy = true;
   a.old = how->old_logprobs;
   a.advantages = how->advantages;
   a.ref = how->ref_logprobs;
   a.weights = how->weights;
-  a.clip_low = 1.f - how->clip_low;
-  a.clip_high = 1.f + how->clip_high;
+  a.clip_low = 1.0 - how->clip_low;
+  a.clip_high = 1.0 + how->clip_high;
   a.kl_weight = how->kl_weight;
   a.loss = out_loss;
   a.kl = out_kl;
@@ -1656,7 +1657,7 @@ int profk_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, i
 }
 
 int profk_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int64_t* tokens,
-                          const uint8_t* mask, float temperature, const profk_preference* how, float* out_loss,
+                          const uint8_t* mask, double temperature, const profk_preference* how, float* out_loss,
                           float* out_margins, float* out_sequence_logprobs, int64_t* out_rows, float* out_logprobs,
                           float* out_coefficients, void* scratch, int64_t scratch_bytes, void* stream) {
   PairArgs p{};
@@ -1666,7 +1667,7 @@ int profk_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t 
     return PROFK_EINVAL;
   if (how->pairs >= (int64_t(1) << 30)) return PROFK_EUNSUPPORTED;
   if (T && (!out_logprobs || !out_coefficients)) return PROFK_EINVAL;
-  if (!std::isfinite(how->beta) || !std::isfinite(how->margin) || !(how->smoothing >= 0.f && how->smoothing <= 1.f))
+  if (!std::isfinite(how->beta) || !std::isfinite(how->margin) || !(how->smoothing >= 0 && how->smoothing <= 1))
     return PROFK_EINVAL;
   p.v.pairs = true;
   p.v.logprobs = out_logprobs;
@@ -1676,9 +1677,9 @@ int profk_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t 
   p.v.rows = out_rows;
   p.offsets = how->offsets;
   p.pairs = (u64)how->pairs;
-  p.beta = (double)how->beta;
-  p.smoothing = (double)how->smoothing;
-  p.margin = (double)how->margin;
+  p.beta = how->beta;
+  p.smoothing = how->smoothing;
+  p.margin = how->margin;
   p.average = how->average != 0;
   p.margins = out_margins;
   p.sequence_logprobs = out_sequence_logprobs;

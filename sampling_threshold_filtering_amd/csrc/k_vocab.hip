@@ -36,7 +36,8 @@ struct Terms {
 };
 // Of a slice of a row that is split.
 struct Part {
-  float top, rest;
+  double rest;
+  float top;
 };
 
 // All of it is written before it is read within a call.
@@ -119,47 +120,71 @@ __device__ __forceinline__ T none_entry() {
   return v;
 }
 
-// exp(d / tau) for d <= 0.  32-bit rows make up for the rounding of d log2(e) / tau, which
-// grows with |d|; of 16-bit ones its 1e-6 is lost in the gradient's rounding, and terms so far
-// below the top do not count in the sum.
+// exp((x - top) / tau).  log2(e) / tau is taken to 48 bits, hi + lo: the rounding of its upper half
+// alone would make every sum too large or too small by some 1e-7, and a sequence's with its length.
 struct Exponent {
-  float hi, lo;  // log2(e) / tau
-  template <class T>
-  __device__ __forceinline__ float of(float d) const {
-    const float t = d * hi;
-    const float e = __builtin_amdgcn_exp2f(t);
-    if constexpr (sizeof(T) == 2) return e;
-    // past -150 the result is 0, also where t is infinite (d of a masked entry)
-    const float r = t > -150.f ? __builtin_fmaf(d, lo, __builtin_fmaf(d, hi, -t)) : 0.f;
-    return __builtin_fmaf(e * 0.693147182f, r, e);
+  float hi, lo;
+  __device__ __forceinline__ float of(float d) const {  // of a difference, for all of them: -inf too
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(d, lo, d * hi));
   }
 };
 
+// The same from x itself: x hi + (-top hi), each in one rounding, is as exact as x - top and a
+// product, in one instruction less; what the second product's rounding left is a factor of all
+// terms, `left`.  Where a top is so large that the products could overflow (2^100: of a row whose
+// every entry is masked by the type's lowest value, say), it is at least 2^76 from any other value:
+// then 2^-24 in place of the factors, whose products are exact, gives the same terms, 1 or 0.
+struct Shifted {
+  float hi, lo, from, left;
+  __device__ __forceinline__ Shifted(const Exponent& ex, float top, bool both) {
+    const bool fits = __builtin_fabsf(top) <= 0x1p100f;
+    hi = fits ? ex.hi : both ? 0x1p-25f : 0x1p-24f;
+    lo = fits ? ex.lo : 0x1p-25f;
+    from = fits ? -top * ex.hi : -top * 0x1p-24f;
+    const float rest = __builtin_fmaf(-top, hi, -from);
+    left = fits ? __builtin_amdgcn_exp2f(both ? __builtin_fmaf(-top, lo, rest) : rest) : 1.f;
+  }
+  // BOTH: with lo.  A 16-bit gradient's rounding hides what it adds.
+  template <bool BOTH>
+  __device__ __forceinline__ float of(float x) const {
+    const float t = __builtin_fmaf(x, hi, from);
+    return __builtin_amdgcn_exp2f(BOTH ? __builtin_fmaf(x, lo, t) : t);
+  }
+};
+
+// Sum over groups of G lanes in 64 bits.
+template <int G>
+__device__ __forceinline__ double lanes_sum(double v) {
+#pragma unroll
+  for (int d = 1; d < G; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
 // A row's sums: what the gradient and the loss need of it.
 struct RowSums {
-  float top, rest, token;  // M, R, x_a
+  float top, token;  // M, x_a
+  double rest;       // R
 };
 
 struct RowEnd {
-  double lp;
-  float total;   // s
-  bool absent;   // the token's weight is 0
+  double lp, total;  // total: s
+  bool absent;       // the token's weight is 0
 };
 
 __device__ __forceinline__ RowEnd end_of(const VocabArgs& a, const RowSums& r) {
   RowEnd e;
   const double d = ((double)r.token - (double)r.top) * a.inverse_temperature;
-  e.total = r.rest + expf((float)d);
+  e.total = r.rest + (double)expf((float)d);
   e.absent = false;
-  if (!(e.total < __builtin_huge_valf())) {  // the row holds a NaN or +inf
+  if (!(e.total < __builtin_huge_val())) {  // the row holds a NaN or +inf
     e.lp = __builtin_nan("");
   } else if (r.token == kNone) {
     e.lp = -__builtin_huge_val();
     e.absent = true;
   } else if (r.token == r.top) {
-    e.lp = -(double)log1pf(r.rest);
+    e.lp = -log1p(r.rest);
   } else {
-    e.lp = d - (double)logf(e.total);
+    e.lp = d - log(e.total);
     e.absent = (float)e.lp == kNone;
   }
   return e;
@@ -186,27 +211,42 @@ struct RowTerms {
   float c = 0;  // dloss / dlp, d_loss among it
 };
 
-__device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, u64 t, const RowEnd& e, double d_loss, double share) {
+// What a row's terms need from memory, on its way before the row itself.
+struct RowInputs {
+  float given = 0, old = 0, advantage = 0, ref = 0, weight = 0;
+  __device__ __forceinline__ RowInputs(const VocabArgs& a, u64 t) {
+    if (a.given) given = a.given[t];
+    if (!a.policy) return;
+    old = a.old[t];
+    advantage = a.advantages[t];
+    if (a.ref) ref = a.ref[t];
+    if (a.weights) weight = a.weights[t];
+  }
+};
+
+// share: a row's weight where none are given
+__device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, const RowInputs& in, const RowEnd& e, double d_loss,
+                                             double share) {
   RowTerms o;
   if (a.given) {
-    o.c = (float)((double)a.given[t] * d_loss);
+    o.c = (float)((double)in.given * d_loss);
     return o;
   }
   if (!a.policy || e.absent) return o;
-  const float adv = a.advantages[t];
-  const float ratio = expf((float)(e.lp - (double)a.old[t]));
-  const float cut = __builtin_fminf(__builtin_fmaxf(ratio, a.clip_low), a.clip_high);
+  const double adv = (double)in.advantage;
+  const double ratio = (double)expf((float)(e.lp - (double)in.old));
+  const double cut = __builtin_fmin(__builtin_fmax(ratio, a.clip_low), a.clip_high);
   const bool clipped = cut * adv < ratio * adv;
-  double loss = -(double)adv * (double)(clipped ? cut : ratio);
-  double slope = clipped ? 0.0 : -(double)adv * (double)ratio;
-  const double w = a.weights ? (double)a.weights[t] : share;
+  double loss = -adv * (clipped ? cut : ratio);
+  double slope = clipped ? 0.0 : -adv * ratio;
+  const double w = a.weights ? (double)in.weight : share;
   if (a.ref) {
-    const float q = (float)((double)a.ref[t] - e.lp);
+    const float q = (float)((double)in.ref - e.lp);
     const double k = (double)kl_of(q);
     o.kl = w * k;
-    if (a.kl_weight > 0.f) {  // with weight 0 the term may be infinite (of a token masked by the lowest value)
-      loss += (double)a.kl_weight * k;
-      slope -= (double)a.kl_weight * (double)expm1f(q);
+    if (a.kl_weight > 0) {  // with weight 0 the term may be infinite (of a token masked by the lowest value)
+      loss += a.kl_weight * k;
+      slope -= a.kl_weight * (double)expm1f(q);
     }
   }
   o.loss = w * loss;
@@ -315,11 +355,17 @@ enum { kWhole, kPart, kJoin };
 
 // A team of TEAM threads with N vectors per thread in registers; of more (MULTI) that many at a
 // time, the last of them staying for the gradient.
+// Wavefronts a SIMD: with 4 a gradient's 512 threads come twice to a CU, one's loads beside the
+// other's sums; a forward pass holds fewer registers, and at 5 wavefronts in place of 6, two
+// workgroups in place of three, 12000 x 65536 took 173 us in place of 146.
+constexpr int waves_of(int team, int n, bool grad, bool multi) { return team < 256 || n < 16 ? 1 : grad ? 4 : multi ? 5 : 6; }
+
 template <class T, int TEAM, int N, bool GRAD, bool MULTI, int MODE>
-__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void vocab_kernel(VocabArgs a) {
+__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MULTI)) void vocab_kernel(VocabArgs a) {
   constexpr int kBlock = TEAM < 256 ? 256 : TEAM, kTeams = kBlock / TEAM, kTeamWaves = TEAM / kWave;
   constexpr u32 W = 16 / sizeof(T);
-  __shared__ float s_top[kBlock / kWave], s_rest[kBlock / kWave], s_token[kTeams];
+  __shared__ float s_top[kBlock / kWave], s_token[kTeams];
+  __shared__ double s_rest[kBlock / kWave];
   __shared__ u32 s_n[kBlock / kWave];
   const VocabScratch sc = vocab_scratch(a.scratch, a.T);
   const u32 wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -375,11 +421,12 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
     from_f32(0.f, z);
     if (tid < edges) dx[mine] = z;
   };
-  auto n_of = [&]() {  // the live rows of all
-    return wave_reduce_u32(lane < a.count_blocks ? sc.live[lane] : 0, [](u32 p, u32 q) { return p + q; });
-  };
+  const u32 live_part = MODE != kPart && a.policy && lane < a.count_blocks ? sc.live[lane] : 0;
+  auto n_of = [&]() { return wave_reduce_u32(live_part, [](u32 p, u32 q) { return p + q; }); };  // the live rows of all
+  const RowInputs in(a, t);
+  const double d_loss = GRAD ? (double)(a.d_loss ? *a.d_loss : 1.f) * (double)a.d_loss_scale : 0.0;
   const bool live = row_live(a, t);
-  if (!live || (GRAD && a.given && a.given[t] == 0.f)) {
+  if (!live || (GRAD && a.given && in.given == 0.f)) {
     if (own_grad) zero_row();
     if (tid == 0 && own_terms) {
       if (a.logprobs) a.logprobs[t] = 0.f;
@@ -415,9 +462,9 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
     first = (segments - 1) * (TEAM * N);
     if (own_grad) load();
     if (tid < edges && mine != token) edge = to_f32(x[mine]);
-    const Part p = lane < a.slices ? sc.parts[t * a.slices + lane] : Part{kLowest, 0.f};
+    const Part p = lane < a.slices ? sc.parts[t * a.slices + lane] : Part{0, kLowest};
     row.top = group_reduce<kWave>(p.top, max_f);
-    row.rest = group_reduce<kWave>(p.rest * ex.of<T>(p.top - row.top), add_f);
+    row.rest = lanes_sum<kWave>(p.rest * (double)ex.of(p.top - row.top));
     row.token = to_f32(x[token]);
     const int at = slot_of();
 #pragma unroll
@@ -432,12 +479,14 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
         edge = kNone;
       }
     }
-    float top = edge > kLowest ? edge : kLowest, rest[4] = {0.f, 0.f, 0.f, 0.f};
+    float top = kLowest;  // of the wavefront
+    double rest = 0;
     load();
     for (u32 seg = 0; seg < segments; ++seg) {
       first = seg * TEAM * N;
       const int at = slot_of(), n = count(first), next = seg + 1 < segments ? count(first + TEAM * N) : 0;
       const float before = top;
+      float m = seg == 0 && edge > kLowest ? edge : kLowest;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (i >= n) continue;
@@ -446,26 +495,34 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
           set_entry<T>(v[i], place, none_entry<T>());
         }
 #pragma unroll
-        for (u32 k = 0; k < W; k += 2) top = max3(top, entry<T>(v[i], k), entry<T>(v[i], k + 1));
+        for (u32 k = 0; k < W; k += 2) m = max3(m, entry<T>(v[i], k), entry<T>(v[i], k + 1));
       }
-      if (MULTI && seg) {
-        const float f = ex.of<T>(before - top);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) rest[k] *= f;
-      }
+      top = max_f(top, __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(group_reduce<kWave>(m, max_f)))));
+      if (MULTI && seg) rest *= (double)ex.of(before - top);
+      const Shifted sh(ex, top, true);
+      double sum = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (i >= n) continue;
+        // a vector's terms by pairs, the vectors in 64 bits: one after the other in 32, those beside
+        // the largest would lose 2e-7 of it
+        float e[W];
 #pragma unroll
-        for (u32 k = 0; k < W; ++k) rest[k % 4] += ex.of<T>(entry<T>(v[i], k) - top);
+        for (u32 k = 0; k < W; ++k) e[k] = sh.of<true>(entry<T>(v[i], k));
+#pragma unroll
+        for (u32 d = 1; d < W; d <<= 1)
+#pragma unroll
+          for (u32 k = 0; k < W; k += 2 * d) e[k] += e[k + d];
+        sum += (double)e[0];
         // its place for the next segment's, on its way while the others are dealt with
         if (MULTI && i < next) load_one(first + TEAM * N, i, next);
       }
+      rest += sum * (double)sh.left;
     }
-    rest[0] += ex.of<T>(edge - top);
+    rest += (double)ex.of(edge - top);
     // over the lanes, then over the team's wavefronts
-    row.top = group_reduce<kWave>(top, max_f);
-    row.rest = group_reduce<kWave>((rest[0] + rest[1] + (rest[2] + rest[3])) * ex.of<T>(top - row.top), add_f);
+    row.top = top;
+    row.rest = lanes_sum<kWave>(rest);
     if constexpr (kTeamWaves == 1) {
       const u32 l = in_vecs ? owner : (token < head ? token : token - all * W);
       row.token = __uint_as_float((u32)__builtin_amdgcn_readlane((int)__float_as_uint(x_token), (int)l));
@@ -476,24 +533,23 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
       }
       if (in_vecs ? tid == owner : (tid < edges && mine == token)) s_token[team] = x_token;
       lds_barrier();
-      const float m = s_top[tid % kTeamWaves], s = s_rest[tid % kTeamWaves];
+      const float m = s_top[tid % kTeamWaves];
       row.top = group_reduce<kTeamWaves>(m, max_f);
-      row.rest = group_reduce<kTeamWaves>(s * ex.of<T>(m - row.top), add_f);
+      row.rest = lanes_sum<kTeamWaves>(s_rest[tid % kTeamWaves] * (double)ex.of(m - row.top));
       row.token = s_token[team];  // (nobody's, in a slice that does not hold it)
     }
     if constexpr (MODE == kPart) {
-      if (tid == 0) sc.parts[t * a.slices + slice] = Part{row.top, row.rest};
+      if (tid == 0) sc.parts[t * a.slices + slice] = Part{row.rest, row.top};
       return;
     }
   }
   if (row.token > row.top) {
-    row.rest *= ex.of<T>(row.top - row.token);
+    row.rest *= (double)ex.of(row.top - row.token);
     row.top = row.token;
   }
   const u32 n = a.policy ? n_of() : 0;
-  const double d_loss = GRAD ? (double)(a.d_loss ? *a.d_loss : 1.f) * (double)a.d_loss_scale : 0.0;
   const RowEnd end = end_of(a, row);
-  const RowTerms o = terms_of(a, t, end, d_loss, n ? 1.0 / (double)n : 0.0);
+  const RowTerms o = terms_of(a, in, end, d_loss, n ? 1.0 / (double)n : 0.0);
   if (tid == 0 && own_terms) {
     if (a.logprobs) a.logprobs[t] = (float)end.lp;
     if (a.pairs) sc.lp[t] = end.lp;
@@ -503,14 +559,17 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
       zero_row();
     } else {
       const float c = (float)((double)o.c * a.inverse_temperature);
-      const float scale = -c / end.total;
+      const float scale = (float)(-(double)c / end.total);
       T at_token;
-      from_f32(c * (row.rest / end.total), at_token);
+      from_f32((float)((double)c * (row.rest / end.total)), at_token);
       if (tid < edges) {
         T g;
-        from_f32(scale * ex.of<T>(edge - row.top), g);
+        from_f32(scale * ex.of(edge - row.top), g);
         dx[mine] = mine == token ? at_token : g;
       }
+      constexpr bool kBoth = sizeof(T) == 4;
+      const Shifted sh(ex, row.top, kBoth);
+      const float scaled = scale * sh.left;
       for (u32 seg = segments; seg-- > 0;) {
         if (MULTI && (seg + 1 < segments)) {
           first = seg * TEAM * N;
@@ -526,7 +585,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, TEAM < 256 ? 0 : 4) void v
             T g[4 / sizeof(T)];
 #pragma unroll
             for (u32 h = 0; h < 4 / sizeof(T); ++h)
-              from_f32(scale * ex.of<T>(entry<T>(v[i], k * (4 / sizeof(T)) + h) - row.top), g[h]);
+              from_f32(scaled * sh.of<kBoth>(entry<T>(v[i], k * (4 / sizeof(T)) + h)), g[h]);
             u32 bits;
             __builtin_memcpy(&bits, g, 4);
             w[k] = bits;
@@ -566,14 +625,14 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   auto lp_of = [&](u64 t, bool here) {
     if (!a.v.slices) return sc.lp[t];
     if (!here) return 0.0;
-    RowSums row = {kLowest, 0.f, logit_of(a, t)};
+    RowSums row = {kLowest, logit_of(a, t), 0};
     for (u32 i = 0; i < a.v.slices; ++i) row.top = max_f(row.top, sc.parts[t * a.v.slices + i].top);
     for (u32 i = 0; i < a.v.slices; ++i) {
       const Part p = sc.parts[t * a.v.slices + i];
-      row.rest += p.rest * ex.of<float>(p.top - row.top);
+      row.rest += p.rest * (double)ex.of(p.top - row.top);
     }
     if (row.token > row.top) {
-      row.rest *= ex.of<float>(row.top - row.token);
+      row.rest *= (double)ex.of(row.top - row.token);
       row.top = row.token;
     }
     return end_of(a.v, row).lp;

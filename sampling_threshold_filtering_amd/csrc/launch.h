@@ -351,13 +351,13 @@ struct VocabArgs {
   const int64_t* tokens;       // T
   const unsigned char* mask;   // nonzero: the row takes part; or nullptr
   double inverse_temperature;
-  float exponent_hi, exponent_lo;  // log2(e) / temperature
+  float exponent_hi, exponent_lo;  // log2(e) / temperature; both above 0, so that -inf times them is -inf
   // each row's coefficient of the gradient, or nullptr
   const float* given;
   bool policy;                 // the policy loss
   const float *old, *advantages, *ref, *weights;  // T each; the last two may be nullptr
-  float clip_low, clip_high;   // the ratio's borders
-  float kl_weight;
+  double clip_low, clip_high;  // the ratio's borders
+  double kl_weight;
   const float* d_loss;         // 1, or nullptr
   float d_loss_scale;
   float* logprobs;             // T, or nullptr

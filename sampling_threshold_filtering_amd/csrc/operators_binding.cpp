@@ -366,17 +366,17 @@ PyObject* balance_grad(PyObject* const* a) {
   return rc ? status(rc) : THPVariable_Wrap(dx);
 }
 
-float temperature_of(PyObject* o) {
+double temperature_of(PyObject* o) {
   const double t = number(o, "temperature");
   if (!(t >= 0x1p-20 && t <= 0x1p20)) refuse("temperature must be within 2^-20 .. 2^20");
-  return (float)t;
+  return t;
 }
 
 // What the losses over given tokens have in common: one token per row, the mask, scratch.
 struct TokenRows {
   Logits x;
   at::Tensor tokens, mask;
-  float temperature;
+  double temperature;
   int64_t need;
   TokenRows(PyObject* logits, PyObject* tok, PyObject* m, PyObject* temp) : x(logits) {
     no_tangent(x.x, "logits");
@@ -429,7 +429,7 @@ PyObject* policy(PyObject* const* a) {
   const at::Tensor old = r.row_values(a[2], "old_logprobs", true), adv = r.row_values(a[3], "advantages", true),
                    ref = r.row_values(a[4], "ref_logprobs", false), weights = r.row_values(a[5], "weights", false);
   const double low = number(a[7], "clip_low"), high = number(a[8], "clip_high"), kl = number(a[9], "kl_weight");
-  if (!(low >= 0 && high >= 0 && kl >= 0 && kl < 3e38)) refuse("need clip_low >= 0, clip_high >= 0 and a finite kl_weight >= 0");
+  if (!(low >= 0 && high >= 0 && kl >= 0 && std::isfinite(kl))) refuse("need clip_low >= 0, clip_high >= 0 and a finite kl_weight >= 0");
   if (kl > 0 && !ref.defined()) refuse("a kl_weight needs ref_logprobs");
   const bool grad = a[11] != Py_None;
   at::Tensor d_loss, dx;
@@ -443,9 +443,8 @@ PyObject* policy(PyObject* const* a) {
   const Scratch scratch(r.x, r.need);
   const at::Tensor loss = r.x.empty({}, at::kFloat), logprobs = r.x.empty({r.x.rows}, at::kFloat),
                    gap = r.x.empty({}, at::kFloat), clipped = r.x.empty({}, at::kLong), rows = r.x.empty({}, at::kLong);
-  const profk_policy how = {address<const float>(old),     address<const float>(adv), address<const float>(ref),
-                            address<const float>(weights), (float)low,                (float)high,
-                            (float)kl,                     0};
+  const profk_policy how = {address<const float>(old), address<const float>(adv), address<const float>(ref),
+                            address<const float>(weights), low, high, kl};
   const int rc = profk_policy_loss(
       r.x.x.data_ptr(), r.x.dtype, r.x.rows, r.x.cols, r.x.ld, address<const int64_t>(r.tokens),
       address<const uint8_t>(r.mask), r.temperature, &how, address<float>(loss), address<float>(gap),
@@ -466,10 +465,10 @@ PyObject* preference(PyObject* const* a) {
   const int64_t pairs = offsets.size(0) / 2;
   const at::Tensor ref = r.row_values(a[3], "ref_logprobs", false);
   const double beta = number(a[5], "beta"), smoothing = number(a[6], "smoothing"), margin = number(a[7], "margin");
-  if (!(std::abs(beta) < 3e38 && std::abs(margin) < 3e38 && smoothing >= 0 && smoothing <= 1))
+  if (!(std::isfinite(beta) && std::isfinite(margin) && smoothing >= 0 && smoothing <= 1))
     refuse("need a finite beta and margin and 0 <= smoothing <= 1");
-  const profk_preference how = {address<const int64_t>(offsets), address<const float>(ref), pairs,         (float)beta,
-                                (float)smoothing,                (float)margin,             truth(a[8], "average")};
+  const profk_preference how = {address<const int64_t>(offsets), address<const float>(ref), pairs, beta, smoothing, margin,
+                                truth(a[8], "average"), 0};
   const Scratch scratch(r.x, r.need);
   const at::Tensor loss = r.x.empty({}, at::kFloat), margins = r.x.empty({pairs}, at::kFloat),
                    sums = r.x.empty({2 * pairs}, at::kFloat), rows = r.x.empty({}, at::kLong),

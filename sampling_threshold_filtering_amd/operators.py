@@ -50,8 +50,8 @@ class PolicySettings(ctypes.Structure):
     """profk_policy"""
     _fields_ = [
         ("old_logprobs", ctypes.c_void_p), ("advantages", ctypes.c_void_p), ("ref_logprobs", ctypes.c_void_p),
-        ("weights", ctypes.c_void_p), ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
-        ("kl_weight", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("weights", ctypes.c_void_p), ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+        ("kl_weight", ctypes.c_double),
     ]
 
 
@@ -59,7 +59,8 @@ class PreferenceSettings(ctypes.Structure):
     """profk_preference"""
     _fields_ = [
         ("offsets", ctypes.c_void_p), ("ref_logprobs", ctypes.c_void_p), ("pairs", ctypes.c_int64),
-        ("beta", ctypes.c_float), ("smoothing", ctypes.c_float), ("margin", ctypes.c_float), ("average", ctypes.c_int32),
+        ("beta", ctypes.c_double), ("smoothing", ctypes.c_double), ("margin", ctypes.c_double), ("average", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 

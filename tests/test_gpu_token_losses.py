@@ -72,7 +72,7 @@ def check_grad(g, x, r, c, c_err=None):
 
 def check_logprobs(x, tokens, tau=1.0, mask=None, d=None):
     m = mask.cpu().numpy() if mask is not None else None
-    r = ref.rows(host(x), tokens.cpu().numpy(), float(np.float32(tau)), m)
+    r = ref.rows(host(x), tokens.cpu().numpy(), tau, m)
     got = stf.token_logprobs(x, tokens, mask=mask, temperature=tau)
     close(host(got), r["lp"], r["err"] + H * np.abs(r["lp"]), "logprobs")
     if d is not None:
@@ -111,7 +111,7 @@ def test_policy(T, V, dtype):
         say("policy", T, V, dtype, kl, weighted, masked)
         mask = torch.from_numpy(rng.random(T) < 0.7).cuda() if masked else None
         m = mask.cpu().numpy() if masked else None
-        r = ref.rows(host(x), tokens.cpu().numpy(), float(np.float32(tau)), m)
+        r = ref.rows(host(x), tokens.cpu().numpy(), tau, m)
         moved = 0.25 * rng.standard_normal(T)
         for border in (np.log(0.8), np.log(1.3)):
             moved = np.where(np.abs(moved - border) < 1e-3, moved + 3e-3, moved)
@@ -122,7 +122,7 @@ def test_policy(T, V, dtype):
         kw = dict(ref_logprobs=rf, weights=w, mask=mask, clip_low=0.2, clip_high=0.3, kl_weight=kl, temperature=tau)
         got, g = stf.policy_loss_and_grad(x, tokens, old, adv, d_loss=d_loss, **kw)
         want = ref.policy(r, host(old), host(adv), host(rf) if kl else None, host(w) if weighted else None,
-                          float(np.float32(0.2)), float(np.float32(0.3)), float(np.float32(kl)), d_loss)
+                          0.2, 0.3, kl, d_loss)
         assert want["near"] > 2
         assert int(got.rows) == want["rows"] and int(got.clipped) == want["clipped"]
         close(host(got.logprobs), r["lp"], r["err"] + H * np.abs(r["lp"]), "logprobs")
@@ -152,8 +152,8 @@ def test_preference(pairs, T, V, dtype):
         rf = values(r["lp"] + 0.3 * rng.standard_normal(T)) if not average else None
         got = stf.preference_loss(x, tokens, offsets, rf, mask, beta=0.3, smoothing=smoothing, margin=margin,
                                   average=average)
-        want = ref.preference(r, cut, pairs, host(rf) if rf is not None else None, float(np.float32(0.3)),
-                              float(np.float32(smoothing)), margin, average)
+        want = ref.preference(r, cut, pairs, host(rf) if rf is not None else None, 0.3, smoothing, margin,
+                              average)
         close(host(got.logprobs), r["lp"], r["err"] + H * np.abs(r["lp"]), "logprobs")
         close(host(got.margins), want["margins"], want["z_err"], "margins")
         close(host(got.sequence_logprobs), want["sequence_logprobs"], want["sums_err"], "sums")

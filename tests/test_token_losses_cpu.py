@@ -25,8 +25,8 @@ BAD_ROWS = (dict(x=None), dict(dtype=3), dict(dtype=-1), dict(T=-1), dict(V=0), 
 
 def each_call(**kw):
     """The status of every entry point with these common arguments."""
-    policy = PolicySettings(FAKE, FAKE, None, None, 0.2, 0.2, 0.0, 0)
-    pairs = PreferenceSettings(FAKE, None, 1, 0.1, 0.0, 0.0, 0)
+    policy = PolicySettings(FAKE, FAKE, None, None, 0.2, 0.2, 0.0)
+    pairs = PreferenceSettings(FAKE, None, 1, 0.1, 0.0, 0.0, 0, 0)
     scratch = [kw.pop("scratch", FAKE), kw.pop("size", 1 << 40), None]
     c = common(**kw)
     return [lib().profk_token_logprobs(*c, FAKE, *scratch),
