@@ -23,16 +23,18 @@ namespace {
 
 constexpr int kCountThreads = 1024;
 constexpr u32 kCountBlocks = 64;  // a lane per part of the count
-constexpr u64 kChunk = 1024;      // rows whose terms one wavefront adds up
+constexpr int kTermThreads = 256;
+constexpr u32 kTermBlocks = 512;
 constexpr int kPairThreads = 512;
 constexpr u32 kPairBlocks = 1024;
 constexpr u32 kSlices = 64;       // most parts of a row: a lane each
 constexpr u64 kSplitRows = 512;   // most rows that are split
 
-// A row's part of the policy loss, or a chunk's, or a block of pairs'.
+// A row's terms of the policy loss (times its weight, where there are weights), or a block's sums
+// of them or of its pairs.
 struct Terms {
   double loss, kl;
-  u64 count;  // clipped rows, or live ones
+  u32 clipped, rows;
 };
 // Of a slice of a row that is split.
 struct Part {
@@ -42,29 +44,22 @@ struct Part {
 
 // All of it is written before it is read within a call.
 struct VocabScratch {
-  u32* last;      // a ticket for the chunks (or the pairs' blocks)
+  u32* last;      // a ticket for the blocks that add up
   u32* live;      // kCountBlocks parts of the number of live rows
-  u32* tickets;   // for the rows of each chunk
-  Terms* chunks;  // of each chunk (or of each of kPairBlocks blocks)
+  Terms* blocks;  // of each block that adds up: kTermBlocks or kPairBlocks at most
   Terms* rows;    // T, with the policy loss
   double* lp;     // T, with the preference loss
   Part* parts;    // T * kSlices, where rows are split
 };
-__host__ __device__ inline u64 vocab_chunks(u64 T) { return (T + kChunk - 1) / kChunk; }
 __host__ __device__ inline VocabScratch vocab_scratch(char* s, u64 T) {
   VocabScratch v;
   v.last = (u32*)s;
   v.live = (u32*)(s + 128);
-  s += 512;
-  const u64 chunks = vocab_chunks(T);
-  v.chunks = (Terms*)s;
-  s += sizeof(Terms) * (chunks > kPairBlocks ? chunks : kPairBlocks);
+  v.blocks = (Terms*)(s + 512);
+  s += 512 + sizeof(Terms) * (kTermBlocks > kPairBlocks ? kTermBlocks : kPairBlocks);
   v.rows = (Terms*)s;
   v.lp = (double*)s;
-  s += sizeof(Terms) * T;
-  v.tickets = (u32*)s;
-  s += 8 * (chunks / 2 + 1);
-  v.parts = (Part*)s;
+  v.parts = (Part*)(s + sizeof(Terms) * T);
   return v;
 }
 
@@ -208,7 +203,7 @@ __device__ __forceinline__ float kl_of(float q) {
 struct RowTerms {
   double loss = 0, kl = 0;
   bool clipped = false;
-  float c = 0;  // dloss / dlp, d_loss among it
+  float c = 0;  // dloss / dlp, d_loss and the share among it
 };
 
 // What a row's terms need from memory, on its way before the row itself.
@@ -224,7 +219,7 @@ struct RowInputs {
   }
 };
 
-// share: a row's weight where none are given
+// share: a row's weight in the gradient where none are given (the sums are scaled when added up)
 __device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, const RowInputs& in, const RowEnd& e, double d_loss,
                                              double share) {
   RowTerms o;
@@ -239,7 +234,7 @@ __device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, const RowInputs
   const bool clipped = cut * adv < ratio * adv;
   double loss = -adv * (clipped ? cut : ratio);
   double slope = clipped ? 0.0 : -adv * ratio;
-  const double w = a.weights ? (double)in.weight : share;
+  const double w = a.weights ? (double)in.weight : 1.0;
   if (a.ref) {
     const float q = (float)((double)in.ref - e.lp);
     const double k = (double)kl_of(q);
@@ -251,7 +246,7 @@ __device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, const RowInputs
   }
   o.loss = w * loss;
   o.clipped = clipped;
-  o.c = (float)(w * slope * d_loss);
+  o.c = (float)((a.weights ? w : share) * slope * d_loss);
   return o;
 }
 
@@ -280,7 +275,7 @@ __device__ __forceinline__ double ld_double(const double* p) { return __builtin_
 
 }  // namespace
 
-// The live rows, in kCountBlocks parts at most, and the tickets at 0.
+// The live rows, in kCountBlocks parts at most.
 __global__ __launch_bounds__(kCountThreads) void vocab_count_kernel(VocabArgs a) {
   __shared__ u32 s_n[kCountThreads / kWave];
   const VocabScratch sc = vocab_scratch(a.scratch, a.T);
@@ -288,69 +283,108 @@ __global__ __launch_bounds__(kCountThreads) void vocab_count_kernel(VocabArgs a)
   for (u64 t = (u64)blockIdx.x * kCountThreads + threadIdx.x; t < a.T; t += (u64)gridDim.x * kCountThreads)
     n += row_live(a, t);
   n = block_total<kCountThreads / kWave>(n, s_n);
-  if (threadIdx.x == 0) {
-    sc.live[blockIdx.x] = n;
-    if (blockIdx.x == 0) *sc.last = 0;
-  }
-  for (u64 i = (u64)blockIdx.x * kCountThreads + threadIdx.x; i < vocab_chunks(a.T); i += (u64)gridDim.x * kCountThreads)
-    sc.tickets[i] = 0;
+  if (threadIdx.x == 0) sc.live[blockIdx.x] = n;
 }
 
-// Adds up the policy's terms, in a fixed order: a chunk's by the wavefront that ends its last
-// row, the chunks' by the one that ends the last chunk.  By all lanes of a row's first wavefront.
-__device__ __forceinline__ void add_terms(const VocabArgs& a, const VocabScratch& sc, u64 t, const RowTerms& o, u32 live) {
-  const u32 lane = lane_id();
-  auto store = [&](Terms* to, double loss, double kl, u64 count) {
-    st_double(&to->loss, loss);
-    st_double(&to->kl, kl);
-    st_agent(&to->count, count);
-    drain_memory_ops();
-  };
-  auto total = [&](const Terms* from, u64 n) {
-    Terms s = {0, 0, 0};
+// The sums of a row that is split, from its parts, by one thread.
+template <class T>
+__device__ __forceinline__ RowSums sums_of(const VocabArgs& a, const Part* parts, u64 t) {
+  const Exponent ex = {a.exponent_hi, a.exponent_lo};
+  RowSums row = {kLowest, to_f32(reinterpret_cast<const T*>(a.x)[t * a.ld + (u64)a.tokens[t]]), 0};
+  const Part* p = parts + t * a.slices;
 #pragma unroll 4
-    for (u64 i = lane; i < n; i += kWave) {
-      s.loss += ld_double(&from[i].loss);
-      s.kl += ld_double(&from[i].kl);
-      s.count += ld_agent(&from[i].count);
+  for (u32 i = 0; i < a.slices; ++i) row.top = max_f(row.top, p[i].top);
+#pragma unroll 4
+  for (u32 i = 0; i < a.slices; ++i) row.rest += p[i].rest * (double)ex.of(p[i].top - row.top);
+  if (row.token > row.top) {
+    row.rest *= (double)ex.of(row.top - row.token);
+    row.top = row.token;
+  }
+  return row;
+}
+
+// Block `block` of `blocks` adds up its rows' terms of the policy loss; the last one to end, the
+// blocks' (sums in a fixed order).  Of rows that are split it works the terms out, a thread a row,
+// and the log-probabilities.  (A ticket per 1024 rows, drawn by every row when its terms were
+// written, was one launch less and took 8 ns a row: 131072 x 512 1080 us in place of 110; and a
+// workgroup alone on its CU waited for it.)
+template <class T>
+__device__ __forceinline__ void add_terms(const VocabArgs& a, u32 block, u32 blocks) {
+  constexpr int kWaves = kTermThreads / kWave;
+  __shared__ double s_loss[kWaves], s_kl[kWaves];
+  __shared__ u32 s_clipped[kWaves], s_rows[kWaves], s_last;
+  const VocabScratch sc = vocab_scratch(a.scratch, a.T);
+  Terms sum = {0, 0, 0, 0};
+  for (u64 t = (u64)block * kTermThreads + threadIdx.x; t < a.T; t += (u64)blocks * kTermThreads) {
+    const bool live = row_live(a, t);
+    if (a.slices) {
+      RowEnd end = {0, 1, false};
+      if (live) {
+        const RowInputs in(a, t);
+        end = end_of(a, sums_of<T>(a, sc.parts, t));
+        const RowTerms o = terms_of(a, in, end, 0, 0);
+        sum.loss += o.loss;
+        sum.kl += o.kl;
+        sum.clipped += o.clipped;
+      }
+      if (a.logprobs) a.logprobs[t] = (float)end.lp;
+    } else {
+      const Terms o = sc.rows[t];
+      sum.loss += o.loss;
+      sum.kl += o.kl;
+      sum.clipped += o.clipped;
     }
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      s.loss += __shfl_xor(s.loss, d);
-      s.kl += __shfl_xor(s.kl, d);
-      s.count += __shfl_xor(s.count, d);
-    }
-    return s;
+    sum.rows += live;
+  }
+  if (!a.policy) return;
+  auto total = [&](double& loss, double& kl, u64& clipped, u64& rows) {
+    loss = block_total<kWaves>(loss, s_loss);
+    kl = block_total<kWaves>(kl, s_kl);
+    clipped = block_total<kWaves>((u32)clipped, s_clipped);  // T < 2^31
+    rows = block_total<kWaves>((u32)rows, s_rows);
   };
-  const u64 chunk = t / kChunk, first = chunk * kChunk, rows = a.T - first < kChunk ? a.T - first : kChunk;
-  u32 before = 0;
-  if (lane == 0) {
-    store(sc.rows + t, o.loss, o.kl, o.clipped);
-    before = __hip_atomic_fetch_add(sc.tickets + chunk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  if ((u64)__builtin_amdgcn_readfirstlane(before) + 1 < rows) return;
-  Terms s = total(sc.rows + first, rows);
-  const u64 chunks = vocab_chunks(a.T);
-  if (chunks > 1) {
-    if (lane == 0) {
-      store(sc.chunks + chunk, s.loss, s.kl, s.count);
-      before = __hip_atomic_fetch_add(sc.last, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  double loss = sum.loss, kl = sum.kl;
+  u64 clipped = sum.clipped, rows = sum.rows;
+  total(loss, kl, clipped, rows);
+  if (blocks > 1) {
+    if (threadIdx.x == 0) {
+      Terms* o = sc.blocks + block;
+      st_double(&o->loss, loss);
+      st_double(&o->kl, kl);
+      st_agent((u64*)&o->clipped, rows << 32 | clipped);
+      drain_memory_ops();
+      s_last = __hip_atomic_fetch_add(sc.last, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == blocks;
     }
-    if ((u64)__builtin_amdgcn_readfirstlane(before) + 1 < chunks) return;
-    s = total(sc.chunks, chunks);
+    __syncthreads();
+    if (!s_last) return;
+    loss = kl = 0;
+    clipped = rows = 0;
+    for (u32 i = threadIdx.x; i < blocks; i += kTermThreads) {
+      loss += ld_double(&sc.blocks[i].loss);
+      kl += ld_double(&sc.blocks[i].kl);
+      const u64 both = ld_agent((const u64*)&sc.blocks[i].clipped);
+      clipped += (u32)both;
+      rows += both >> 32;
+    }
+    total(loss, kl, clipped, rows);
   }
-  if (lane == 0) {
-    *a.loss = (float)s.loss;
-    *a.kl = (float)s.kl;
-    *a.clipped = (int64_t)s.count;
-    *a.rows = (int64_t)live;
+  if (threadIdx.x == 0) {
+    const double share = a.weights ? 1.0 : rows ? 1.0 / (double)rows : 0.0;
+    *a.loss = (float)(loss * share);
+    *a.kl = (float)(kl * share);
+    *a.clipped = (int64_t)clipped;
+    *a.rows = (int64_t)rows;
   }
+}
+
+template <class T>
+__global__ __launch_bounds__(kTermThreads) void vocab_terms_kernel(VocabArgs a) {
+  add_terms<T>(a, blockIdx.x, gridDim.x);
 }
 
 // WHOLE: a team takes a row.  PART: a block takes a slice of a row, and leaves its sums; one block
-// more counts the live rows.  JOIN: a block takes a slice of a row again, with the row's sums from
-// all its parts; with the policy loss one block more per row deals with its terms (without a
-// gradient, that one alone).
+// more counts the live rows.  JOIN: a block takes a slice of a row again for its gradient, with the
+// row's sums from all its parts; with the policy loss, blocks behind those add up the terms.
 enum { kWhole, kPart, kJoin };
 
 // A team of TEAM threads with N vectors per thread in registers; of more (MULTI) that many at a
@@ -371,13 +405,13 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
   const u32 wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const u32 team = wave / kTeamWaves, tid = threadIdx.x % TEAM, base = wave % kTeamWaves * kWave, lane = lane_id();
   const Exponent ex = {a.exponent_hi, a.exponent_lo};
-  constexpr bool kSliced = MODE == kPart || (MODE == kJoin && GRAD);  // else a block (or a team) to a row
-  const u32 per = kSliced ? a.slices + (MODE == kJoin && a.policy) : 1;
-  const u32 slice = kSliced ? blockIdx.x % per : 0;
-  const u64 t = kSliced ? blockIdx.x / per : a.row0 + (u64)blockIdx.x * kTeams + team;
-  // this block's are the row's terms and its log-probability
-  const bool own_terms = MODE == kWhole || (MODE == kJoin && slice + 1 == per);
-  const bool own_grad = GRAD && (MODE != kJoin || slice < a.slices);
+  constexpr bool kSliced = MODE != kWhole;
+  if constexpr (MODE == kJoin) {
+    const u32 slices = (u32)a.T * a.slices;
+    if (blockIdx.x >= slices) return add_terms<T>(a, blockIdx.x - slices, gridDim.x - slices);
+  }
+  const u32 slice = kSliced ? blockIdx.x % a.slices : 0;
+  const u64 t = kSliced ? blockIdx.x / a.slices : a.row0 + (u64)blockIdx.x * kTeams + team;
   if constexpr (MODE == kPart) {
     if (t == a.T) {
       u32 n = 0;
@@ -386,10 +420,10 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
       if (tid == 0) {
         *sc.live = n;
         *sc.last = 0;
-        *sc.tickets = 0;  // no more rows than a chunk
       }
     }
   }
+  if (MODE == kWhole && t == 0 && tid == 0 && (a.policy || a.pairs)) *sc.last = 0;  // for the kernel behind this one
   if (t >= a.T) return;  // no barrier below joins teams of a wavefront each
   const T* x = reinterpret_cast<const T*>(a.x) + t * a.ld;
   T* dx = GRAD ? reinterpret_cast<T*>(a.d_x) + t * a.V : nullptr;
@@ -421,18 +455,17 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
     from_f32(0.f, z);
     if (tid < edges) dx[mine] = z;
   };
-  const u32 live_part = MODE != kPart && a.policy && lane < a.count_blocks ? sc.live[lane] : 0;
-  auto n_of = [&]() { return wave_reduce_u32(live_part, [](u32 p, u32 q) { return p + q; }); };  // the live rows of all
+  const u32 live_part = GRAD && a.policy && !a.weights && lane < a.count_blocks ? sc.live[lane] : 0;
   const RowInputs in(a, t);
   const double d_loss = GRAD ? (double)(a.d_loss ? *a.d_loss : 1.f) * (double)a.d_loss_scale : 0.0;
   const bool live = row_live(a, t);
   if (!live || (GRAD && a.given && in.given == 0.f)) {
-    if (own_grad) zero_row();
-    if (tid == 0 && own_terms) {
+    if (GRAD) zero_row();
+    if (MODE == kWhole && tid == 0) {
       if (a.logprobs) a.logprobs[t] = 0.f;
+      if (a.policy) sc.rows[t] = Terms{0, 0, 0, 0};
       if (a.pairs) sc.lp[t] = 0;
     }
-    if (a.policy && own_terms && base == 0) add_terms(a, sc, t, RowTerms(), n_of());
     return;
   }
   const u32 token = (u32)a.tokens[t];
@@ -460,7 +493,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
   RowSums row;
   if constexpr (MODE == kJoin) {
     first = (segments - 1) * (TEAM * N);
-    if (own_grad) load();
+    load();
     if (tid < edges && mine != token) edge = to_f32(x[mine]);
     const Part p = lane < a.slices ? sc.parts[t * a.slices + lane] : Part{0, kLowest};
     row.top = group_reduce<kWave>(p.top, max_f);
@@ -469,7 +502,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
     const int at = slot_of();
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (own_grad && i == at && tid == owner) set_entry<T>(v[i], place, none_entry<T>());
+      if (i == at && tid == owner) set_entry<T>(v[i], place, none_entry<T>());
   } else {
     float x_token = kNone;
     if (tid < edges) {
@@ -547,14 +580,15 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
     row.rest *= (double)ex.of(row.top - row.token);
     row.top = row.token;
   }
-  const u32 n = a.policy ? n_of() : 0;
+  const u32 n = wave_reduce_u32(live_part, [](u32 p, u32 q) { return p + q; });  // the live rows of all
   const RowEnd end = end_of(a, row);
   const RowTerms o = terms_of(a, in, end, d_loss, n ? 1.0 / (double)n : 0.0);
-  if (tid == 0 && own_terms) {
+  if (MODE == kWhole && tid == 0) {
     if (a.logprobs) a.logprobs[t] = (float)end.lp;
+    if (a.policy) sc.rows[t] = Terms{o.loss, o.kl, o.clipped, 0};
     if (a.pairs) sc.lp[t] = end.lp;
   }
-  if (own_grad) {
+  if constexpr (GRAD) {
     if (o.c == 0.f || end.absent) {
       zero_row();
     } else {
@@ -596,23 +630,18 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
       }
     }
   }
-  if (a.policy && own_terms && base == 0) add_terms(a, sc, t, o, n);
 }
 
-// The policy loss of no rows.
+// No rows at all.
 __global__ void vocab_empty_kernel(VocabArgs a) {
+  *vocab_scratch(a.scratch, 0).last = 0;
+  if (!a.policy) return;
   *a.loss = *a.kl = 0.f;
   *a.clipped = *a.rows = 0;
 }
 
-__device__ __forceinline__ float logit_of(const PairArgs& a, u64 t) {
-  const u64 at = t * a.v.ld + (u64)a.v.tokens[t];
-  if (a.dtype == PROFK_FP32) return reinterpret_cast<const float*>(a.v.x)[at];
-  if (a.dtype == PROFK_FP16) return to_f32(reinterpret_cast<const Half16*>(a.v.x)[at]);
-  return to_f32(reinterpret_cast<const Brain16*>(a.v.x)[at]);
-}
-
 // The pairs' losses, and every row's coefficient.  A block takes a pair at a time.
+template <class T>
 __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   constexpr int kWaves = kPairThreads / kWave;
   __shared__ double s_d[kWaves], s_own[2][kWaves], s_ref[2][kWaves];
@@ -620,22 +649,10 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   __shared__ u32 s_rise[4][kWaves];
   __shared__ u32 s_last;
   const VocabScratch sc = vocab_scratch(a.v.scratch, a.v.T);
-  const Exponent ex = {a.v.exponent_hi, a.v.exponent_lo};
   // A live row's log-probability; of rows that are split, from their parts.
   auto lp_of = [&](u64 t, bool here) {
     if (!a.v.slices) return sc.lp[t];
-    if (!here) return 0.0;
-    RowSums row = {kLowest, logit_of(a, t), 0};
-    for (u32 i = 0; i < a.v.slices; ++i) row.top = max_f(row.top, sc.parts[t * a.v.slices + i].top);
-    for (u32 i = 0; i < a.v.slices; ++i) {
-      const Part p = sc.parts[t * a.v.slices + i];
-      row.rest += p.rest * (double)ex.of(p.top - row.top);
-    }
-    if (row.token > row.top) {
-      row.rest *= (double)ex.of(row.top - row.token);
-      row.top = row.token;
-    }
-    return end_of(a.v, row).lp;
+    return here ? end_of(a.v, sums_of<T>(a.v, sc.parts, t)).lp : 0.0;
   };
   // Rows that no sequence takes.
   auto outside = [&](u64 t) {
@@ -742,8 +759,8 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
       for (u64 t = end[1] + threadIdx.x; t < a.v.T; t += kPairThreads) outside(t);
   }
   if (threadIdx.x == 0) {
-    st_double(&sc.chunks[blockIdx.x].loss, total);
-    st_agent(&sc.chunks[blockIdx.x].count, rows);
+    st_double(&sc.blocks[blockIdx.x].loss, total);
+    st_agent((u64*)&sc.blocks[blockIdx.x].clipped, rows);
     drain_memory_ops();
     s_last = __hip_atomic_fetch_add(sc.last, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == gridDim.x;
   }
@@ -752,8 +769,8 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   double loss = 0;
   u64 n = 0;
   for (u32 i = threadIdx.x; i < gridDim.x; i += kPairThreads) {
-    loss += ld_double(&sc.chunks[i].loss);
-    n += ld_agent(&sc.chunks[i].count);
+    loss += ld_double(&sc.blocks[i].loss);
+    n += ld_agent((const u64*)&sc.blocks[i].clipped);
   }
   loss = block_total<kWaves>(loss, s_d);
   n = block_total<kWaves>(n, s_n);
@@ -795,24 +812,48 @@ hipError_t vocab_shape(const VocabArgs& a, hipStream_t s) {
 
 constexpr int kSliceThreads = 256, kSliceVectors = 8;
 
+u32 term_blocks(const VocabArgs& a) {
+  const u64 b = (a.T + kTermThreads - 1) / kTermThreads;
+  return b < 1 ? 1 : b < kTermBlocks ? (u32)b : kTermBlocks;
+}
+
 template <class T>
 hipError_t vocab_split(const VocabArgs& a, hipStream_t s) {
   vocab_kernel<T, kSliceThreads, kSliceVectors, false, true, kPart>
       <<<(u32)a.T * a.slices + 1, kSliceThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.pairs) return e;
+  static_assert(kSliceThreads == kTermThreads, "blocks of one launch");
+  const u32 terms = term_blocks(a);
   if (a.d_x)
     vocab_kernel<T, kSliceThreads, kSliceVectors, true, true, kJoin>
-        <<<(u32)a.T * (a.slices + (a.policy ? 1 : 0)), kSliceThreads, 0, s>>>(a);
+        <<<(u32)a.T * a.slices + (a.policy ? terms : 0), kSliceThreads, 0, s>>>(a);
   else
-    vocab_kernel<T, kSliceThreads, kSliceVectors, false, true, kJoin><<<(u32)a.T, kSliceThreads, 0, s>>>(a);
+    vocab_terms_kernel<T><<<terms, kTermThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t vocab_type(const VocabArgs& a, hipStream_t s) {
+hipError_t vocab_type(VocabArgs a, hipStream_t s) {
   if (a.slices) return vocab_split<T>(a, s);
-  return a.d_x ? vocab_shape<T, true>(a, s) : vocab_shape<T, false>(a, s);
+  hipError_t e;
+  if (a.policy && a.d_x && !a.weights) {  // each row's share
+    const u64 rounds = (a.T + kCountThreads - 1) / kCountThreads;
+    a.count_blocks = rounds < kCountBlocks ? (u32)rounds : kCountBlocks;
+    vocab_count_kernel<<<a.count_blocks, kCountThreads, 0, s>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  e = a.d_x ? vocab_shape<T, true>(a, s) : vocab_shape<T, false>(a, s);
+  if (e != hipSuccess || !a.policy) return e;
+  vocab_terms_kernel<T><<<term_blocks(a), kTermThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t pairs_type(const PairArgs& a, hipStream_t s) {
+  pair_kernel<T><<<a.pairs < kPairBlocks ? (u32)a.pairs : kPairBlocks, kPairThreads, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -830,32 +871,22 @@ u32 vocab_slices(const VocabArgs& a, int dtype) {
 }
 
 hipError_t launch_vocab(VocabArgs a, int dtype, hipStream_t s) {
-  if (!a.T) {
-    if (a.policy)
-      vocab_empty_kernel<<<1, 1, 0, s>>>(a);
-    else if (a.pairs)
-      vocab_count_kernel<<<1, kCountThreads, 0, s>>>(a);
+  if (!a.T) {  // the policy loss of no rows; the pairs' ticket
+    if (a.policy || a.pairs) vocab_empty_kernel<<<1, 1, 0, s>>>(a);
     return hipGetLastError();
   }
   a.slices = vocab_slices(a, dtype);
   a.count_blocks = 1;
-  if ((a.policy || a.pairs) && !a.slices) {
-    const u64 rounds = (a.T + kCountThreads - 1) / kCountThreads;
-    a.count_blocks = rounds < kCountBlocks ? (u32)rounds : kCountBlocks;
-    vocab_count_kernel<<<a.count_blocks, kCountThreads, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
   if (dtype == PROFK_FP32) return vocab_type<float>(a, s);
   if (dtype == PROFK_FP16) return vocab_type<Half16>(a, s);
   return vocab_type<Brain16>(a, s);
 }
 
 hipError_t launch_pairs(PairArgs a, int dtype, hipStream_t s) {
-  a.dtype = dtype;
   a.v.slices = a.v.T ? vocab_slices(a.v, dtype) : 0;
-  pair_kernel<<<a.pairs < kPairBlocks ? (u32)a.pairs : kPairBlocks, kPairThreads, 0, s>>>(a);
-  return hipGetLastError();
+  if (dtype == PROFK_FP32) return pairs_type<float>(a, s);
+  if (dtype == PROFK_FP16) return pairs_type<Half16>(a, s);
+  return pairs_type<Brain16>(a, s);
 }
 
 }  // namespace profk

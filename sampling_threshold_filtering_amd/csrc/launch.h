@@ -376,7 +376,6 @@ struct PairArgs {
   u64 pairs;
   double beta, smoothing, margin;
   bool average;
-  int dtype;                   // set by launch_pairs
   float *margins, *sequence_logprobs, *coefficients;  // pairs, 2 * pairs, T
 };
 size_t vocab_scratch_bytes(u64 T);
