@@ -169,7 +169,7 @@ struct RowEnd {
 __device__ __forceinline__ RowEnd end_of(const VocabArgs& a, const RowSums& r) {
   RowEnd e;
   const double d = ((double)r.token - (double)r.top) * a.inverse_temperature;
-  e.total = r.rest + (double)expf((float)d);
+  e.total = r.rest + exp(d);
   e.absent = false;
   if (!(e.total < __builtin_huge_val())) {  // the row holds a NaN or +inf
     e.lp = __builtin_nan("");
@@ -183,21 +183,6 @@ __device__ __forceinline__ RowEnd end_of(const VocabArgs& a, const RowSums& r) {
     e.absent = (float)e.lp == kNone;
   }
   return e;
-}
-
-// e^q - 1 - q: near 0 by its series, where the difference would lose its digits (the next
-// term is below 2^-26 of the sum).
-__device__ __forceinline__ float kl_of(float q) {
-  if (__builtin_fabsf(q) >= 0.5f) return expm1f(q) - q;
-  float p = 1.f / 362880;
-  p = __builtin_fmaf(p, q, 1.f / 40320);
-  p = __builtin_fmaf(p, q, 1.f / 5040);
-  p = __builtin_fmaf(p, q, 1.f / 720);
-  p = __builtin_fmaf(p, q, 1.f / 120);
-  p = __builtin_fmaf(p, q, 1.f / 24);
-  p = __builtin_fmaf(p, q, 1.f / 6);
-  p = __builtin_fmaf(p, q, 0.5f);
-  return p * q * q;
 }
 
 struct RowTerms {
@@ -229,19 +214,18 @@ __device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, const RowInputs
   }
   if (!a.policy || e.absent) return o;
   const double adv = (double)in.advantage;
-  const double ratio = (double)expf((float)(e.lp - (double)in.old));
+  const double ratio = exp(e.lp - (double)in.old);
   const double cut = __builtin_fmin(__builtin_fmax(ratio, a.clip_low), a.clip_high);
   const bool clipped = cut * adv < ratio * adv;
   double loss = -adv * (clipped ? cut : ratio);
   double slope = clipped ? 0.0 : -adv * ratio;
   const double w = a.weights ? (double)in.weight : 1.0;
   if (a.ref) {
-    const float q = (float)((double)in.ref - e.lp);
-    const double k = (double)kl_of(q);
+    const double q = (double)in.ref - e.lp, rise = expm1(q), k = rise - q;
     o.kl = w * k;
     if (a.kl_weight > 0) {  // with weight 0 the term may be infinite (of a token masked by the lowest value)
       loss += a.kl_weight * k;
-      slope -= a.kl_weight * (double)expm1f(q);
+      slope -= a.kl_weight * rise;
     }
   }
   o.loss = w * loss;
