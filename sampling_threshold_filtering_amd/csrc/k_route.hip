@@ -419,10 +419,12 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       const float p0 = first ? weight(first_e) : 0.f;
       const float d0 = first ? first_d : 0.f;  // where there is no expert d_weights may hold anything
       float wsum = p0, wd = p0 * d0;
+      u32 slots = first;
       if (row.live)
         for (u32 j = g + G; j < a.k; j += G) {
           const u32 e = slot(tr, j);
           if (e >= a.E) continue;
+          ++slots;
           const float p = weight(e);
           wsum += p;
           wd = __builtin_fmaf(p, a.d_weights[tr * a.k + j] * a.scale, wd);
@@ -433,13 +435,16 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       const float mean = wd * r, from = a.normalize ? mean : 0.f;
       if (!a.normalize && !SIGMOID) dot += mean;
       // the only one of a row has weight 1 and gradient 0, exactly, also where its exponential is not 1
-      const u64 firsts = __ballot(first) >> (lane_id() / G * G) & (~0ull >> (kWave - G));
-      const bool lone = a.normalize && a.k <= (u32)G && __popcll(firsts) == 1;
+      bool lone = false;
+      if (a.normalize) {
+        const u64 firsts = __ballot(first) >> (lane_id() / G * G) & (~0ull >> (kWave - G));
+        lone = (a.k <= (u32)G ? (u32)__popcll(firsts) : group_reduce<G>(slots, [](u32 p, u32 q) { return p + q; })) == 1;
+      }
       if (first && !lone) atomicAdd(&d[first_e], p0 * r * (d0 - from));
       if (row.live)
         for (u32 j = g + G; j < a.k; j += G) {
           const u32 e = slot(tr, j);
-          if (e < a.E) atomicAdd(&d[e], weight(e) * r * (a.d_weights[tr * a.k + j] * a.scale - from));
+          if (e < a.E && !lone) atomicAdd(&d[e], weight(e) * r * (a.d_weights[tr * a.k + j] * a.scale - from));
         }
       wave_lds_sync();
 #pragma unroll
