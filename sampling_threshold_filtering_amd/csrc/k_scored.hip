@@ -9,13 +9,12 @@
 // The choice is that of c in 64 bits.  The gradient is k_route.hip's.
 //
 // The choice goes by keys of 32 bits, as in k_route.hip: c in units of (its possible range) /
-// 2^24, from the lowest bias up, above the entry's complement.  A unit is a few times the
-// error of c in 32 bits, so where two neighbours among the first k + 1 keys are within that
-// error of each other, the wavefront ranks those that may be among the first k in 64 bits, a
-// lane each; and where the worst group kept and the best left out are, it chooses the whole row
-// again in 64 bits.  A fixed point rather than the float's own bits:
-// its low bits are what the index leaves of a float's 24 (at 256 experts 15, too few for one
-// row in 30; the fixed point's 24 leave one row in 600).
+// 2^24, from the lowest bias up, above the entry's complement.  c in 32 bits is off by up to
+// some units, so where two neighbours among the first k + 1 keys are within that error of each
+// other, the wavefront ranks those that may be among the first k in 64 bits, a lane each; where
+// the worst group kept and the best left out are, it scores the groups that near in 64 bits; and
+// rows with NaN, or with more near ties than lanes, it chooses again whole.  A fixed point rather
+// than the float's own bits: beside the index a float keeps 15 of its 24 at 256 experts.
 #include "route_device.h"
 
 namespace profk {
@@ -559,8 +558,19 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs arg
         last = n;
         some = j + 1;
       }
+      // Those beyond the wavefront's lanes, a bit each: with one of another logit or bias among them
+      // the whole row is chosen in 64 bits.
+      u32 beyond = 0;
+      if (closes && some == (u32)kWave) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) beyond |= (u32)(key[i] > K::kLow && key[i] < last && border - key[i] <= close) << i;
+      }
+      bool other = false;
+      for (u32 left = beyond; left; left &= left - 1)
+        other |= !same(last, K::kLow - R::index(__builtin_ctz(left), g));
+      differ |= group_reduce<G>((u32)other, max_u) != 0;
       closes = closes && differ;
-      if (some == (u32)kWave && experts > (u32)kWave) unsure = closes;  // more than there are lanes
+      if (group_reduce<G>((u32)(beyond != 0), max_u)) unsure = closes;
       wave_lds_sync();
       for (u64 left = __ballot(closes && !unsure && g == 0); left; left &= left - 1) {
         const RouteArgs& b = arguments_again();
