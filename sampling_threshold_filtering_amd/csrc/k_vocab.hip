@@ -779,6 +779,16 @@ hipError_t vocab_launch(VocabArgs a, hipStream_t s) {
   return hipSuccess;
 }
 
+// The fewest threads whose registers hold the row in 16 vectors each (one wavefront: in 4, where
+// those do).  Few threads wait little for one another, and many rows a CU cover each other's loads.
+// With the next more threads (64 with 16 vectors in place of 4), bf16, 8192 rows, log-probabilities
+// and policy loss with gradient, us: 500 entries 7 -> 9 and 17 -> 21, 2048: 10 -> 11 and 22 -> 26,
+// 8192: 26 -> 34 and 59 -> 68, 32768: 97 -> 94 and 206 -> 202 (the gradient alone 187 -> 214),
+// 65536: 170 -> 260 and 383 -> 453.
+// Longer rows go in segments, twice where there is a gradient: without one 256 threads, six
+// workgroups a CU (512 with 16 vectors: 8192 x 131072 257 us in place of 220).  One workgroup of
+// 1024 holds the longest gradient rows, one a CU: 512 in segments read the row twice, and took 622
+// us in place of 493 for 4096 x 131072 bf16.
 template <class T, bool GRAD>
 hipError_t vocab_shape(const VocabArgs& a, hipStream_t s) {
   const u64 bytes = a.V * sizeof(T);
@@ -847,9 +857,23 @@ size_t vocab_scratch_bytes(u64 T) {
   return (size_t)(uintptr_t)v.parts + sizeof(Part) * kSlices * (T < kSplitRows ? T : kSplitRows);
 }
 
+// Few rows leave most of the 256 CUs idle, so they go in slices of 16 KB that a second launch
+// joins: for the losses, a launch that follows anyway.  A gradient reads its slices again then,
+// where a workgroup with the whole row in registers does not.  bf16, split / whole, us:
+//   log-probabilities  1 x 131072 9.4 / 18, 512 x 131072 32 / 41, 768 x 131072 48 / 48;
+//                      64 x 65536 8.6 / 9.2, 256 x 65536 13 / 9.9, 1 x 32768 8.4 / 7.2
+//   their gradient     64 x 131072 14 / 21, 256 x 131072 44 / 28, 64 x 32768 9.8 / 11, 64 x 16384 9.4 / 7.7
+//   policy loss        64 x 65536 9.9 / 12, 512 x 65536 22 / 21, 512 x 16384 13 / 13, 512 x 8192 11 / 13
+//     with gradient    64 x 131072 15 / 24, 256 x 131072 44 / 32, 64 x 32768 11 / 15, 512 x 16384 18 / 16,
+//                      256 x 16384 12 / 12, 512 x 8192 13 / 17
+//   preference loss    512 x 131072 43 / 49, 512 x 65536 27 / 23, 64 x 65536 13 / 16, 512 x 8192 13 / 15
 u32 vocab_slices(const VocabArgs& a, int dtype) {
-  const u64 bytes = a.V * (dtype == PROFK_FP32 ? 4 : 2);
-  if (a.T > kSplitRows || bytes < (a.policy || a.pairs || a.d_x ? 32768 : 131072)) return 0;
+  const u64 bytes = a.V * (dtype == PROFK_FP32 ? 4 : 2), whole = a.d_x ? 262144 : 131072;  // what registers hold
+  const bool loss = a.policy || a.pairs;
+  if (bytes < (loss ? 16384 : a.d_x ? 65536 : 131072)) return 0;
+  u64 most = kSplitRows;
+  if (bytes <= whole) most = a.d_x && !loss ? 64 : (1 << 24) / bytes < most ? (1 << 24) / bytes : most;
+  if (a.T > most) return 0;
   const u64 s = (bytes + 16383) / 16384;
   return (u32)(s < kSlices ? s : kSlices);
 }

@@ -5,7 +5,7 @@ import pytest
 import sampling_threshold_filtering_amd as stf
 from tests import losses_ref as ref
 from tests.test_gpu_scored import logits as router
-from tests.test_gpu_token_losses import TYPES, H, batch, check_logprobs, close, host, say, some_tokens, values
+from tests.test_gpu_token_losses import TYPES, H, batch, check_grad, check_logprobs, close, host, say, some_tokens, values
 
 pytestmark = pytest.mark.gpu
 
@@ -373,3 +373,81 @@ def test_more_near_ties_than_lanes(E, k, scores):
     say("more than lanes", E, k, scores)
     r = stf.route_tokens(torch.from_numpy(x).cuda(), k, scores=scores, bias=torch.zeros(E, device="cuda"))
     assert np.array_equal(host(r.experts), want)
+
+
+@pytest.mark.parametrize("V,dtype,counts", [
+    (4095, "float32", (512, 513)), (4097, "float32", (512, 513)), (8193, "bfloat16", (511, 513)),
+    (16384, "float16", (255, 256, 257)), (16390, "float32", (64, 65, 127, 128)), (32769, "bfloat16", (64, 65, 129)),
+    (32768, "bfloat16", (64, 65, 256)), (32768, "float32", (64, 65, 129)), (65535, "float16", (64, 65, 129, 513)),
+    (65600, "float32", (64, 65, 512, 513)), (131072, "float16", (64, 65, 512, 513)), (131080, "bfloat16", (5, 512, 513))])
+def test_few_rows_and_one_more(V, dtype, counts):
+    """Around the numbers of rows and lengths up to which a row goes in slices: some rows of each
+    against the formulas."""
+    import torch
+    rng = np.random.default_rng(V)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(V)
+    T = max(counts)
+    wide = (2 * torch.randn((T, V + 3), generator=gen, device="cuda")).to(getattr(torch, dtype))
+    x = wide[:, 1:V + 1]
+    at = np.unique(np.concatenate([[0, counts[0] - 1], rng.integers(0, counts[0], 4)]))
+    tokens = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    tokens[at[0]] = x[at[0]].argmax()
+    r = ref.rows(host(x[at.tolist()]), tokens.cpu().numpy()[at], 0.8)
+    d = values(rng.standard_normal(T))
+    old = torch.full((T,), 0.1 - float(np.log(V)) - 3.0, device="cuda")
+    old[at.tolist()] = values(r["lp"] + 0.1)
+    adv, w = values(rng.standard_normal(T)), values(rng.random(T))
+    want = ref.policy(r, host(old)[at], host(adv)[at], None, host(w)[at], d_loss=64.0)
+    assert want["near"] > 2
+    for n in counts:
+        say("rows and lengths", V, dtype, n)
+        rows = at[at < n]
+        assert rows.size == at.size
+        y, t = x[:n], tokens[:n]
+        err = r["err"] + H * np.abs(r["lp"])
+        close(host(stf.token_logprobs(y, t, temperature=0.8))[at], r["lp"], err, "logprobs")
+        check_grad(stf.token_logprobs_grad(y, t, d[:n], temperature=0.8)[at.tolist()], x[at.tolist()], r, host(d)[at])
+        got, g = stf.policy_loss_and_grad(y, t, old[:n], adv[:n], weights=w[:n], temperature=0.8, d_loss=64.0)
+        close(host(got.logprobs)[at], r["lp"], err, "policy's logprobs")
+        check_grad(g[at.tolist()], x[at.tolist()], r, want["c"], want["c_err"])
+        alone = stf.policy_loss(y, t, old[:n], adv[:n], weights=w[:n], temperature=0.8)
+        close(host(alone.logprobs)[at], r["lp"], err, "logprobs without gradient")
+        pref = stf.preference_loss(y, t, torch.tensor([0, n // 2, n], device="cuda"), temperature=0.8)
+        close(host(pref.logprobs)[at], r["lp"], err, "preference's logprobs")
+        # sums over all rows, of the rows' own values (rounded once: H of each)
+        lp = got.logprobs.double()
+        ratio = torch.exp(lp - old[:n].double())
+        a, ww = adv[:n].double(), w[:n].double()
+        terms = -ww * torch.minimum(ratio * a, ratio.clamp(0.8, 1.2) * a)
+        off = (ww * ratio * a.abs() * (H * lp.abs() + 4 * H)).sum()
+        for z in (got, alone):
+            assert abs(float(z.loss) - float(terms.sum())) <= float(2 * off + 2 * H * terms.sum().abs())
+        gap = float(pref.logprobs[:n // 2].double().sum() - pref.logprobs[n // 2:].double().sum())
+        assert abs(float(pref.margins) - 0.1 * gap) <= 0.1 * float((lp.abs() * H).sum()) + 2 * H * abs(0.1 * gap)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_longest_rows(dtype):
+    import torch
+    V = 1 << 24
+    x = torch.randn((3, V), device="cuda").to(getattr(torch, dtype))
+    tokens = torch.tensor([V - 1, 0, V // 2], device="cuda")
+    say("longest", dtype)
+    lp = stf.token_logprobs(x, tokens)
+    z = torch.logsumexp(x.double(), dim=1, keepdim=True)
+    want = x.gather(1, tokens[:, None]).double() - z
+    # 2^24 exponentials, each off by 4 h at most, of a sum that dominates: 8 h of it with the rest
+    assert ((lp.double() - want[:, 0]).abs() <= 8 * H + H * want[:, 0].abs()).all()
+    d = torch.full((3,), 65536.0, device="cuda")
+    g = stf.token_logprobs_grad(x, tokens, d).double()
+    formula = -65536.0 * torch.exp(x.double() - z)
+    formula.scatter_add_(1, tokens[:, None], d.double()[:, None])
+    assert ((g - formula).abs() <= (16 * H + torch.finfo(x.dtype).eps / 2) * formula.abs() + 1e-30).all()
+
+
+def test_scratch_covers_every_number_of_rows():
+    """More rows need more scratch, also where fewer go in slices."""
+    L = stf.load_library()
+    need = [L.profk_token_loss_scratch(t, 1 << 20) for t in (1, 511, 512, 513, 1024)]
+    assert all(a < b for a, b in zip(need, need[1:]))
