@@ -542,6 +542,18 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs arg
     if (__builtin_expect(__ballot(closes) != 0, 0)) {
       // Whatever may be among the first k: the keys down to as far below the k-th as two may be off
       // each other.  The wavefront ranks them in 64 bits, a lane each.
+      // (m is the k-th.)  Many of one logit and bias, as of a router that starts at zero, are told
+      // apart by their index in any arithmetic, and are not gone through one by one.
+      u32 these = 0;
+      if (closes && m > K::kLow) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) these |= (u32)(key[i] > K::kLow && (key[i] >= m || m - key[i] <= close)) << i;
+      }
+      if (group_reduce<G>((u32)__popc(these), [](u32 p, u32 q) { return p + q; }) > slots + 8) {
+        bool others = false;
+        for (; these && !others; these &= these - 1) others = !same(m, K::kLow - R::index(__builtin_ctz(these), g));
+        closes = group_reduce<G>((u32)others, max_u) != 0;
+      }
       u32 last = 0, border = 0, some = 0;
       bool differ = false;  // neighbours of the same logit and bias go by their index in any arithmetic
       for (u32 j = 0; j < (u32)kWave && j < experts; ++j) {
