@@ -15,6 +15,19 @@
 //   preference: D = sum (or mean) over a sequence's live rows of lp - ref,
 //     z = beta (D_chosen - D_rejected) - margin, l = (1 - h) softplus(-z) + h softplus(z),
 //     dl/dz = sigmoid(z) - (1 - h);  c_t = +-beta dl/dz / pairs (/ the sequence's live rows)
+//
+// Bound by HBM: a row is read once into registers, where its top, its sum and its gradient are
+// taken from, and the gradient written; each row's end is one thread's, in 64 bits.  Kernels'
+// times (MI355X, whose copy reaches 5.0 TB/s and whose reads alone up to 6.5):
+//   log-probabilities  4096 x 131072 bf16 211 to 224 us (4.8 to 5.1 TB/s), 4099 x 50257 fp32 with 30 %
+//                      of the rows masked, which are not read, 111 (5.2), 12000 x 65536 bf16 with 40 %
+//                      masked 171 (5.5), one row of 32000 6.4
+//   gradient           4096 x 131072 bf16 513 (4.2 TB/s read and written), the 12000 x 65536 458 (5.5)
+//   policy loss and gradient  8192 x 131072 bf16 889 (4.8) and 6 for the sum of the terms, 3001 x 50257
+//                      fp16 with 40 % masked 105 (4.6) and 5.6, 48 x 32000 bf16 in slices 4.6 and 6.3
+//   pairs              10 us for 16 pairs of 12000 rows
+// Exponentials and sums take 60 to 77 % of the vector units' time beside that (98 % where rows of
+// 16 bits are only read).
 #include "ops_device.h"
 
 namespace profk {
@@ -122,24 +135,39 @@ struct Exponent {
   __device__ __forceinline__ float of(float d) const {  // of a difference, for all of them: -inf too
     return __builtin_amdgcn_exp2f(__builtin_fmaf(d, lo, d * hi));
   }
+  // In 64 bits, where a likely token's whole R takes the factor; a part of a row joins the others by
+  // `of`, whose rounding, d 2^-24 of a part of weight e^-d, is below 3e-8 of the sum.
+  __device__ __forceinline__ double exactly(float d) const { return exp2((double)d * ((double)hi + (double)lo)); }
 };
 
 // The same from x itself: x hi + (-top hi), each in one rounding, is as exact as x - top and a
 // product, in one instruction less; what the second product's rounding left is a factor of all
-// terms, `left`.  Where a top is so large that the products could overflow (2^100: of a row whose
-// every entry is masked by the type's lowest value, say), it is at least 2^76 from any other value:
-// then 2^-24 in place of the factors, whose products are exact, gives the same terms, 1 or 0.
+// terms, `left`.  Where a top's product passes 2^31 that factor
+// would leave 32 bits' range (half a unit is 64 there), and any other value is at least 64 below it:
+// the terms are 1 or, as 2^-64 of it or less, 0, which a power of two in place of the factors gives,
+// whose products are exact; one that puts the top's at 2^40 puts the next one 2^15 below.
 struct Shifted {
-  float hi, lo, from, left;
+  float hi, lo, from;
   __device__ __forceinline__ Shifted(const Exponent& ex, float top, bool both) {
-    const bool fits = __builtin_fabsf(top) <= 0x1p100f;
-    hi = fits ? ex.hi : both ? 0x1p-25f : 0x1p-24f;
-    lo = fits ? ex.lo : 0x1p-25f;
-    from = fits ? -top * ex.hi : -top * 0x1p-24f;
-    const float rest = __builtin_fmaf(-top, hi, -from);
-    left = fits ? __builtin_amdgcn_exp2f(both ? __builtin_fmaf(-top, lo, rest) : rest) : 1.f;
+    from = -top * ex.hi;
+    const bool fits = __builtin_fabsf(from) < 0x1p31f || !(__builtin_fabsf(top) < __builtin_huge_valf());
+    const float power = __builtin_ldexpf(1.f, 40 - __builtin_amdgcn_frexp_expf(top));
+    hi = fits ? ex.hi : both ? 0.5f * power : power;
+    lo = fits ? ex.lo : 0.5f * power;
+    from = fits ? from : -top * power;
   }
-  // BOTH: with lo.  A 16-bit gradient's rounding hides what it adds.
+  // sum * left.  Rounded to 32 bits, left would put its own error on the whole row; 1 and the rest
+  // apart keep it where |top| / tau is below 2^14.
+  __device__ __forceinline__ double whole(double sum, float top, bool both) const {
+    if (__builtin_fabsf(from) >= 0x1p31f) return sum;  // a power of two
+    const float part = __builtin_fmaf(-top, hi, -from), rest = both ? __builtin_fmaf(-top, lo, part) : part;
+    const float z = rest * 0.693147181f;
+    const bool small = __builtin_fabsf(rest) < 0x1p-10f;
+    const float most = small ? 1.f : __builtin_amdgcn_exp2f(rest), more = small ? __builtin_fmaf(0.5f * z, z, z) : 0.f;
+    return __builtin_fma(sum, (double)more, sum * (double)most);
+  }
+  // BOTH: with lo.  A 16-bit gradient's rounding hides what it adds.  It counts where x is large:
+  // below half a unit of t it changes nothing, which leaves a row's sum off by 1e-8 to 3e-8.
   template <bool BOTH>
   __device__ __forceinline__ float of(float x) const {
     const float t = __builtin_fmaf(x, hi, from);
@@ -281,7 +309,7 @@ __device__ __forceinline__ RowSums sums_of(const VocabArgs& a, const Part* parts
 #pragma unroll 4
   for (u32 i = 0; i < a.slices; ++i) row.rest += p[i].rest * (double)ex.of(p[i].top - row.top);
   if (row.token > row.top) {
-    row.rest *= (double)ex.of(row.top - row.token);
+    row.rest *= ex.exactly(row.top - row.token);
     row.top = row.token;
   }
   return row;
@@ -375,8 +403,10 @@ enum { kWhole, kPart, kJoin };
 // time, the last of them staying for the gradient.
 // Wavefronts a SIMD: with 4 a gradient's 512 threads come twice to a CU, one's loads beside the
 // other's sums; a forward pass holds fewer registers, and at 5 wavefronts in place of 6, two
-// workgroups in place of three, 12000 x 65536 took 173 us in place of 146.
-constexpr int waves_of(int team, int n, bool grad, bool multi) { return team < 256 || n < 16 ? 1 : grad ? 4 : multi ? 5 : 6; }
+// workgroups in place of three, 12000 x 65536 took 173 us in place of 146.  Of 256 threads there
+// are as many workgroups as wavefronts a SIMD; at 5 nothing spills (8192 x 30001 fp16 76 us, at 6
+// 83; 40000 x 9001 bf16 182 and 177).
+constexpr int waves_of(int team, int n, bool grad, bool multi) { return team < 256 || n < 16 ? 1 : grad ? 4 : team == 256 ? 5 : 6; }
 
 template <class T, int TEAM, int N, bool GRAD, bool MULTI, int MODE>
 __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MULTI)) void vocab_kernel(VocabArgs a) {
@@ -534,7 +564,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
         // its place for the next segment's, on its way while the others are dealt with
         if (MULTI && i < next) load_one(first + TEAM * N, i, next);
       }
-      rest += sum * (double)sh.left;
+      rest += sh.whole(sum, top, true);
     }
     rest += (double)ex.of(edge - top);
     // over the lanes, then over the team's wavefronts
@@ -561,7 +591,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
     }
   }
   if (row.token > row.top) {
-    row.rest *= (double)ex.of(row.top - row.token);
+    row.rest *= ex.exactly(row.top - row.token);
     row.top = row.token;
   }
   const u32 n = wave_reduce_u32(live_part, [](u32 p, u32 q) { return p + q; });  // the live rows of all
@@ -587,7 +617,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM, waves_of(TEAM, N, GRAD, MU
       }
       constexpr bool kBoth = sizeof(T) == 4;
       const Shifted sh(ex, row.top, kBoth);
-      const float scaled = scale * sh.left;
+      const float scaled = (float)sh.whole((double)scale, row.top, kBoth);
       for (u32 seg = segments; seg-- > 0;) {
         if (MULTI && (seg + 1 < segments)) {
           first = seg * TEAM * N;

@@ -451,3 +451,37 @@ def test_scratch_covers_every_number_of_rows():
     L = stf.load_library()
     need = [L.profk_token_loss_scratch(t, 1 << 20) for t in (1, 511, 512, 513, 1024)]
     assert all(a < b for a, b in zip(need, need[1:]))
+
+
+@pytest.mark.parametrize("size", [1e6, 3e7, 1e9, 1e10, 1.1e10, 7e11, 1e15, 1e20, 1e30, 3e38])
+@pytest.mark.parametrize("T,V", [(9, 60), (5, 20000), (700, 17000)])
+def test_rows_far_from_zero(T, V, size):
+    """Rows whose largest entries are as large as fp32 holds, of either sign: all of one value (what
+    a mask of -1e10 leaves), and with neighbouring values among them, whose distances are exact."""
+    import torch
+    rng = np.random.default_rng(V)
+    say("far from zero", T, V, size)
+    for sign in (1.0, -1.0):
+        top = np.float32(sign * size)
+        steps = [top]
+        for _ in range(3):
+            steps.append(np.nextafter(steps[-1], np.float32(-np.inf)))
+        x = np.full((T, V), top, dtype=np.float32)
+        x[1] = rng.choice(np.array(steps), size=V)
+        x[2] = rng.choice(np.array(steps + [-np.inf, np.float32(-3.4e38), np.float32(min(top, -2e9))], dtype=np.float32), size=V)
+        x[2, 5] = top
+        x[3] = steps[1]
+        x[3, 7] = top
+        tokens = rng.integers(0, V, T)
+        tokens[2:4] = (5, 7)
+        for tau in (1.0, 0.3, 50.0):
+            r = ref.rows(x, tokens, tau)
+            y, t = torch.from_numpy(x).cuda(), torch.from_numpy(tokens).cuda()
+            got = host(stf.token_logprobs(y, t, temperature=tau))
+            # one entry of weight 2^-64 or less may count as none
+            close(got, r["lp"], r["err"] + H * np.abs(r["lp"]) + V * 2.0 ** -64, "logprobs")
+            c = rng.standard_normal(T)
+            g = host(stf.token_logprobs_grad(y, t, values(c), temperature=tau))
+            c = c.astype(np.float32).astype(np.float64)
+            want, off = ref.grad(r, c)
+            close(g, want, off + H * (np.abs(want) + off) + np.abs(c)[:, None] / tau * V * 2.0 ** -64, "d_logits")
