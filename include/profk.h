@@ -468,7 +468,8 @@ int profk_balance_loss_grad(const void* logits, int32_t dtype, int64_t T, int64_
  *   lp = x_token / temperature - ln sum_j exp(x_j / temperature)
  * A token whose logit is -inf (so too in a row of -inf alone) has lp = -inf; it
  * adds nothing to a loss and its row gets gradient 0 from one.  A row that holds
- * a NaN or +inf has lp = NaN.  Probabilities below 2^-126 count as 0.  Sums over
+ * a NaN or +inf has lp = NaN.  Probabilities below 2^-126 count as 0, and below
+ * 2^-64 where the row's largest |logit| / temperature passes 2^30.  Sums over
  * rows are in 64 bits and have the same bits on every run.  Gradients are of the
  * logits' type, T*V contiguous, rounded once.  `scratch` as above, of at least
  * profk_token_loss_scratch's size.
