@@ -660,7 +660,7 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   constexpr int kWaves = kPairThreads / kWave;
   __shared__ double s_d[kWaves], s_own[2][kWaves], s_ref[2][kWaves];
   __shared__ u64 s_n[kWaves], s_live[2][kWaves];
-  __shared__ u32 s_rise[4][kWaves];
+  __shared__ u32 s_rise[2][kWaves];
   __shared__ u32 s_last;
   const VocabScratch sc = vocab_scratch(a.v.scratch, a.v.T);
   // A live row's log-probability; of rows that are split, from their parts.
@@ -675,32 +675,41 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   };
   double total = 0;
   u64 rows = 0;
-  for (u64 p = blockIdx.x; p < a.pairs; p += gridDim.x) {
-    // Offsets as far as they rise, within [0, T] (T < 2^31): one below an earlier one counts as that.
-    u32 rise[4] = {0, 0, 0, 0};
-    const u64 at[4] = {p, p + 1, p + a.pairs, p + a.pairs + 1};
-    for (u64 k = threadIdx.x; k <= at[3]; k += kPairThreads) {
-      const int64_t o = a.offsets[k];
-      const u32 within = o < 0 ? 0 : (u64)o < a.v.T ? (u32)o : (u32)a.v.T;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) rise[h] = k <= at[h] && within > rise[h] ? within : rise[h];
+  // Offsets as far as they rise, within [0, T] (T < 2^31): one below an earlier one counts as that.
+  // A block takes neighbouring pairs, so it looks at all that come before once.
+  const u64 chunk = (a.pairs + gridDim.x - 1) / gridDim.x, p0 = blockIdx.x * chunk;
+  const u64 p1 = p0 + chunk < a.pairs ? p0 + chunk : a.pairs;
+  auto within = [&](u64 k) {
+    const int64_t o = a.offsets[k];
+    return o < 0 ? 0u : (u64)o < a.v.T ? (u32)o : (u32)a.v.T;
+  };
+  u32 risen[2] = {0, 0};  // up to offsets p and p + pairs
+  if (p0 < p1) {
+    for (u64 k = threadIdx.x; k <= p0 + a.pairs; k += kPairThreads) {
+      const u32 o = within(k);
+      risen[1] = o > risen[1] ? o : risen[1];
+      if (k <= p0) risen[0] = risen[1];
     }
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      rise[h] = wave_reduce_u32(rise[h], [](u32 x, u32 y) { return x > y ? x : y; });
-      if (lane_id() == 0) s_rise[h][threadIdx.x / kWave] = rise[h];
+    for (int h = 0; h < 2; ++h) {
+      risen[h] = wave_reduce_u32(risen[h], [](u32 x, u32 y) { return x > y ? x : y; });
+      if (lane_id() == 0) s_rise[h][threadIdx.x / kWave] = risen[h];
     }
     lds_barrier();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) risen[h] = s_rise[h][w] > risen[h] ? s_rise[h][w] : risen[h];
+  }
+  for (u64 p = p0; p < p1; ++p) {
+    lds_barrier();  // the last pair's sums have been read
     u64 start[2], end[2], live[2] = {0, 0};
     double own[2] = {0, 0}, ref[2] = {0, 0}, ratio[2];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) rise[h] = s_rise[h][w] > rise[h] ? s_rise[h][w] : rise[h];
-      if (h & 1)
-        end[h / 2] = rise[h];
-      else
-        start[h / 2] = rise[h];
+    for (int h = 0; h < 2; ++h) {
+      const u32 o = within(p + h * a.pairs + 1);
+      start[h] = risen[h];
+      end[h] = risen[h] = o > risen[h] ? o : risen[h];
     }
     // the rows of both, all of a row's loads at once
     const u64 first = end[0] - start[0], both = first + (end[1] - start[1]);

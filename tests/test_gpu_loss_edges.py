@@ -485,3 +485,25 @@ def test_rows_far_from_zero(T, V, size):
             c = c.astype(np.float32).astype(np.float64)
             want, off = ref.grad(r, c)
             close(g, want, off + H * (np.abs(want) + off) + np.abs(c)[:, None] / tau * V * 2.0 ** -64, "d_logits")
+
+
+@pytest.mark.parametrize("pairs,T,V", [(1023, 5000, 7), (1025, 3000, 7), (3000, 20000, 5), (5000, 600, 9000), (2500, 0, 5)])
+def test_many_pairs(pairs, T, V):
+    """More pairs than workgroups; offsets that rise and fall, below 0 and beyond T."""
+    import torch
+    rng = np.random.default_rng(pairs)
+    say("many pairs", pairs, T, V)
+    x = batch(rng, T, V, "float32")
+    tokens = some_tokens(rng, x)
+    mask = torch.from_numpy(rng.random(T) < 0.8).cuda()
+    r = ref.rows(host(x), tokens.cpu().numpy(), 1.0, mask.cpu().numpy())
+    rises = np.sort(rng.integers(-5, T + 6, 2 * pairs + 1))
+    jumps = np.where(rng.random(2 * pairs + 1) < 0.2, rng.integers(-5, T // 2 + 1, 2 * pairs + 1), rises)
+    for offsets in (rises, jumps):
+        got = stf.preference_loss(x, tokens, torch.from_numpy(offsets).cuda(), mask=mask)
+        want = ref.preference(r, offsets, pairs)
+        close(host(got.margins), want["margins"], want["z_err"], "margins")
+        close(host(got.loss), want["loss"], want["loss_err"], "loss")
+        assert int(got.rows) == want["rows"]
+        again = stf.preference_loss(x, tokens, torch.from_numpy(offsets).cuda(), mask=mask)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
