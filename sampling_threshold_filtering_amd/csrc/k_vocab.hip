@@ -265,7 +265,7 @@ __device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, const RowInputs
 __device__ __forceinline__ bool row_live(const VocabArgs& a, u64 t) {
   const int64_t k = a.tokens[t];
   const unsigned char m = a.mask ? a.mask[t] : 1;  // both loads at once
-  return m & (u32)((u64)k < a.V) ? true : false;
+  return (u32)(m != 0) & (u32)((u64)k < a.V);
 }
 
 // Sum of one value per thread over the block, in a fixed order; every thread has it.
