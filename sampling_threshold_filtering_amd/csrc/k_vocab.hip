@@ -765,7 +765,8 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
     const double up = (z < 0 ? -z : 0.0) + tail, down = (z > 0 ? z : 0.0) + tail;
     const double sigmoid = (z < 0 ? e : 1.0) / (1.0 + e), other = (z < 0 ? 1.0 : e) / (1.0 + e);
     const double keep = 1.0 - a.smoothing;
-    total += z == z ? keep * up + a.smoothing * down : z;
+    // up and down may be infinite, where the reference gives a token nothing: 0 of that is 0
+    total += z == z ? (keep != 0 ? keep * up : 0.0) + (a.smoothing != 0 ? a.smoothing * down : 0.0) : z;
     if (threadIdx.x == 0) a.margins[p] = (float)z;
     const double slope = a.beta / (double)a.pairs * (a.smoothing * sigmoid - keep * other);
     float c[2];

@@ -44,3 +44,39 @@ def test_any_mask_byte_but_zero_is_set(T, V):
     odd = step(byte.view(torch.bool))
     assert int(odd[4]) == int((byte != 0).sum())  # the live rows
     assert same(odd, step(byte != 0))
+
+
+@pytest.mark.parametrize("T,V", SIZES)
+def test_infinite_margins(T, V):
+    """A token that the reference gives no probability makes a margin infinite: its pair's loss is 0
+    or infinite, and never 0 times infinity."""
+    import torch
+    x, tokens, _, _, _, _ = policy_inputs(T, V, "float32", T)
+    offsets = torch.tensor([0, 10, 20, 30, 40], device="cuda")  # two pairs
+    lp = stf.token_logprobs(x, tokens)
+    beta = 0.5
+    for at, sign in ((3, 1.0), (25, -1.0)):  # in the first pair's preferred sequence, in its other one
+        rf = lp - 0.01
+        rf[12] -= 0.5
+        rf[at] = -INF
+        r = ref.rows(host(x), tokens.cpu().numpy(), 1.0)
+        for smoothing in (0.0, 1.0, 0.25):
+            say("margin", T, V, sign, smoothing)
+            p = stf.preference_loss(x, tokens, offsets, rf, beta=beta, smoothing=smoothing)
+            want = ref.preference(r, host(offsets), 2, host(rf), beta, smoothing)
+            assert float(p.margins[0]) == sign * INF
+            close(host(p.margins[1]), want["margins"][1], want["z_err"][1], "margin")
+            z, e = want["margins"][1], want["z_err"][1]
+            # of the pair with the infinite margin: what weighs nothing adds nothing
+            first = (0.0 if smoothing == 0 else INF) if sign > 0 else (0.0 if smoothing == 1 else INF)
+            second = (1 - smoothing) * np.logaddexp(0, -z) + smoothing * np.logaddexp(0, z)
+            if first == 0:
+                close(host(p.loss), second / 2, e / 2 + 2 * H * second, "loss")
+            else:
+                assert float(p.loss) == INF
+            slope = beta / 2 * (smoothing * (sign > 0) - (1 - smoothing) * (sign < 0))
+            c = host(p.coefficients)
+            assert np.all(c[:10] == slope) and np.all(c[20:30] == -slope)
+            close(c[10:20], want["c"][10:20], want["c_err"][10:20], "coefficients")
+            g = stf.preference_loss_grad(x, tokens, p)
+            assert bool(torch.isfinite(g).all()) and bool(g[:10].any()) == (slope != 0)
