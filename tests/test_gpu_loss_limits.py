@@ -80,3 +80,35 @@ def test_infinite_margins(T, V):
             close(c[10:20], want["c"][10:20], want["c_err"][10:20], "coefficients")
             g = stf.preference_loss_grad(x, tokens, p)
             assert bool(torch.isfinite(g).all()) and bool(g[:10].any()) == (slope != 0)
+
+
+@pytest.mark.parametrize("T,V", SIZES)
+def test_a_factor_of_zero_makes_a_term_zero(T, V):
+    """exp(logprob - old) and exp(ref - logprob) are finite numbers, but 64 bits end at e^709: an
+    advantage or a weight of 0 takes such a row's term away all the same."""
+    import torch
+    x, tokens, old, adv, w, mask = policy_inputs(T, V, "float32", T, True)
+    mask[:3] = True
+    rf = old.clone()
+    adv[0], adv[1], w[1], w[2] = 0.0, -1.0, 0.0, 0.0
+    far, far_ref = old.clone(), rf.clone()
+    lp = stf.token_logprobs(x, tokens)
+    old[1] = lp[1]  # a ratio of 1: clipped no more than one beyond 64 bits is, of a negative advantage
+    far[0], far[1], far_ref[2] = -1000.0, -2000.0, 1000.0
+    for kw, other in ((dict(weights=w, ref_logprobs=rf, kl_weight=0.1), dict(weights=w, ref_logprobs=far_ref, kl_weight=0.1)),
+                      (dict(weights=w, ref_logprobs=rf), dict(weights=w, ref_logprobs=far_ref)),
+                      (dict(weights=w), dict(weights=w))):
+        say("factor", T, V, sorted(kw))
+        p, g = stf.policy_loss_and_grad(x, tokens, old, adv, mask=mask, **kw)
+        q, h = stf.policy_loss_and_grad(x, tokens, far, adv, mask=mask, **other)
+        assert bool(torch.isfinite(p.loss)) and bool(torch.isfinite(g).all())
+        assert same(q, p) and torch.equal(h, g)
+        assert same(stf.policy_loss(x, tokens, far, adv, mask=mask, **other), stf.policy_loss(x, tokens, old, adv, mask=mask, **kw))
+    # a share of the live rows in place of weights
+    far[1] = old[1]
+    p, g = stf.policy_loss_and_grad(x, tokens, old, adv, mask=mask)
+    q, h = stf.policy_loss_and_grad(x, tokens, far, adv, mask=mask)
+    assert bool(torch.isfinite(p.loss)) and same(q, p) and torch.equal(h, g) and not bool(h[0].any())
+    # a row without numbers has no such excuse
+    x[1, 0] = float("nan")
+    assert bool(torch.isnan(stf.policy_loss(x, tokens, old, adv, weights=w).loss))
