@@ -112,3 +112,49 @@ def test_a_factor_of_zero_makes_a_term_zero(T, V):
     # a row without numbers has no such excuse
     x[1, 0] = float("nan")
     assert bool(torch.isnan(stf.policy_loss(x, tokens, old, adv, weights=w).loss))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradients_at_the_temperatures_limits(dtype):
+    """Distances of up to 2^25 over the temperature are rounded to 2^-24 of themselves: by at most 2,
+    where the exponential is below e^-150 and so 0 in either arithmetic, and by u of losses_ref.py up
+    to there."""
+    import torch
+    rng = np.random.default_rng(9)
+    x = batch(rng, 7, 500, dtype)
+    tokens = some_tokens(rng, x)
+    half = torch.finfo(x.dtype).eps / 2
+    least = 2.0 ** -25 if dtype == "float16" else 2.0 ** -134 if dtype == "bfloat16" else 2.0 ** -150
+    for tau in (2.0 ** -20, 2.0 ** -8, 2.0 ** 20):
+        r = ref.rows(host(x), tokens.cpu().numpy(), tau)
+        for d in (1.0, tau):  # entries up to 1 / tau, and up to 1
+            say("temperature", tau, dtype, d)
+            g = stf.token_logprobs_grad(x, tokens, values(np.full(7, d)), temperature=tau)
+            want, off = ref.grad(r, np.full(7, d))
+            off = off + half * (np.abs(want) + off) + least
+            if dtype == "float16":  # beyond its greatest number, 65504, to infinity
+                want = np.where(np.abs(want) > 65520, np.sign(want) * INF, want)
+            assert np.abs(want).max() >= min(d / tau, 1.0) / 2
+            close(host(g), want, off, "d_logits")
+
+
+def test_preferences_at_their_limits():
+    import torch
+    x, tokens, *_ = policy_inputs(300, 700, "float32", 5)
+    offsets = torch.tensor([0, 100, 300], device="cuda")
+    r = ref.rows(host(x), tokens.cpu().numpy(), 1.0)
+    for beta, smoothing, margin in ((0.0, 0.0, 0.0), (0.0, 0.3, 1.0), (1e30, 1.0, 0.0), (-1.0, 0.5, 1e30), (1e4, 0.0, 0.0),
+                                    (-1e4, 0.0, 0.0), (-1e4, 0.25, -1e3)):
+        say("settings", beta, smoothing, margin)
+        p = stf.preference_loss(x, tokens, offsets, beta=beta, smoothing=smoothing, margin=margin)
+        with np.errstate(over="ignore"):
+            want = ref.preference(r, host(offsets), 1, None, beta, smoothing, margin)
+        close(host(p.margins), want["margins"], want["z_err"], "margins")
+        # the loss rises by no more than the margin does
+        close(host(p.loss), want["loss"], want["loss_err"], "loss")
+        z, e = abs(want["margins"][0]), want["z_err"][0]
+        # the sigmoid's own slope is below e^-|z|
+        off = abs(beta) * min(0.25, np.exp(-min(max(z - e, 0.0), 700.0))) * min(e, 1e300) + 4 * H * np.abs(want["c"])
+        close(host(p.coefficients), want["c"], off, "coefficients")
+        g = stf.preference_loss_grad(x, tokens, p)
+        assert bool(torch.isfinite(g).all())
