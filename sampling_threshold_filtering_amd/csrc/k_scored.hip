@@ -142,11 +142,12 @@ __device__ __forceinline__ double softmax_sum(const RouteArgs& a, const T* x, fl
   return sum;
 }
 
-// The code of the choice score of an entry of logit l and bias b; 0: none.
+// The code of the choice score of an entry of logit l and bias b; 0: none.  (A bias of -inf is asked
+// for by itself: beside a score of NaN the sum does not show it.)
 __device__ __forceinline__ u64 choice_code(const RouteArgs& a, float l, float b, float top, double sum) {
   const double s = a.sigmoid ? 1.0 / (1.0 + exp_64(-(double)l)) : exp_64((double)l - (double)top) / sum;
   const double c = a.bias ? s + (double)b : s;
-  return l == kNone || c == -__builtin_huge_val() ? 0 : code_of(c);
+  return l == kNone || b == kNone ? 0 : code_of(c);
 }
 
 // The first keys of a row, `n` of them and among them its k experts, in the order of 64 bits:
