@@ -419,6 +419,9 @@ int profk_route_tokens_grad(const void* logits, int32_t dtype, int64_t T, int64_
  * are scale * s, with `normalize` scale * s over the chosen ones' sum (0 where
  * that is 0).  Live rows, empty slots, counts, rows, scratch and limits as for
  * profk_route_tokens; loss = E * sum_e f_e P_e with P the mean of s / sum_e s.
+ * In both quotients s is what 64 bits hold of it (0 below 2^-1074), however far
+ * below 1 a row's or the chosen scores are; a share below 2^-95 counts as 0, and
+ * so does a weight below 2^-126 without `normalize`.
  * Limits: groups <= 64 (PROFK_EUNSUPPORTED).
  *
  * profk_route_scored_grad: as profk_route_tokens_grad (bias and groups only

@@ -412,35 +412,59 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
       // A normalised weight is of the exponentials themselves: the only one of its row is 1, and
       // its gradient 0, exactly.
       const float unit = a.normalize ? 1.f : inv;
+      bool far = false;  // the chosen scores are relative to the largest of them
+      float largest = kNone, least = kNone;
       auto weight = [&](u32 e) {
-        if constexpr (SIGMOID) return sigmoid_of(to_f32(xt[e])).up;
-        return exp_f(to_f32(xt[e]) - row.top) * unit;
+        const float l = to_f32(xt[e]);
+        if (far) return far_share(l, largest, least);
+        if constexpr (SIGMOID) return sigmoid_of(l).up;
+        return exp_f(l - row.top) * unit;
       };
       const bool first = row.live && first_e < a.E;
-      const float p0 = first ? weight(first_e) : 0.f;
       const float d0 = first ? first_d : 0.f;  // where there is no expert d_weights may hold anything
-      float wsum = p0, wd = p0 * d0;
-      u32 slots = first;
-      if (row.live)
+      float p0 = 0.f, wsum = 0.f, wd = 0.f;
+      auto add_up = [&]() {
+        p0 = first ? weight(first_e) : 0.f;
+        wsum = p0;
+        wd = p0 * d0;
+        if (row.live)
+          for (u32 j = g + G; j < a.k; j += G) {
+            const u32 e = slot(tr, j);
+            if (e >= a.E) continue;
+            const float p = weight(e);
+            wsum += p;
+            wd = __builtin_fmaf(p, a.d_weights[tr * a.k + j] * a.scale, wd);
+          }
+        wsum = group_reduce<G>(wsum, add_f);
+        wd = group_reduce<G>(wd, add_f);
+      };
+      add_up();
+      bool lone = false;
+      if (a.normalize && row.live && wsum < 1.f) {  // (of the row's top or more it is 1 or more)
+        // the only one of a row has weight 1 and gradient 0, exactly, also where its exponential is not 1
+        u32 slots = first;
+        if (first) largest = to_f32(xt[first_e]);
         for (u32 j = g + G; j < a.k; j += G) {
           const u32 e = slot(tr, j);
           if (e >= a.E) continue;
           ++slots;
-          const float p = weight(e);
-          wsum += p;
-          wd = __builtin_fmaf(p, a.d_weights[tr * a.k + j] * a.scale, wd);
+          largest = max_f(largest, to_f32(xt[e]));
         }
-      wsum = group_reduce<G>(wsum, add_f);
-      wd = group_reduce<G>(wd, add_f);
-      const float r = !a.normalize ? 1.f : wsum == 0.f ? 0.f : 1.f / wsum;  // 0: all far below the row's top
+        lone = group_reduce<G>(slots, [](u32 p, u32 q) { return p + q; }) == 1;
+        if (wsum < kFarScores) {
+          largest = group_reduce<G>(largest, max_f);
+          least = SIGMOID ? kLeastLogit : least_held(row.top, inv);
+          far = true;
+          add_up();
+          if constexpr (SIGMOID) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) falling[i] = row.e[i] == 0.f ? 1.f : falling[i];  // of scores that were flushed
+          }
+        }
+      }
+      const float r = !a.normalize ? 1.f : wsum == 0.f ? 0.f : 1.f / wsum;  // 0: no score that 64 bits hold
       const float mean = wd * r, from = a.normalize ? mean : 0.f;
       if (!a.normalize && !SIGMOID) dot += mean;
-      // the only one of a row has weight 1 and gradient 0, exactly, also where its exponential is not 1
-      bool lone = false;
-      if (a.normalize) {
-        const u64 firsts = __ballot(first) >> (lane_id() / G * G) & (~0ull >> (kWave - G));
-        lone = (a.k <= (u32)G ? (u32)__popcll(firsts) : group_reduce<G>(slots, [](u32 p, u32 q) { return p + q; })) == 1;
-      }
       if (first && !lone) atomicAdd(&d[first_e], p0 * r * (d0 - from));
       if (row.live)
         for (u32 j = g + G; j < a.k; j += G) {

@@ -378,7 +378,8 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs arg
     rows += row.live && g == 0;
     // keys
     u32 key[C];
-    const float per = SIGMOID ? unit : unit * inv;
+    // (beside a bias a row of far scores has none: 2^-30 of it, 1/64 of a unit)
+    const float per = !SIGMOID ? unit * inv : row.far ? 0.f : unit;
     float base[C];
     const u32 low = opaque_u32(K::kLow - R::index(0, g));  // of entry 0; here, so that 16 of them do not stay in registers
     from_lds<QUAD, G, C>(s_base, g, base);
@@ -632,6 +633,23 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs arg
       }
       if (a.normalize) {
         chosen = group_reduce<G>(chosen, add_f);
+        if (__builtin_expect(row.live && chosen < kFarScores, 0)) {
+          float largest = kNone;
+          for (u32 j = g; j < a.k; j += G) {
+            const u32 n = a.k > (u32)G ? key_row[j] : mine;
+            if (n > K::kLow) largest = max_f(largest, to_f32(xt[K::kLow - (n & K::kLow)]));
+          }
+          largest = group_reduce<G>(largest, max_f);
+          const float least = SIGMOID ? kLeastLogit : least_held(row.top, inv);
+          chosen = 0.f;
+          for (u32 j = g; j < a.k; j += G) {
+            const u32 n = a.k > (u32)G ? key_row[j] : mine;
+            w = n > K::kLow ? far_share(to_f32(xt[K::kLow - (n & K::kLow)]), largest, least) : 0.f;
+            chosen += w;
+            if (a.k > (u32)G) a.weights[at + j] = w;
+          }
+          chosen = group_reduce<G>(chosen, add_f);
+        }
         if (a.k <= (u32)G) {
           if (g < a.k) a.weights[at + g] = share_of(a, w, chosen);
         } else {
@@ -647,12 +665,18 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs arg
       const float top = __shfl(row.top, (int)from), inverse = __shfl(inv, (int)from);
       const u32 e = choose_exactly<T>(b, r, top, reinterpret_cast<u64*>(s_key[wave][0]));
       const bool slot = lane_id() < b.k, some = slot && e < b.E;
-      float w = 0.f;
+      float w = 0.f, l = kNone;
       if (some) {
-        w = weight_of(b, to_f32(reinterpret_cast<const T*>(b.x)[r * b.ld + e]), top, inverse);
+        l = to_f32(reinterpret_cast<const T*>(b.x)[r * b.ld + e]);
+        w = weight_of(b, l, top, inverse);
         atomicAdd(&s_cnt[e], 1u);
       }
-      const float chosen = group_reduce<kWave>(w, add_f);
+      float chosen = group_reduce<kWave>(w, add_f);
+      if (b.normalize && chosen < kFarScores) {
+        const float largest = group_reduce<kWave>(l, max_f);
+        w = some ? far_share(l, largest, SIGMOID ? kLeastLogit : least_held(top, inverse)) : 0.f;
+        chosen = group_reduce<kWave>(w, add_f);
+      }
       if (slot) {
         b.experts[r * b.k + lane_id()] = some ? (int64_t)e : -1;
         b.weights[r * b.k + lane_id()] = b.normalize ? share_of(b, w, chosen) : w * b.scale;

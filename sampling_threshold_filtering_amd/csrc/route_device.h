@@ -42,6 +42,19 @@ __device__ __forceinline__ Sigmoid sigmoid_of(float x) {
   return s;
 }
 
+// Scores far below 1.  A sigmoid up to e^-21 is its exponential to 2^-30 of itself, so a row that
+// has no larger one, and chosen scores whose sum is below 2^-30, share by their distances from the
+// largest of them: in 32 bits the scores themselves would be 0 from 2^-126 down.  The definition's
+// are 0 where 64 bits hold none, below 2^-1075 (e^-745.13).
+constexpr float kFarScores = 0x1p-30f, kFarLogit = -21.f, kLeastLogit = -745.133f;
+// of a softmax, relative to the row's top and sum
+__device__ __forceinline__ float least_held(float top, float inverse) {
+  return top + __builtin_fmaf(__builtin_amdgcn_logf(inverse), 0.693147181f, kLeastLogit);
+}
+__device__ __forceinline__ float far_share(float l, float largest, float least) {
+  return l < least ? 0.f : exp_f(l - largest);
+}
+
 // Four neighbouring entries with one load or store.
 template <class T>
 struct alignas(4 * sizeof(T)) Four {
@@ -54,6 +67,7 @@ struct Row {
   float v[C];
   float e[C];  // exp(v - top)
   bool live;
+  bool far;  // with sigmoid scores: e is relative to the largest one's
   float top;
 
   static __device__ __forceinline__ u32 index(int i, u32 g) {
@@ -138,9 +152,9 @@ struct Row {
     }
   }
   // Sigmoid scores for e, and falling = 1 - e where the caller has room for it, each to 8 units of
-  // 2^-24 of itself; top is not set.  nan: this lane has one.  e is 0 in a row that does not take
-  // part, and for logits up to -87.4 (the reciprocal's result is flushed; beyond -88 differences do
-  // not count, so that nothing overflows on the way).
+  // 2^-24 of itself.  nan: this lane has one.  e is 0 in a row that does not take part, and beside a
+  // larger score than e^-21 for logits up to -87.4 (the reciprocal's result is flushed; beyond -88
+  // differences do not count, so that nothing overflows on the way); so is falling there.
   template <int N>
   __device__ __forceinline__ void score(bool in, bool& nan, float (&falling)[N]) {
     static_assert(C % 2 == 0, "pairs behind the first, and one");
@@ -150,7 +164,8 @@ struct Row {
     m = max_f(m, v[C - 1]);
 #pragma unroll
     for (int i = 0; i < C; i += 2) nan |= __builtin_isunordered(v[i], v[i + 1]);
-    live = in && !(group_reduce<G>(m, max_f) == kNone);
+    top = group_reduce<G>(m, max_f);
+    live = in && !(top == kNone);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const float x = __builtin_amdgcn_fmed3f(v[i], -88.f, 150.f), y = x * -1.44269502f;
@@ -162,6 +177,14 @@ struct Row {
     if (!in) {  // rows that are not live hold -inf
 #pragma unroll
       for (int i = 0; i < C; ++i) e[i] = 0.f;
+    }
+    far = live && top < kFarLogit;
+    if (__builtin_expect(__ballot(far) != 0, 0)) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        e[i] = far ? far_share(v[i], top, kLeastLogit) : e[i];
+        if constexpr (N == C) falling[i] = far ? 1.f : falling[i];
+      }
     }
     if (__builtin_expect(__ballot(nan) != 0, 0)) {
       if (group_reduce<G>((u32)nan, max_u)) live = in;

@@ -101,3 +101,106 @@ def check_far(x, k, how, mask=None, d_weights=None, d_loss=1.0):
     one = stf.route_tokens_grad(x, r, d_weights, None, normalize=normalize, mask=mask, scores=how["scores"], scale=scale)
     assert bool(torch.isfinite(one).all())
     return r, want
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,k,groups,top", [(8, 1, 1, 1), (24, 5, 8, 3), (60, 20, 6, 5), (160, 6, 8, 3), (700, 20, 7, 3),
+                                            (1024, 64, 64, 33)])
+def test_sigmoid_scores_far_below_one(E, k, groups, top, dtype):
+    """Rows whose every score is next to nothing share as others do, down to where 64 bits hold no
+    score (e^-745)."""
+    import torch
+    rng = np.random.default_rng(E)
+    T = 90
+    x = rng.standard_normal((T, E)) * rng.choice([0.5, 3.0, 20.0], (T, 1))
+    x += np.resize([-18.0, -24.0, -60.0, -87.0, -88.5, -100.0, -150.0, -300.0, -500.0, 0.0], T)[:, None]
+    x = np.maximum(x, -690.0)  # scores that 64 bits hold to the full
+    x[5] = -60000.0            # and none
+    x[6, 1:] = -60000.0
+    x[7, ::2] = -INF
+    x[8, 2:] = -800.0
+    x = torch.from_numpy(x).to("cuda", dtype=getattr(torch, dtype))
+    mask = torch.from_numpy(rng.random(T) < 0.9).cuda()
+    mask[5:9] = True
+    dw = values(rng.standard_normal((T, k)))
+    # steps of 1/16, beside which a far score does not count: the lower index decides among equal ones
+    steps = values(rng.integers(-8, 9, E) / 16.0)
+    off = values(np.where(rng.random(E) < 0.3, -INF, 0.0))
+    for bias in (None, off) if dtype != "float32" else (None, off, steps):
+        for normalize, scale in ((True, 2.5), (False, 1.0)):
+            if bias is steps:
+                rows = (host(x) < -45).all(axis=1)
+                y, m, d = x[torch.from_numpy(rows).cuda()], None, dw[torch.from_numpy(rows).cuda()]
+            else:
+                y, m, d = x, mask, dw
+            say("far sigmoid", E, k, dtype, normalize, bias is None)
+            r, want = check_far(y, k, dict(scores="sigmoid", bias=bias, groups=groups, top_groups=top, group_best=1,
+                                           normalize=normalize, scale=scale), m, d)
+            if normalize and k == 1:
+                held = host(y).astype(np.float64)[np.arange(len(want["experts"])), want["experts"][:, 0]] > -745
+                held &= want["experts"][:, 0] >= 0
+                assert np.all(host(r.weights)[held] == scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,k,groups", [(8, 1, 4), (24, 5, 4), (60, 20, 6), (256, 8, 8), (700, 20, 7)])
+def test_a_softmax_whose_top_is_not_chosen(E, k, groups, dtype):
+    """With the row's top switched off, or its group left out, the others share what is left, however
+    far below they are."""
+    import torch
+    rng = np.random.default_rng(E + 1)
+    T = 60
+    x = rng.standard_normal((T, E)) * rng.choice([1.0, 5.0], (T, 1))
+    x[:, 1] = np.resize([18.0, 25.0, 90.0, 130.0, 400.0, 600.0, 2.0, 60000.0], T)
+    x = torch.from_numpy(x).to("cuda", dtype=getattr(torch, dtype))
+    dw = values(rng.standard_normal((T, k)))
+    off = np.zeros(E)
+    off[1] = -INF
+    left_out = np.zeros(E)
+    left_out[:E // groups] = -4.0
+    for bias, top in ((off, groups), (left_out, groups - 1)):
+        for normalize in (True, False):
+            say("far softmax", E, k, dtype, normalize, top)
+            r, want = check_far(x, k, dict(scores="softmax", bias=values(bias), groups=groups, top_groups=top, group_best=1,
+                                           normalize=normalize, scale=1.5), None, dw)
+            if normalize:
+                sums = host(r.weights).astype(np.float64).sum(axis=1)
+                far = np.resize([1, 1, 1, 1, 1, 1, 1, 0], T)  # beyond e^-745 there is no score
+                assert np.all(np.abs(sums - 1.5 * far) <= 64 * H)
+
+
+def test_gradients_of_far_scores_against_differences():
+    """Through backward(), against differences of the 64-bit definition."""
+    import torch
+    rng = np.random.default_rng(8)
+    T, E, k = 4, 12, 3
+    base = np.stack([rng.permutation(E) for _ in range(T)]).astype(np.float32) * 0.25
+    dw = values(rng.standard_normal((T, k)))
+    d = host(dw).astype(np.float64)
+    bias = np.zeros(E)
+    bias[4] = -INF
+    for scores, far in (("sigmoid", -100.0), ("sigmoid", -300.0), ("softmax", 150.0)):
+        n = base.copy()
+        if scores == "sigmoid":
+            n += np.float32(far)
+        else:
+            n[:, 4] = far
+        leaf = torch.from_numpy(n).cuda().requires_grad_()
+        r = stf.route_tokens(leaf, k, scores=scores, bias=values(bias), balance=True, scale=2.0)
+        ((r.weights * dw).sum() + 3.0 * r.loss).backward()
+        how = dict(scores=scores, bias=bias, scale=2.0)
+
+        def value(v):
+            w = scored_ref(v, k, how)
+            assert np.array_equal(w["experts"], host(r.experts))
+            return float((w["weights"] * d).sum()) + 3.0 * w["loss"]
+
+        n = n.astype(np.float64)
+        say("differences", scores, far)
+        for t in range(T):
+            for e in range(E):
+                up, down = n.copy(), n.copy()
+                up[t, e] += 1e-5
+                down[t, e] -= 1e-5
+                slope = (value(up) - value(down)) / 2e-5
+                assert abs(slope - float(leaf.grad[t, e])) <= 2 * TOL * (4 * np.abs(d).max() + 3.0 * E) + 1e-8
