@@ -245,24 +245,40 @@ __device__ __forceinline__ RowTerms terms_of(const VocabArgs& a, const RowInputs
   const double ratio = exp(e.lp - (double)in.old);
   const double cut = __builtin_fmin(__builtin_fmax(ratio, a.clip_low), a.clip_high);
   const bool clipped = cut * adv < ratio * adv;
-  // A ratio and an e^q that 64 bits do not hold are finite numbers all the same: an advantage or a
-  // weight of 0 makes 0 of them.
-  const bool flat = adv == 0 && ratio == __builtin_huge_val();
-  double loss = flat ? 0.0 : -adv * (clipped ? cut : ratio);
-  double slope = clipped || flat ? 0.0 : -adv * ratio;
   const double w = a.weights ? (double)in.weight : 1.0;
-  auto weighed = [&](double v) { return w == 0 && __builtin_fabs(v) == __builtin_huge_val() ? 0.0 : w * v; };
+  double loss = -adv * (clipped ? cut : ratio);
+  double slope = clipped ? 0.0 : -adv * ratio;
+  double rise = 0, k = 0;
+  // with weight 0 the term may be infinite (of a token masked by the lowest value)
+  const double kl_weight = a.ref ? a.kl_weight : 0.0;
   if (a.ref) {
-    const double q = (double)in.ref - e.lp, rise = expm1(q), k = rise - q;
-    o.kl = weighed(k);
-    if (a.kl_weight > 0) {  // with weight 0 the term may be infinite (of a token masked by the lowest value)
-      loss += a.kl_weight * k;
-      slope -= a.kl_weight * rise;
+    const double q = (double)in.ref - e.lp;
+    rise = expm1(q);
+    k = rise - q;
+  }
+  auto with_kl = [&]() {
+    if (kl_weight > 0) {
+      loss += kl_weight * k;
+      slope -= kl_weight * rise;
+    }
+  };
+  with_kl();
+  o.kl = w * k;
+  o.loss = w * loss;
+  if (__builtin_expect(!(__builtin_fabs(o.loss + o.kl) < __builtin_huge_val()), 0)) {
+    // A ratio and an e^q that 64 bits do not hold are finite numbers all the same: a weight or an
+    // advantage of 0 makes 0 of them.
+    const bool numbers = e.lp == e.lp && in.old == in.old && in.advantage - in.advantage == 0 && in.ref == in.ref;
+    if (w == 0 && numbers) {
+      o.loss = o.kl = slope = 0;
+    } else if (adv == 0 && ratio == __builtin_huge_val()) {
+      loss = slope = 0;
+      with_kl();
+      o.loss = w * loss;
     }
   }
-  o.loss = weighed(loss);
   o.clipped = clipped;
-  o.c = (float)((a.weights ? weighed(slope) : share * slope) * d_loss);
+  o.c = (float)((a.weights ? w : share) * slope * d_loss);
   return o;
 }
 

@@ -104,6 +104,12 @@ def test_a_factor_of_zero_makes_a_term_zero(T, V):
         assert bool(torch.isfinite(p.loss)) and bool(torch.isfinite(g).all())
         assert same(q, p) and torch.equal(h, g)
         assert same(stf.policy_loss(x, tokens, far, adv, mask=mask, **other), stf.policy_loss(x, tokens, old, adv, mask=mask, **kw))
+    # infinite the one way and the other: without a border above, and with the other term
+    adv[1], far[1], far_ref[1] = 1.0, -2000.0, 2000.0
+    kw = dict(weights=w, mask=mask, clip_high=INF, kl_weight=0.1)
+    p, g = stf.policy_loss_and_grad(x, tokens, old, adv, ref_logprobs=rf, **kw)
+    q, h = stf.policy_loss_and_grad(x, tokens, far, adv, ref_logprobs=far_ref, **kw)
+    assert bool(torch.isfinite(p.loss)) and same(q, p) and torch.equal(h, g)
     # a share of the live rows in place of weights
     far[1] = old[1]
     p, g = stf.policy_loss_and_grad(x, tokens, old, adv, mask=mask)
