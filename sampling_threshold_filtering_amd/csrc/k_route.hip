@@ -397,7 +397,7 @@ __global__ __launch_bounds__(kGradThreads) void route_grad_kernel(RouteGradArgs 
     } else {
       row.weigh(in);
     }
-    const float inv = row.inverse();
+    const float inv = row.template inverse<SIGMOID>();
     float out[C];
     float dot = 0.f;
 #pragma unroll

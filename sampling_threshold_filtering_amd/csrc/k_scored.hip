@@ -365,7 +365,7 @@ __global__ __launch_bounds__(kScoredThreads, 4) void scored_kernel(RouteArgs arg
       row.weigh(in);
       nan = !(row.top < __builtin_huge_valf());
     }
-    const float inv = row.inverse();
+    const float inv = row.template inverse<SIGMOID>();
     if (a.loss) {
 #pragma unroll
       for (int i = 0; i < C; i += 4) {

@@ -195,13 +195,16 @@ struct Row {
       }
     }
   }
-  // 1 / the row's sum; 0 for a row that is not live, or all of whose scores are 0
+  // 1 / the row's sum; 0 for a row that is not live.  ALL_NONE: or all of whose scores are 0, which
+  // sigmoid scores may be.
+  template <bool ALL_NONE = false>
   __device__ __forceinline__ float inverse() const {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) s += e[i];
     s = group_reduce<G>(s, add_f);
-    return live && s != 0.f ? 1.f / s : 0.f;
+    if constexpr (ALL_NONE) return live && s != 0.f ? 1.f / s : 0.f;
+    return live ? 1.f / s : 0.f;
   }
 };
 
