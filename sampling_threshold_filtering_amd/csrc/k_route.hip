@@ -25,8 +25,8 @@
 // a fixed order (no floating-point atomics: the loss has the same bits on every run).  Summed
 // in 32 bits to the end, the error grew with the batch: 3e-6 of P_e at 128 rows a lane.
 //
-// 65536 x 256 bf16, k = 8: forward 24 us and 4.7 to join the blocks, backward 21 us;
-// 131072 x 160 bf16, loss alone: forward 17 and 4.7, backward 24 us (3.5 TB/s); backward of
+// 65536 x 256 bf16, k = 8: forward 24 us and 4.8 to join the blocks, backward 21.3 us;
+// 131072 x 160 bf16, loss alone: forward 17 and 4.9, backward 24 us (3.5 TB/s); backward of
 // sigmoid scores, a sum and a factor more, 65536 x 256: 23 us.  The forward
 // is bound by its vector instructions (90 % of the cycles in both): per entry 3 to load and
 // convert, 7 for the exponential and its sum, 4 for a selection key and 2 for each of the k

@@ -18,10 +18,12 @@
 //
 // Bound by vector instructions: 65536 x 256 bf16, sigmoid, bias, 4 of 8 groups, k = 8 with the loss
 // takes 54 us (74 % of the busy cycles; 33 MB of logits) and 5 for the joining launch, and the
-// gradient 23 (79 %); the plain routing of that size 24, 5 and 21.  What it has on top: the keys'
-// bias from LDS and groups' two best through LDS, a third of the cycles, and rows chosen in 64 bits,
-// some 9 us.  8 x 256 fp32 11.5 us, one row's chain.  512 threads and four wavefronts a SIMD: the
-// 64-bit choice takes 110 to 128 registers; with fewer it spills.
+// gradient 23 (78 %); the plain routing of that size 24, 5 and 21.  What it has on top: the keys'
+// bias from LDS and groups' two best through LDS, a third of the cycles (half of those bank
+// conflicts), and the 64-bit paths, some 9 us: less by the rows that take them, one in a thousand
+// there, than by standing in the rows' loop.  They take 108 to 142 vector registers, so four
+// wavefronts a SIMD fit, and 68 to 87 scalar registers live in lanes of vector ones; 16 entries a
+// lane spill up to 9 vector registers.  8 x 256 fp32 11.3 us, one row's chain.
 #include "route_device.h"
 
 namespace profk {

@@ -19,15 +19,17 @@
 // Bound by HBM: a row is read once into registers, where its top, its sum and its gradient are
 // taken from, and the gradient written; each row's end is one thread's, in 64 bits.  Kernels'
 // times (MI355X, whose copy reaches 5.0 TB/s and whose reads alone up to 6.5):
-//   log-probabilities  4096 x 131072 bf16 211 to 224 us (4.8 to 5.1 TB/s), 4099 x 50257 fp32 with 30 %
-//                      of the rows masked, which are not read, 111 (5.2), 12000 x 65536 bf16 with 40 %
-//                      masked 171 (5.5), one row of 32000 6.4
-//   gradient           4096 x 131072 bf16 513 (4.2 TB/s read and written), the 12000 x 65536 458 (5.5)
-//   policy loss and gradient  8192 x 131072 bf16 889 (4.8) and 6 for the sum of the terms, 3001 x 50257
-//                      fp16 with 40 % masked 105 (4.6) and 5.6, 48 x 32000 bf16 in slices 4.6 and 6.3
-//   pairs              10 us for 16 pairs of 12000 rows
-// Exponentials and sums take 60 to 77 % of the vector units' time beside that (98 % where rows of
-// 16 bits are only read).
+//   log-probabilities  4096 x 131072 bf16 217 us (4.9 TB/s), 4099 x 50257 fp32 with 30 % of the rows
+//                      masked, which are not read, 111 (5.2), 12000 x 65536 bf16 with 40 % masked 167
+//                      (5.7), one row of 32000 6.8
+//   gradient           4096 x 131072 bf16 478 to 518 (4.1 to 4.5 TB/s read and written), the 12000 x 65536
+//                      463 (5.4)
+//   policy loss and gradient  8192 x 131072 bf16 890 to 980 (4.4 to 4.8) and 6 for the sum of the terms,
+//                      3001 x 50257 fp16 with 40 % masked 105 (4.6) and 5.7, 48 x 32000 bf16 in slices 4.7
+//                      and 6.6
+//   pairs              10.8 us for 16 pairs of 12000 rows
+// Beside that exponentials and sums take 45 % (32 bits) to 84 % of the vector units' cycles, and all of
+// them in the 12000 x 65536 log-probabilities.
 #include "ops_device.h"
 
 namespace profk {
@@ -422,10 +424,13 @@ enum { kWhole, kPart, kJoin };
 // A team of TEAM threads with N vectors per thread in registers; of more (MULTI) that many at a
 // time, the last of them staying for the gradient.
 // Wavefronts a SIMD: with 4 a gradient's 512 threads come twice to a CU, one's loads beside the
-// other's sums; a forward pass holds fewer registers, and at 5 wavefronts in place of 6, two
-// workgroups in place of three, 12000 x 65536 took 173 us in place of 146.  Of 256 threads there
-// are as many workgroups as wavefronts a SIMD; at 5 nothing spills (8192 x 30001 fp16 76 us, at 6
-// 83; 40000 x 9001 bf16 182 and 177).
+// other's sums; a forward pass holds fewer registers, and of 512 threads at 6 wavefronts there are
+// three workgroups (12000 x 65536 bf16, 40 % masked, 189 us a call; at 5, with two, 212).  Of 256
+// threads there are as many workgroups as wavefronts; at 6 rows in segments spill most of theirs
+// (8192 x 131072 bf16 410 us at 5 and 666 at 6, 8192 x 30001 fp16 88 and 94, 40000 x 9001 bf16 183
+// and 178).  What spills at these bounds: two vector registers of 16-bit forward rows of 512
+// threads and in segments, 35 of gradients in segments; scalar ones, into lanes of a vector one: 42
+// to 44 of the gradients, 24 of joins and forward segments.
 constexpr int waves_of(int team, int n, bool grad, bool multi) { return team < 256 || n < 16 ? 1 : grad ? 4 : team == 256 ? 5 : 6; }
 
 template <class T, int TEAM, int N, bool GRAD, bool MULTI, int MODE>
@@ -674,7 +679,9 @@ __global__ void vocab_empty_kernel(VocabArgs a) {
   *a.clipped = *a.rows = 0;
 }
 
-// The pairs' losses, and every row's coefficient.  A block takes a pair at a time.
+// The pairs' losses, and every row's coefficient.  A block takes a run of neighbouring pairs, one at a
+// time with all of its threads: few pairs of long sequences leave the other CUs idle (131072 rows in
+// one pair 299 us with their log-probabilities, in 64 pairs 87).
 template <class T>
 __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs a) {
   constexpr int kWaves = kPairThreads / kWave;
@@ -845,10 +852,10 @@ hipError_t vocab_launch(VocabArgs a, hipStream_t s) {
 // and policy loss with gradient, us: 500 entries 7 -> 9 and 17 -> 21, 2048: 10 -> 11 and 22 -> 26,
 // 8192: 26 -> 34 and 59 -> 68, 32768: 97 -> 94 and 206 -> 202 (the gradient alone 187 -> 214),
 // 65536: 170 -> 260 and 383 -> 453.
-// Longer rows go in segments, twice where there is a gradient: without one 256 threads, six
-// workgroups a CU (512 with 16 vectors: 8192 x 131072 257 us in place of 220).  One workgroup of
-// 1024 holds the longest gradient rows, one a CU: 512 in segments read the row twice, and took 622
-// us in place of 493 for 4096 x 131072 bf16.
+// Longer rows go in segments, twice where there is a gradient: without one 256 threads, five
+// workgroups a CU (8192 x 131072 bf16 410 us; 512 threads in segments, which spill at their bound,
+// 637; 1024, which hold the row, 450).  One workgroup of 1024 holds the longest gradient rows, one a
+// CU: 512 in segments read the row twice, and took 590 us in place of 450 for 4096 x 131072 bf16.
 template <class T, bool GRAD>
 hipError_t vocab_shape(const VocabArgs& a, hipStream_t s) {
   const u64 bytes = a.V * sizeof(T);
