@@ -426,8 +426,8 @@ enum { kWhole, kPart, kJoin };
 // Wavefronts a SIMD: with 4 a gradient's 512 threads come twice to a CU, one's loads beside the
 // other's sums; a forward pass holds fewer registers, and of 512 threads at 6 wavefronts there are
 // three workgroups (12000 x 65536 bf16, 40 % masked, 189 us a call; at 5, with two, 212).  Of 256
-// threads there are as many workgroups as wavefronts; at 6 rows in segments spill most of theirs
-// (8192 x 131072 bf16 410 us at 5 and 666 at 6, 8192 x 30001 fp16 88 and 94, 40000 x 9001 bf16 183
+// threads there are as many workgroups as wavefronts; at 6 rows in segments spill 19 to 25 vector
+// registers (8192 x 131072 bf16 410 us at 5 and 666 at 6, 8192 x 30001 fp16 88 and 94, 40000 x 9001 bf16 183
 // and 178).  What spills at these bounds: two vector registers of 16-bit forward rows of 512
 // threads and in segments, 35 of gradients in segments; scalar ones, into lanes of a vector one: 42
 // to 44 of the gradients, 24 of joins and forward segments.
@@ -853,8 +853,8 @@ hipError_t vocab_launch(VocabArgs a, hipStream_t s) {
 // 8192: 26 -> 34 and 59 -> 68, 32768: 97 -> 94 and 206 -> 202 (the gradient alone 187 -> 214),
 // 65536: 170 -> 260 and 383 -> 453.
 // Longer rows go in segments, twice where there is a gradient: without one 256 threads, five
-// workgroups a CU (8192 x 131072 bf16 410 us; 512 threads in segments, which spill at their bound,
-// 637; 1024, which hold the row, 450).  One workgroup of 1024 holds the longest gradient rows, one a
+// workgroups a CU (8192 x 131072 bf16 410 us; 512 threads in segments, which spill 25 registers at
+// their bound, 637; 1024, which hold the row, 450).  One workgroup of 1024 holds the longest gradient rows, one a
 // CU: 512 in segments read the row twice, and took 590 us in place of 450 for 4096 x 131072 bf16.
 template <class T, bool GRAD>
 hipError_t vocab_shape(const VocabArgs& a, hipStream_t s) {

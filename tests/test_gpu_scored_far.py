@@ -204,3 +204,43 @@ def test_gradients_of_far_scores_against_differences():
                 down[t, e] -= 1e-5
                 slope = (value(up) - value(down)) / 2e-5
                 assert abs(slope - float(leaf.grad[t, e])) <= 2 * TOL * (4 * np.abs(d).max() + 3.0 * E) + 1e-8
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(24, 5, 4), (60, 20, 6), (256, 8, 8)])
+def test_far_rows_among_others_in_long_batches(E, k, groups, scores):
+    """A group of lanes takes far and ordinary rows in turn: each is what it is in a batch of its own.
+    Up to 64 experts a long batch has 8 lanes a row and a short one 16, so shares are summed in another
+    order: each of the two sums is off by 22 h at most, as are the gradient's sums, and the products by
+    4 h; from 65 experts on the bits are the same."""
+    import torch
+    rng = np.random.default_rng(E + 2)
+    T, few = 70001, 257
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E)
+    x = torch.randn((T, E), generator=gen, device="cuda") * 2
+    far = torch.rand(T, generator=gen, device="cuda") < 0.3
+    if scores == "sigmoid":
+        x[far] -= 120.0
+    else:
+        x[far, 1] = 150.0
+    bias = np.zeros(E)
+    bias[1] = -INF
+    dw = torch.randn((T, k), generator=gen, device="cuda")
+    how = dict(scores=scores, bias=values(bias), groups=groups, top_groups=groups - 1, group_best=1, scale=2.0)
+    say("long far", scores, E, k)
+    r = stf.route_tokens(x, k, **how)
+    g = stf.route_tokens_grad(x, r, dw, scores=scores, scale=2.0)
+    assert np.all(np.abs(r.weights.double().sum(dim=1).cpu().numpy() - 2.0) <= 64 * H)
+    for s in (slice(0, few), slice(T // 2, T // 2 + few), slice(T - few, T)):
+        q = stf.route_tokens(x[s], k, **how)
+        h = stf.route_tokens_grad(x[s], q, dw[s], scores=scores, scale=2.0)
+        assert torch.equal(q.experts, r.experts[s])
+        if E > 64:
+            assert torch.equal(q.weights, r.weights[s]) and torch.equal(h, g[s])
+        else:
+            assert bool(((q.weights - r.weights[s]).abs() <= 52 * H * q.weights).all())
+            size = 2.0 * dw[s].abs().amax(dim=1, keepdim=True)
+            assert bool(((h - g[s]).abs() <= 4 * 52 * H * size).all())
+    at = torch.from_numpy(np.sort(rng.choice(T, 200, replace=False))).cuda()
+    check_far(x[at], k, how, None, dw[at], 0.5)
